@@ -14,7 +14,9 @@ The functions carry the names of the C entry points in ``include/gemm.h``:
 returns a new fp32 tensor): it checks the
 tensors' device, dtype, shape and contiguity on the host, passes their data
 pointers and torch's current HIP stream, and raises ``GemmError`` on a
-negative status.  Importing this module fails loudly when the library has not
+negative status.  The vocabulary losses (``linear_cross_entropy``,
+``linear_distill`` and their backward calls) are in ``loss.py`` and offered here
+too.  Importing this module fails loudly when the library has not
 been built; there is no fallback path.
 """
 from __future__ import annotations
@@ -29,6 +31,8 @@ __all__ = [
     "gemm_workspace_size", "gemm_unit_range",
     "gemm_set_stream", "gemm_sync_status", "gemm_release", "gemm_last_error", "gemm_num_cus",
     "gemm_version", "gemm_tensors", "matmul", "plan_dict", "library_path",
+    "GemmLossArgs", "GemmLossPlan", "gemm_loss_forward", "gemm_loss_backward", "gemm_loss_plan",
+    "linear_cross_entropy", "linear_cross_entropy_backward", "linear_distill", "linear_distill_backward",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -497,3 +501,10 @@ def matmul(a, b, b_layout: str = "kn", out=None, alpha: Optional[float] = None, 
     gemm_tensors(a, b, out, b_layout=b_layout, mode=mode, splits=splits, atomic=atomic, alpha=alpha, beta=beta,
                  bias=bias, act=act)
     return out
+
+
+from .loss import (  # noqa: E402  (needs the loaded library)
+    GEMM_LOSS_BF16, GEMM_LOSS_DISTILL, GEMM_LOSS_DW_FP32, GEMM_LOSS_DW_FP32_ADD, GEMM_LOSS_DW_SAME, GEMM_LOSS_FP16,
+    GEMM_LOSS_FP32, GEMM_LOSS_MAX_ENTRIES, GEMM_LOSS_MAX_H, GEMM_LOSS_MAX_T, GEMM_LOSS_MAX_V, GEMM_LOSS_XENT,
+    GemmLossArgs, GemmLossPlan, gemm_loss_backward, gemm_loss_forward, gemm_loss_plan, linear_cross_entropy,
+    linear_cross_entropy_backward, linear_distill, linear_distill_backward)

@@ -15,7 +15,7 @@ from pathlib import Path
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libdgw_gemm.so"
-SOURCES = ["gemm_kernels.hip", "gemm_api.hip", "plan.cpp"]
+SOURCES = ["gemm_kernels.hip", "gemm_api.hip", "plan.cpp", "loss_kernels.hip", "loss_api.hip"]
 ARCH = "gfx950"
 
 
@@ -77,7 +77,7 @@ def is_stale() -> bool:
     if not LIB.exists():
         return True
     t = LIB.stat().st_mtime
-    srcs = [CSRC / s for s in SOURCES] + list(CSRC.glob("*.h")) + [PKG.parent / "include" / "gemm.h"]
+    srcs = [CSRC / s for s in SOURCES] + list(CSRC.glob("*.h")) + list((PKG.parent / "include").glob("*.h"))
     return any(p.stat().st_mtime > t for p in srcs if p.exists())
 
 

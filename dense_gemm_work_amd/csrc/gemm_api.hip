@@ -27,6 +27,7 @@
 #include <vector>
 
 #include "../../include/gemm.h"
+#include "internal.h"
 #include "kernels.h"
 #include "plan.h"
 
@@ -604,6 +605,38 @@ int run(const gemm_args_t &a, bool noalloc = false, const gemm_group_t *groups =
 }
 
 }  // namespace
+
+namespace dgw {
+
+int set_error(int code, const std::string &msg) { return fail(code, msg); }
+int set_hip_error(hipError_t e, const char *what) { return fail_hip(e, what); }
+void clear_error() { g_err.clear(); }
+hipStream_t thread_stream() { return g_stream; }
+
+int current_device_cus(int *out) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState *ds = nullptr;
+    const int rc = device_state(dev, &ds);
+    if (rc == GEMM_OK) *out = ds->num_cus;
+    return rc;
+}
+
+int library_workspace(int64_t bytes, hipStream_t stream, void **out) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState *ds = nullptr;
+    int rc = device_state(dev, &ds);
+    if (rc == GEMM_OK) rc = ensure_data(*ds, bytes, stream);
+    if (rc == GEMM_OK) *out = ds->data;
+    return rc;
+}
+
+}  // namespace dgw
 
 extern "C" {
 

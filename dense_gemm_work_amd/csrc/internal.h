@@ -1,0 +1,27 @@
+// internal.h -- what the library's entry points share: the thread's error text
+// and stream, and the library workspace (gemm_api.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <string>
+
+namespace dgw {
+
+// Set the thread's error text and return `code`.
+int set_error(int code, const std::string &msg);
+int set_hip_error(hipError_t e, const char *what);
+void clear_error();
+
+// The calling thread's stream (gemm_set_stream).
+hipStream_t thread_stream();
+
+// Compute units of the current device.
+int current_device_cus(int *out);
+
+// At least `bytes` of the current device's library workspace.  Refused while
+// `stream` is being captured if the workspace would have to grow.
+int library_workspace(int64_t bytes, hipStream_t stream, void **out);
+
+}  // namespace dgw

@@ -1,0 +1,106 @@
+// loss.h -- launch interface of the vocabulary-loss kernels (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm_loss.h"
+
+namespace dgw {
+
+// Tile shapes (P x Q; P: the dimension contiguous in the result).
+enum LossTile : int { LT_128x128 = 0 };
+struct LossTileShape {
+    int p, q, per_cu;   // rows of P and Q, workgroups resident per CU
+};
+LossTileShape loss_tile_shape(int tile);
+
+// An operand as it lies in memory: element (row, k) at base[row * ld + k]
+// (kc) or base[k * ld + row].
+struct LossMatrix {
+    const uint16_t *base;
+    int64_t ld;
+    int rows;
+    bool kc;
+};
+
+// The rows' sparse targets as the logits' epilogues read them: XENT: the int64
+// target itself, weight 1; DISTILL: [T][stride] int32 entries (-1: none) and
+// their probabilities.
+struct LossTargets {
+    const int64_t *target;
+    const int32_t *index;
+    const float *weight;
+    int stride;          // entries per row in memory, a multiple of 4
+};
+
+// Forward statistics of a logits launch: per tile of the vocabulary and row, the
+// maximum logit, the sum of exp2((z - max) c) and the targets' weighted logits.
+struct LossStats {
+    float *max, *sum, *dot;   // [tiles_v][T]
+};
+
+// What a row contributes to the logits' gradient, dz = a p - b q (0 when !on).
+struct LossRow {
+    float lse2;   // lse * log2 e
+    float a, b;
+    float on;
+};
+
+struct LossProblem {
+    int T, V, H;
+    float c;              // log2(e) / tau
+    LossMatrix x, w;      // w offset to the piece's first entry
+    int64_t v0;           // that entry's index
+    LossTargets targets;
+};
+
+// Logits of p.T rows over p.V entries, reduced to statistics.
+hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const LossStats &s, hipStream_t stream);
+
+// Logits again, as their gradient dz [T][ldd] (16 bits; ldd a multiple of 8,
+// zeros behind p.V), times *scale when scale != nullptr.
+hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz,
+                          int64_t ldd, hipStream_t stream);
+
+// out[q][p] = sum_k P[p][k] Q[q][k], times *unscale when unscale != nullptr.
+enum LossOut : int {
+    LO_16 = 0,         // the operands' type
+    LO_F32 = 1,        // fp32
+    LO_F32_ADD = 2,    // fp32, added to out
+    LO_SLOTS = 3,      // fp32 partials per (slice, tile), register order
+    LO_SLOTS_ADD = 4,  // the same, added to what the slots hold
+};
+struct LossProduct {
+    LossMatrix P, Q;
+    int K;
+    int splits;
+    int out_kind;
+    void *out;
+    int64_t ldo;
+    const float *unscale;   // not applied to slots
+};
+hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStream_t stream);
+
+// out from the slots of `splits` slices: out_kind LO_16, LO_F32 or LO_F32_ADD.
+hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream);
+int64_t loss_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits);
+
+// The teacher's entries: probabilities, int32 indices and sum q log q per row
+// (NaN where an entry is out of range; -infinity marks rows without entries).
+hipError_t launch_loss_teacher(int64_t T, int K, int stride, int64_t V, const int64_t *index, const void *logits,
+                               uint32_t type, float tau, int32_t *index_out, float *weight, float *entropy,
+                               hipStream_t stream);
+
+// loss and lse from the statistics of `tiles` tiles.
+hipError_t launch_loss_finish(const gemm_loss_args_t &a, int tiles, const LossStats &s, const float *entropy,
+                              hipStream_t stream);
+
+// The rows' factors; for fp16 also scale[0] (multiplied into dz) and scale[1] = 1 / scale[0].
+hipError_t launch_loss_rows(const gemm_loss_args_t &a, const float *entropy, LossRow *rows, float *scale,
+                            hipStream_t stream);
+
+hipError_t launch_loss_zero(void *out, int64_t rows, int64_t row_bytes, int64_t ld_bytes, hipStream_t stream);
+
+}  // namespace dgw

@@ -1,0 +1,355 @@
+// loss_api.hip -- the C ABI declared in include/gemm_loss.h: argument checks,
+// planning, workspace layout and kernel launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <string>
+
+#include "../../include/gemm_loss.h"
+#include "internal.h"
+#include "loss.h"
+
+namespace {
+
+using dgw::set_error;
+using dgw::set_hip_error;
+
+constexpr int64_t MAX_LD = int64_t(1) << 21;   // a tile's rows then stay within 32-bit byte offsets
+constexpr int64_t PIECE_BYTES = int64_t(256) << 20;   // the logits' gradient of one piece
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
+
+int64_t row_of_w(const gemm_loss_args_t &a) { return (a.layout & 0xFu) == GEMM_B_NK ? a.H : a.V; }
+int64_t rows_of_w(const gemm_loss_args_t &a) { return (a.layout & 0xFu) == GEMM_B_NK ? a.V : a.H; }
+int64_t or_packed(int64_t ld, int64_t packed) { return ld ? ld : packed; }
+
+int bad(const char *msg) { return set_error(GEMM_ERR_INVALID, msg); }
+
+// What the host can tell from sizes, words and flags alone.
+int check_sizes(const gemm_loss_args_t &a) {
+    if (a.layout & ~0x1Fu || (a.layout & 0xEu)) return bad("layout word has unknown bits");
+    if (a.kind > GEMM_LOSS_DISTILL) return bad("unknown kind of loss");
+    if (a.T < 0 || a.V < 1 || a.H < 1) return bad("T >= 0, V >= 1 and H >= 1");
+    if (a.T > GEMM_LOSS_MAX_T || a.V > GEMM_LOSS_MAX_V || a.H > GEMM_LOSS_MAX_H)
+        return set_error(GEMM_ERR_UNSUPPORTED, "T, V or H exceeds GEMM_LOSS_MAX_T, GEMM_LOSS_MAX_V or GEMM_LOSS_MAX_H");
+    if (a.H % 8) return set_error(GEMM_ERR_UNSUPPORTED, "H must be a multiple of 8");
+    if ((a.layout & 0xFu) == GEMM_B_KN && a.V % 8)
+        return set_error(GEMM_ERR_UNSUPPORTED, "V must be a multiple of 8 for GEMM_B_KN");
+    if (a.kind == GEMM_LOSS_DISTILL) {
+        if (a.entries < 1 || a.entries > GEMM_LOSS_MAX_ENTRIES) return bad("entries must be 1 .. GEMM_LOSS_MAX_ENTRIES");
+        if (a.teacher_type > GEMM_LOSS_FP16) return bad("unknown type of the teacher's logits");
+    }
+    if (a.dw_type > GEMM_LOSS_DW_FP32_ADD) return bad("unknown dw_type");
+    return GEMM_OK;
+}
+
+int check_ld(int64_t ld, int64_t row, int64_t unit, const char *what) {
+    if (ld < row) return set_error(GEMM_ERR_INVALID, std::string(what) + ": rows overlap");
+    if (ld % unit || ld > MAX_LD)
+        return set_error(GEMM_ERR_UNSUPPORTED, std::string(what) + ": rows must start at multiples of 16 bytes, at most 2^21 elements apart");
+    return GEMM_OK;
+}
+
+bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a && b && a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+}
+
+int64_t span_bytes(int64_t rows, int64_t row, int64_t ld, int64_t size) {
+    return rows > 0 ? ((rows - 1) * ld + row) * size : 0;
+}
+
+int check_args(const gemm_loss_args_t &a, bool backward) {
+    int rc = check_sizes(a);
+    if (rc != GEMM_OK) return rc;
+    const int64_t ldx = or_packed(a.ldx, a.H), ldw = or_packed(a.ldw, row_of_w(a));
+    if ((rc = check_ld(ldx, a.H, 8, "x")) != GEMM_OK || (rc = check_ld(ldw, row_of_w(a), 8, "w")) != GEMM_OK) return rc;
+    if (a.kind == GEMM_LOSS_XENT && !(a.z_loss >= 0.0f && std::isfinite(a.z_loss))) return bad("z_loss must be finite and >= 0");
+    if (a.kind == GEMM_LOSS_DISTILL && !(a.temperature > 0.0f && std::isfinite(a.temperature)))
+        return bad("temperature must be finite and > 0");
+    if (a.num_cus < 0) return bad("num_cus must be >= 0");
+    const bool dw32 = a.dw_type != GEMM_LOSS_DW_SAME;
+    const int64_t lddx = or_packed(a.lddx, a.H), lddw = or_packed(a.lddw, row_of_w(a));
+    if (backward) {
+        if (a.dx && (rc = check_ld(lddx, a.H, 8, "dx")) != GEMM_OK) return rc;
+        if (a.dw && (rc = check_ld(lddw, row_of_w(a), dw32 ? 4 : 8, "dw")) != GEMM_OK) return rc;
+        if (a.dw && (reinterpret_cast<uintptr_t>(a.dw) & 15)) return set_error(GEMM_ERR_UNSUPPORTED, "dw must be 16-byte aligned");
+    }
+    if (a.T == 0) return GEMM_OK;
+    if (!a.x || !a.w || !a.lse) return bad("x, w and lse must be non-null");
+    if ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.dx)) & 15)
+        return set_error(GEMM_ERR_UNSUPPORTED, "x, w and dx must be 16-byte aligned");
+    if (a.kind == GEMM_LOSS_XENT ? !a.target : !a.teacher_index || !a.teacher_logits)
+        return bad("the loss's targets must be non-null");
+    if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
+    if (!backward) {
+        if (!a.loss) return bad("loss must be non-null");
+        return GEMM_OK;
+    }
+    if (!a.grad) return bad("grad must be non-null");
+    const int64_t xb = span_bytes(a.T, a.H, ldx, 2), wb = span_bytes(rows_of_w(a), row_of_w(a), ldw, 2);
+    const int64_t dxb = span_bytes(a.T, a.H, lddx, 2), dwb = span_bytes(rows_of_w(a), row_of_w(a), lddw, dw32 ? 4 : 2);
+    if (overlap(a.dx, dxb, a.x, xb) || overlap(a.dx, dxb, a.w, wb) || overlap(a.dw, dwb, a.x, xb) ||
+        overlap(a.dw, dwb, a.w, wb) || overlap(a.dx, dxb, a.dw, dwb))
+        return bad("dx and dw must not overlap x, w or each other");
+    return GEMM_OK;
+}
+
+// Byte offsets of a call's parts in its workspace.
+struct Layout {
+    int64_t index = 0, weight = 0, entropy = 0;   // the teacher's entries
+    int64_t stats = 0;                            // forward
+    int64_t rows = 0, scale = 0, dz = 0, dx = 0, dw = 0;   // backward
+    int64_t ldd = 0;
+    int64_t bytes = 0;
+    int64_t take(int64_t n) {
+        const int64_t at = bytes;
+        bytes += round_up(n, 256);
+        return at;
+    }
+};
+
+int stride_of(const gemm_loss_args_t &a) { return a.kind == GEMM_LOSS_DISTILL ? (int)round_up(a.entries, 4) : 0; }
+
+// Slices of a product's k: as many as fill the chip once, of at least 8 slabs.
+int splits_for(int tile, int64_t rows_p, int64_t rows_q, int64_t k, int cus) {
+    const dgw::LossTileShape s = dgw::loss_tile_shape(tile);
+    const int64_t tiles = ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q), slabs = ceil_div(k, 64);
+    return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)cus * s.per_cu / tiles, slabs / 8));
+}
+
+struct Plan {
+    int logits = dgw::LT_128x128, dx = dgw::LT_128x128, dw = dgw::LT_128x128;   // tiles
+    int64_t piece = 0;
+    int pieces = 0, dx_splits = 1, dw_splits = 1;
+    Layout at;
+};
+
+Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
+    Plan p;
+    Layout &l = p.at;
+    const int stride = stride_of(a);
+    if (stride) {
+        l.index = l.take(a.T * stride * 4);
+        l.weight = l.take(a.T * stride * 4);
+        l.entropy = l.take(a.T * 4);
+    }
+    if (!backward) {
+        l.stats = l.take(3 * ceil_div(a.V, dgw::loss_tile_shape(p.logits).p) * a.T * 4);
+        return p;
+    }
+    p.piece = std::min(round_up(a.V, 64), std::max<int64_t>(1024, PIECE_BYTES / 2 / std::max<int64_t>(a.T, 1) / 1024 * 1024));
+    p.pieces = (int)ceil_div(a.V, p.piece);
+    l.ldd = p.piece;
+    l.rows = l.take(a.T * (int64_t)sizeof(dgw::LossRow));
+    l.scale = l.take(8);
+    l.dz = l.take(a.T * l.ldd * 2);
+    const int64_t first = std::min(a.V, p.piece);
+    if (a.dx) {
+        p.dx_splits = splits_for(p.dx, a.H, a.T, first, cus);
+        if (p.dx_splits > 1 || p.pieces > 1) l.dx = l.take(dgw::loss_slots_bytes(p.dx, a.H, a.T, p.dx_splits));
+    }
+    if (a.dw) {
+        const bool nk = (a.layout & 0xFu) == GEMM_B_NK;
+        const int64_t rp = nk ? a.H : first, rq = nk ? first : a.H;
+        p.dw_splits = splits_for(p.dw, rp, rq, a.T, cus);
+        if (p.dw_splits > 1) l.dw = l.take(dgw::loss_slots_bytes(p.dw, rp, rq, p.dw_splits));
+    }
+    return p;
+}
+
+template <class T>
+T *part(void *ws, int64_t at) {
+    return reinterpret_cast<T *>(static_cast<char *>(ws) + at);
+}
+
+// The workspace, the stream and the teacher's entries of a call.
+struct Call {
+    hipStream_t stream;
+    void *ws = nullptr;
+    int dtype;
+    bool nk;
+    Plan plan;
+    dgw::LossTargets targets;
+    const float *entropy = nullptr;
+};
+
+int begin(const gemm_loss_args_t &a, bool backward, Call *c) {
+    c->stream = a.stream ? reinterpret_cast<hipStream_t>(a.stream) : dgw::thread_stream();
+    c->dtype = (a.layout & 0xF0u) == GEMM_FP16 ? 1 : 0;
+    c->nk = (a.layout & 0xFu) == GEMM_B_NK;
+    int cus = a.num_cus, rc;
+    if (!cus && (rc = dgw::current_device_cus(&cus)) != GEMM_OK) return rc;
+    c->plan = make_plan(a, backward, cus);
+    const Layout &l = c->plan.at;
+    c->ws = a.workspace;
+    if (a.workspace) {
+        if ((int64_t)a.workspace_bytes < l.bytes)
+            return set_error(GEMM_ERR_WORKSPACE, "caller workspace is smaller than plan.workspace_bytes (" + std::to_string(l.bytes) + ")");
+    } else if ((rc = dgw::library_workspace(l.bytes, c->stream, &c->ws)) != GEMM_OK) {
+        return rc;
+    }
+    if (a.kind == GEMM_LOSS_XENT) {
+        c->targets = {a.target, nullptr, nullptr, 0};
+        return GEMM_OK;
+    }
+    const int stride = stride_of(a);
+    int32_t *index = part<int32_t>(c->ws, l.index);
+    float *weight = part<float>(c->ws, l.weight), *entropy = part<float>(c->ws, l.entropy);
+    const hipError_t e = dgw::launch_loss_teacher(a.T, a.entries, stride, a.V, a.teacher_index, a.teacher_logits,
+                                                  a.teacher_type, a.temperature, index, weight, entropy, c->stream);
+    if (e != hipSuccess) return set_hip_error(e, "launch the teacher's softmax");
+    c->targets = {nullptr, index, weight, stride};
+    c->entropy = entropy;
+    return GEMM_OK;
+}
+
+// The logits' problem over entries [v0, v0 + n).
+dgw::LossProblem problem(const gemm_loss_args_t &a, const Call &c, int64_t v0, int64_t n) {
+    dgw::LossProblem p;
+    const int64_t ldw = or_packed(a.ldw, row_of_w(a));
+    p.T = (int)a.T;
+    p.V = (int)n;
+    p.H = (int)a.H;
+    p.c = 1.44269504088896340736f / (a.kind == GEMM_LOSS_DISTILL ? a.temperature : 1.0f);
+    p.x = {static_cast<const uint16_t *>(a.x), or_packed(a.ldx, a.H), (int)a.T, true};
+    p.w = {static_cast<const uint16_t *>(a.w) + (c.nk ? v0 * ldw : v0), ldw, (int)n, c.nk};
+    p.v0 = v0;
+    p.targets = c.targets;
+    return p;
+}
+
+int forward(const gemm_loss_args_t &a) {
+    dgw::clear_error();
+    int rc = check_args(a, false);
+    if (rc != GEMM_OK || a.T == 0) return rc;
+    Call c;
+    if ((rc = begin(a, false, &c)) != GEMM_OK) return rc;
+    const int tiles = (int)ceil_div(a.V, dgw::loss_tile_shape(c.plan.logits).p);
+    float *st = part<float>(c.ws, c.plan.at.stats);
+    const dgw::LossStats s{st, st + tiles * a.T, st + 2 * tiles * a.T};
+    hipError_t e = dgw::launch_loss_stats(c.dtype, c.plan.logits, problem(a, c, 0, a.V), s, c.stream);
+    if (e != hipSuccess) return set_hip_error(e, "launch the logits' statistics");
+    if ((e = dgw::launch_loss_finish(a, tiles, s, c.entropy, c.stream)) != hipSuccess) return set_hip_error(e, "launch the losses");
+    return GEMM_OK;
+}
+
+int backward(const gemm_loss_args_t &a) {
+    dgw::clear_error();
+    int rc = check_args(a, true);
+    if (rc != GEMM_OK || (!a.dx && !a.dw)) return rc;
+    const int64_t ldw = or_packed(a.ldw, row_of_w(a)), lddx = or_packed(a.lddx, a.H), lddw = or_packed(a.lddw, row_of_w(a));
+    const int dw_size = a.dw_type == GEMM_LOSS_DW_SAME ? 2 : 4;
+    hipError_t e;
+    if (a.T == 0) {
+        if (!a.dw || a.dw_type == GEMM_LOSS_DW_FP32_ADD) return GEMM_OK;
+        hipStream_t stream = a.stream ? reinterpret_cast<hipStream_t>(a.stream) : dgw::thread_stream();
+        if ((e = dgw::launch_loss_zero(a.dw, rows_of_w(a), row_of_w(a) * dw_size, lddw * dw_size, stream)) != hipSuccess)
+            return set_hip_error(e, "zero dw");
+        return GEMM_OK;
+    }
+    Call c;
+    if ((rc = begin(a, true, &c)) != GEMM_OK) return rc;
+    const Plan &pl = c.plan;
+    dgw::LossRow *rows = part<dgw::LossRow>(c.ws, pl.at.rows);
+    float *scale = c.dtype == 1 ? part<float>(c.ws, pl.at.scale) : nullptr;
+    uint16_t *dz = part<uint16_t>(c.ws, pl.at.dz);
+    if ((e = dgw::launch_loss_rows(a, c.entropy, rows, scale, c.stream)) != hipSuccess) return set_hip_error(e, "launch the rows' factors");
+    const float *unscale = scale ? scale + 1 : nullptr;
+    dgw::LossProduct px;
+    for (int i = 0; i < pl.pieces; ++i) {
+        const int64_t v0 = i * pl.piece, n = std::min(pl.piece, a.V - v0);
+        const dgw::LossProblem p = problem(a, c, v0, n);
+        if ((e = dgw::launch_loss_dz(c.dtype, pl.logits, p, rows, scale, dz, pl.at.ldd, c.stream)) != hipSuccess)
+            return set_hip_error(e, "launch the logits' gradient");
+        if (a.dx) {   // dx[t][h] += sum_v w[v][h] dz[t][v]
+            px.P = {p.w.base, ldw, (int)a.H, !c.nk};
+            px.Q = {dz, pl.at.ldd, (int)a.T, true};
+            px.K = (int)n;
+            px.splits = pl.dx_splits;
+            px.unscale = unscale;
+            px.out = a.dx;
+            px.ldo = lddx;
+            px.out_kind = dgw::LO_16;
+            if (pl.dx_splits > 1 || pl.pieces > 1) {
+                px.out = part<float>(c.ws, pl.at.dx);
+                px.out_kind = i == 0 ? dgw::LO_SLOTS : dgw::LO_SLOTS_ADD;
+            }
+            if ((e = dgw::launch_loss_product(c.dtype, pl.dx, px, c.stream)) != hipSuccess) return set_hip_error(e, "launch dx");
+        }
+        if (a.dw) {   // dw[v][h] = sum_t x[t][h] dz[t][v], as stored
+            const dgw::LossMatrix mx{static_cast<const uint16_t *>(a.x), or_packed(a.ldx, a.H), (int)a.H, false};
+            const dgw::LossMatrix mz{dz, pl.at.ldd, (int)n, false};
+            dgw::LossProduct q;
+            q.P = c.nk ? mx : mz;
+            q.Q = c.nk ? mz : mx;
+            q.K = (int)a.T;
+            q.splits = pl.dw_splits;
+            q.unscale = unscale;
+            q.out = static_cast<char *>(a.dw) + (c.nk ? v0 * lddw : v0) * dw_size;
+            q.ldo = lddw;
+            q.out_kind = a.dw_type == GEMM_LOSS_DW_SAME ? dgw::LO_16 : a.dw_type == GEMM_LOSS_DW_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
+            const dgw::LossProduct join = q;
+            if (pl.dw_splits > 1) {
+                q.out = part<float>(c.ws, pl.at.dw);
+                q.out_kind = dgw::LO_SLOTS;
+            }
+            if ((e = dgw::launch_loss_product(c.dtype, pl.dw, q, c.stream)) != hipSuccess) return set_hip_error(e, "launch dw");
+            if (pl.dw_splits > 1 &&
+                (e = dgw::launch_loss_join(c.dtype, pl.dw, join, part<float>(c.ws, pl.at.dw), c.stream)) != hipSuccess)
+                return set_hip_error(e, "launch dw's join");
+        }
+    }
+    if (a.dx && (pl.dx_splits > 1 || pl.pieces > 1)) {
+        px.out = a.dx;
+        px.out_kind = dgw::LO_16;
+        if ((e = dgw::launch_loss_join(c.dtype, pl.dx, px, part<float>(c.ws, pl.at.dx), c.stream)) != hipSuccess)
+            return set_hip_error(e, "launch dx's join");
+    }
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_loss_plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out) {
+    dgw::clear_error();
+    if (!args || !out) return bad("args and out must be non-null");
+    if (num_cus < 1) return bad("num_cus must be >= 1");
+    const int rc = check_sizes(*args);
+    if (rc != GEMM_OK) return rc;
+    std::memset(out, 0, sizeof *out);
+    const Plan p = make_plan(*args, backward != 0, num_cus);
+    const dgw::LossTileShape l = dgw::loss_tile_shape(p.logits), x = dgw::loss_tile_shape(p.dx), w = dgw::loss_tile_shape(p.dw);
+    out->tile_v = l.p;
+    out->tile_t = l.q;
+    out->num_cus = num_cus;
+    out->workspace_bytes = p.at.bytes;
+    if (backward) {
+        out->pieces = p.pieces;
+        out->piece = p.piece;
+        out->dx_tile_h = x.p;
+        out->dx_tile_t = x.q;
+        out->dx_splits = p.dx_splits;
+        out->dw_tile_p = w.p;
+        out->dw_tile_q = w.q;
+        out->dw_splits = p.dw_splits;
+    }
+    return GEMM_OK;
+}
+
+int gemm_loss_forward(const gemm_loss_args_t *args) {
+    if (!args) return bad("args is null");
+    return forward(*args);
+}
+
+int gemm_loss_backward(const gemm_loss_args_t *args) {
+    if (!args) return bad("args is null");
+    return backward(*args);
+}
+
+}  // extern "C"

@@ -1,0 +1,688 @@
+// loss_kernels.hip -- gfx950 kernels of the vocabulary losses (gemm_loss.h).
+//
+// Forward: loss_stats computes a tile of logits (vocabulary x rows) with the loop
+// of tile.h and reduces it where it stands: per row the maximum, the sum of
+// exponentials and the targets' weighted logits, 12 bytes per row and tile
+// instead of the tile itself.  loss_finish joins the tiles' statistics.
+// Backward, per piece of the vocabulary: loss_dz computes the logits again and
+// writes their gradient in 16 bits, loss_product multiplies it with w (dx) and x
+// (dw).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "loss.h"
+#include "tile.h"
+
+namespace dgw {
+
+using namespace tile;
+
+namespace {
+
+constexpr float LOG2E = 1.44269504088896340736f;
+constexpr float INF = __builtin_inff();
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+struct LogitParams {
+    Matrix w, x;
+    int T, V, H;
+    int64_t v0;
+    float c;
+    Grid g;
+    LossTargets targets;
+};
+
+// Calls f(hit, slot, weight) for the row's targets that fall into the wave's part
+// of the tile: slot 16 i + e is the register that holds the entry's logit in the
+// lane that hits.  Every lane of the wave calls f together, and f is skipped
+// where no lane has a hit (one entry in WAVE_P / V tiles has one).  `first` is the
+// vocabulary index of the wave's first row of P; `row` is negative for lanes
+// without a row.
+template <int WAVE_P, class F>
+__device__ __forceinline__ void for_targets(const LossTargets &t, int64_t first, int64_t row, int half, F &&f) {
+    auto visit = [&](int64_t index, float weight) {
+        const int64_t at = index - first;
+        const bool hit = row >= 0 && index >= 0 && at >= 0 && at < WAVE_P && (((int)at >> 2) & 1) == half && weight != 0.0f;
+        if (__any(hit)) {
+            const int p = (int)at;
+            f(hit, (p >> 5) * 16 + ((p >> 3) & 3) * 4 + (p & 3), weight);
+        }
+    };
+    const int64_t r = row < 0 ? 0 : row;
+    if (t.target) {
+        visit(t.target[r], 1.0f);
+        return;
+    }
+    const int4 *index = reinterpret_cast<const int4 *>(t.index + r * t.stride);
+    const float4 *weight = reinterpret_cast<const float4 *>(t.weight + r * t.stride);
+    for (int k = 0; k < t.stride / 4; ++k) {
+        const int4 i = index[k];
+        const float4 w = weight[k];
+        visit(i.x, w.x);
+        visit(i.y, w.y);
+        visit(i.z, w.z);
+        visit(i.w, w.w);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward statistics of one tile.  A lane holds 16 RB logits of one row per
+// block column, so maximum and sum run over registers; the two half waves that
+// share a row meet by one lane exchange, the WP waves through LDS.
+// ---------------------------------------------------------------------------
+template <class L>
+__global__ __launch_bounds__(L::NT) void loss_stats(LogitParams p, LossStats s) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    static_assert(3 * L::WP * L::TQ * 4 <= L::LDS_BYTES, "the waves' statistics fit");
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    loop.run_any(p.w, p0, p.x, q0, p.H, 0, p.g.slabs, acc);
+    if (p0 + L::TP > p.V) {   // entries beyond the vocabulary take no part
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (p0 + loop.p_of(i, e) >= p.V)
+#pragma unroll
+                    for (int j = 0; j < L::CB; ++j) acc.v[i][j][e] = -INF;
+    }
+    float *st = reinterpret_cast<float *>(lds);
+    const int half = loop.lane >> 5;
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) {
+        float m = -INF;
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) m = fmaxf(m, acc.v[i][j][e]);
+        m = fmaxf(m, __shfl_xor(m, 32));
+        const float base = m == -INF ? 0.0f : -m * p.c;   // a row of -infinity sums to 0
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum += exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, base));
+        sum += __shfl_xor(sum, 32);
+        const int64_t row = q0 + loop.q_of(j);
+        float dot = 0.0f;
+        for_targets<L::WAVE_P>(p.targets, p.v0 + p0 + loop.wp * L::WAVE_P, row < p.T ? row : -1, half,
+                               [&](bool hit, int slot, float weight) {
+                                   float z = 0.0f;
+#pragma unroll
+                                   for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+                                       for (int e = 0; e < 16; ++e) z = slot == i * 16 + e ? acc.v[i][j][e] : z;
+                                   if (hit) dot = __builtin_fmaf(weight, z, dot);
+                               });
+        dot += __shfl_xor(dot, 32);
+        if (half == 0) {
+            const int at = loop.wp * L::TQ + loop.q_of(j);
+            st[at] = m;
+            st[L::WP * L::TQ + at] = sum;
+            st[2 * L::WP * L::TQ + at] = dot;
+        }
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < L::TQ; t += L::NT) {
+        if (q0 + t >= p.T) break;
+        float m = st[t];
+#pragma unroll
+        for (int w = 1; w < L::WP; ++w) m = fmaxf(m, st[w * L::TQ + t]);
+        float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int w = 0; w < L::WP; ++w) {
+            const float mw = st[w * L::TQ + t], sw = st[(L::WP + w) * L::TQ + t];
+            sum += mw == -INF ? sw : sw * exp2_fast((mw - m) * p.c);
+            dot += st[(2 * L::WP + w) * L::TQ + t];
+        }
+        const int64_t at = (int64_t)tp * p.T + q0 + t;
+        s.max[at] = m;
+        s.sum[at] = sum;
+        s.dot[at] = dot;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 16-bit stores of a tile: packed into LDS row by row (16-byte chunk c of row r
+// at c ^ r), then whole rows go out 16 bytes a lane.
+// ---------------------------------------------------------------------------
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (DT == 0) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
+}
+
+// The LDS must be free.  Chunks at or beyond cols8 (a multiple of 8) and rows at
+// or beyond rows_q are not stored.
+template <int DT, class L>
+__device__ __forceinline__ void store16(const L &loop, const typename L::Acc &acc, char *lds, uint16_t *out, int64_t ld,
+                                        int64_t p0, int64_t q0, int64_t cols8, int64_t rows_q) {
+    constexpr int CH = L::TP / 8;   // chunks per row
+    static_assert(L::TP * L::TQ * 2 <= L::LDS_BYTES, "the tile fits");
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) {
+        const int r = loop.q_of(j);
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int p = loop.p_of(i, 4 * g);
+                const int chunk = (p >> 3) ^ (r & (CH - 1));
+                *reinterpret_cast<u32x2 *>(lds + r * (2 * L::TP) + chunk * 16 + (p & 4) * 2) =
+                    u32x2{pack2<DT>(acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1]),
+                          pack2<DT>(acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3])};
+            }
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int f = threadIdx.x; f < L::TQ * CH; f += L::NT) {
+        const int r = f / CH, c = f % CH;
+        if (q0 + r < rows_q && p0 + 8 * c < cols8)
+            *reinterpret_cast<u32x4 *>(out + (q0 + r) * ld + p0 + 8 * c) =
+                *reinterpret_cast<const u32x4 *>(lds + r * (2 * L::TP) + ((c ^ (r & (CH - 1))) << 4));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The logits' gradient of one tile: dz = a p - b q, p = exp2(z c - lse2).
+// ---------------------------------------------------------------------------
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT) void loss_dz(LogitParams p, const LossRow *rows, const float *scale, uint16_t *dz,
+                                                 int64_t ldd) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    loop.run_any(p.w, p0, p.x, q0, p.H, 0, p.g.slabs, acc);
+    const float S = scale ? scale[0] : 1.0f;
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) {
+        const int64_t row = q0 + loop.q_of(j);
+        const LossRow r = rows[row < p.T ? row : p.T - 1];
+        const float a = r.a * S, b = r.b * S;
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc.v[i][j][e] = a * exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, -r.lse2));
+        for_targets<L::WAVE_P>(p.targets, p.v0 + p0 + loop.wp * L::WAVE_P, row < p.T ? row : -1, loop.lane >> 5,
+                               [&](bool hit, int slot, float weight) {
+                                   const float d = hit ? b * weight : 0.0f;
+#pragma unroll
+                                   for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+                                       for (int e = 0; e < 16; ++e)
+                                           if (slot == i * 16 + e) acc.v[i][j][e] -= d;
+                               });
+        // rows without a target, whatever their logits are, and the padding
+        // behind the vocabulary
+        const bool ragged = p0 + L::TP > p.V;
+        if (ragged || __any(r.on == 0.0f)) {
+#pragma unroll
+            for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (r.on == 0.0f || p0 + loop.p_of(i, e) >= p.V) acc.v[i][j][e] = 0.0f;
+        }
+    }
+    store16<DT>(loop, acc, lds, dz, ldd, p0, q0, ldd, p.T);
+}
+
+// ---------------------------------------------------------------------------
+// Plain products: dx and dw.
+// ---------------------------------------------------------------------------
+struct ProductParams {
+    Matrix P, Q;
+    int K;
+    Grid g;
+    int out_kind;
+    void *out;
+    int64_t ldo;
+    const float *unscale;
+};
+
+// Slot of (slice, tile): a wave's blocks one after the other, each 4 x 64 float4
+// (element quad, lane), so every access moves 1 KiB of contiguous memory.
+template <class L>
+__device__ __forceinline__ f32x4 *slot_base(float *slots, const Grid &g, int tp, int tq, int split, int wave, int lane) {
+    const int64_t tile = ((int64_t)split * g.tiles_q + tq) * g.tiles_p + tp;
+    return reinterpret_cast<f32x4 *>(slots + tile * (L::TP * L::TQ)) + wave * (L::RB * L::CB * 256) + lane;
+}
+
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT) void loss_product(ProductParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    const int s0 = (int)((int64_t)p.g.slabs * split / p.g.splits), s1 = (int)((int64_t)p.g.slabs * (split + 1) / p.g.splits);
+    loop.run_any(p.P, p0, p.Q, q0, p.K, s0, s1, acc);
+    if (p.out_kind >= LO_SLOTS) {
+        f32x4 *slot = slot_base<L>(static_cast<float *>(p.out), p.g, tp, tq, split, loop.wave, loop.lane);
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < L::CB; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    f32x4 v = {acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3]};
+                    f32x4 *at = slot + ((i * L::CB + j) * 4 + g) * 64;
+                    if (p.out_kind == LO_SLOTS_ADD) v += *at;
+                    *at = v;
+                }
+        return;
+    }
+    const float u = p.unscale ? *p.unscale : 1.0f;
+#pragma unroll
+    for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc.v[i][j][e] *= u;
+    if (p.out_kind == LO_16) {
+        store16<DT>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, (p.P.rows + 7) & ~7, p.Q.rows);
+        return;
+    }
+    float *out = static_cast<float *>(p.out);
+#pragma unroll
+    for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t col = p0 + loop.p_of(i, 4 * g), row = q0 + loop.q_of(j);
+                if (row < p.Q.rows && col < p.P.rows) {
+                    f32x4 v = {acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3]};
+                    f32x4 *at = reinterpret_cast<f32x4 *>(out + row * p.ldo + col);
+                    if (p.out_kind == LO_F32_ADD) v += *at;
+                    *at = v;
+                }
+            }
+}
+
+// The slices' slots added in slice order.  One thread per float4 of a slot.
+template <int DT, class L>
+__global__ __launch_bounds__(256) void loss_join(ProductParams p, const float *slots) {
+    constexpr int QUADS = L::TP * L::TQ / 4;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int tile = (int)(id / QUADS), f = (int)(id % QUADS);
+    const int tp = tile % p.g.tiles_p, tq = tile / p.g.tiles_p;
+    const int lane = f & 63, g = (f >> 6) & 3, block = (f >> 8) % (L::RB * L::CB), wave = (f >> 8) / (L::RB * L::CB);
+    const int i = block / L::CB, j = block % L::CB, wp = wave % L::WP, wq = wave / L::WP;
+    const int64_t col = (int64_t)tp * L::TP + wp * L::WAVE_P + i * 32 + 8 * g + 4 * (lane >> 5);
+    const int64_t row = (int64_t)tq * L::TQ + wq * L::WAVE_Q + j * 32 + (lane & 31);
+    if (row >= p.Q.rows || col >= p.P.rows) return;
+    const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * QUADS;
+    const f32x4 *at = reinterpret_cast<const f32x4 *>(slots) + id;
+    f32x4 v = at[0];
+    for (int s = 1; s < p.g.splits; ++s) v += at[s * step];
+    v *= p.unscale ? *p.unscale : 1.0f;
+    if (p.out_kind == LO_16) {
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.out) + row * p.ldo + col) =
+            u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+        return;
+    }
+    f32x4 *out = reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + row * p.ldo + col);
+    if (p.out_kind == LO_F32_ADD) v += *out;
+    *out = v;
+}
+
+// ---------------------------------------------------------------------------
+// Small kernels around the products.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+}
+
+struct TeacherParams {
+    int64_t T, V;
+    int K, stride;
+    const int64_t *index;
+    const void *logits;
+    uint32_t type;
+    float inv_tau;
+    int32_t *index_out;
+    float *weight, *entropy;
+};
+
+__device__ __forceinline__ float teacher_logit(const TeacherParams &p, int64_t at) {
+    if (p.type == GEMM_LOSS_FP32) return static_cast<const float *>(p.logits)[at];
+    if (p.type == GEMM_LOSS_BF16) return __uint_as_float((uint32_t) static_cast<const uint16_t *>(p.logits)[at] << 16);
+    return (float)static_cast<const _Float16 *>(p.logits)[at];
+}
+
+// One wave per row.
+__global__ __launch_bounds__(256) void loss_teacher(TeacherParams p) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if (row >= p.T) return;
+    const int64_t base = row * p.K;
+    float m = -INF;
+    bool bad = false, nan = false;
+    for (int k = lane; k < p.K; k += 64) {
+        const int64_t i = p.index[base + k];
+        if (i < 0) continue;
+        const float t = teacher_logit(p, base + k) * p.inv_tau;
+        bad |= i >= p.V;
+        nan |= t != t;
+        m = fmaxf(m, t);
+    }
+    m = wave_max(m);
+    bad = __any(bad || nan);
+    float total = 0.0f, dot = 0.0f;   // sum e, sum e (t - m)
+    for (int k = lane; k < p.K; k += 64) {
+        if (p.index[base + k] < 0) continue;
+        const float t = teacher_logit(p, base + k) * p.inv_tau - m;
+        const float e = t == -INF || m == -INF ? 0.0f : expf(t);
+        total += e;
+        dot += e > 0.0f ? e * t : 0.0f;
+    }
+    total = wave_sum(total);
+    dot = wave_sum(dot);
+    const bool none = m == -INF;
+    for (int k = lane; k < p.stride; k += 64) {
+        const int64_t i = k < p.K ? p.index[base + k] : -1;
+        const bool on = i >= 0 && i < p.V && !none;
+        const float t = on ? teacher_logit(p, base + k) * p.inv_tau - m : -INF;
+        const float q = on && t > -INF ? expf(t) / total : 0.0f;
+        p.index_out[row * p.stride + k] = on ? (int32_t)i : -1;
+        p.weight[row * p.stride + k] = q;
+    }
+    // sum q log q = sum e (t - m) / total - log total
+    if (lane == 0) p.entropy[row] = bad ? __builtin_nanf("") : none ? -INF : dot / total - logf(total);
+}
+
+struct FinishParams {
+    int64_t T, V;
+    int tiles;
+    float c, inv_tau, tau2, zeta;
+    LossStats s;
+    const float *entropy;
+    const int64_t *target;
+    int64_t ignore;
+    float *loss, *lse;
+};
+
+// Block of 256 threads: `per` rows (a power of two), 256 / per threads a row.
+__global__ __launch_bounds__(256) void loss_finish(FinishParams p, int per) {
+    __shared__ float sm[256], ss[256], sd[256];
+    const int r = threadIdx.x & (per - 1), part = threadIdx.x / per, parts = 256 / per;
+    const int64_t row = (int64_t)blockIdx.x * per + r;
+    float m = -INF, sum = 0.0f, dot = 0.0f;
+    if (row < p.T) {
+        for (int i = part; i < p.tiles; i += parts) {
+            const int64_t at = (int64_t)i * p.T + row;
+            const float mi = p.s.max[at], si = p.s.sum[at];
+            const float top = fmaxf(m, mi);
+            // a NaN sum stays one; a part of -infinity has sum 0
+            sum = (m == -INF ? sum : sum * exp2_fast((m - top) * p.c)) + (mi == -INF ? si : si * exp2_fast((mi - top) * p.c));
+            m = top;
+            dot += p.s.dot[at];
+        }
+    }
+    sm[threadIdx.x] = m;
+    ss[threadIdx.x] = sum;
+    sd[threadIdx.x] = dot;
+    __syncthreads();
+    if (part != 0 || row >= p.T) return;
+    for (int i = 1; i < parts; ++i) m = fmaxf(m, sm[i * per + r]);
+    sum = 0.0f;
+    dot = 0.0f;
+    for (int i = 0; i < parts; ++i) {
+        const float mi = sm[i * per + r], si = ss[i * per + r];
+        sum += mi == -INF ? si : si * exp2_fast((mi - m) * p.c);
+        dot += sd[i * per + r];
+    }
+    // loss from (max - target) + log(sum): exact where the target is the maximum
+    const float log_sum = logf(sum);
+    const float lse = m == -INF && sum == 0.0f ? -INF : __builtin_fmaf(m, p.inv_tau, log_sum);
+    p.lse[row] = lse;
+    float loss;
+    if (p.target) {
+        const int64_t y = p.target[row];
+        loss = (m - dot) + log_sum;
+        if (p.zeta != 0.0f) loss = __builtin_fmaf(p.zeta * lse, lse, loss);
+        if (y < 0 || y >= p.V) loss = __builtin_nanf("");
+        if (y == p.ignore) loss = 0.0f;
+    } else {
+        const float h = p.entropy[row];
+        loss = h == -INF ? 0.0f : p.tau2 * (h + __builtin_fmaf(m - dot, p.inv_tau, log_sum));
+    }
+    p.loss[row] = loss;
+}
+
+struct RowParams {
+    int64_t T, V;
+    float zeta, tau;
+    const int64_t *target;
+    int64_t ignore;
+    const float *entropy, *grad, *lse;
+    LossRow *rows;
+    float *scale;
+};
+
+__global__ __launch_bounds__(256) void loss_rows(RowParams p) {
+    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (row >= p.T) return;
+    const float lse = p.lse[row], g = p.grad[row];
+    LossRow r;
+    r.lse2 = lse * LOG2E;
+    if (p.target) {
+        const int64_t y = p.target[row];
+        const float bad = y < 0 || y >= p.V ? __builtin_nanf("") : 0.0f;
+        r.on = y == p.ignore ? 0.0f : 1.0f;
+        r.a = g * __builtin_fmaf(2.0f * p.zeta, lse, 1.0f) + bad;
+        r.b = g;
+    } else {
+        const float h = p.entropy[row];
+        r.on = h == -INF ? 0.0f : 1.0f;
+        r.a = h != h ? h : g * p.tau;
+        r.b = g * p.tau;
+    }
+    if (r.on == 0.0f) r.a = r.b = r.lse2 = 0.0f;
+    p.rows[row] = r;
+}
+
+// The fp16 scale: the power of two that brings the largest |a| or |b| into
+// [2^13, 2^14), so dz, at most that in size, neither overflows nor loses the
+// small probabilities to fp16's smallest values.  One block.
+__global__ __launch_bounds__(1024) void loss_scale(RowParams p) {
+    __shared__ float part[16];
+    float m = 0.0f;
+    for (int64_t i = threadIdx.x; i < p.T; i += 1024) m = fmaxf(m, fmaxf(fabsf(p.rows[i].a), fabsf(p.rows[i].b)));
+    m = wave_max(m);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, part[i]);
+    int e = 0;
+    if (m > 0.0f && m < INF) {
+        e = 14 - (ilogbf(m) + 1);
+        e = min(max(e, -120), 120);
+    }
+    p.scale[0] = ldexpf(1.0f, e);
+    p.scale[1] = ldexpf(1.0f, -e);
+}
+
+__global__ __launch_bounds__(256) void loss_zero(char *out, int64_t rows, int64_t words, int64_t ld_bytes) {
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256)
+            reinterpret_cast<uint32_t *>(out + r * ld_bytes)[i] = 0u;
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch
+// ---------------------------------------------------------------------------
+// 128 x 128: four waves of 64 x 64, two stages of 32 KiB, two workgroups a CU.
+template <int DT, bool PK, bool QK>
+using Loop128 = Loop<DT, PK, QK, 128, 128, 2, 2, 2>;
+
+Matrix matrix(const LossMatrix &m) { return Matrix{m.base, m.ld, m.rows}; }
+
+template <class L>
+Grid grid_of(int64_t rows_p, int64_t rows_q, int K, int splits) {
+    Grid g;
+    g.tiles_p = (int)((rows_p + L::TP - 1) / L::TP);
+    g.tiles_q = (int)((rows_q + L::TQ - 1) / L::TQ);
+    g.band = std::min(8, g.tiles_p);
+    g.splits = splits;
+    g.slabs = (K + KB - 1) / KB;
+    return g;
+}
+
+unsigned blocks_of(const Grid &g) { return (unsigned)(g.tiles_p * g.tiles_q * g.splits); }
+
+template <class L>
+LogitParams logit_params(const LossProblem &p) {
+    LogitParams q;
+    q.w = matrix(p.w);
+    q.x = matrix(p.x);
+    q.T = p.T;
+    q.V = p.V;
+    q.H = p.H;
+    q.v0 = p.v0;
+    q.c = p.c;
+    q.g = grid_of<L>(p.V, p.T, p.H, 1);
+    q.targets = p.targets;
+    return q;
+}
+
+template <class L>
+hipError_t run_stats(const LossProblem &p, const LossStats &s, hipStream_t stream) {
+    const LogitParams q = logit_params<L>(p);
+    hipLaunchKernelGGL(loss_stats<L>, dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q, s);
+    return hipGetLastError();
+}
+template <int DT, class L>
+hipError_t run_dz(const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz, int64_t ldd, hipStream_t stream) {
+    const LogitParams q = logit_params<L>(p);
+    hipLaunchKernelGGL((loss_dz<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q, rows, scale, dz, ldd);
+    return hipGetLastError();
+}
+template <class L>
+ProductParams product_params(const LossProduct &p) {
+    return ProductParams{matrix(p.P), matrix(p.Q), p.K, grid_of<L>(p.P.rows, p.Q.rows, p.K, p.splits),
+                         p.out_kind, p.out, p.ldo, p.unscale};
+}
+template <int DT, class L>
+hipError_t run_product(const LossProduct &p, hipStream_t stream) {
+    const ProductParams q = product_params<L>(p);
+    hipLaunchKernelGGL((loss_product<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q);
+    return hipGetLastError();
+}
+template <int DT, class L>
+hipError_t run_join(const LossProduct &p, const float *slots, hipStream_t stream) {
+    const ProductParams q = product_params<L>(p);
+    const int64_t quads = (int64_t)q.g.tiles_p * q.g.tiles_q * (L::TP * L::TQ / 4);
+    hipLaunchKernelGGL((loss_join<DT, L>), dim3((unsigned)(quads / 256)), dim3(256), 0, stream, q, slots);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+LossTileShape loss_tile_shape(int tile) {
+    switch (tile) {
+    default: return {128, 128, 2};
+    }
+}
+
+hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const LossStats &s, hipStream_t stream) {
+    if (tile != LT_128x128 || !p.x.kc) return hipErrorInvalidValue;
+    if (dtype == 0) return p.w.kc ? run_stats<Loop128<0, true, true>>(p, s, stream) : run_stats<Loop128<0, false, true>>(p, s, stream);
+    return p.w.kc ? run_stats<Loop128<1, true, true>>(p, s, stream) : run_stats<Loop128<1, false, true>>(p, s, stream);
+}
+
+hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz,
+                          int64_t ldd, hipStream_t stream) {
+    if (tile != LT_128x128 || !p.x.kc) return hipErrorInvalidValue;
+    if (dtype == 0)
+        return p.w.kc ? run_dz<0, Loop128<0, true, true>>(p, rows, scale, dz, ldd, stream)
+                      : run_dz<0, Loop128<0, false, true>>(p, rows, scale, dz, ldd, stream);
+    return p.w.kc ? run_dz<1, Loop128<1, true, true>>(p, rows, scale, dz, ldd, stream)
+                  : run_dz<1, Loop128<1, false, true>>(p, rows, scale, dz, ldd, stream);
+}
+
+template <int DT>
+static hipError_t product_of(const LossProduct &p, hipStream_t stream) {
+    if (p.Q.kc) return p.P.kc ? run_product<DT, Loop128<DT, true, true>>(p, stream) : run_product<DT, Loop128<DT, false, true>>(p, stream);
+    return p.P.kc ? hipErrorInvalidValue : run_product<DT, Loop128<DT, false, false>>(p, stream);
+}
+
+hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStream_t stream) {
+    if (tile != LT_128x128) return hipErrorInvalidValue;
+    return dtype == 0 ? product_of<0>(p, stream) : product_of<1>(p, stream);
+}
+
+hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream) {
+    if (tile != LT_128x128) return hipErrorInvalidValue;
+    // the operands' storage does not matter here
+    return dtype == 0 ? run_join<0, Loop128<0, true, true>>(p, slots, stream) : run_join<1, Loop128<1, true, true>>(p, slots, stream);
+}
+
+int64_t loss_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits) {
+    const LossTileShape s = loss_tile_shape(tile);
+    return (rows_p + s.p - 1) / s.p * ((rows_q + s.q - 1) / s.q) * splits * (int64_t)s.p * s.q * 4;
+}
+
+hipError_t launch_loss_teacher(int64_t T, int K, int stride, int64_t V, const int64_t *index, const void *logits,
+                               uint32_t type, float tau, int32_t *index_out, float *weight, float *entropy,
+                               hipStream_t stream) {
+    const TeacherParams p{T, V, K, stride, index, logits, type, 1.0f / tau, index_out, weight, entropy};
+    hipLaunchKernelGGL(loss_teacher, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_finish(const gemm_loss_args_t &a, int tiles, const LossStats &s, const float *entropy,
+                              hipStream_t stream) {
+    const float tau = a.kind == GEMM_LOSS_DISTILL ? a.temperature : 1.0f;
+    FinishParams p{a.T, a.V, tiles, LOG2E / tau, 1.0f / tau, tau * tau, a.z_loss, s, entropy,
+                   a.kind == GEMM_LOSS_XENT ? a.target : nullptr, a.ignore_index, a.loss, a.lse};
+    int per = 1;   // rows per block: 32 where there are that many, else more threads a row
+    while (per < 32 && per < a.T) per *= 2;
+    hipLaunchKernelGGL(loss_finish, dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, stream, p, per);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_rows(const gemm_loss_args_t &a, const float *entropy, LossRow *rows, float *scale,
+                            hipStream_t stream) {
+    const RowParams p{a.T, a.V, a.z_loss, a.kind == GEMM_LOSS_DISTILL ? a.temperature : 1.0f,
+                      a.kind == GEMM_LOSS_XENT ? a.target : nullptr, a.ignore_index, entropy, a.grad, a.lse, rows, scale};
+    hipLaunchKernelGGL(loss_rows, dim3((unsigned)((a.T + 255) / 256)), dim3(256), 0, stream, p);
+    if (scale) hipLaunchKernelGGL(loss_scale, dim3(1), dim3(1024), 0, stream, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_zero(void *out, int64_t rows, int64_t row_bytes, int64_t ld_bytes, hipStream_t stream) {
+    if (rows <= 0 || row_bytes <= 0) return hipSuccess;
+    const int64_t words = row_bytes / 4;
+    hipLaunchKernelGGL(loss_zero, dim3((unsigned)std::min<int64_t>((words + 255) / 256, 64), (unsigned)std::min<int64_t>(rows, 4096)),
+                       dim3(256), 0, stream, static_cast<char *>(out), rows, words, ld_bytes);
+    return hipGetLastError();
+}
+
+}  // namespace dgw
