@@ -9,8 +9,10 @@
 
 namespace dgw {
 
-// Tile shapes (P x Q; P: the dimension contiguous in the result).
-enum LossTile : int { LT_128x128 = 0 };
+// Tile shapes (P x Q; P: the dimension contiguous in the result).  The tiles of
+// few rows take a Q operand with k contiguous, the 32- and 64-row ones a P
+// operand with k contiguous too.
+enum LossTile : int { LT_128x128 = 0, LT_256x256, LT_32x32, LT_128x32, LT_64x64, LT_128x64 };
 struct LossTileShape {
     int p, q, per_cu;   // rows of P and Q, workgroups resident per CU
 };

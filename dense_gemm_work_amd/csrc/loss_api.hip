@@ -114,11 +114,51 @@ struct Layout {
 
 int stride_of(const gemm_loss_args_t &a) { return a.kind == GEMM_LOSS_DISTILL ? (int)round_up(a.entries, 4) : 0; }
 
-// Slices of a product's k: as many as fill the chip once, of at least 8 slabs.
-int splits_for(int tile, int64_t rows_p, int64_t rows_q, int64_t k, int cus) {
-    const dgw::LossTileShape s = dgw::loss_tile_shape(tile);
-    const int64_t tiles = ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q), slabs = ceil_div(k, 64);
-    return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)cus * s.per_cu / tiles, slabs / 8));
+// The tile of a product of rows_p x rows_q and, where its k may be sliced
+// (k > 0), the slices: as many as fill the chip once, of at least 8 slabs.  The
+// cheaper of the two tiles by whole waves of workgroups: a 256 x 256 tile has a
+// CU to itself and takes 4 units; two 128 x 128 tiles share one and together
+// take 2.4 (measured on 4096 x 131072 x 4096: 1262 against 1060 TFLOP/s).
+struct Choice {
+    int tile, splits;
+};
+Choice choose(int64_t rows_p, int64_t rows_q, int64_t k, int cus) {
+    auto consider = [&](int tile, double unit, double *cost) {
+        const dgw::LossTileShape s = dgw::loss_tile_shape(tile);
+        const int64_t tiles = ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q), slots = (int64_t)cus * s.per_cu;
+        const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, ceil_div(k, 64) / 8));
+        *cost = (double)ceil_div(tiles * splits, slots) / splits * unit;
+        return Choice{tile, (int)splits};
+    };
+    double c128, c256;
+    const Choice t128 = consider(dgw::LT_128x128, 2.4, &c128), t256 = consider(dgw::LT_256x256, 4.0, &c256);
+    return c256 < c128 ? t256 : t128;
+}
+
+// The logits' tile.  Up to 64 rows the stream of w is the cost and thin tiles
+// keep more of it in flight (V = 32768, H = 2048, T = 32: 35 us on 64 x 64 tiles,
+// 43 us on 128 x 128); a vocabulary of fewer 64-entry tiles than CUs is cut finer
+// (V = 8192, H = 1536, T = 1: 11.6 us on 32 x 32, 13.8 us on 64 x 64).
+int logits_tile(const gemm_loss_args_t &a, int64_t V, int cus) {
+    if (a.T > 64) return choose(V, a.T, 0, cus).tile;
+    if ((a.layout & 0xFu) == GEMM_B_KN) return a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
+    return a.T <= 32 && V < 64 * (int64_t)cus ? dgw::LT_32x32 : dgw::LT_64x64;
+}
+
+// dx's tile and slices.  Few rows: one workgroup a CU (V = 32768, H = 2048, T = 2:
+// 16 slices 61 us for dz and dx together, 32 slices 68 us, which add up more).
+Choice dx_choice(const gemm_loss_args_t &a, int64_t V, int cus) {
+    if (a.T > 64) return choose(a.H, a.T, V, cus);
+    const int tile = a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
+    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(a.H, 128), ceil_div(V, 64) / 8))};
+}
+
+// dw's tile and slices.  Below 768 rows its stores weigh more than its products,
+// and two workgroups a CU overlap the two (T = 333, V = 50001, H = 2048: 110 us
+// against 118 us on 256 x 256 tiles; T = 777, H = 1536: 147 against 135 us).
+Choice dw_choice(int64_t rows_p, int64_t rows_q, int64_t T, int cus) {
+    if (T < 768) return {dgw::LT_128x128, 1};
+    return choose(rows_p, rows_q, T, cus);
 }
 
 struct Plan {
@@ -138,6 +178,7 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
         l.entropy = l.take(a.T * 4);
     }
     if (!backward) {
+        p.logits = logits_tile(a, a.V, cus);
         l.stats = l.take(3 * ceil_div(a.V, dgw::loss_tile_shape(p.logits).p) * a.T * 4);
         return p;
     }
@@ -148,14 +189,19 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
     l.scale = l.take(8);
     l.dz = l.take(a.T * l.ldd * 2);
     const int64_t first = std::min(a.V, p.piece);
+    p.logits = logits_tile(a, first, cus);
     if (a.dx) {
-        p.dx_splits = splits_for(p.dx, a.H, a.T, first, cus);
+        const Choice c = dx_choice(a, first, cus);
+        p.dx = c.tile;
+        p.dx_splits = c.splits;
         if (p.dx_splits > 1 || p.pieces > 1) l.dx = l.take(dgw::loss_slots_bytes(p.dx, a.H, a.T, p.dx_splits));
     }
     if (a.dw) {
         const bool nk = (a.layout & 0xFu) == GEMM_B_NK;
         const int64_t rp = nk ? a.H : first, rq = nk ? first : a.H;
-        p.dw_splits = splits_for(p.dw, rp, rq, a.T, cus);
+        const Choice c = dw_choice(rp, rq, a.T, cus);
+        p.dw = c.tile;
+        p.dw_splits = c.splits;
         if (p.dw_splits > 1) l.dw = l.take(dgw::loss_slots_bytes(p.dw, rp, rq, p.dw_splits));
     }
     return p;

@@ -75,7 +75,7 @@ __device__ __forceinline__ void for_targets(const LossTargets &t, int64_t first,
 // share a row meet by one lane exchange, the WP waves through LDS.
 // ---------------------------------------------------------------------------
 template <class L>
-__global__ __launch_bounds__(L::NT) void loss_stats(LogitParams p, LossStats s) {
+__global__ __launch_bounds__(L::NT, 2) void loss_stats(LogitParams p, LossStats s) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     static_assert(3 * L::WP * L::TQ * 4 <= L::LDS_BYTES, "the waves' statistics fit");
     int tp, tq, split;
@@ -96,6 +96,7 @@ __global__ __launch_bounds__(L::NT) void loss_stats(LogitParams p, LossStats s) 
     }
     float *st = reinterpret_cast<float *>(lds);
     const int half = loop.lane >> 5;
+    if (loop.active())
 #pragma unroll
     for (int j = 0; j < L::CB; ++j) {
         float m = -INF;
@@ -152,7 +153,8 @@ __global__ __launch_bounds__(L::NT) void loss_stats(LogitParams p, LossStats s) 
 
 // ---------------------------------------------------------------------------
 // 16-bit stores of a tile: packed into LDS row by row (16-byte chunk c of row r
-// at c ^ r), then whole rows go out 16 bytes a lane.
+// at c ^ r), then whole rows go out 16 bytes a lane.  NT: non-temporal, for results
+// that the call does not read again (dw of 64 x 50001 x 2048: 62 against 52 us).
 // ---------------------------------------------------------------------------
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -166,11 +168,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // The LDS must be free.  Chunks at or beyond cols8 (a multiple of 8) and rows at
 // or beyond rows_q are not stored.
-template <int DT, class L>
+template <int DT, bool NT, class L>
 __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &acc, char *lds, uint16_t *out, int64_t ld,
                                         int64_t p0, int64_t q0, int64_t cols8, int64_t rows_q) {
     constexpr int CH = L::TP / 8;   // chunks per row
     static_assert(L::TP * L::TQ * 2 <= L::LDS_BYTES, "the tile fits");
+    if (loop.active())
 #pragma unroll
     for (int j = 0; j < L::CB; ++j) {
         const int r = loop.q_of(j);
@@ -189,9 +192,12 @@ __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &ac
 #pragma unroll 4
     for (int f = threadIdx.x; f < L::TQ * CH; f += L::NT) {
         const int r = f / CH, c = f % CH;
-        if (q0 + r < rows_q && p0 + 8 * c < cols8)
-            *reinterpret_cast<u32x4 *>(out + (q0 + r) * ld + p0 + 8 * c) =
-                *reinterpret_cast<const u32x4 *>(lds + r * (2 * L::TP) + ((c ^ (r & (CH - 1))) << 4));
+        if (q0 + r < rows_q && p0 + 8 * c < cols8) {
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * (2 * L::TP) + ((c ^ (r & (CH - 1))) << 4));
+            u32x4 *at = reinterpret_cast<u32x4 *>(out + (q0 + r) * ld + p0 + 8 * c);
+            if constexpr (NT) __builtin_nontemporal_store(v, at);
+            else *at = v;
+        }
     }
 }
 
@@ -199,7 +205,7 @@ __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &ac
 // The logits' gradient of one tile: dz = a p - b q, p = exp2(z c - lse2).
 // ---------------------------------------------------------------------------
 template <int DT, class L>
-__global__ __launch_bounds__(L::NT) void loss_dz(LogitParams p, const LossRow *rows, const float *scale, uint16_t *dz,
+__global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow *rows, const float *scale, uint16_t *dz,
                                                  int64_t ldd) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     int tp, tq, split;
@@ -210,6 +216,7 @@ __global__ __launch_bounds__(L::NT) void loss_dz(LogitParams p, const LossRow *r
     L::zero(acc);
     loop.run_any(p.w, p0, p.x, q0, p.H, 0, p.g.slabs, acc);
     const float S = scale ? scale[0] : 1.0f;
+    if (loop.active())
 #pragma unroll
     for (int j = 0; j < L::CB; ++j) {
         const int64_t row = q0 + loop.q_of(j);
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(L::NT) void loss_dz(LogitParams p, const LossRow *r
                     if (r.on == 0.0f || p0 + loop.p_of(i, e) >= p.V) acc.v[i][j][e] = 0.0f;
         }
     }
-    store16<DT>(loop, acc, lds, dz, ldd, p0, q0, ldd, p.T);
+    store16<DT, false>(loop, acc, lds, dz, ldd, p0, q0, ldd, p.T);
 }
 
 // ---------------------------------------------------------------------------
@@ -265,7 +272,7 @@ __device__ __forceinline__ f32x4 *slot_base(float *slots, const Grid &g, int tp,
 }
 
 template <int DT, class L>
-__global__ __launch_bounds__(L::NT) void loss_product(ProductParams p) {
+__global__ __launch_bounds__(L::NT, 2) void loss_product(ProductParams p) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     int tp, tq, split;
     place(p.g, tp, tq, split);
@@ -276,6 +283,7 @@ __global__ __launch_bounds__(L::NT) void loss_product(ProductParams p) {
     const int s0 = (int)((int64_t)p.g.slabs * split / p.g.splits), s1 = (int)((int64_t)p.g.slabs * (split + 1) / p.g.splits);
     loop.run_any(p.P, p0, p.Q, q0, p.K, s0, s1, acc);
     if (p.out_kind >= LO_SLOTS) {
+        if (!loop.active()) return;
         f32x4 *slot = slot_base<L>(static_cast<float *>(p.out), p.g, tp, tq, split, loop.wave, loop.lane);
 #pragma unroll
         for (int i = 0; i < L::RB; ++i)
@@ -287,6 +295,7 @@ __global__ __launch_bounds__(L::NT) void loss_product(ProductParams p) {
                     f32x4 *at = slot + ((i * L::CB + j) * 4 + g) * 64;
                     if (p.out_kind == LO_SLOTS_ADD) v += *at;
                     *at = v;
+                    if (g == 3) __builtin_amdgcn_sched_barrier(0);   // one block's loads in flight: no more registers are free
                 }
         return;
     }
@@ -298,10 +307,11 @@ __global__ __launch_bounds__(L::NT) void loss_product(ProductParams p) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc.v[i][j][e] *= u;
     if (p.out_kind == LO_16) {
-        store16<DT>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, (p.P.rows + 7) & ~7, p.Q.rows);
+        store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, (p.P.rows + 7) & ~7, p.Q.rows);
         return;
     }
     float *out = static_cast<float *>(p.out);
+    if (!loop.active()) return;
 #pragma unroll
     for (int i = 0; i < L::RB; ++i)
 #pragma unroll
@@ -315,6 +325,7 @@ __global__ __launch_bounds__(L::NT) void loss_product(ProductParams p) {
                     if (p.out_kind == LO_F32_ADD) v += *at;
                     *at = v;
                 }
+                if (g == 3) __builtin_amdgcn_sched_barrier(0);
             }
 }
 
@@ -434,30 +445,33 @@ __global__ __launch_bounds__(256) void loss_finish(FinishParams p, int per) {
     const int r = threadIdx.x & (per - 1), part = threadIdx.x / per, parts = 256 / per;
     const int64_t row = (int64_t)blockIdx.x * per + r;
     float m = -INF, sum = 0.0f, dot = 0.0f;
+    // the sums of (m, sum) and (mi, si); a NaN sum stays one, a part whose maximum
+    // is -infinity has sum 0
+    auto join = [&](float mi, float si) {
+        const float top = fmaxf(m, mi);
+        sum = (m == -INF ? sum : sum * exp2_fast((m - top) * p.c)) + (mi == -INF ? si : si * exp2_fast((mi - top) * p.c));
+        m = top;
+    };
     if (row < p.T) {
         for (int i = part; i < p.tiles; i += parts) {
             const int64_t at = (int64_t)i * p.T + row;
-            const float mi = p.s.max[at], si = p.s.sum[at];
-            const float top = fmaxf(m, mi);
-            // a NaN sum stays one; a part of -infinity has sum 0
-            sum = (m == -INF ? sum : sum * exp2_fast((m - top) * p.c)) + (mi == -INF ? si : si * exp2_fast((mi - top) * p.c));
-            m = top;
+            join(p.s.max[at], p.s.sum[at]);
             dot += p.s.dot[at];
         }
     }
-    sm[threadIdx.x] = m;
-    ss[threadIdx.x] = sum;
-    sd[threadIdx.x] = dot;
-    __syncthreads();
-    if (part != 0 || row >= p.T) return;
-    for (int i = 1; i < parts; ++i) m = fmaxf(m, sm[i * per + r]);
-    sum = 0.0f;
-    dot = 0.0f;
-    for (int i = 0; i < parts; ++i) {
-        const float mi = sm[i * per + r], si = ss[i * per + r];
-        sum += mi == -INF ? si : si * exp2_fast((mi - m) * p.c);
-        dot += sd[i * per + r];
+    for (int half = parts / 2; half; half /= 2) {   // a tree over the row's threads
+        sm[threadIdx.x] = m;
+        ss[threadIdx.x] = sum;
+        sd[threadIdx.x] = dot;
+        __syncthreads();
+        if (part < half) {
+            const int o = threadIdx.x + half * per;
+            join(sm[o], ss[o]);
+            dot += sd[o];
+        }
+        __syncthreads();
     }
+    if (part != 0 || row >= p.T) return;
     // loss from (max - target) + log(sum): exact where the target is the maximum
     const float log_sum = logf(sum);
     const float lse = m == -INF && sum == 0.0f ? -INF : __builtin_fmaf(m, p.inv_tau, log_sum);
@@ -539,8 +553,39 @@ __global__ __launch_bounds__(256) void loss_zero(char *out, int64_t rows, int64_
 // Dispatch
 // ---------------------------------------------------------------------------
 // 128 x 128: four waves of 64 x 64, two stages of 32 KiB, two workgroups a CU.
+// 256 x 256: eight waves of 128 x 64, two stages of 64 KiB, one workgroup a CU.
+template <int TILE, int DT, bool PK, bool QK>
+struct LoopOf;
 template <int DT, bool PK, bool QK>
-using Loop128 = Loop<DT, PK, QK, 128, 128, 2, 2, 2>;
+struct LoopOf<LT_128x128, DT, PK, QK> {
+    using type = Loop<DT, PK, QK, 128, 128, 2, 2, 2>;
+};
+template <int DT, bool PK, bool QK>
+struct LoopOf<LT_256x256, DT, PK, QK> {
+    using type = Loop<DT, PK, QK, 256, 256, 2, 4, 2>;
+};
+// Few rows: ThinLoop tiles, several workgroups a CU (48 to 80 KiB of LDS).
+template <int DT, bool PK, bool QK>
+struct LoopOf<LT_32x32, DT, PK, QK> {
+    using type = ThinLoop<DT, PK, QK, 32, 32, 6>;
+};
+template <int DT, bool PK, bool QK>
+struct LoopOf<LT_128x32, DT, PK, QK> {
+    using type = ThinLoop<DT, PK, QK, 128, 32, 4>;
+};
+template <int DT, bool PK, bool QK>
+struct LoopOf<LT_64x64, DT, PK, QK> {
+    using type = ThinLoop<DT, PK, QK, 64, 64, 5>;
+};
+template <int DT, bool PK, bool QK>
+struct LoopOf<LT_128x64, DT, PK, QK> {
+    using type = ThinLoop<DT, PK, QK, 128, 64, 3>;
+};
+template <class L_, int DT_>
+struct Choice {
+    using L = L_;
+    static constexpr int DT = DT_;
+};
 
 Matrix matrix(const LossMatrix &m) { return Matrix{m.base, m.ld, m.rows}; }
 
@@ -607,41 +652,69 @@ hipError_t run_join(const LossProduct &p, const float *slots, hipStream_t stream
 
 LossTileShape loss_tile_shape(int tile) {
     switch (tile) {
+    case LT_256x256: return {256, 256, 1};
+    case LT_32x32: return {32, 32, 3};
+    case LT_128x32: return {128, 32, 2};
+    case LT_64x64: return {64, 64, 2};
+    case LT_128x64: return {128, 64, 2};
     default: return {128, 128, 2};
     }
 }
 
+// f(loop type) for a tile, type and the operands' storage; an invalid value for
+// what no call asks for.
+template <int TILE, bool PK, bool QK, class F>
+static hipError_t with_type(int dtype, F &&f) {
+    return dtype == 0 ? f(Choice<typename LoopOf<TILE, 0, PK, QK>::type, 0>()) : f(Choice<typename LoopOf<TILE, 1, PK, QK>::type, 1>());
+}
+template <bool PK, bool QK, class F>
+static hipError_t with_tile(int dtype, int tile, F &&f) {
+    if constexpr (PK && QK) {   // their P slabs are too narrow for k-rows
+        if (tile == LT_32x32) return with_type<LT_32x32, PK, QK>(dtype, f);
+        if (tile == LT_64x64) return with_type<LT_64x64, PK, QK>(dtype, f);
+    }
+    if constexpr (QK) {
+        if (tile == LT_128x32) return with_type<LT_128x32, PK, QK>(dtype, f);
+        if (tile == LT_128x64) return with_type<LT_128x64, PK, QK>(dtype, f);
+    }
+    switch (tile) {
+    case LT_128x128: return with_type<LT_128x128, PK, QK>(dtype, f);
+    case LT_256x256: return with_type<LT_256x256, PK, QK>(dtype, f);
+    default: return hipErrorInvalidValue;
+    }
+}
+
 hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const LossStats &s, hipStream_t stream) {
-    if (tile != LT_128x128 || !p.x.kc) return hipErrorInvalidValue;
-    if (dtype == 0) return p.w.kc ? run_stats<Loop128<0, true, true>>(p, s, stream) : run_stats<Loop128<0, false, true>>(p, s, stream);
-    return p.w.kc ? run_stats<Loop128<1, true, true>>(p, s, stream) : run_stats<Loop128<1, false, true>>(p, s, stream);
+    auto run = [&](auto c) { return run_stats<typename decltype(c)::L>(p, s, stream); };
+    if (!p.x.kc) return hipErrorInvalidValue;
+    return p.w.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
 }
 
 hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz,
                           int64_t ldd, hipStream_t stream) {
-    if (tile != LT_128x128 || !p.x.kc) return hipErrorInvalidValue;
-    if (dtype == 0)
-        return p.w.kc ? run_dz<0, Loop128<0, true, true>>(p, rows, scale, dz, ldd, stream)
-                      : run_dz<0, Loop128<0, false, true>>(p, rows, scale, dz, ldd, stream);
-    return p.w.kc ? run_dz<1, Loop128<1, true, true>>(p, rows, scale, dz, ldd, stream)
-                  : run_dz<1, Loop128<1, false, true>>(p, rows, scale, dz, ldd, stream);
-}
-
-template <int DT>
-static hipError_t product_of(const LossProduct &p, hipStream_t stream) {
-    if (p.Q.kc) return p.P.kc ? run_product<DT, Loop128<DT, true, true>>(p, stream) : run_product<DT, Loop128<DT, false, true>>(p, stream);
-    return p.P.kc ? hipErrorInvalidValue : run_product<DT, Loop128<DT, false, false>>(p, stream);
+    auto run = [&](auto c) {
+        using C = decltype(c);
+        return run_dz<C::DT, typename C::L>(p, rows, scale, dz, ldd, stream);
+    };
+    if (!p.x.kc) return hipErrorInvalidValue;
+    return p.w.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
 }
 
 hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStream_t stream) {
-    if (tile != LT_128x128) return hipErrorInvalidValue;
-    return dtype == 0 ? product_of<0>(p, stream) : product_of<1>(p, stream);
+    auto run = [&](auto c) {
+        using C = decltype(c);
+        return run_product<C::DT, typename C::L>(p, stream);
+    };
+    if (p.Q.kc) return p.P.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
+    return p.P.kc ? hipErrorInvalidValue : with_tile<false, false>(dtype, tile, run);
 }
 
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream) {
-    if (tile != LT_128x128) return hipErrorInvalidValue;
-    // the operands' storage does not matter here
-    return dtype == 0 ? run_join<0, Loop128<0, true, true>>(p, slots, stream) : run_join<1, Loop128<1, true, true>>(p, slots, stream);
+    auto run = [&](auto c) {
+        using C = decltype(c);
+        return run_join<C::DT, typename C::L>(p, slots, stream);
+    };
+    return with_tile<true, true>(dtype, tile, run);   // the operands' storage does not matter here
 }
 
 int64_t loss_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits) {
@@ -662,8 +735,10 @@ hipError_t launch_loss_finish(const gemm_loss_args_t &a, int tiles, const LossSt
     const float tau = a.kind == GEMM_LOSS_DISTILL ? a.temperature : 1.0f;
     FinishParams p{a.T, a.V, tiles, LOG2E / tau, 1.0f / tau, tau * tau, a.z_loss, s, entropy,
                    a.kind == GEMM_LOSS_XENT ? a.target : nullptr, a.ignore_index, a.loss, a.lse};
-    int per = 1;   // rows per block: 32 where there are that many, else more threads a row
-    while (per < 32 && per < a.T) per *= 2;
+    // rows per block: 32 (whole cache lines) where that makes a block for every CU,
+    // else fewer rows and more threads a row
+    int per = 1;
+    while (per < 32 && (int64_t)per * 256 < a.T) per *= 2;
     hipLaunchKernelGGL(loss_finish, dim3((unsigned)((a.T + per - 1) / per)), dim3(256), 0, stream, p, per);
     return hipGetLastError();
 }

@@ -84,6 +84,10 @@ __device__ __forceinline__ void wait_vm_lgkm() {
 template <int PER>
 __device__ __forceinline__ void wait_stages(int stages) {
     switch (stages) {
+    case 7: wait_vm_lgkm<7 * PER <= 63 ? 7 * PER : 0>(); break;
+    case 6: wait_vm_lgkm<6 * PER <= 63 ? 6 * PER : 0>(); break;
+    case 5: wait_vm_lgkm<5 * PER <= 63 ? 5 * PER : 0>(); break;
+    case 4: wait_vm_lgkm<4 * PER <= 63 ? 4 * PER : 0>(); break;
     case 3: wait_vm_lgkm<3 * PER>(); break;
     case 2: wait_vm_lgkm<2 * PER>(); break;
     case 1: wait_vm_lgkm<1 * PER>(); break;
@@ -398,11 +402,184 @@ struct Loop {
         else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
     }
 
+    __device__ __forceinline__ bool active() const { return true; }
+
     // Register e of block (i, j) is element (p, q) of the tile.
     __device__ __forceinline__ int p_of(int i, int e) const {
         return wp * WAVE_P + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
     }
     __device__ __forceinline__ int q_of(int j) const { return wq * WAVE_Q + j * 32 + (lane & 31); }
+};
+
+// The product loop for few rows of Q, where P's stream from memory is the cost:
+// four waves that split every slab's four k-steps between them, each holding the
+// whole TP x TQ tile's sums over a quarter of k.  So every staged byte is read
+// from LDS once (P) or once per P block (Q), and a chain of fp32 additions is a
+// quarter as long.  Small tiles and several stages keep enough bytes in flight
+// per CU.  After the loop the waves add their sums through LDS in wave order:
+// wave w < TP / 32 then owns 32-row block w (the others own nothing), and the
+// members below describe that state, as Loop's do.
+template <int DT, bool PK, bool QK, int TP_, int TQ_, int NS_>
+struct ThinLoop {
+    static constexpr int TP = TP_, TQ = TQ_, NS = NS_;
+    static constexpr int NW = 4, NT = 256;
+    static constexpr int WP = TP / 32, WQ = 1;
+    static constexpr int WAVE_P = 32, WAVE_Q = TQ;
+    static constexpr int RB = 1, CB = TQ / 32;
+    static constexpr int PB = TP / 32;                         // P blocks during the loop
+    using OpP = Operand<PK, TP, NW>;
+    using OpQ = Operand<QK, TQ, NW>;
+    static constexpr int LOADS = OpP::LOADS + OpQ::LOADS;
+    static constexpr int STAGE = OpP::SLAB + OpQ::SLAB;
+    static constexpr int MERGE_BYTES = 4 * PB * 4096;          // four waves' sums of one block column
+    static constexpr int LDS_BYTES = NS * STAGE > MERGE_BYTES ? NS * STAGE : MERGE_BYTES;
+    static_assert(NS >= 2 && NS <= 8 && (NS - 1) * LOADS < 64, "the wait counter holds the loads in flight");
+    static_assert(PB <= 4, "a wave per block");
+
+    struct Acc {
+        f32x16 v[RB][CB];
+    };
+
+    int lane, wave, wp, wq;
+    uint32_t lds0;
+    char *lds_;
+    OpP P;
+    OpQ Q;
+    uint32_t pa[PK ? 1 : PB], qa[QK ? 1 : CB];
+
+    __device__ __forceinline__ ThinLoop(char *lds) : lds_(lds) {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        wp = wave;
+        wq = 0;
+        lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
+        // the wave's k-step: a chunk of KC rows, 16 k-rows of RC slabs
+#pragma unroll
+        for (int i = 0; i < (PK ? 1 : PB); ++i)
+            pa[i] = OpP::read_base(lds0, 0, lane, wave, i) + (PK ? 0 : wave * 32 * TP);
+#pragma unroll
+        for (int i = 0; i < (QK ? 1 : CB); ++i)
+            qa[i] = OpQ::read_base(lds0 + OpP::SLAB, 0, lane, wave, i) + (QK ? 0 : wave * 32 * TQ);
+    }
+
+    static __device__ __forceinline__ void zero(Acc &a) {
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) a.v[0][j][e] = 0.0f;
+    }
+
+    struct Frags {
+        u32x4 p[PB], q[CB];
+    };
+    __device__ __forceinline__ void read(Frags &f, int st) const {
+        const uint32_t o = st * STAGE;
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+            if constexpr (PK) {
+                f.p[i] = lds_b128<0>(pa[0] + o + i * 4096);
+            } else {
+                const u32x2 a = lds_tr16<0>(pa[i] + o), b = lds_tr16<8 * TP>(pa[i] + o);
+                f.p[i] = u32x4{a[0], a[1], b[0], b[1]};
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+            if constexpr (QK) {
+                f.q[j] = lds_b128<0>(qa[0] + o + j * 4096);
+            } else {
+                const u32x2 a = lds_tr16<0>(qa[j] + o), b = lds_tr16<8 * TQ>(qa[j] + o);
+                f.q[j] = u32x4{a[0], a[1], b[0], b[1]};
+            }
+        }
+    }
+    template <bool RAGGED>
+    __device__ __forceinline__ void load_all(int slab, int st) const {
+        const i32x4 rp = P.rsrc(slab), rq = Q.rsrc(slab);
+        const uint32_t dp = lds0 + st * STAGE + wave * OpP::LOADS * 1024;
+        const uint32_t dq = lds0 + st * STAGE + OpP::SLAB + wave * OpQ::LOADS * 1024;
+#pragma unroll
+        for (int x = 0; x < OpP::LOADS; ++x) P.template load<RAGGED>(rp, slab, x, dp);
+#pragma unroll
+        for (int x = 0; x < OpQ::LOADS; ++x) Q.template load<RAGGED>(rq, slab, x, dq);
+    }
+
+    template <bool RAGGED>
+    __device__ __forceinline__ void run(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
+                                        Acc &out) {
+        P.init(mp, p0, K, wave, lane);
+        Q.init(mq, q0, K, wave, lane);
+        const int n = s1 - s0;
+        if (n <= 0) return;
+        f32x16 acc[PB][CB];
+#pragma unroll
+        for (int i = 0; i < PB; ++i)
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        for (int i = 0; i < min(NS, n); ++i) load_all<RAGGED>(s0 + i, i);
+        wait_stages<LOADS>(min(NS, n) - 1);
+        __builtin_amdgcn_s_barrier();
+        Frags f[2];
+        read(f[0], 0);
+        int st = 0;   // stage of iteration i
+        // Iteration i: this wave's loads of i + 1 and its reads of i are done; after
+        // the barrier every wave's are, so slab i + NS may go into stage i; read
+        // i + 1, multiply i.
+        auto iter = [&](int i, Frags &cur, Frags &next) {
+            __builtin_amdgcn_sched_barrier(0);
+            wait_stages<LOADS>(max(0, min(NS - 2, n - i - 2)));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + NS < n) load_all<RAGGED>(s0 + i + NS, st);
+            st = st + 1 == NS ? 0 : st + 1;
+            if (i + 1 < n) read(next, st);
+#pragma unroll
+            for (int a = 0; a < PB; ++a)
+#pragma unroll
+                for (int b = 0; b < CB; ++b) acc[a][b] = mfma<DT>(cur.p[a], cur.q[b], acc[a][b]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        for (int i = 0; i < n; i += 2) {
+            iter(i, f[0], f[1]);
+            if (i + 1 < n) iter(i + 1, f[1], f[0]);
+        }
+        wait_vm_lgkm<0>();
+        __builtin_amdgcn_s_barrier();
+        // the waves' sums of one block column at a time, [wave][block][quad][lane]
+        f32x4 *buf = reinterpret_cast<f32x4 *>(lds_);
+#pragma unroll
+        for (int j = 0; j < CB; ++j) {
+#pragma unroll
+            for (int i = 0; i < PB; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    buf[(wave * PB + i) * 256 + g * 64 + lane] =
+                        f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+            __syncthreads();
+            if (active()) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    f32x4 v = buf[wave * 256 + g * 64 + lane];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w) v += buf[(w * PB + wave) * 256 + g * 64 + lane];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) out.v[0][j][4 * g + x] = v[x];
+                }
+            }
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0,
+                                            int s1, Acc &acc) {
+        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc);
+        else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
+    }
+
+    __device__ __forceinline__ bool active() const { return wave < WP; }
+    __device__ __forceinline__ int p_of(int, int e) const { return wp * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3); }
+    __device__ __forceinline__ int q_of(int j) const { return j * 32 + (lane & 31); }
 };
 
 }  // namespace tile

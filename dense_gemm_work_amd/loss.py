@@ -12,8 +12,9 @@ not share one), unless ``workspace`` is given.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-from typing import Optional
+import threading
 
 from . import _check, _lib, layout_word
 
@@ -84,6 +85,9 @@ def gemm_loss_plan(args: GemmLossArgs, backward: bool, num_cus: int) -> GemmLoss
     return p
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 # ---- on torch tensors ------------------------------------------------------------------
 def _rows(name, t, rows, cols, dtype, device):
     """The element stride between the rows of a [rows, cols] tensor whose rows are contiguous."""
@@ -99,8 +103,6 @@ def _rows(name, t, rows, cols, dtype, device):
 
 
 def _vector(name, t, shape, dtypes, device):
-    import torch
-
     if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
         raise TypeError(f"{name} must be {dtypes}")
     if t.device != device:
@@ -154,33 +156,44 @@ def _distill(a, x, teacher_index, teacher_logits, temperature):
     a.temperature = temperature
 
 
+_CUS: dict = {}   # device index -> compute units
+_PLAN = threading.local()
+
+
 def _call(a, x, backward, workspace, outputs):
     """Runs the call on torch's current stream, its workspace torch's unless given."""
     import torch
 
-    a.stream = torch.cuda.current_stream(x.device).cuda_stream
+    device = x.device
+    a.stream = torch.cuda.current_stream(device).cuda_stream
     if workspace is None:
-        a.num_cus = torch.cuda.get_device_properties(x.device).multi_processor_count
-        need = gemm_loss_plan(a, backward, a.num_cus).workspace_bytes
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
-    elif not workspace.is_cuda or workspace.device != x.device or not workspace.is_contiguous():
+        a.num_cus = _CUS.get(device.index) or _CUS.setdefault(
+            device.index, torch.cuda.get_device_properties(device).multi_processor_count)
+        plan = getattr(_PLAN, "plan", None)
+        if plan is None:
+            plan = _PLAN.plan = GemmLossPlan()
+        _check(_lib.gemm_loss_plan(ctypes.byref(a), backward, a.num_cus, ctypes.byref(plan)))
+        workspace = torch.empty(max(plan.workspace_bytes, 1), dtype=torch.uint8, device=device)
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on x's device")
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel() * workspace.element_size()
-    _check((gemm_loss_backward if backward else gemm_loss_forward)(a))
+    _check((_lib.gemm_loss_backward if backward else _lib.gemm_loss_forward)(ctypes.byref(a)))
     return outputs
 
 
 def _on(x, stream):
-    import contextlib
-
+    """x's device and the call's stream made current."""
     import torch
 
-    stack = contextlib.ExitStack()
-    stack.enter_context(torch.cuda.device(x.device))
     if stream is not None:
+        stack = contextlib.ExitStack()
+        stack.enter_context(torch.cuda.device(x.device))
         stack.enter_context(torch.cuda.stream(stream))
-    return stack
+        return stack
+    if x.device.index == torch.cuda.current_device():
+        return _NOTHING
+    return torch.cuda.device(x.device)
 
 
 def _forward(a, x, loss, lse, workspace, stream):
