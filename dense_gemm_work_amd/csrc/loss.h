@@ -27,14 +27,18 @@ struct LossMatrix {
     bool kc;
 };
 
-// The rows' sparse targets as the logits' epilogues read them: XENT: the int64
-// target itself, weight 1; DISTILL: [T][stride] int32 entries (-1: none) and
-// their probabilities.
+// The rows' sparse targets as the logits' epilogues read them.  XENT: the int64
+// target itself, weight 1.  DISTILL: a row's entries {index, probability} sorted
+// by bucket of the vocabulary (64 buckets of `width` entries), and where each
+// bucket starts among them.
+constexpr int LOSS_BUCKETS = 64;
+constexpr int LOSS_STARTS = LOSS_BUCKETS + 2;   // per row: 64 starts, the end, and one to keep rows aligned
 struct LossTargets {
     const int64_t *target;
-    const int32_t *index;
-    const float *weight;
-    int stride;          // entries per row in memory, a multiple of 4
+    const uint2 *entries;     // [T][stride]
+    const uint16_t *starts;   // [T][LOSS_STARTS]
+    int stride;
+    int width;
 };
 
 // Forward statistics of a logits launch: per tile of the vocabulary and row, the
@@ -89,11 +93,11 @@ hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStr
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream);
 int64_t loss_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits);
 
-// The teacher's entries: probabilities, int32 indices and sum q log q per row
-// (NaN where an entry is out of range; -infinity marks rows without entries).
-hipError_t launch_loss_teacher(int64_t T, int K, int stride, int64_t V, const int64_t *index, const void *logits,
-                               uint32_t type, float tau, int32_t *index_out, float *weight, float *entropy,
-                               hipStream_t stream);
+// The teacher's entries as LossTargets holds them, and sum q log q per row (NaN
+// where an entry is out of range; -infinity marks rows without entries).
+hipError_t launch_loss_teacher(int64_t T, int K, int64_t V, const int64_t *index, const void *logits, uint32_t type,
+                               float tau, uint2 *entries, uint16_t *starts, float *entropy, hipStream_t stream);
+int loss_bucket_width(int64_t V);
 
 // loss and lse from the statistics of `tiles` tiles.
 hipError_t launch_loss_finish(const gemm_loss_args_t &a, int tiles, const LossStats &s, const float *entropy,

@@ -100,7 +100,7 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
 
 // Byte offsets of a call's parts in its workspace.
 struct Layout {
-    int64_t index = 0, weight = 0, entropy = 0;   // the teacher's entries
+    int64_t entries = 0, starts = 0, entropy = 0;  // the teacher's entries
     int64_t stats = 0;                            // forward
     int64_t rows = 0, scale = 0, dz = 0, dx = 0, dw = 0;   // backward
     int64_t ldd = 0;
@@ -111,8 +111,6 @@ struct Layout {
         return at;
     }
 };
-
-int stride_of(const gemm_loss_args_t &a) { return a.kind == GEMM_LOSS_DISTILL ? (int)round_up(a.entries, 4) : 0; }
 
 // The tile of a product of rows_p x rows_q and, where its k may be sliced
 // (k > 0), the slices: as many as fill the chip once, of at least 8 slabs.  The
@@ -171,10 +169,9 @@ struct Plan {
 Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
     Plan p;
     Layout &l = p.at;
-    const int stride = stride_of(a);
-    if (stride) {
-        l.index = l.take(a.T * stride * 4);
-        l.weight = l.take(a.T * stride * 4);
+    if (a.kind == GEMM_LOSS_DISTILL) {
+        l.entries = l.take(a.T * a.entries * (int64_t)sizeof(uint2));
+        l.starts = l.take(a.T * dgw::LOSS_STARTS * 2);
         l.entropy = l.take(a.T * 4);
     }
     if (!backward) {
@@ -239,16 +236,16 @@ int begin(const gemm_loss_args_t &a, bool backward, Call *c) {
         return rc;
     }
     if (a.kind == GEMM_LOSS_XENT) {
-        c->targets = {a.target, nullptr, nullptr, 0};
+        c->targets = {a.target, nullptr, nullptr, 0, 0};
         return GEMM_OK;
     }
-    const int stride = stride_of(a);
-    int32_t *index = part<int32_t>(c->ws, l.index);
-    float *weight = part<float>(c->ws, l.weight), *entropy = part<float>(c->ws, l.entropy);
-    const hipError_t e = dgw::launch_loss_teacher(a.T, a.entries, stride, a.V, a.teacher_index, a.teacher_logits,
-                                                  a.teacher_type, a.temperature, index, weight, entropy, c->stream);
+    uint2 *entries = part<uint2>(c->ws, l.entries);
+    uint16_t *starts = part<uint16_t>(c->ws, l.starts);
+    float *entropy = part<float>(c->ws, l.entropy);
+    const hipError_t e = dgw::launch_loss_teacher(a.T, a.entries, a.V, a.teacher_index, a.teacher_logits, a.teacher_type,
+                                                  a.temperature, entries, starts, entropy, c->stream);
     if (e != hipSuccess) return set_hip_error(e, "launch the teacher's softmax");
-    c->targets = {nullptr, index, weight, stride};
+    c->targets = {nullptr, entries, starts, a.entries, dgw::loss_bucket_width(a.V)};
     c->entropy = entropy;
     return GEMM_OK;
 }

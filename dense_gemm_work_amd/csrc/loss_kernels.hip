@@ -36,36 +36,92 @@ struct LogitParams {
     LossTargets targets;
 };
 
-// Calls f(hit, slot, weight) for the row's targets that fall into the wave's part
-// of the tile: slot 16 i + e is the register that holds the entry's logit in the
-// lane that hits.  Every lane of the wave calls f together, and f is skipped
-// where no lane has a hit (one entry in WAVE_P / V tiles has one).  `first` is the
-// vocabulary index of the wave's first row of P; `row` is negative for lanes
-// without a row.
-template <int WAVE_P, class F>
-__device__ __forceinline__ void for_targets(const LossTargets &t, int64_t first, int64_t row, int half, F &&f) {
-    auto visit = [&](int64_t index, float weight) {
-        const int64_t at = index - first;
-        const bool hit = row >= 0 && index >= 0 && at >= 0 && at < WAVE_P && (((int)at >> 2) & 1) == half && weight != 0.0f;
-        if (__any(hit)) {
-            const int p = (int)at;
-            f(hit, (p >> 5) * 16 + ((p >> 3) & 3) * 4 + (p & 3), weight);
-        }
-    };
-    const int64_t r = row < 0 ? 0 : row;
+// Where a lane's row has its targets: the int64 target, or the range of its
+// entries whose buckets meet the wave's part of the tile.
+struct TargetRange {
+    int64_t target;
+    const uint2 *entries;
+    int at, end;
+};
+
+// `first`: the vocabulary index of the wave's first row of P.
+template <int WAVE_P>
+__device__ __forceinline__ TargetRange target_range(const LossTargets &t, int64_t first, int64_t row, bool valid) {
+    TargetRange r{-1, nullptr, 0, 0};
+    if (!valid) return r;
     if (t.target) {
-        visit(t.target[r], 1.0f);
+        r.target = t.target[row];
+        return r;
+    }
+    const uint16_t *s = t.starts + row * LOSS_STARTS;
+    const int lo = (int)first / t.width, hi = ((int)first + WAVE_P - 1) / t.width;
+    r.entries = t.entries + row * t.stride;
+    r.at = s[min(lo, LOSS_BUCKETS)];
+    r.end = s[min(hi, LOSS_BUCKETS - 1) + 1];
+    return r;
+}
+
+// A lane's registers of one block column, laid down in LDS so that they can be
+// indexed: quad s of the lane at [s][lane], so every access is free of bank
+// conflicts and no lane touches another's.  (Picking one of 64 registers by
+// comparisons costs 128 instructions an entry; with 128 entries a row dz of
+// 1024 x 32768 x 1536 took 177 us that way.)
+template <class L>
+struct LaneArray {
+    f32x4 *quads;
+    static constexpr int BYTES = L::RB * 4096;   // per wave
+    __device__ __forceinline__ LaneArray(char *lds, const L &loop)
+        : quads(reinterpret_cast<f32x4 *>(lds + loop.wave * BYTES) + loop.lane) {
+        static_assert(L::NW * BYTES <= L::LDS_BYTES, "an array for every wave");
+    }
+    __device__ __forceinline__ void put(const typename L::Acc &acc, int j) {
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                quads[(i * 4 + g) * 64] = f32x4{acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3]};
+    }
+    __device__ __forceinline__ void get(typename L::Acc &acc, int j) const {
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = quads[(i * 4 + g) * 64];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc.v[i][j][4 * g + x] = v[x];
+            }
+    }
+    __device__ __forceinline__ float &at(int slot) { return reinterpret_cast<float *>(quads + (slot >> 2) * 64)[slot & 3]; }
+};
+
+// Whether any lane of the wave may have a target in the wave's part of the tile.
+template <int WAVE_P>
+__device__ __forceinline__ bool any_target(const LossTargets &t, const TargetRange &r, int64_t first) {
+    return __any(t.target ? r.target >= first && r.target < first + WAVE_P : r.at < r.end);
+}
+
+// Calls f(slot, weight) in the lanes that hold a target's logit, for the row's
+// targets in the wave's part of the tile, in their order: slot 16 i + e is
+// register e of block i.  Of the two lanes that share a row each calls f for the
+// entries it holds.  Entries are read four at a time, so their loads overlap.
+template <int WAVE_P, class F>
+__device__ __forceinline__ void for_targets(const LossTargets &t, const TargetRange &r, int64_t first, int half, F &&f) {
+    auto visit = [&](int64_t at, float weight) {
+        if (at < 0 || at >= WAVE_P || (((int)at >> 2) & 1) != half || weight == 0.0f) return;
+        const int p = (int)at;
+        f((p >> 5) * 16 + ((p >> 3) & 3) * 4 + (p & 3), weight);
+    };
+    if (t.target) {
+        if (r.target >= 0) visit(r.target - first, 1.0f);
         return;
     }
-    const int4 *index = reinterpret_cast<const int4 *>(t.index + r * t.stride);
-    const float4 *weight = reinterpret_cast<const float4 *>(t.weight + r * t.stride);
-    for (int k = 0; k < t.stride / 4; ++k) {
-        const int4 i = index[k];
-        const float4 w = weight[k];
-        visit(i.x, w.x);
-        visit(i.y, w.y);
-        visit(i.z, w.z);
-        visit(i.w, w.w);
+    for (int k = r.at; k < r.end; k += 4) {
+        uint2 e[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) e[x] = r.entries[min(k + x, r.end - 1)];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (k + x < r.end) visit((int64_t)(int)e[x].x - first, __uint_as_float(e[x].y));
     }
 }
 
@@ -96,41 +152,46 @@ __global__ __launch_bounds__(L::NT, 2) void loss_stats(LogitParams p, LossStats 
     }
     float *st = reinterpret_cast<float *>(lds);
     const int half = loop.lane >> 5;
+    const int64_t first = p.v0 + p0 + loop.wp * L::WAVE_P;
+    TargetRange range[L::CB];
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) range[j] = target_range<L::WAVE_P>(p.targets, first, q0 + loop.q_of(j), q0 + loop.q_of(j) < p.T);
+    float max[L::CB], sum[L::CB], dot[L::CB];
+    LaneArray<L> array(lds, loop);
     if (loop.active())
 #pragma unroll
-    for (int j = 0; j < L::CB; ++j) {
-        float m = -INF;
+        for (int j = 0; j < L::CB; ++j) {
+            float m = -INF;
 #pragma unroll
-        for (int i = 0; i < L::RB; ++i)
+            for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = fmaxf(m, acc.v[i][j][e]);
-        m = fmaxf(m, __shfl_xor(m, 32));
-        const float base = m == -INF ? 0.0f : -m * p.c;   // a row of -infinity sums to 0
-        float sum = 0.0f;
+                for (int e = 0; e < 16; ++e) m = fmaxf(m, acc.v[i][j][e]);
+            m = fmaxf(m, __shfl_xor(m, 32));
+            const float base = m == -INF ? 0.0f : -m * p.c;   // a row of -infinity sums to 0
+            float se = 0.0f;
 #pragma unroll
-        for (int i = 0; i < L::RB; ++i)
+            for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum += exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, base));
-        sum += __shfl_xor(sum, 32);
-        const int64_t row = q0 + loop.q_of(j);
-        float dot = 0.0f;
-        for_targets<L::WAVE_P>(p.targets, p.v0 + p0 + loop.wp * L::WAVE_P, row < p.T ? row : -1, half,
-                               [&](bool hit, int slot, float weight) {
-                                   float z = 0.0f;
-#pragma unroll
-                                   for (int i = 0; i < L::RB; ++i)
-#pragma unroll
-                                       for (int e = 0; e < 16; ++e) z = slot == i * 16 + e ? acc.v[i][j][e] : z;
-                                   if (hit) dot = __builtin_fmaf(weight, z, dot);
-                               });
-        dot += __shfl_xor(dot, 32);
-        if (half == 0) {
-            const int at = loop.wp * L::TQ + loop.q_of(j);
-            st[at] = m;
-            st[L::WP * L::TQ + at] = sum;
-            st[2 * L::WP * L::TQ + at] = dot;
+                for (int e = 0; e < 16; ++e) se += exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, base));
+            float d = 0.0f;
+            if (any_target<L::WAVE_P>(p.targets, range[j], first)) {
+                array.put(acc, j);
+                for_targets<L::WAVE_P>(p.targets, range[j], first, half,
+                                       [&](int slot, float weight) { d = __builtin_fmaf(weight, array.at(slot), d); });
+            }
+            max[j] = m;
+            sum[j] = se + __shfl_xor(se, 32);
+            dot[j] = d + __shfl_xor(d, 32);
         }
-    }
+    __syncthreads();   // the lanes' arrays give way to the statistics
+    if (loop.active() && half == 0)
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j) {
+            const int at = loop.wp * L::TQ + loop.q_of(j);
+            st[at] = max[j];
+            st[L::WP * L::TQ + at] = sum[j];
+            st[2 * L::WP * L::TQ + at] = dot[j];
+        }
     __syncthreads();
     for (int t = threadIdx.x; t < L::TQ; t += L::NT) {
         if (q0 + t >= p.T) break;
@@ -216,6 +277,11 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
     L::zero(acc);
     loop.run_any(p.w, p0, p.x, q0, p.H, 0, p.g.slabs, acc);
     const float S = scale ? scale[0] : 1.0f;
+    const int64_t first = p.v0 + p0 + loop.wp * L::WAVE_P;
+    TargetRange range[L::CB];
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) range[j] = target_range<L::WAVE_P>(p.targets, first, q0 + loop.q_of(j), q0 + loop.q_of(j) < p.T);
+    LaneArray<L> array(lds, loop);
     if (loop.active())
 #pragma unroll
     for (int j = 0; j < L::CB; ++j) {
@@ -227,15 +293,12 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 acc.v[i][j][e] = a * exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, -r.lse2));
-        for_targets<L::WAVE_P>(p.targets, p.v0 + p0 + loop.wp * L::WAVE_P, row < p.T ? row : -1, loop.lane >> 5,
-                               [&](bool hit, int slot, float weight) {
-                                   const float d = hit ? b * weight : 0.0f;
-#pragma unroll
-                                   for (int i = 0; i < L::RB; ++i)
-#pragma unroll
-                                       for (int e = 0; e < 16; ++e)
-                                           if (slot == i * 16 + e) acc.v[i][j][e] -= d;
-                               });
+        if (any_target<L::WAVE_P>(p.targets, range[j], first)) {
+            array.put(acc, j);
+            for_targets<L::WAVE_P>(p.targets, range[j], first, loop.lane >> 5,
+                                   [&](int slot, float weight) { array.at(slot) -= b * weight; });
+            array.get(acc, j);
+        }
         // rows without a target, whatever their logits are, and the padding
         // behind the vocabulary
         const bool ragged = p0 + L::TP > p.V;
@@ -247,6 +310,7 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
                     if (r.on == 0.0f || p0 + loop.p_of(i, e) >= p.V) acc.v[i][j][e] = 0.0f;
         }
     }
+    __syncthreads();   // the lanes' arrays give way to the packed tile
     store16<DT, false>(loop, acc, lds, dz, ldd, p0, q0, ldd, p.T);
 }
 
@@ -372,13 +436,14 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 struct TeacherParams {
     int64_t T, V;
-    int K, stride;
+    int K, width;
     const int64_t *index;
     const void *logits;
     uint32_t type;
     float inv_tau;
-    int32_t *index_out;
-    float *weight, *entropy;
+    uint2 *entries;
+    uint16_t *starts;
+    float *entropy;
 };
 
 __device__ __forceinline__ float teacher_logit(const TeacherParams &p, int64_t at) {
@@ -387,45 +452,91 @@ __device__ __forceinline__ float teacher_logit(const TeacherParams &p, int64_t a
     return (float)static_cast<const _Float16 *>(p.logits)[at];
 }
 
-// One wave per row.
+// One wave per row: the softmax over its entries, then a counting sort of them
+// by bucket, entries of one bucket in the order they came.
 __global__ __launch_bounds__(256) void loss_teacher(TeacherParams p) {
+    __shared__ int counts[4][LOSS_BUCKETS];
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
+    int *count = counts[threadIdx.x >> 6];
     if (row >= p.T) return;
     const int64_t base = row * p.K;
     float m = -INF;
-    bool bad = false, nan = false;
+    bool bad = false;
     for (int k = lane; k < p.K; k += 64) {
         const int64_t i = p.index[base + k];
         if (i < 0) continue;
         const float t = teacher_logit(p, base + k) * p.inv_tau;
-        bad |= i >= p.V;
-        nan |= t != t;
+        bad |= i >= p.V || t != t;
         m = fmaxf(m, t);
     }
     m = wave_max(m);
-    bad = __any(bad || nan);
+    bad = __any(bad);
+    const bool none = m == -INF;
     float total = 0.0f, dot = 0.0f;   // sum e, sum e (t - m)
     for (int k = lane; k < p.K; k += 64) {
-        if (p.index[base + k] < 0) continue;
+        if (none || p.index[base + k] < 0) continue;
         const float t = teacher_logit(p, base + k) * p.inv_tau - m;
-        const float e = t == -INF || m == -INF ? 0.0f : expf(t);
+        const float e = t == -INF ? 0.0f : expf(t);
         total += e;
         dot += e > 0.0f ? e * t : 0.0f;
     }
     total = wave_sum(total);
     dot = wave_sum(dot);
-    const bool none = m == -INF;
-    for (int k = lane; k < p.stride; k += 64) {
-        const int64_t i = k < p.K ? p.index[base + k] : -1;
-        const bool on = i >= 0 && i < p.V && !none;
-        const float t = on ? teacher_logit(p, base + k) * p.inv_tau - m : -INF;
-        const float q = on && t > -INF ? expf(t) / total : 0.0f;
-        p.index_out[row * p.stride + k] = on ? (int32_t)i : -1;
-        p.weight[row * p.stride + k] = q;
-    }
     // sum q log q = sum e (t - m) / total - log total
     if (lane == 0) p.entropy[row] = bad ? __builtin_nanf("") : none ? -INF : dot / total - logf(total);
+
+    // each lane's bucket and its rank among the lanes of the same bucket (-1: no entry)
+    auto place = [&](int k, int &bucket, int &rank, bool &last) {
+        const int64_t i = k < p.K ? p.index[base + k] : -1;
+        const bool on = i >= 0 && i < p.V && !none;
+        bucket = on ? (int)i / p.width : -1;
+        uint64_t same = __ballot(on);
+#pragma unroll
+        for (int b = 0; b < 6; ++b) {
+            const uint64_t set = __ballot((bucket >> b) & 1);
+            same &= (bucket >> b) & 1 ? set : ~set;
+        }
+        rank = on ? __popcll(same & ((1ull << lane) - 1)) : -1;
+        last = on && (same >> lane) == 1;
+    };
+    // the wave's LDS operations run in program order; the fences keep the compiler to it
+    count[lane] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    const int rounds = (p.K + 63) / 64;
+    for (int c = 0; c < rounds; ++c) {
+        int bucket, rank;
+        bool last;
+        place(c * 64 + lane, bucket, rank, last);
+        if (last) count[bucket] += rank + 1;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    }
+    const int mine = count[lane];
+    int upto = mine;   // entries in buckets 0 .. lane
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(upto, o);
+        if (lane >= o) upto += x;
+    }
+    p.starts[row * LOSS_STARTS + lane] = (uint16_t)(upto - mine);
+    if (lane == 63) p.starts[row * LOSS_STARTS + 64] = (uint16_t)upto;
+    count[lane] = upto - mine;
+    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    for (int c = 0; c < rounds; ++c) {
+        const int k = c * 64 + lane;
+        int bucket, rank;
+        bool last;
+        place(k, bucket, rank, last);
+        if (rank >= 0) {
+            const int at = count[bucket] + rank;
+            const float t = teacher_logit(p, base + k) * p.inv_tau - m;
+            const float q = t == -INF ? 0.0f : expf(t) / total;
+            p.entries[base + at] = uint2{(uint32_t)p.index[base + k], __float_as_uint(q)};
+        }
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        if (last) count[bucket] += rank + 1;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    }
 }
 
 struct FinishParams {
@@ -722,10 +833,11 @@ int64_t loss_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits) {
     return (rows_p + s.p - 1) / s.p * ((rows_q + s.q - 1) / s.q) * splits * (int64_t)s.p * s.q * 4;
 }
 
-hipError_t launch_loss_teacher(int64_t T, int K, int stride, int64_t V, const int64_t *index, const void *logits,
-                               uint32_t type, float tau, int32_t *index_out, float *weight, float *entropy,
-                               hipStream_t stream) {
-    const TeacherParams p{T, V, K, stride, index, logits, type, 1.0f / tau, index_out, weight, entropy};
+int loss_bucket_width(int64_t V) { return (int)((V + LOSS_BUCKETS - 1) / LOSS_BUCKETS); }
+
+hipError_t launch_loss_teacher(int64_t T, int K, int64_t V, const int64_t *index, const void *logits, uint32_t type,
+                               float tau, uint2 *entries, uint16_t *starts, float *entropy, hipStream_t stream) {
+    const TeacherParams p{T, V, K, loss_bucket_width(V), index, logits, type, 1.0f / tau, entries, starts, entropy};
     hipLaunchKernelGGL(loss_teacher, dim3((unsigned)((T + 3) / 4)), dim3(256), 0, stream, p);
     return hipGetLastError();
 }
