@@ -62,34 +62,25 @@ __device__ __forceinline__ TargetRange target_range(const LossTargets &t, int64_
 }
 
 // A lane's registers of one block column, laid down in LDS so that they can be
-// indexed: quad s of the lane at [s][lane], so every access is free of bank
+// indexed: quad i of the lane at [i][lane], so every access is free of bank
 // conflicts and no lane touches another's.  (Picking one of 64 registers by
 // comparisons costs 128 instructions an entry; with 128 entries a row dz of
 // 1024 x 32768 x 1536 took 177 us that way.)
 template <class L>
 struct LaneArray {
     f32x4 *quads;
-    static constexpr int BYTES = L::RB * 4096;   // per wave
+    static constexpr int BYTES = L::RB * 1024;   // per wave
     __device__ __forceinline__ LaneArray(char *lds, const L &loop)
         : quads(reinterpret_cast<f32x4 *>(lds + loop.wave * BYTES) + loop.lane) {
         static_assert(L::NW * BYTES <= L::LDS_BYTES, "an array for every wave");
     }
     __device__ __forceinline__ void put(const typename L::Acc &acc, int j) {
 #pragma unroll
-        for (int i = 0; i < L::RB; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-                quads[(i * 4 + g) * 64] = f32x4{acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3]};
+        for (int i = 0; i < L::RB; ++i) quads[i * 64] = acc.v[i][j];
     }
     __device__ __forceinline__ void get(typename L::Acc &acc, int j) const {
 #pragma unroll
-        for (int i = 0; i < L::RB; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 v = quads[(i * 4 + g) * 64];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) acc.v[i][j][4 * g + x] = v[x];
-            }
+        for (int i = 0; i < L::RB; ++i) acc.v[i][j] = quads[i * 64];
     }
     __device__ __forceinline__ float &at(int slot) { return reinterpret_cast<float *>(quads + (slot >> 2) * 64)[slot & 3]; }
 };
@@ -101,15 +92,15 @@ __device__ __forceinline__ bool any_target(const LossTargets &t, const TargetRan
 }
 
 // Calls f(slot, weight) in the lanes that hold a target's logit, for the row's
-// targets in the wave's part of the tile, in their order: slot 16 i + e is
-// register e of block i.  Of the two lanes that share a row each calls f for the
+// targets in the wave's part of the tile, in their order: slot 4 i + e is
+// register e of block i.  Of the four lanes that share a row each calls f for the
 // entries it holds.  Entries are read four at a time, so their loads overlap.
 template <int WAVE_P, class F>
-__device__ __forceinline__ void for_targets(const LossTargets &t, const TargetRange &r, int64_t first, int half, F &&f) {
+__device__ __forceinline__ void for_targets(const LossTargets &t, const TargetRange &r, int64_t first, int group, F &&f) {
     auto visit = [&](int64_t at, float weight) {
-        if (at < 0 || at >= WAVE_P || (((int)at >> 2) & 1) != half || weight == 0.0f) return;
+        if (at < 0 || at >= WAVE_P || (((int)at >> 2) & 3) != group || weight == 0.0f) return;
         const int p = (int)at;
-        f((p >> 5) * 16 + ((p >> 3) & 3) * 4 + (p & 3), weight);
+        f((p >> 4) * 4 + (p & 3), weight);
     };
     if (t.target) {
         if (r.target >= 0) visit(r.target - first, 1.0f);
@@ -126,9 +117,9 @@ __device__ __forceinline__ void for_targets(const LossTargets &t, const TargetRa
 }
 
 // ---------------------------------------------------------------------------
-// Forward statistics of one tile.  A lane holds 16 RB logits of one row per
-// block column, so maximum and sum run over registers; the two half waves that
-// share a row meet by one lane exchange, the WP waves through LDS.
+// Forward statistics of one tile.  A lane holds 4 RB logits of one row per block
+// column, so maximum and sum run over registers; the four lanes that share a row
+// meet by two lane exchanges, the WP waves through LDS.
 // ---------------------------------------------------------------------------
 template <class L>
 __global__ __launch_bounds__(L::NT, 2) void loss_stats(LogitParams p, LossStats s) {
@@ -145,13 +136,13 @@ __global__ __launch_bounds__(L::NT, 2) void loss_stats(LogitParams p, LossStats 
 #pragma unroll
         for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 4; ++e)
                 if (p0 + loop.p_of(i, e) >= p.V)
 #pragma unroll
                     for (int j = 0; j < L::CB; ++j) acc.v[i][j][e] = -INF;
     }
     float *st = reinterpret_cast<float *>(lds);
-    const int half = loop.lane >> 5;
+    const int group = loop.lane >> 4;
     const int64_t first = p.v0 + p0 + loop.wp * L::WAVE_P;
     TargetRange range[L::CB];
 #pragma unroll
@@ -165,26 +156,29 @@ __global__ __launch_bounds__(L::NT, 2) void loss_stats(LogitParams p, LossStats 
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) m = fmaxf(m, acc.v[i][j][e]);
+                for (int e = 0; e < 4; ++e) m = fmaxf(m, acc.v[i][j][e]);
+            m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
             const float base = m == -INF ? 0.0f : -m * p.c;   // a row of -infinity sums to 0
             float se = 0.0f;
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) se += exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, base));
+                for (int e = 0; e < 4; ++e) se += exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, base));
             float d = 0.0f;
             if (any_target<L::WAVE_P>(p.targets, range[j], first)) {
                 array.put(acc, j);
-                for_targets<L::WAVE_P>(p.targets, range[j], first, half,
+                for_targets<L::WAVE_P>(p.targets, range[j], first, group,
                                        [&](int slot, float weight) { d = __builtin_fmaf(weight, array.at(slot), d); });
             }
             max[j] = m;
+            se += __shfl_xor(se, 16);
             sum[j] = se + __shfl_xor(se, 32);
+            d += __shfl_xor(d, 16);
             dot[j] = d + __shfl_xor(d, 32);
         }
     __syncthreads();   // the lanes' arrays give way to the statistics
-    if (loop.active() && half == 0)
+    if (loop.active() && group == 0)
 #pragma unroll
         for (int j = 0; j < L::CB; ++j) {
             const int at = loop.wp * L::TQ + loop.q_of(j);
@@ -231,7 +225,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // or beyond rows_q are not stored.
 template <int DT, bool NT, class L>
 __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &acc, char *lds, uint16_t *out, int64_t ld,
-                                        int64_t p0, int64_t q0, int64_t cols8, int64_t rows_q) {
+                                        int64_t p0, int64_t q0, int64_t cols8, int64_t rows_q, float u = 1.0f) {
     constexpr int CH = L::TP / 8;   // chunks per row
     static_assert(L::TP * L::TQ * 2 <= L::LDS_BYTES, "the tile fits");
     if (loop.active())
@@ -240,14 +234,12 @@ __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &ac
         const int r = loop.q_of(j);
 #pragma unroll
         for (int i = 0; i < L::RB; ++i)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int p = loop.p_of(i, 4 * g);
-                const int chunk = (p >> 3) ^ (r & (CH - 1));
-                *reinterpret_cast<u32x2 *>(lds + r * (2 * L::TP) + chunk * 16 + (p & 4) * 2) =
-                    u32x2{pack2<DT>(acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1]),
-                          pack2<DT>(acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3])};
-            }
+        {
+            const int p = loop.p_of(i, 0);
+            const int chunk = (p >> 3) ^ (r & (CH - 1));
+            *reinterpret_cast<u32x2 *>(lds + r * (2 * L::TP) + chunk * 16 + (p & 4) * 2) =
+                u32x2{pack2<DT>(acc.v[i][j][0] * u, acc.v[i][j][1] * u), pack2<DT>(acc.v[i][j][2] * u, acc.v[i][j][3] * u)};
+        }
     }
     __syncthreads();
 #pragma unroll 4
@@ -291,11 +283,11 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
 #pragma unroll
         for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
+            for (int e = 0; e < 4; ++e)
                 acc.v[i][j][e] = a * exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, -r.lse2));
         if (any_target<L::WAVE_P>(p.targets, range[j], first)) {
             array.put(acc, j);
-            for_targets<L::WAVE_P>(p.targets, range[j], first, loop.lane >> 5,
+            for_targets<L::WAVE_P>(p.targets, range[j], first, loop.lane >> 4,
                                    [&](int slot, float weight) { array.at(slot) -= b * weight; });
             array.get(acc, j);
         }
@@ -306,7 +298,7 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 4; ++e)
                     if (r.on == 0.0f || p0 + loop.p_of(i, e) >= p.V) acc.v[i][j][e] = 0.0f;
         }
     }
@@ -327,12 +319,12 @@ struct ProductParams {
     const float *unscale;
 };
 
-// Slot of (slice, tile): a wave's blocks one after the other, each 4 x 64 float4
-// (element quad, lane), so every access moves 1 KiB of contiguous memory.
+// Slot of (slice, tile): a wave's blocks one after the other, each 64 float4 (one
+// a lane), so every access moves 1 KiB of contiguous memory.
 template <class L>
 __device__ __forceinline__ f32x4 *slot_base(float *slots, const Grid &g, int tp, int tq, int split, int wave, int lane) {
     const int64_t tile = ((int64_t)split * g.tiles_q + tq) * g.tiles_p + tp;
-    return reinterpret_cast<f32x4 *>(slots + tile * (L::TP * L::TQ)) + wave * (L::RB * L::CB * 256) + lane;
+    return reinterpret_cast<f32x4 *>(slots + tile * (L::TP * L::TQ)) + wave * (L::RB * L::CB * 64) + lane;
 }
 
 template <int DT, class L>
@@ -349,48 +341,38 @@ __global__ __launch_bounds__(L::NT, 2) void loss_product(ProductParams p) {
     if (p.out_kind >= LO_SLOTS) {
         if (!loop.active()) return;
         f32x4 *slot = slot_base<L>(static_cast<float *>(p.out), p.g, tp, tq, split, loop.wave, loop.lane);
+        const bool add = p.out_kind == LO_SLOTS_ADD;
 #pragma unroll
-        for (int i = 0; i < L::RB; ++i)
+        for (int i = 0; i < L::RB; ++i) {
 #pragma unroll
-            for (int j = 0; j < L::CB; ++j)
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    f32x4 v = {acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3]};
-                    f32x4 *at = slot + ((i * L::CB + j) * 4 + g) * 64;
-                    if (p.out_kind == LO_SLOTS_ADD) v += *at;
-                    *at = v;
-                    if (g == 3) __builtin_amdgcn_sched_barrier(0);   // one block's loads in flight: no more registers are free
-                }
+            for (int j = 0; j < L::CB; ++j) {
+                f32x4 *at = slot + (i * L::CB + j) * 64;
+                *at = add ? acc.v[i][j] + *at : acc.v[i][j];
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one block row's loads in flight: no more registers are free
+        }
         return;
     }
     const float u = p.unscale ? *p.unscale : 1.0f;
-#pragma unroll
-    for (int i = 0; i < L::RB; ++i)
-#pragma unroll
-        for (int j = 0; j < L::CB; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc.v[i][j][e] *= u;
     if (p.out_kind == LO_16) {
-        store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, (p.P.rows + 7) & ~7, p.Q.rows);
+        store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, (p.P.rows + 7) & ~7, p.Q.rows, u);
         return;
     }
     float *out = static_cast<float *>(p.out);
     if (!loop.active()) return;
+    const bool add = p.out_kind == LO_F32_ADD;
 #pragma unroll
-    for (int i = 0; i < L::RB; ++i)
+    for (int i = 0; i < L::RB; ++i) {
 #pragma unroll
-        for (int j = 0; j < L::CB; ++j)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t col = p0 + loop.p_of(i, 4 * g), row = q0 + loop.q_of(j);
-                if (row < p.Q.rows && col < p.P.rows) {
-                    f32x4 v = {acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2], acc.v[i][j][4 * g + 3]};
-                    f32x4 *at = reinterpret_cast<f32x4 *>(out + row * p.ldo + col);
-                    if (p.out_kind == LO_F32_ADD) v += *at;
-                    *at = v;
-                }
-                if (g == 3) __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < L::CB; ++j) {
+            const int64_t col = p0 + loop.p_of(i, 0), row = q0 + loop.q_of(j);
+            if (row < p.Q.rows && col < p.P.rows) {
+                f32x4 *at = reinterpret_cast<f32x4 *>(out + row * p.ldo + col);
+                *at = add ? acc.v[i][j] * u + *at : acc.v[i][j] * u;
             }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
 // The slices' slots added in slice order.  One thread per float4 of a slot.
@@ -400,10 +382,10 @@ __global__ __launch_bounds__(256) void loss_join(ProductParams p, const float *s
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int tile = (int)(id / QUADS), f = (int)(id % QUADS);
     const int tp = tile % p.g.tiles_p, tq = tile / p.g.tiles_p;
-    const int lane = f & 63, g = (f >> 6) & 3, block = (f >> 8) % (L::RB * L::CB), wave = (f >> 8) / (L::RB * L::CB);
+    const int lane = f & 63, block = (f >> 6) % (L::RB * L::CB), wave = (f >> 6) / (L::RB * L::CB);
     const int i = block / L::CB, j = block % L::CB, wp = wave % L::WP, wq = wave / L::WP;
-    const int64_t col = (int64_t)tp * L::TP + wp * L::WAVE_P + i * 32 + 8 * g + 4 * (lane >> 5);
-    const int64_t row = (int64_t)tq * L::TQ + wq * L::WAVE_Q + j * 32 + (lane & 31);
+    const int64_t col = (int64_t)tp * L::TP + wp * L::WAVE_P + i * 16 + 4 * (lane >> 4);
+    const int64_t row = (int64_t)tq * L::TQ + wq * L::WAVE_Q + j * 16 + (lane & 15);
     if (row >= p.Q.rows || col >= p.P.rows) return;
     const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * QUADS;
     const f32x4 *at = reinterpret_cast<const f32x4 *>(slots) + id;
@@ -663,17 +645,22 @@ __global__ __launch_bounds__(256) void loss_zero(char *out, int64_t rows, int64_
 // ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
-// 128 x 128: four waves of 64 x 64, two stages of 32 KiB, two workgroups a CU.
-// 256 x 256: eight waves of 128 x 64, two stages of 64 KiB, one workgroup a CU.
+// 128 x 128: four waves of 64 x 64, two workgroups a CU.
+// 256 x 256: eight waves of 128 x 64, one workgroup a CU.
+// A third stage of P (all of the LDS then) lets P's loads, most of which miss the
+// L2, travel for two iterations instead of one: 4096 x 131072 x 4096, logits and
+// dz 3 and 5 % faster, dx 2 %.  With both operands' rows contiguous (dw) its
+// registers spill (3.3 against 3.7 ms), and on 128 x 128 tiles it pays where both
+// have k contiguous (333 x 50001 x 2048: dz 95 against 107 us; dx 91 against 85).
 template <int TILE, int DT, bool PK, bool QK>
 struct LoopOf;
 template <int DT, bool PK, bool QK>
 struct LoopOf<LT_128x128, DT, PK, QK> {
-    using type = Loop<DT, PK, QK, 128, 128, 2, 2, 2>;
+    using type = Loop<DT, PK, QK, 128, 128, 2, 2, PK && QK ? 3 : 2, 2>;
 };
 template <int DT, bool PK, bool QK>
 struct LoopOf<LT_256x256, DT, PK, QK> {
-    using type = Loop<DT, PK, QK, 256, 256, 2, 4, 2>;
+    using type = Loop<DT, PK, QK, 256, 256, 2, 4, PK || QK ? 3 : 2, 2>;
 };
 // Few rows: ThinLoop tiles, several workgroups a CU (48 to 80 KiB of LDS).
 template <int DT, bool PK, bool QK>

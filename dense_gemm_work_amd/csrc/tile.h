@@ -14,14 +14,20 @@
 // slabs of k move from global memory straight into LDS (16 bytes a lane, no
 // registers) into NS stages; KC slabs are read with 128-bit LDS reads, RC slabs
 // with the transposing 64-bit read.  The XOR swizzles leave both free of bank
-// conflicts (16 consecutive KC rows cover all 64 banks; the four k-rows that a
-// transposing read touches fall on distinct ones).
+// conflicts: 16 consecutive KC rows read at one chunk cover all 64 banks, and so
+// do the four k-rows that a transposing read touches.
+//
+// The products are 16x16x32 matrix instructions.  Under them the chip runs at its
+// power cap, and their accumulator traffic is half that of the 32x32x16 ones:
+// 4096 x 131072 x 4096 logits took 3.23 ms on those (1.36 PFLOP/s at 1.55 GHz, the
+// matrix cores busy 75 % of the time), 2.99 ms on these.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
 #include <type_traits>
+#include <utility>
 
 namespace dgw {
 namespace tile {
@@ -29,7 +35,6 @@ namespace tile {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -38,19 +43,21 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
-constexpr int KB = 64;                        // k per slab: four 16-wide matrix steps
+constexpr int KB = 64;                        // k per slab: two 32-wide matrix steps
 constexpr uint32_t OOB = 0x7ffffff0u;         // beyond every buffer range used here: such loads return zero
 constexpr uint32_t RSRC_DW3 = 0x00020000u;    // raw buffer, 32-bit data format
 
-__device__ __forceinline__ int swz_kc(int r) { return (r & 7) ^ ((r >> 3) & 3); }
-__device__ __forceinline__ int swz_rc(int k) { return ((k & 1) << 2) ^ ((k & 2) * 5); }
+__device__ __forceinline__ int swz_kc(int r) { return r & 7; }
+__device__ __forceinline__ int swz_rc(int k) { return ((k & 1) << 2) ^ ((k & 2) * 5) ^ ((k >> 2) & 2); }
 
+// D[row][col] += sum_k A[row][k] B[col][k]: lane l holds A row l % 16 and B column
+// l % 16 at k = 8 (l / 16) .. + 7, and D column l % 16, rows 4 (l / 16) .. + 3.
 template <int DT>
-__device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     if constexpr (DT == 0)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
 __device__ __forceinline__ i32x4 make_rsrc(const void *base, uint32_t bytes) {
@@ -129,7 +136,7 @@ struct Operand {
     uint32_t range;                // KC: bytes from base to the end of the last row
     int width;                     // RC: rows, rounded up to whole chunks
     uint32_t off[LOADS];           // the lane's byte offset at slab 0
-    int kc[LOADS];                 // KC: first k of the lane's chunk
+    int kc;                        // KC: first k of the lane's chunk
 
     __device__ __forceinline__ void init(const Matrix &m, int64_t row0, int K_, int wave, int lane) {
         const int rows = (int)min((int64_t)R, m.rows - row0);
@@ -139,24 +146,23 @@ struct Operand {
             base = reinterpret_cast<const char *>(m.base + row0 * ld);
             range = (uint32_t)(((int64_t)(rows - 1) * ld + ((K + 7) & ~7)) * 2);
             width = 0;
+            kc = 8 * ((lane & 7) ^ swz_kc(lane >> 3));   // the rows of one lane are a multiple of 8 apart
 #pragma unroll
             for (int x = 0; x < LOADS; ++x) {
                 const int r = 8 * (wave * LOADS + x) + (lane >> 3);
-                const int c = (lane & 7) ^ swz_kc(r);
-                off[x] = r < rows ? (uint32_t)(r * ld + 8 * c) * 2 : OOB;
-                kc[x] = 8 * c;
+                off[x] = r < rows ? (uint32_t)(r * ld + kc) * 2 : OOB;
             }
         } else {
             constexpr int CH = R / 8;                // 16-byte chunks per k-row
             base = reinterpret_cast<const char *>(m.base + row0);
             range = 0;
             width = (rows + 7) & ~7;
+            kc = 0;
 #pragma unroll
             for (int x = 0; x < LOADS; ++x) {
                 const int k = (64 / CH) * (wave * LOADS + x) + lane / CH;
                 const int c = (lane % CH) ^ swz_rc(k);
                 off[x] = 8 * c < rows ? (uint32_t)(k * ld + 8 * c) * 2 : OOB;
-                kc[x] = k;
             }
         }
     }
@@ -173,22 +179,34 @@ struct Operand {
     template <bool RAGGED>
     __device__ __forceinline__ void load(i32x4 r, int slab, int x, uint32_t dst) const {
         uint32_t o = off[x];
-        if constexpr (RAGGED) o = slab * KB + kc[x] < K ? o : OOB;
+        if constexpr (RAGGED && KC) o = slab * KB + kc < K ? o : OOB;
         load_lds16(r, dst + x * 1024, o);
     }
 
-    // Where the lane reads 32-row block 0 of the wave's rows (from `first`, a
-    // multiple of 32) at k-step 0.
-    static __device__ __forceinline__ uint32_t read_base(uint32_t lds, int first, int lane, int kk, int block) {
-        const int half = lane >> 5;
+    // Where the lane reads its share of 16-row block `block` of the rows from
+    // `first` (a multiple of 16) at matrix step `step` (32 k): one of ADDRESSES
+    // registers plus a constant.  KC rows 16 apart share their swizzle, so a block
+    // is a constant and a step an address; with RC it is the other way round.
+    template <int BLOCKS>
+    static constexpr int addresses() { return KC ? 2 : BLOCKS; }
+    static constexpr int which(int block, int step) { return KC ? step : block; }
+    static constexpr int constant(int block, int step) { return KC ? block * 2048 : step * 64 * R; }
+    static __device__ __forceinline__ uint32_t address(uint32_t lds, int first, int lane, int number) {
+        const int group = lane >> 4;
         if constexpr (KC) {
-            const int r = lane & 31;
-            return lds + first * 128 + r * 128 + ((((2 * kk + half) ^ swz_kc(r)) & 7) << 4);
+            const int r = first + (lane & 15);
+            return lds + r * 128 + (((4 * number + group) ^ swz_kc(r)) << 4);
         } else {
-            const int n = first + block * 32 + ((lane >> 4) & 1) * 16 + 4 * (lane & 3);
-            const int k = 8 * half + ((lane & 15) >> 2);
+            const int n = first + number * 16 + 4 * (lane & 3);
+            const int k = 8 * group + ((lane & 15) >> 2);
             return lds + k * (2 * R) + ((((n >> 3) ^ swz_rc(k)) & (R / 8 - 1)) << 4) + ((n & 7) << 1);
         }
+    }
+    // The fragment at `addr`: eight consecutive k of the lane's row.
+    static __device__ __forceinline__ u32x4 fragment(uint32_t addr) {
+        if constexpr (KC) return lds_b128<0>(addr);
+        const u32x2 a = lds_tr16<0>(addr), b = lds_tr16<0>(addr + 8 * R);
+        return u32x4{a[0], a[1], b[0], b[1]};
     }
 };
 
@@ -197,7 +215,7 @@ struct Grid {
     int tiles_p, tiles_q;    // tiles along P and Q
     int band;                // ids run along P inside bands of this many P tiles
     int splits;              // slices of k (slowest)
-    int slabs;               // 64-wide slabs of k
+    int slabs;               // slabs of k
 };
 
 // The workgroup's tile and slice.  Workgroup b runs on XCD b % 8; each XCD gets a
@@ -218,32 +236,33 @@ __device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &spli
     tp = bnd * g.band + (w - tq * rows);
 }
 
-// The product loop of a TP x TQ tile on WP x WQ waves with NS stages.
-template <int DT, bool PK, bool QK, int TP_, int TQ_, int WP_, int WQ_, int NS_>
+// The product loop of a TP x TQ tile on WP x WQ waves with NSP stages of P and NSQ
+// of Q (NSP >= NSQ).
+template <int DT, bool PK, bool QK, int TP_, int TQ_, int WP_, int WQ_, int NSP_, int NSQ_>
 struct Loop {
-    static constexpr int TP = TP_, TQ = TQ_, WP = WP_, WQ = WQ_, NS = NS_;
+    static constexpr int TP = TP_, TQ = TQ_, WP = WP_, WQ = WQ_, NSP = NSP_, NSQ = NSQ_;
     static constexpr int NW = WP * WQ, NT = 64 * NW;
     static constexpr int WAVE_P = TP / WP, WAVE_Q = TQ / WQ;
-    static constexpr int RB = WAVE_P / 32, CB = WAVE_Q / 32;   // 32 x 32 blocks of a wave
+    static constexpr int RB = WAVE_P / 16, CB = WAVE_Q / 16;   // 16 x 16 blocks of a wave
+    static constexpr int HB = RB / 2;                          // P blocks of half a step
     using OpP = Operand<PK, TP, NW>;
     using OpQ = Operand<QK, TQ, NW>;
     static constexpr int LOADS = OpP::LOADS + OpQ::LOADS;      // per wave and slab
-    static constexpr int QREG = NS * OpP::SLAB;                // Q's slabs lie behind P's
-    static constexpr int LDS_BYTES = NS * (OpP::SLAB + OpQ::SLAB);
-    static_assert(NS >= 2 && NS <= 4, "two to four stages");
+    static constexpr int QREG = NSP * OpP::SLAB;               // Q's slabs lie behind P's
+    static constexpr int LDS_BYTES = NSP * OpP::SLAB + NSQ * OpQ::SLAB;
+    static constexpr int PA = OpP::template addresses<RB>(), QA = OpQ::template addresses<CB>();
+    static_assert(NSQ == 2 && (NSP == 2 || NSP == 3), "two stages, or three of P");
+    static constexpr int ROUND = NSP == NSQ ? 2 : 6;           // iterations until the stages repeat
 
     struct Acc {
-        f32x16 v[RB][CB];
-    };
-    struct Frags {
-        u32x4 p[RB], q[CB];
+        f32x4 v[RB][CB];
     };
 
     int lane, wave, wp, wq;
     uint32_t lds0;
     OpP P;
     OpQ Q;
-    uint32_t pa[PK ? 4 : RB], qa[QK ? 4 : CB];
+    uint32_t pa[PA], qa[QA];
 
     __device__ __forceinline__ Loop(char *lds) {
         lane = threadIdx.x & 63;
@@ -252,93 +271,84 @@ struct Loop {
         wq = wave / WP;
         lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
 #pragma unroll
-        for (int i = 0; i < (PK ? 4 : RB); ++i) pa[i] = OpP::read_base(lds0, wp * WAVE_P, lane, PK ? i : 0, PK ? 0 : i);
+        for (int i = 0; i < PA; ++i) pa[i] = OpP::address(lds0, wp * WAVE_P, lane, i);
 #pragma unroll
-        for (int i = 0; i < (QK ? 4 : CB); ++i)
-            qa[i] = OpQ::read_base(lds0 + QREG, wq * WAVE_Q, lane, QK ? i : 0, QK ? 0 : i);
+        for (int i = 0; i < QA; ++i) qa[i] = OpQ::address(lds0 + QREG, wq * WAVE_Q, lane, i);
     }
 
     static __device__ __forceinline__ void zero(Acc &a) {
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) a.v[i][j][e] = 0.0f;
+            for (int j = 0; j < CB; ++j) a.v[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    template <int ST, int KK>
-    __device__ __forceinline__ void read(Frags &f) const {
-        if constexpr (PK) {
-#pragma unroll
-            for (int i = 0; i < RB; ++i) f.p[i] = lds_b128<ST * OpP::SLAB>(pa[KK] + i * 4096);
+    // P's fragments of half a step, Q's of a step.
+    struct FragP {
+        u32x4 v[HB];
+    };
+    struct FragQ {
+        u32x4 v[CB];
+    };
+    // Fragment R of what half HALF of step STEP of iteration IT (modulo ROUND)
+    // needs: of the first half Q's fragments and P's, of the second P's.
+    template <int IT, int STEP, int HALF, int R>
+    __device__ __forceinline__ void read(FragP &p, FragQ &q) const {
+        if constexpr (HALF == 0 && R > 0 && R <= CB) {
+            q.v[R - 1] = OpQ::fragment(qa[OpQ::which(R - 1, STEP)] + IT % NSQ * OpQ::SLAB + OpQ::constant(R - 1, STEP));
         } else {
-#pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const u32x2 a = lds_tr16<ST * OpP::SLAB + KK * 32 * TP>(pa[i]);
-                const u32x2 b = lds_tr16<ST * OpP::SLAB + KK * 32 * TP + 8 * TP>(pa[i]);
-                f.p[i] = u32x4{a[0], a[1], b[0], b[1]};
-            }
-        }
-        if constexpr (QK) {
-#pragma unroll
-            for (int j = 0; j < CB; ++j) f.q[j] = lds_b128<ST * OpQ::SLAB>(qa[KK] + j * 4096);
-        } else {
-#pragma unroll
-            for (int j = 0; j < CB; ++j) {
-                const u32x2 a = lds_tr16<ST * OpQ::SLAB + KK * 32 * TQ>(qa[j]);
-                const u32x2 b = lds_tr16<ST * OpQ::SLAB + KK * 32 * TQ + 8 * TQ>(qa[j]);
-                f.q[j] = u32x4{a[0], a[1], b[0], b[1]};
-            }
+            constexpr int i = HALF == 0 && R > 0 ? R - CB : R, b = HALF * HB + i;
+            p.v[i] = OpP::fragment(pa[OpP::which(b, STEP)] + IT % NSP * OpP::SLAB + OpP::constant(b, STEP));
         }
     }
+    static constexpr int reads(int half) { return half == 0 ? HB + CB : HB; }
 
-    static __device__ __forceinline__ void mma(const Frags &f, Acc &acc) {
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < CB; ++j) acc.v[i][j] = mfma<DT>(f.p[i], f.q[j], acc.v[i][j]);
-    }
-
-    // The loads of one slab into one stage.
+    // The loads of an iteration: slab sq of Q into its stage, then slab sp of P.
     struct Issue {
         i32x4 rp, rq;
         uint32_t dp, dq;
-        int slab;
+        int sp, sq;
+        bool p, q;   // whether there are such slabs
     };
-    __device__ __forceinline__ Issue prepare(int slab, int st) const {
-        return Issue{P.rsrc(slab), Q.rsrc(slab), lds0 + st * OpP::SLAB + wave * OpP::LOADS * 1024,
-                     lds0 + QREG + st * OpQ::SLAB + wave * OpQ::LOADS * 1024, slab};
+    __device__ __forceinline__ Issue prepare(int sp, int stp, bool p, int sq, int stq, bool q) const {
+        return Issue{P.rsrc(sp), Q.rsrc(sq), lds0 + stp * OpP::SLAB + wave * OpP::LOADS * 1024,
+                     lds0 + QREG + stq * OpQ::SLAB + wave * OpQ::LOADS * 1024, sp, sq, p, q};
     }
     template <bool RAGGED>
     __device__ __forceinline__ void load_one(const Issue &q, int x) const {
-        if (x < OpP::LOADS) P.template load<RAGGED>(q.rp, q.slab, x, q.dp);
-        else Q.template load<RAGGED>(q.rq, q.slab, x - OpP::LOADS, q.dq);
+        if (x < OpQ::LOADS) {
+            if (q.q) Q.template load<RAGGED>(q.rq, q.sq, x, q.dq);
+        } else if (q.p) {
+            P.template load<RAGGED>(q.rp, q.sp, x - OpQ::LOADS, q.dp);
+        }
     }
-    template <bool RAGGED>
-    __device__ __forceinline__ void load_all(int slab, int st) const {
-        const Issue q = prepare(slab, st);
+
+    // Products [M0, M1) of half HALF of a step, and evenly between them the reads of
+    // the next half's fragments (half NH of step NSTEP of iteration NIT) when READ, and
+    // the loads of `issue` when LOAD: the matrix pipe keeps running while they go
+    // out.  Reads in one burst ahead of the products leave it idle while eight
+    // waves queue for the LDS.
+    template <int HALF, int M0, int M1, bool READ, int NIT, int NSTEP, int NH, bool LOAD, bool RAGGED>
+    __device__ __forceinline__ void products(const FragP &p, const FragQ &q, Acc &acc, FragP &np, FragQ &nq,
+                                             const Issue &issue) const {
+        auto one = [&](auto MC) {
+            constexpr int m = decltype(MC)::value, k = m - M0, n = M1 - M0, i = HALF * HB + m / CB, j = m % CB;
+            acc.v[i][j] = mfma<DT>(p.v[m / CB], q.v[j], acc.v[i][j]);
+            constexpr int NR = READ ? reads(NH) : 0, r0 = k * NR / n, r1 = (k + 1) * NR / n;
+            constexpr int NL = LOAD ? LOADS : 0, x0 = k * NL / n, x1 = (k + 1) * NL / n;
+            if constexpr (r1 > r0 || x1 > x0) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (r1 > r0) read<NIT, NSTEP, NH, r0>(np, nq);
+            if constexpr (r1 > r0 + 1) read<NIT, NSTEP, NH, r0 + 1>(np, nq);
+            static_assert(r1 <= r0 + 2, "at most two reads after a product");
 #pragma unroll
-        for (int x = 0; x < LOADS; ++x) load_one<RAGGED>(q, x);
+            for (int x = x0; x < x1; ++x) load_one<RAGGED>(issue, x);
+            if constexpr (r1 > r0 || x1 > x0) __builtin_amdgcn_sched_barrier(0);
+        };
+        each(std::make_integer_sequence<int, M1 - M0>(), [&](auto I) { one(std::integral_constant<int, M0 + decltype(I)::value>()); });
     }
-    // f's products with the loads of `q` (when `load`) between them, so that the
-    // matrix pipe keeps running while they go out
-    template <bool RAGGED>
-    __device__ __forceinline__ void mma_load(const Frags &f, Acc &acc, bool load, const Issue &q) const {
-        constexpr int NM = RB * CB;
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < CB; ++j) {
-                acc.v[i][j] = mfma<DT>(f.p[i], f.q[j], acc.v[i][j]);
-                __builtin_amdgcn_sched_barrier(0);
-                if (load) {
-                    const int m = i * CB + j;
-#pragma unroll
-                    for (int x = m * LOADS / NM; x < (m + 1) * LOADS / NM; ++x) load_one<RAGGED>(q, x);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+    template <class F, int... I>
+    static __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F &&f) {
+        (f(std::integral_constant<int, I>()), ...);
     }
 
     // acc += the products over slabs [s0, s1) of K.  Ends with a barrier: the LDS
@@ -350,54 +360,63 @@ struct Loop {
         Q.init(mq, q0, K, wave, lane);
         const int n = s1 - s0;
         if (n <= 0) return;
-        Frags f[2];
-        load_all<RAGGED>(s0, 0);
-        if (n > 1) load_all<RAGGED>(s0 + 1, 1);
-        if (NS > 2 && n > 2) load_all<RAGGED>(s0 + 2, 2 % NS);
-        if (NS > 3 && n > 3) load_all<RAGGED>(s0 + 3, 3 % NS);
-        wait_stages<LOADS>(min(NS, n) - 1);
+        FragP p[2];
+        FragQ q[2];
+        // Slabs in the order in which they are waited for: Q 0, P 0, Q 1, P 1, (P 2).
+        // Iteration i then loads Q i + 2 and P i + NSP.
+#pragma unroll
+        for (int i = 0; i < NSP; ++i) {
+            const Issue first = prepare(s0 + (i < n ? i : 0), i, i < n, s0 + (i < n ? i : 0), i % NSQ, i < NSQ && i < n);
+#pragma unroll
+            for (int x = 0; x < LOADS; ++x) load_one<RAGGED>(first, x);
+        }
+        if (n > NSP - 1) wait_vm_lgkm<LOADS + (NSP - 2) * OpP::LOADS>();
+        else if (n > 1) wait_vm_lgkm<LOADS>();
+        else wait_vm_lgkm<0>();
         __builtin_amdgcn_s_barrier();
-        read<0, 0>(f[0]);
-        // Iteration i on stage ST: k-steps 0..2 read the next step's fragments and
-        // multiply the current ones.  Step 3 hands the stage over: wait for this
-        // wave's loads of i + 1 and its reads of (i, 3); after the barrier every
-        // wave's loads of i + 1 are there and nobody reads stage ST any more; read
-        // (i + 1, 0), then multiply step 3 while slab i + NS goes into stage ST.
-        auto iter = [&](int i, auto STC) {
-            constexpr int st = decltype(STC)::value;
+        each(std::make_integer_sequence<int, reads(0)>(), [&](auto R) { read<0, 0, 0, decltype(R)::value>(p[0], q[0]); });
+        // Iteration i (IT modulo ROUND): four half steps, each of which reads the next
+        // one's fragments while it multiplies its own.  The last hands the stages
+        // over on its way: wait for this wave's loads of i + 1 (P i + 2 may still be
+        // on its way) and its own reads; after the barrier every wave's loads of
+        // i + 1 are there and nobody reads i's stages any more; read i + 1's first
+        // fragments and load into i's stages.  STEADY: all slabs named here exist.
+        auto iter = [&](int i, auto ITC, auto STEADY) {
+            constexpr int it = decltype(ITC)::value, nit = (it + 1) % ROUND, NM = HB * CB, BAR = NM / 4;
+            constexpr bool steady = decltype(STEADY)::value;
+            const Issue none{};
             __builtin_amdgcn_sched_barrier(0);
-            read<st, 1>(f[1]);
-            mma(f[0], acc);
-            __builtin_amdgcn_sched_barrier(0);
-            read<st, 2>(f[0]);
-            mma(f[1], acc);
-            __builtin_amdgcn_sched_barrier(0);
-            read<st, 3>(f[1]);
-            mma(f[0], acc);
-            __builtin_amdgcn_sched_barrier(0);
-            if (i + 1 < n) {
-                wait_stages<LOADS>(max(0, min(NS - 2, n - i - 2)));
+            products<0, 0, NM, true, it, 0, 1, false, RAGGED>(p[0], q[0], acc, p[1], q[1], none);
+            products<1, 0, NM, true, it, 1, 0, false, RAGGED>(p[1], q[0], acc, p[0], q[1], none);
+            products<0, 0, NM, true, it, 1, 1, false, RAGGED>(p[0], q[1], acc, p[1], q[0], none);
+            products<1, 0, BAR, false, it, 0, 0, false, RAGGED>(p[1], q[1], acc, p[0], q[0], none);
+            if (steady || i + 1 < n) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (NSP > 2 && (steady || i + 2 < n)) wait_vm_lgkm<(NSP - 2) * OpP::LOADS>();
+                else wait_vm_lgkm<0>();
                 __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
-                read<(st + 1) % NS, 0>(f[0]);
+                const bool more_p = steady || i + NSP < n, more_q = steady || i + NSQ < n;
+                products<1, BAR, NM, true, nit, 0, 0, true, RAGGED>(
+                    p[1], q[1], acc, p[0], q[0],
+                    prepare(s0 + (more_p ? i + NSP : i), it % NSP, more_p, s0 + (more_q ? i + NSQ : i), it % NSQ, more_q));
+            } else {
+                products<1, BAR, NM, false, it, 0, 0, false, RAGGED>(p[1], q[1], acc, p[0], q[0], none);
             }
-            const bool more = i + NS < n;
-            mma_load<RAGGED>(f[1], acc, more, prepare(s0 + (more ? i + NS : i), st));
             __builtin_amdgcn_sched_barrier(0);
         };
-        for (int i = 0; i < n; i += NS) {
-            iter(i, std::integral_constant<int, 0>());
-            if (i + 1 < n) iter(i + 1, std::integral_constant<int, 1>());
-            if constexpr (NS > 2)
-                if (i + 2 < n) iter(i + 2, std::integral_constant<int, 2>());
-            if constexpr (NS > 3)
-                if (i + 3 < n) iter(i + 3, std::integral_constant<int, 3>());
-        }
+        int i = 0;
+        for (; i + ROUND + NSP <= n; i += ROUND)
+            each(std::make_integer_sequence<int, ROUND>(), [&](auto I) { iter(i + decltype(I)::value, I, std::true_type()); });
+        for (; i < n; i += ROUND)
+            each(std::make_integer_sequence<int, ROUND>(), [&](auto I) {
+                if (i + decltype(I)::value < n) iter(i + decltype(I)::value, I, std::false_type());
+            });
         wait_vm_lgkm<0>();
         __builtin_amdgcn_s_barrier();
     }
-    __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0,
-                                            int s1, Acc &acc) {
+    __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
+                                            Acc &acc) {
         if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc);
         else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
     }
@@ -405,39 +424,37 @@ struct Loop {
     __device__ __forceinline__ bool active() const { return true; }
 
     // Register e of block (i, j) is element (p, q) of the tile.
-    __device__ __forceinline__ int p_of(int i, int e) const {
-        return wp * WAVE_P + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-    }
-    __device__ __forceinline__ int q_of(int j) const { return wq * WAVE_Q + j * 32 + (lane & 31); }
+    __device__ __forceinline__ int p_of(int i, int e) const { return wp * WAVE_P + i * 16 + 4 * (lane >> 4) + e; }
+    __device__ __forceinline__ int q_of(int j) const { return wq * WAVE_Q + j * 16 + (lane & 15); }
 };
 
-// The product loop for few rows of Q, where P's stream from memory is the cost:
-// four waves that split every slab's four k-steps between them, each holding the
-// whole TP x TQ tile's sums over a quarter of k.  So every staged byte is read
-// from LDS once (P) or once per P block (Q), and a chain of fp32 additions is a
-// quarter as long.  Small tiles and several stages keep enough bytes in flight
-// per CU.  After the loop the waves add their sums through LDS in wave order:
-// wave w < TP / 32 then owns 32-row block w (the others own nothing), and the
-// members below describe that state, as Loop's do.
+// The product loop for few rows of Q, where P's stream from memory is the cost.
+// Four waves: wave 2 h + s takes half h of P's rows and matrix step s of every
+// slab, so every staged byte of P is read from LDS once, and a chain of fp32
+// additions is half as long.  Small tiles and several stages keep enough bytes in
+// flight per CU.  After the loop the two waves of a half swap sums through LDS:
+// each then owns half of their blocks (of a 32-row tile, which has one block a
+// half, the wave of step 0 owns it and the other nothing), and the members below
+// describe that state, as Loop's do.
 template <int DT, bool PK, bool QK, int TP_, int TQ_, int NS_>
 struct ThinLoop {
     static constexpr int TP = TP_, TQ = TQ_, NS = NS_;
     static constexpr int NW = 4, NT = 256;
-    static constexpr int WP = TP / 32, WQ = 1;
-    static constexpr int WAVE_P = 32, WAVE_Q = TQ;
-    static constexpr int RB = 1, CB = TQ / 32;
-    static constexpr int PB = TP / 32;                         // P blocks during the loop
+    static constexpr int PB = TP / 32;                         // P blocks of a wave during the loop
+    static constexpr int RB = PB > 1 ? PB / 2 : 1, CB = TQ / 16;
+    static constexpr int WAVE_P = 16 * RB, WAVE_Q = TQ, WP = TP / WAVE_P, WQ = 1;
     using OpP = Operand<PK, TP, NW>;
     using OpQ = Operand<QK, TQ, NW>;
     static constexpr int LOADS = OpP::LOADS + OpQ::LOADS;
     static constexpr int STAGE = OpP::SLAB + OpQ::SLAB;
-    static constexpr int MERGE_BYTES = 4 * PB * 4096;          // four waves' sums of one block column
-    static constexpr int LDS_BYTES = NS * STAGE > MERGE_BYTES ? NS * STAGE : MERGE_BYTES;
+    static constexpr int LDS_BYTES = NS * STAGE;
+    static constexpr int PA = PK ? 1 : PB, QA = QK ? 1 : CB;
+    static_assert(PB == 1 || PB == 2 || PB == 4, "32, 64 or 128 rows of P");
     static_assert(NS >= 2 && NS <= 8 && (NS - 1) * LOADS < 64, "the wait counter holds the loads in flight");
-    static_assert(PB <= 4, "a wave per block");
+    static_assert(NW * RB * CB * 1024 <= LDS_BYTES, "the sums that are swapped fit");
 
     struct Acc {
-        f32x16 v[RB][CB];
+        f32x4 v[RB][CB];
     };
 
     int lane, wave, wp, wq;
@@ -445,28 +462,28 @@ struct ThinLoop {
     char *lds_;
     OpP P;
     OpQ Q;
-    uint32_t pa[PK ? 1 : PB], qa[QK ? 1 : CB];
+    uint32_t pa[PA], qa[QA];
 
     __device__ __forceinline__ ThinLoop(char *lds) : lds_(lds) {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-        wp = wave;
+        wp = PB > 1 ? wave : wave >> 1;
         wq = 0;
+        const int step = wave & 1;
         lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
-        // the wave's k-step: a chunk of KC rows, 16 k-rows of RC slabs
 #pragma unroll
-        for (int i = 0; i < (PK ? 1 : PB); ++i)
-            pa[i] = OpP::read_base(lds0, 0, lane, wave, i) + (PK ? 0 : wave * 32 * TP);
+        for (int i = 0; i < PA; ++i)
+            pa[i] = OpP::address(lds0, (wave >> 1) * (TP / 2), lane, PK ? step : i) + (PK ? 0 : OpP::constant(0, step));
 #pragma unroll
-        for (int i = 0; i < (QK ? 1 : CB); ++i)
-            qa[i] = OpQ::read_base(lds0 + OpP::SLAB, 0, lane, wave, i) + (QK ? 0 : wave * 32 * TQ);
+        for (int i = 0; i < QA; ++i)
+            qa[i] = OpQ::address(lds0 + OpP::SLAB, 0, lane, QK ? step : i) + (QK ? 0 : OpQ::constant(0, step));
     }
 
     static __device__ __forceinline__ void zero(Acc &a) {
 #pragma unroll
-        for (int j = 0; j < CB; ++j)
+        for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) a.v[0][j][e] = 0.0f;
+            for (int j = 0; j < CB; ++j) a.v[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
     struct Frags {
@@ -475,23 +492,9 @@ struct ThinLoop {
     __device__ __forceinline__ void read(Frags &f, int st) const {
         const uint32_t o = st * STAGE;
 #pragma unroll
-        for (int i = 0; i < PB; ++i) {
-            if constexpr (PK) {
-                f.p[i] = lds_b128<0>(pa[0] + o + i * 4096);
-            } else {
-                const u32x2 a = lds_tr16<0>(pa[i] + o), b = lds_tr16<8 * TP>(pa[i] + o);
-                f.p[i] = u32x4{a[0], a[1], b[0], b[1]};
-            }
-        }
+        for (int i = 0; i < PB; ++i) f.p[i] = OpP::fragment(pa[PK ? 0 : i] + o + (PK ? OpP::constant(i, 0) : 0));
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
-            if constexpr (QK) {
-                f.q[j] = lds_b128<0>(qa[0] + o + j * 4096);
-            } else {
-                const u32x2 a = lds_tr16<0>(qa[j] + o), b = lds_tr16<8 * TQ>(qa[j] + o);
-                f.q[j] = u32x4{a[0], a[1], b[0], b[1]};
-            }
-        }
+        for (int j = 0; j < CB; ++j) f.q[j] = OpQ::fragment(qa[QK ? 0 : j] + o + (QK ? OpQ::constant(j, 0) : 0));
     }
     template <bool RAGGED>
     __device__ __forceinline__ void load_all(int slab, int st) const {
@@ -511,13 +514,11 @@ struct ThinLoop {
         Q.init(mq, q0, K, wave, lane);
         const int n = s1 - s0;
         if (n <= 0) return;
-        f32x16 acc[PB][CB];
+        f32x4 acc[PB][CB];
 #pragma unroll
         for (int i = 0; i < PB; ++i)
 #pragma unroll
-            for (int j = 0; j < CB; ++j)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+            for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int i = 0; i < min(NS, n); ++i) load_all<RAGGED>(s0 + i, i);
         wait_stages<LOADS>(min(NS, n) - 1);
         __builtin_amdgcn_s_barrier();
@@ -547,29 +548,29 @@ struct ThinLoop {
         }
         wait_vm_lgkm<0>();
         __builtin_amdgcn_s_barrier();
-        // the waves' sums of one block column at a time, [wave][block][quad][lane]
+        const bool second = wave & 1;
+        // a wave's gift to its partner, [wave][block][lane]
         f32x4 *buf = reinterpret_cast<f32x4 *>(lds_);
+        if constexpr (PB > 1) {
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
+            for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int i = 0; i < PB; ++i)
+                for (int j = 0; j < CB; ++j) buf[(wave * RB * CB + i * CB + j) * 64 + lane] = second ? acc[i][j] : acc[RB + i][j];
+        } else if (second) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    buf[(wave * PB + i) * 256 + g * 64 + lane] =
-                        f32x4{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-            __syncthreads();
-            if (active()) {
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    f32x4 v = buf[wave * 256 + g * 64 + lane];
-#pragma unroll
-                    for (int w = 1; w < 4; ++w) v += buf[(w * PB + wave) * 256 + g * 64 + lane];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) out.v[0][j][4 * g + x] = v[x];
-                }
-            }
-            __syncthreads();
+            for (int j = 0; j < CB; ++j) buf[(wave * CB + j) * 64 + lane] = acc[0][j];
         }
+        __syncthreads();
+        if (active()) {
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < CB; ++j) {
+                    const f32x4 mine = PB > 1 && second ? acc[(RB + i) % PB][j] : acc[i][j];
+                    out.v[i][j] = mine + buf[((wave ^ 1) * RB * CB + i * CB + j) * 64 + lane];
+                }
+        }
+        __syncthreads();
     }
     __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0,
                                             int s1, Acc &acc) {
@@ -577,9 +578,9 @@ struct ThinLoop {
         else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
     }
 
-    __device__ __forceinline__ bool active() const { return wave < WP; }
-    __device__ __forceinline__ int p_of(int, int e) const { return wp * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3); }
-    __device__ __forceinline__ int q_of(int j) const { return j * 32 + (lane & 31); }
+    __device__ __forceinline__ bool active() const { return PB > 1 || !(wave & 1); }
+    __device__ __forceinline__ int p_of(int i, int e) const { return wp * WAVE_P + i * 16 + 4 * (lane >> 4) + e; }
+    __device__ __forceinline__ int q_of(int j) const { return j * 16 + (lane & 15); }
 };
 
 }  // namespace tile
