@@ -548,28 +548,28 @@ struct ThinLoop {
         }
         wait_vm_lgkm<0>();
         __builtin_amdgcn_s_barrier();
-        const bool second = wave & 1;
         // a wave's gift to its partner, [wave][block][lane]
         f32x4 *buf = reinterpret_cast<f32x4 *>(lds_);
-        if constexpr (PB > 1) {
+        const bool second = (threadIdx.x >> 6) & 1;
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
+        for (int i = 0; i < RB; ++i)
 #pragma unroll
-                for (int j = 0; j < CB; ++j) buf[(wave * RB * CB + i * CB + j) * 64 + lane] = second ? acc[i][j] : acc[RB + i][j];
-        } else if (second) {
+            for (int j = 0; j < CB; ++j) {
+                // by value: chosen by address the sums would go through memory
+                const f32x4 low = acc[i][j], high = acc[PB > 1 ? RB + i : i][j];
+                f32x4 give;
 #pragma unroll
-            for (int j = 0; j < CB; ++j) buf[(wave * CB + j) * 64 + lane] = acc[0][j];
-        }
-        __syncthreads();
-        if (active()) {
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int j = 0; j < CB; ++j) {
-                    const f32x4 mine = PB > 1 && second ? acc[(RB + i) % PB][j] : acc[i][j];
-                    out.v[i][j] = mine + buf[((wave ^ 1) * RB * CB + i * CB + j) * 64 + lane];
+                for (int e = 0; e < 4; ++e) {
+                    give[e] = second ? low[e] : high[e];
+                    out.v[i][j][e] = second ? high[e] : low[e];
                 }
-        }
+                buf[(wave * RB * CB + i * CB + j) * 64 + lane] = give;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < CB; ++j) out.v[i][j] += buf[((wave ^ 1) * RB * CB + i * CB + j) * 64 + lane];
         __syncthreads();
     }
     __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0,
