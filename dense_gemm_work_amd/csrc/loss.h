@@ -12,7 +12,7 @@ namespace dgw {
 // Tile shapes (P x Q; P: the dimension contiguous in the result).  The tiles of
 // few rows take a Q operand with k contiguous, the 32- and 64-row ones a P
 // operand with k contiguous too.
-enum LossTile : int { LT_128x128 = 0, LT_256x256, LT_32x32, LT_128x32, LT_64x64, LT_128x64 };
+enum LossTile : int { LT_128x128 = 0, LT_256x256, LT_32x32, LT_128x32, LT_64x64, LT_64x128, LT_128x64 };
 struct LossTileShape {
     int p, q, per_cu;   // rows of P and Q, workgroups resident per CU
 };
@@ -47,11 +47,14 @@ struct LossStats {
     float *max, *sum, *dot;   // [tiles_v][T]
 };
 
-// What a row contributes to the logits' gradient, dz = a p - b q (0 when !on).
-struct LossRow {
-    float lse2;   // lse * log2 e
-    float a, b;
-    float on;
+// What the rows' contributions to the logits' gradient follow from.
+struct LossRows {
+    int64_t V;
+    float zeta, tau;
+    const int64_t *target;   // XENT
+    int64_t ignore;
+    const float *entropy;    // DISTILL
+    const float *grad, *lse;
 };
 
 struct LossProblem {
@@ -67,7 +70,7 @@ hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const Lo
 
 // Logits again, as their gradient dz [T][ldd] (16 bits; ldd a multiple of 8,
 // zeros behind p.V), times *scale when scale != nullptr.
-hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz,
+hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz,
                           int64_t ldd, hipStream_t stream);
 
 // out[q][p] = sum_k P[p][k] Q[q][k], times *unscale when unscale != nullptr.
@@ -89,6 +92,10 @@ struct LossProduct {
 };
 hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStream_t stream);
 
+// The same for K <= 64 (one slab), both operands' rows contiguous and LO_16, on at
+// most about `workgroups` persistent workgroups (the splits and slots do not apply).
+hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream);
+
 // out from the slots of `splits` slices: out_kind LO_16, LO_F32 or LO_F32_ADD.
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream);
 int64_t loss_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits);
@@ -103,9 +110,8 @@ int loss_bucket_width(int64_t V);
 hipError_t launch_loss_finish(const gemm_loss_args_t &a, int tiles, const LossStats &s, const float *entropy,
                               hipStream_t stream);
 
-// The rows' factors; for fp16 also scale[0] (multiplied into dz) and scale[1] = 1 / scale[0].
-hipError_t launch_loss_rows(const gemm_loss_args_t &a, const float *entropy, LossRow *rows, float *scale,
-                            hipStream_t stream);
+// scale[0], the power of two multiplied into an fp16 dz, and scale[1] = 1 / scale[0].
+hipError_t launch_loss_scale(const LossRows &rows, int64_t T, float *scale, hipStream_t stream);
 
 hipError_t launch_loss_zero(void *out, int64_t rows, int64_t row_bytes, int64_t ld_bytes, hipStream_t stream);
 

@@ -102,7 +102,7 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
 struct Layout {
     int64_t entries = 0, starts = 0, entropy = 0;  // the teacher's entries
     int64_t stats = 0;                            // forward
-    int64_t rows = 0, scale = 0, dz = 0, dx = 0, dw = 0;   // backward
+    int64_t scale = 0, dz = 0, dx = 0, dw = 0;    // backward
     int64_t ldd = 0;
     int64_t bytes = 0;
     int64_t take(int64_t n) {
@@ -136,10 +136,16 @@ Choice choose(int64_t rows_p, int64_t rows_q, int64_t k, int cus) {
 // The logits' tile.  Up to 64 rows the stream of w is the cost and thin tiles
 // keep more of it in flight (V = 32768, H = 2048, T = 32: 35 us on 64 x 64 tiles,
 // 43 us on 128 x 128); a vocabulary of fewer 64-entry tiles than CUs is cut finer
-// (V = 8192, H = 1536, T = 1: 11.6 us on 32 x 32, 13.8 us on 64 x 64).
+// (V = 8192, H = 1536, T = 1: 11.6 us on 32 x 32, 13.8 us on 64 x 64).  So are more
+// rows where 128 x 128 tiles would leave half the CUs idle (V = 16000, H = 4096,
+// T = 100: 54 us on 128 x 128, 44 us on 64 x 128).
 int logits_tile(const gemm_loss_args_t &a, int64_t V, int cus) {
-    if (a.T > 64) return choose(V, a.T, 0, cus).tile;
-    if ((a.layout & 0xFu) == GEMM_B_KN) return a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
+    const bool kn = (a.layout & 0xFu) == GEMM_B_KN;
+    if (a.T > 64) {
+        if (!kn && 2 * ceil_div(V, 128) * ceil_div(a.T, 128) <= cus) return dgw::LT_64x128;
+        return choose(V, a.T, 0, cus).tile;
+    }
+    if (kn) return a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
     return a.T <= 32 && V < 64 * (int64_t)cus ? dgw::LT_32x32 : dgw::LT_64x64;
 }
 
@@ -163,6 +169,7 @@ struct Plan {
     int logits = dgw::LT_128x128, dx = dgw::LT_128x128, dw = dgw::LT_128x128;   // tiles
     int64_t piece = 0;
     int pieces = 0, dx_splits = 1, dw_splits = 1;
+    bool dw_outer = false;   // dw by the kernel of at most 64 rows
     Layout at;
 };
 
@@ -182,7 +189,6 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
     p.piece = std::min(round_up(a.V, 64), std::max<int64_t>(1024, PIECE_BYTES / 2 / std::max<int64_t>(a.T, 1) / 1024 * 1024));
     p.pieces = (int)ceil_div(a.V, p.piece);
     l.ldd = p.piece;
-    l.rows = l.take(a.T * (int64_t)sizeof(dgw::LossRow));
     l.scale = l.take(8);
     l.dz = l.take(a.T * l.ldd * 2);
     const int64_t first = std::min(a.V, p.piece);
@@ -199,6 +205,7 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
         const Choice c = dw_choice(rp, rq, a.T, cus);
         p.dw = c.tile;
         p.dw_splits = c.splits;
+        p.dw_outer = a.T <= 64 && a.dw_type == GEMM_LOSS_DW_SAME;
         if (p.dw_splits > 1) l.dw = l.take(dgw::loss_slots_bytes(p.dw, rp, rq, p.dw_splits));
     }
     return p;
@@ -213,6 +220,7 @@ T *part(void *ws, int64_t at) {
 struct Call {
     hipStream_t stream;
     void *ws = nullptr;
+    int cus;
     int dtype;
     bool nk;
     Plan plan;
@@ -224,9 +232,10 @@ int begin(const gemm_loss_args_t &a, bool backward, Call *c) {
     c->stream = a.stream ? reinterpret_cast<hipStream_t>(a.stream) : dgw::thread_stream();
     c->dtype = (a.layout & 0xF0u) == GEMM_FP16 ? 1 : 0;
     c->nk = (a.layout & 0xFu) == GEMM_B_NK;
-    int cus = a.num_cus, rc;
-    if (!cus && (rc = dgw::current_device_cus(&cus)) != GEMM_OK) return rc;
-    c->plan = make_plan(a, backward, cus);
+    int rc;
+    c->cus = a.num_cus;
+    if (!c->cus && (rc = dgw::current_device_cus(&c->cus)) != GEMM_OK) return rc;
+    c->plan = make_plan(a, backward, c->cus);
     const Layout &l = c->plan.at;
     c->ws = a.workspace;
     if (a.workspace) {
@@ -297,10 +306,12 @@ int backward(const gemm_loss_args_t &a) {
     Call c;
     if ((rc = begin(a, true, &c)) != GEMM_OK) return rc;
     const Plan &pl = c.plan;
-    dgw::LossRow *rows = part<dgw::LossRow>(c.ws, pl.at.rows);
+    const bool xent = a.kind == GEMM_LOSS_XENT;
+    const dgw::LossRows rows{a.V, a.z_loss, xent ? 1.0f : a.temperature, xent ? a.target : nullptr, a.ignore_index,
+                             c.entropy, a.grad, a.lse};
     float *scale = c.dtype == 1 ? part<float>(c.ws, pl.at.scale) : nullptr;
     uint16_t *dz = part<uint16_t>(c.ws, pl.at.dz);
-    if ((e = dgw::launch_loss_rows(a, c.entropy, rows, scale, c.stream)) != hipSuccess) return set_hip_error(e, "launch the rows' factors");
+    if (scale && (e = dgw::launch_loss_scale(rows, a.T, scale, c.stream)) != hipSuccess) return set_hip_error(e, "launch dz's scale");
     const float *unscale = scale ? scale + 1 : nullptr;
     dgw::LossProduct px;
     for (int i = 0; i < pl.pieces; ++i) {
@@ -340,7 +351,9 @@ int backward(const gemm_loss_args_t &a) {
                 q.out = part<float>(c.ws, pl.at.dw);
                 q.out_kind = dgw::LO_SLOTS;
             }
-            if ((e = dgw::launch_loss_product(c.dtype, pl.dw, q, c.stream)) != hipSuccess) return set_hip_error(e, "launch dw");
+            if (pl.dw_outer) e = dgw::launch_loss_outer(c.dtype, q, 2 * c.cus, c.stream);
+            else e = dgw::launch_loss_product(c.dtype, pl.dw, q, c.stream);
+            if (e != hipSuccess) return set_hip_error(e, "launch dw");
             if (pl.dw_splits > 1 &&
                 (e = dgw::launch_loss_join(c.dtype, pl.dw, join, part<float>(c.ws, pl.at.dw), c.stream)) != hipSuccess)
                 return set_hip_error(e, "launch dw's join");

@@ -255,10 +255,37 @@ __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &ac
 }
 
 // ---------------------------------------------------------------------------
+// What a row contributes to the logits' gradient, dz = a p - b q (0 when !on).
+// ---------------------------------------------------------------------------
+struct RowFactors {
+    float lse2;   // lse * log2 e
+    float a, b;
+    bool on;
+};
+__device__ __forceinline__ RowFactors row_factors(const LossRows &p, int64_t row) {
+    const float lse = p.lse[row], g = p.grad[row];
+    RowFactors r{lse * LOG2E, 0.0f, 0.0f, true};
+    if (p.target) {
+        const int64_t y = p.target[row];
+        const float bad = y < 0 || y >= p.V ? __builtin_nanf("") : 0.0f;
+        r.on = y != p.ignore;
+        r.a = g * __builtin_fmaf(2.0f * p.zeta, lse, 1.0f) + bad;
+        r.b = g;
+    } else {
+        const float h = p.entropy[row];
+        r.on = h != -INF;
+        r.a = h != h ? h : g * p.tau;
+        r.b = g * p.tau;
+    }
+    if (!r.on) r.lse2 = r.a = r.b = 0.0f;
+    return r;
+}
+
+// ---------------------------------------------------------------------------
 // The logits' gradient of one tile: dz = a p - b q, p = exp2(z c - lse2).
 // ---------------------------------------------------------------------------
 template <int DT, class L>
-__global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow *rows, const float *scale, uint16_t *dz,
+__global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, LossRows rows, const float *scale, uint16_t *dz,
                                                  int64_t ldd) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     int tp, tq, split;
@@ -278,7 +305,7 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
 #pragma unroll
     for (int j = 0; j < L::CB; ++j) {
         const int64_t row = q0 + loop.q_of(j);
-        const LossRow r = rows[row < p.T ? row : p.T - 1];
+        const RowFactors r = row_factors(rows, row < p.T ? row : p.T - 1);
         const float a = r.a * S, b = r.b * S;
 #pragma unroll
         for (int i = 0; i < L::RB; ++i)
@@ -294,12 +321,12 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, const LossRow
         // rows without a target, whatever their logits are, and the padding
         // behind the vocabulary
         const bool ragged = p0 + L::TP > p.V;
-        if (ragged || __any(r.on == 0.0f)) {
+        if (ragged || __any(!r.on)) {
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (r.on == 0.0f || p0 + loop.p_of(i, e) >= p.V) acc.v[i][j][e] = 0.0f;
+                    if (!r.on || p0 + loop.p_of(i, e) >= p.V) acc.v[i][j][e] = 0.0f;
         }
     }
     __syncthreads();   // the lanes' arrays give way to the packed tile
@@ -372,6 +399,103 @@ __global__ __launch_bounds__(L::NT, 2) void loss_product(ProductParams p) {
             }
         }
         __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dw of at most 64 rows: one slab of k, so the stores are the cost.  A workgroup
+// keeps its 128 rows of P in registers and walks over tiles of Q: the next tile's
+// slab is on its way while this one is multiplied, and a tile's stores while the
+// next is.  64 x 50001 x 2048: 49 us with a workgroup per tile (each waits out its
+// slab's latency alone), 39 us this way (5.3 TB/s written).
+// ---------------------------------------------------------------------------
+template <int DT>
+__global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
+    using Op = Operand<false, 128, 4>;
+    constexpr int OUT = 128 * 128 * 2, CH = 16, STORES = 8;   // result tile bytes; chunks a row; stores a thread
+    __shared__ __attribute__((aligned(16))) char lds[OUT + 2 * Op::SLAB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wp = wave & 1, wq = wave >> 1;
+    const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
+    // the grid is a multiple of tiles_p: a workgroup stays with its tile of P
+    const int tp = (int)blockIdx.x % p.g.tiles_p, step = (int)gridDim.x / p.g.tiles_p;
+    int tq = (int)blockIdx.x / p.g.tiles_p;
+    const int64_t p0 = (int64_t)tp * 128;
+    auto load = [&](const Matrix &m, int64_t row0, uint32_t dst) {
+        Op o;
+        o.init(m, row0, p.K, wave, lane);
+        const i32x4 r = o.rsrc(0);
+#pragma unroll
+        for (int x = 0; x < Op::LOADS; ++x) o.template load<false>(r, 0, x, dst + wave * Op::LOADS * 1024);
+    };
+    load(p.P, p0, lds0);   // P's slab borrows the result's place
+    load(p.Q, (int64_t)tq * 128, lds0 + OUT);
+    wait_vm_lgkm<0>();
+    __builtin_amdgcn_s_barrier();
+    u32x4 pf[2][4];
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pf[st][i] = Op::fragment(Op::address(lds0, wp * 64, lane, i) + Op::constant(0, st));
+    uint32_t qa[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) qa[j] = Op::address(lds0 + OUT, wq * 64, lane, j);
+    wait_vm_lgkm<0>();   // P's fragments are in registers before its place is written
+    const float u = p.unscale ? *p.unscale : 1.0f;
+    const int cols = (int)min((int64_t)128, ((p.P.rows + 7) & ~7) - p0);
+    bool first = true;
+    for (int buf = 0; tq < p.g.tiles_q; tq += step, buf ^= 1) {
+        const int64_t q0 = (int64_t)tq * 128;
+        // This tile's slab is older than the last tile's stores, every one of which
+        // is issued whether it is inside the result or not.  After the barrier the
+        // other buffer and the result's place are free.
+        __builtin_amdgcn_sched_barrier(0);
+        if (first) wait_vm_lgkm<0>();
+        else wait_vm_lgkm<STORES>();
+        first = false;
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        if (tq + step < p.g.tiles_q) load(p.Q, q0 + (int64_t)step * 128, lds0 + OUT + (buf ^ 1) * Op::SLAB);
+        f32x4 acc[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            u32x4 qf[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qf[j] = Op::fragment(qa[j] + buf * Op::SLAB + Op::constant(0, st));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = mfma<DT>(pf[st][i], qf[j], acc[i][j]);
+        }
+        // the packed tile, 16-byte chunk c of row r at c ^ r
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = wq * 64 + j * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = wp * 64 + i * 16 + 4 * (lane >> 4);
+                *reinterpret_cast<u32x2 *>(lds + r * 256 + (((c >> 3) ^ (r & (CH - 1))) << 4) + (c & 4) * 2) =
+                    u32x2{pack2<DT>(acc[i][j][0] * u, acc[i][j][1] * u), pack2<DT>(acc[i][j][2] * u, acc[i][j][3] * u)};
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4));   // this wave's LDS writes; its loads go on
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        const int rows = (int)min((int64_t)128, p.Q.rows - q0);
+        const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+            static_cast<uint16_t *>(p.out) + q0 * p.ldo + p0, (short)0, (int)(((rows - 1) * p.ldo + cols) * 2), (int)RSRC_DW3);
+#pragma unroll
+        for (int x = 0; x < STORES; ++x) {
+            const int f = threadIdx.x + 256 * x, r = f / CH, c = f % CH;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * 256 + ((c ^ (r & (CH - 1))) << 4));
+            const uint32_t off = r < rows && 8 * c < cols ? (uint32_t)(r * p.ldo + 8 * c) * 2 : OOB;
+            __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)off, 0, 2);   // non-temporal
+        }
     }
 }
 
@@ -583,45 +707,16 @@ __global__ __launch_bounds__(256) void loss_finish(FinishParams p, int per) {
     p.loss[row] = loss;
 }
 
-struct RowParams {
-    int64_t T, V;
-    float zeta, tau;
-    const int64_t *target;
-    int64_t ignore;
-    const float *entropy, *grad, *lse;
-    LossRow *rows;
-    float *scale;
-};
-
-__global__ __launch_bounds__(256) void loss_rows(RowParams p) {
-    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (row >= p.T) return;
-    const float lse = p.lse[row], g = p.grad[row];
-    LossRow r;
-    r.lse2 = lse * LOG2E;
-    if (p.target) {
-        const int64_t y = p.target[row];
-        const float bad = y < 0 || y >= p.V ? __builtin_nanf("") : 0.0f;
-        r.on = y == p.ignore ? 0.0f : 1.0f;
-        r.a = g * __builtin_fmaf(2.0f * p.zeta, lse, 1.0f) + bad;
-        r.b = g;
-    } else {
-        const float h = p.entropy[row];
-        r.on = h == -INF ? 0.0f : 1.0f;
-        r.a = h != h ? h : g * p.tau;
-        r.b = g * p.tau;
-    }
-    if (r.on == 0.0f) r.a = r.b = r.lse2 = 0.0f;
-    p.rows[row] = r;
-}
-
 // The fp16 scale: the power of two that brings the largest |a| or |b| into
 // [2^13, 2^14), so dz, at most that in size, neither overflows nor loses the
 // small probabilities to fp16's smallest values.  One block.
-__global__ __launch_bounds__(1024) void loss_scale(RowParams p) {
+__global__ __launch_bounds__(1024) void loss_scale(LossRows p, int64_t T, float *scale) {
     __shared__ float part[16];
     float m = 0.0f;
-    for (int64_t i = threadIdx.x; i < p.T; i += 1024) m = fmaxf(m, fmaxf(fabsf(p.rows[i].a), fabsf(p.rows[i].b)));
+    for (int64_t i = threadIdx.x; i < T; i += 1024) {
+        const RowFactors r = row_factors(p, i);
+        m = fmaxf(m, fmaxf(fabsf(r.a), fabsf(r.b)));
+    }
     m = wave_max(m);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
     __syncthreads();
@@ -632,8 +727,8 @@ __global__ __launch_bounds__(1024) void loss_scale(RowParams p) {
         e = 14 - (ilogbf(m) + 1);
         e = min(max(e, -120), 120);
     }
-    p.scale[0] = ldexpf(1.0f, e);
-    p.scale[1] = ldexpf(1.0f, -e);
+    scale[0] = ldexpf(1.0f, e);
+    scale[1] = ldexpf(1.0f, -e);
 }
 
 __global__ __launch_bounds__(256) void loss_zero(char *out, int64_t rows, int64_t words, int64_t ld_bytes) {
@@ -676,9 +771,15 @@ struct LoopOf<LT_64x64, DT, PK, QK> {
     using type = ThinLoop<DT, PK, QK, 64, 64, 5>;
 };
 template <int DT, bool PK, bool QK>
+struct LoopOf<LT_64x128, DT, PK, QK> {
+    using type = ThinLoop<DT, PK, QK, 64, 128, 3>;
+};
+template <int DT, bool PK, bool QK>
 struct LoopOf<LT_128x64, DT, PK, QK> {
     using type = ThinLoop<DT, PK, QK, 128, 64, 3>;
 };
+template <int DT>
+using Loop128 = typename LoopOf<LT_128x128, DT, false, false>::type;
 template <class L_, int DT_>
 struct Choice {
     using L = L_;
@@ -722,7 +823,7 @@ hipError_t run_stats(const LossProblem &p, const LossStats &s, hipStream_t strea
     return hipGetLastError();
 }
 template <int DT, class L>
-hipError_t run_dz(const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz, int64_t ldd, hipStream_t stream) {
+hipError_t run_dz(const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz, int64_t ldd, hipStream_t stream) {
     const LogitParams q = logit_params<L>(p);
     hipLaunchKernelGGL((loss_dz<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q, rows, scale, dz, ldd);
     return hipGetLastError();
@@ -755,6 +856,7 @@ LossTileShape loss_tile_shape(int tile) {
     case LT_128x32: return {128, 32, 2};
     case LT_64x64: return {64, 64, 2};
     case LT_128x64: return {128, 64, 2};
+    case LT_64x128: return {64, 128, 2};
     default: return {128, 128, 2};
     }
 }
@@ -770,6 +872,7 @@ static hipError_t with_tile(int dtype, int tile, F &&f) {
     if constexpr (PK && QK) {   // their P slabs are too narrow for k-rows
         if (tile == LT_32x32) return with_type<LT_32x32, PK, QK>(dtype, f);
         if (tile == LT_64x64) return with_type<LT_64x64, PK, QK>(dtype, f);
+        if (tile == LT_64x128) return with_type<LT_64x128, PK, QK>(dtype, f);
     }
     if constexpr (QK) {
         if (tile == LT_128x32) return with_type<LT_128x32, PK, QK>(dtype, f);
@@ -788,7 +891,7 @@ hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const Lo
     return p.w.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
 }
 
-hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRow *rows, const float *scale, uint16_t *dz,
+hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz,
                           int64_t ldd, hipStream_t stream) {
     auto run = [&](auto c) {
         using C = decltype(c);
@@ -805,6 +908,15 @@ hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStr
     };
     if (p.Q.kc) return p.P.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
     return p.P.kc ? hipErrorInvalidValue : with_tile<false, false>(dtype, tile, run);
+}
+
+hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream) {
+    if (p.P.kc || p.Q.kc || p.K > KB || p.out_kind != LO_16) return hipErrorInvalidValue;
+    ProductParams q = product_params<Loop128<0>>(p);
+    const int grid = std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;
+    if (dtype == 0) hipLaunchKernelGGL(loss_outer<0>, dim3(grid), dim3(256), 0, stream, q);
+    else hipLaunchKernelGGL(loss_outer<1>, dim3(grid), dim3(256), 0, stream, q);
+    return hipGetLastError();
 }
 
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream) {
@@ -842,12 +954,8 @@ hipError_t launch_loss_finish(const gemm_loss_args_t &a, int tiles, const LossSt
     return hipGetLastError();
 }
 
-hipError_t launch_loss_rows(const gemm_loss_args_t &a, const float *entropy, LossRow *rows, float *scale,
-                            hipStream_t stream) {
-    const RowParams p{a.T, a.V, a.z_loss, a.kind == GEMM_LOSS_DISTILL ? a.temperature : 1.0f,
-                      a.kind == GEMM_LOSS_XENT ? a.target : nullptr, a.ignore_index, entropy, a.grad, a.lse, rows, scale};
-    hipLaunchKernelGGL(loss_rows, dim3((unsigned)((a.T + 255) / 256)), dim3(256), 0, stream, p);
-    if (scale) hipLaunchKernelGGL(loss_scale, dim3(1), dim3(1024), 0, stream, p);
+hipError_t launch_loss_scale(const LossRows &rows, int64_t T, float *scale, hipStream_t stream) {
+    hipLaunchKernelGGL(loss_scale, dim3(1), dim3(1024), 0, stream, rows, T, scale);
     return hipGetLastError();
 }
 

@@ -14,9 +14,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import threading
+import functools
 
 from . import _check, _lib, layout_word
+
+try:
+    import torch
+except ImportError:   # the C entry points need no torch
+    torch = None
 
 GEMM_LOSS_XENT = 0
 GEMM_LOSS_DISTILL = 1
@@ -114,8 +119,6 @@ def _vector(name, t, shape, dtypes, device):
 
 def _product(x, w, b_layout):
     """GemmLossArgs with the product's part filled in."""
-    import torch
-
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w must be 2-D")
     if x.dtype not in (torch.bfloat16, torch.float16) or w.dtype != x.dtype:
@@ -134,8 +137,6 @@ def _product(x, w, b_layout):
 
 
 def _xent(a, x, target, ignore_index, z_loss):
-    import torch
-
     a.kind = GEMM_LOSS_XENT
     a.target = _vector("target", target, (a.T,), torch.int64, x.device)
     a.ignore_index = ignore_index
@@ -143,8 +144,6 @@ def _xent(a, x, target, ignore_index, z_loss):
 
 
 def _distill(a, x, teacher_index, teacher_logits, temperature):
-    import torch
-
     types = {torch.float32: GEMM_LOSS_FP32, torch.bfloat16: GEMM_LOSS_BF16, torch.float16: GEMM_LOSS_FP16}
     if teacher_index.dim() != 2:
         raise ValueError("teacher_index must be [T, K]")
@@ -156,36 +155,38 @@ def _distill(a, x, teacher_index, teacher_logits, temperature):
     a.temperature = temperature
 
 
-_CUS: dict = {}   # device index -> compute units
-_PLAN = threading.local()
+@functools.lru_cache(maxsize=None)
+def _cus(index):
+    return torch.cuda.get_device_properties(index).multi_processor_count
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(T, V, H, layout, kind, entries, dx, dw, dw_type, backward, cus):
+    a = GemmLossArgs(T=T, V=V, H=H, layout=layout, kind=kind, entries=entries, dx=dx, dw=dw, dw_type=dw_type)
+    return gemm_loss_plan(a, backward, cus).workspace_bytes
 
 
 def _call(a, x, backward, workspace, outputs):
     """Runs the call on torch's current stream, its workspace torch's unless given."""
-    import torch
-
     device = x.device
     a.stream = torch.cuda.current_stream(device).cuda_stream
     if workspace is None:
-        a.num_cus = _CUS.get(device.index) or _CUS.setdefault(
-            device.index, torch.cuda.get_device_properties(device).multi_processor_count)
-        plan = getattr(_PLAN, "plan", None)
-        if plan is None:
-            plan = _PLAN.plan = GemmLossPlan()
-        _check(_lib.gemm_loss_plan(ctypes.byref(a), backward, a.num_cus, ctypes.byref(plan)))
-        workspace = torch.empty(max(plan.workspace_bytes, 1), dtype=torch.uint8, device=device)
+        a.num_cus = cus = _cus(device.index)
+        need = _workspace_bytes(a.T, a.V, a.H, a.layout, a.kind, a.entries, 1 if a.dx else 0, 1 if a.dw else 0,
+                                a.dw_type, backward, cus)
+        workspace = torch.empty(need or 1, dtype=torch.uint8, device=device)
+        a.workspace_bytes = need
     elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on x's device")
+    else:
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
     a.workspace = workspace.data_ptr()
-    a.workspace_bytes = workspace.numel() * workspace.element_size()
     _check((_lib.gemm_loss_backward if backward else _lib.gemm_loss_forward)(ctypes.byref(a)))
     return outputs
 
 
 def _on(x, stream):
     """x's device and the call's stream made current."""
-    import torch
-
     if stream is not None:
         stack = contextlib.ExitStack()
         stack.enter_context(torch.cuda.device(x.device))
@@ -197,8 +198,6 @@ def _on(x, stream):
 
 
 def _forward(a, x, loss, lse, workspace, stream):
-    import torch
-
     with _on(x, stream):
         loss = torch.empty(a.T, dtype=torch.float32, device=x.device) if loss is None else loss
         lse = torch.empty(a.T, dtype=torch.float32, device=x.device) if lse is None else lse
@@ -208,8 +207,6 @@ def _forward(a, x, loss, lse, workspace, stream):
 
 
 def _backward(a, x, w, grad, lse, dx, dw, need_dx, need_dw, accumulate_dw, workspace, stream):
-    import torch
-
     a.grad = _vector("grad", grad, (a.T,), torch.float32, x.device)
     a.lse = _vector("lse", lse, (a.T,), torch.float32, x.device)
     if not need_dx and dx is not None or not need_dw and dw is not None:
