@@ -104,7 +104,11 @@ def _rows(name, t, rows, cols, dtype, device):
         raise ValueError(f"{name} must be [{rows}, {cols}]")
     if cols > 1 and rows > 0 and t.stride(1) != 1:
         raise ValueError(f"{name}: every row must be contiguous")
-    return t.stride(0) if rows > 1 else 0
+    if rows <= 1:
+        return 0
+    if t.stride(0) < cols:   # an expanded tensor; 0 would mean packed
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0)
 
 
 def _vector(name, t, shape, dtypes, device):
