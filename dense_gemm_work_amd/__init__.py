@@ -505,6 +505,6 @@ def matmul(a, b, b_layout: str = "kn", out=None, alpha: Optional[float] = None, 
 
 from .loss import (  # noqa: E402  (needs the loaded library)
     GEMM_LOSS_BF16, GEMM_LOSS_DISTILL, GEMM_LOSS_DW_FP32, GEMM_LOSS_DW_FP32_ADD, GEMM_LOSS_DW_SAME, GEMM_LOSS_FP16,
-    GEMM_LOSS_FP32, GEMM_LOSS_MAX_ENTRIES, GEMM_LOSS_MAX_H, GEMM_LOSS_MAX_T, GEMM_LOSS_MAX_V, GEMM_LOSS_XENT,
-    GemmLossArgs, GemmLossPlan, gemm_loss_backward, gemm_loss_forward, gemm_loss_plan, linear_cross_entropy,
-    linear_cross_entropy_backward, linear_distill, linear_distill_backward)
+    GEMM_LOSS_FP32, GEMM_LOSS_MAX_ENTRIES, GEMM_LOSS_MAX_H, GEMM_LOSS_MAX_T, GEMM_LOSS_MAX_TH, GEMM_LOSS_MAX_TV,
+    GEMM_LOSS_MAX_V, GEMM_LOSS_XENT, GemmLossArgs, GemmLossPlan, gemm_loss_backward, gemm_loss_forward, gemm_loss_plan,
+    linear_cross_entropy, linear_cross_entropy_backward, linear_distill, linear_distill_backward)

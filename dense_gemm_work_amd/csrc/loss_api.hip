@@ -35,6 +35,8 @@ int check_sizes(const gemm_loss_args_t &a) {
     if (a.T < 0 || a.V < 1 || a.H < 1) return bad("T >= 0, V >= 1 and H >= 1");
     if (a.T > GEMM_LOSS_MAX_T || a.V > GEMM_LOSS_MAX_V || a.H > GEMM_LOSS_MAX_H)
         return set_error(GEMM_ERR_UNSUPPORTED, "T, V or H exceeds GEMM_LOSS_MAX_T, GEMM_LOSS_MAX_V or GEMM_LOSS_MAX_H");
+    if (a.T * a.V > GEMM_LOSS_MAX_TV || a.T * a.H > GEMM_LOSS_MAX_TH)
+        return set_error(GEMM_ERR_UNSUPPORTED, "T * V or T * H exceeds GEMM_LOSS_MAX_TV or GEMM_LOSS_MAX_TH");
     if (a.H % 8) return set_error(GEMM_ERR_UNSUPPORTED, "H must be a multiple of 8");
     if ((a.layout & 0xFu) == GEMM_B_KN && a.V % 8)
         return set_error(GEMM_ERR_UNSUPPORTED, "V must be a multiple of 8 for GEMM_B_KN");
@@ -112,25 +114,40 @@ struct Layout {
     }
 };
 
-// The tile of a product of rows_p x rows_q and, where its k may be sliced
-// (k > 0), the slices: as many as fill the chip once, of at least 8 slabs.  The
-// cheaper of the two tiles by whole waves of workgroups: a 256 x 256 tile has a
-// CU to itself and takes 4 units; two 128 x 128 tiles share one and together
-// take 2.4 (measured on 4096 x 131072 x 4096: 1262 against 1060 TFLOP/s).
+// The tile of a product of rows_p x rows_q over k and, where its k may be sliced,
+// the slices (of at least 8 slabs): the cheapest by a model of the time in us,
+//   rounds of resident workgroups x (slabs x slab time + fixed time) + joining,
+// for 256 x 256 tiles, one a CU (1.53 us a slab, 8 us fixed), and 128 x 128 tiles,
+// two a CU (0.92 us a slab for the pair, 2.5 us fixed).  Model against measurement:
+// logits of 333 x 50001 x 2048: 114 / 96 us (measured 97-106 / 92-96), of
+// 200 x 50001 x 2048: 57 / 64 (58 / 67), of 777 x 50001 x 1536: 179 / 147 (150-166 /
+// 143), of 500 x 32768 x 4096: 106 / 123 (111 / 143); dw of 500 x 32768 x 4096: 162 /
+// 158 (154 / 158), of 2048 x 32768 x 2048: 228 / 255 (213 / 278); dx of
+// 500 x 32768 x 4096: 124 / 130 (124 / 147), of 200 x 50001 x 2048: 61 / 56 (73 / 64).
+// Joining takes a launch and reads the fp32 slices at 4.5 TB/s.
 struct Choice {
     int tile, splits;
 };
-Choice choose(int64_t rows_p, int64_t rows_q, int64_t k, int cus) {
-    auto consider = [&](int tile, double unit, double *cost) {
+Choice choose(int64_t rows_p, int64_t rows_q, int64_t k, bool sliceable, int cus) {
+    Choice best{dgw::LT_128x128, 1};
+    double least = 0.0;
+    const int64_t slabs = ceil_div(k, 64);
+    auto consider = [&](int tile, double slab, double fixed) {
         const dgw::LossTileShape s = dgw::loss_tile_shape(tile);
         const int64_t tiles = ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q), slots = (int64_t)cus * s.per_cu;
-        const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(slots / tiles, ceil_div(k, 64) / 8));
-        *cost = (double)ceil_div(tiles * splits, slots) / splits * unit;
-        return Choice{tile, (int)splits};
+        const int64_t most = sliceable ? std::max<int64_t>(1, std::min<int64_t>(slots / tiles, slabs / 8)) : 1;
+        for (int64_t n = 1; n <= most; ++n) {
+            double us = (double)ceil_div(tiles * n, slots) * ((double)ceil_div(slabs, n) * slab + fixed);
+            if (n > 1) us += 3.0 + 4.0 * (double)n * (double)rows_p * (double)rows_q / 4.5e6;
+            if (least == 0.0 || us < least) {
+                least = us;
+                best = {tile, (int)n};
+            }
+        }
     };
-    double c128, c256;
-    const Choice t128 = consider(dgw::LT_128x128, 2.4, &c128), t256 = consider(dgw::LT_256x256, 4.0, &c256);
-    return c256 < c128 ? t256 : t128;
+    consider(dgw::LT_128x128, 0.92, 2.5);
+    consider(dgw::LT_256x256, 1.53, 8.0);
+    return best;
 }
 
 // The logits' tile.  Up to 64 rows the stream of w is the cost and thin tiles
@@ -143,7 +160,7 @@ int logits_tile(const gemm_loss_args_t &a, int64_t V, int cus) {
     const bool kn = (a.layout & 0xFu) == GEMM_B_KN;
     if (a.T > 64) {
         if (!kn && 2 * ceil_div(V, 128) * ceil_div(a.T, 128) <= cus) return dgw::LT_64x128;
-        return choose(V, a.T, 0, cus).tile;
+        return choose(V, a.T, a.H, false, cus).tile;
     }
     if (kn) return a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
     return a.T <= 32 && V < 64 * (int64_t)cus ? dgw::LT_32x32 : dgw::LT_64x64;
@@ -152,17 +169,9 @@ int logits_tile(const gemm_loss_args_t &a, int64_t V, int cus) {
 // dx's tile and slices.  Few rows: one workgroup a CU (V = 32768, H = 2048, T = 2:
 // 16 slices 61 us for dz and dx together, 32 slices 68 us, which add up more).
 Choice dx_choice(const gemm_loss_args_t &a, int64_t V, int cus) {
-    if (a.T > 64) return choose(a.H, a.T, V, cus);
+    if (a.T > 64) return choose(a.H, a.T, V, true, cus);
     const int tile = a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
     return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(a.H, 128), ceil_div(V, 64) / 8))};
-}
-
-// dw's tile and slices.  Below 768 rows its stores weigh more than its products,
-// and two workgroups a CU overlap the two (T = 333, V = 50001, H = 2048: 110 us
-// against 118 us on 256 x 256 tiles; T = 777, H = 1536: 147 against 135 us).
-Choice dw_choice(int64_t rows_p, int64_t rows_q, int64_t T, int cus) {
-    if (T < 768) return {dgw::LT_128x128, 1};
-    return choose(rows_p, rows_q, T, cus);
 }
 
 struct Plan {
@@ -202,7 +211,7 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
     if (a.dw) {
         const bool nk = (a.layout & 0xFu) == GEMM_B_NK;
         const int64_t rp = nk ? a.H : first, rq = nk ? first : a.H;
-        const Choice c = dw_choice(rp, rq, a.T, cus);
+        const Choice c = choose(rp, rq, a.T, true, cus);
         p.dw = c.tile;
         p.dw_splits = c.splits;
         p.dw_outer = a.T <= 64 && a.dw_type == GEMM_LOSS_DW_SAME;
@@ -351,7 +360,7 @@ int backward(const gemm_loss_args_t &a) {
                 q.out = part<float>(c.ws, pl.at.dw);
                 q.out_kind = dgw::LO_SLOTS;
             }
-            if (pl.dw_outer) e = dgw::launch_loss_outer(c.dtype, q, 2 * c.cus, c.stream);
+            if (pl.dw_outer) e = dgw::launch_loss_outer(c.dtype, q, 2 * std::min(c.cus, 1 << 16), c.stream);
             else e = dgw::launch_loss_product(c.dtype, pl.dw, q, c.stream);
             if (e != hipSuccess) return set_hip_error(e, "launch dw");
             if (pl.dw_splits > 1 &&

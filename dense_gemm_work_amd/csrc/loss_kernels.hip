@@ -503,7 +503,8 @@ __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
 template <int DT, class L>
 __global__ __launch_bounds__(256) void loss_join(ProductParams p, const float *slots) {
     constexpr int QUADS = L::TP * L::TQ / 4;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+    if (id >= (int64_t)p.g.tiles_p * p.g.tiles_q * QUADS) return;
     const int tile = (int)(id / QUADS), f = (int)(id % QUADS);
     const int tp = tile % p.g.tiles_p, tq = tile / p.g.tiles_p;
     const int lane = f & 63, block = (f >> 6) % (L::RB * L::CB), wave = (f >> 6) / (L::RB * L::CB);
@@ -514,7 +515,12 @@ __global__ __launch_bounds__(256) void loss_join(ProductParams p, const float *s
     const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * QUADS;
     const f32x4 *at = reinterpret_cast<const f32x4 *>(slots) + id;
     f32x4 v = at[0];
-    for (int s = 1; s < p.g.splits; ++s) v += at[s * step];
+    int s = 1;
+    for (; s + 4 <= p.g.splits; s += 4) {   // four loads in flight, added in order
+        const f32x4 a = at[s * step], b = at[(s + 1) * step], c = at[(s + 2) * step], d = at[(s + 3) * step];
+        v = (((v + a) + b) + c) + d;
+    }
+    for (; s < p.g.splits; ++s) v += at[s * step];
     v *= p.unscale ? *p.unscale : 1.0f;
     if (p.out_kind == LO_16) {
         *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.out) + row * p.ldo + col) =
@@ -843,7 +849,8 @@ template <int DT, class L>
 hipError_t run_join(const LossProduct &p, const float *slots, hipStream_t stream) {
     const ProductParams q = product_params<L>(p);
     const int64_t quads = (int64_t)q.g.tiles_p * q.g.tiles_q * (L::TP * L::TQ / 4);
-    hipLaunchKernelGGL((loss_join<DT, L>), dim3((unsigned)(quads / 256)), dim3(256), 0, stream, q, slots);
+    const int64_t blocks = quads / 256, wide = std::min<int64_t>(blocks, 1 << 20);   // a dimension holds 2^32 threads
+    hipLaunchKernelGGL((loss_join<DT, L>), dim3((unsigned)wide, (unsigned)((blocks + wide - 1) / wide)), dim3(256), 0, stream, q, slots);
     return hipGetLastError();
 }
 
@@ -913,7 +920,7 @@ hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStr
 hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream) {
     if (p.P.kc || p.Q.kc || p.K > KB || p.out_kind != LO_16) return hipErrorInvalidValue;
     ProductParams q = product_params<Loop128<0>>(p);
-    const int grid = std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;
+    const int grid = std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;   // tiles_p < 2^14
     if (dtype == 0) hipLaunchKernelGGL(loss_outer<0>, dim3(grid), dim3(256), 0, stream, q);
     else hipLaunchKernelGGL(loss_outer<1>, dim3(grid), dim3(256), 0, stream, q);
     return hipGetLastError();

@@ -35,6 +35,8 @@ GEMM_LOSS_MAX_T = 1 << 24
 GEMM_LOSS_MAX_V = 1 << 21
 GEMM_LOSS_MAX_H = 1 << 20
 GEMM_LOSS_MAX_ENTRIES = 1024
+GEMM_LOSS_MAX_TV = 1 << 37
+GEMM_LOSS_MAX_TH = 1 << 37
 
 
 class GemmLossArgs(ctypes.Structure):
@@ -192,6 +194,8 @@ def _call(a, x, backward, workspace, outputs):
 def _on(x, stream):
     """x's device and the call's stream made current."""
     if stream is not None:
+        if stream.device != x.device:
+            raise ValueError("stream must be on x's device")
         stack = contextlib.ExitStack()
         stack.enter_context(torch.cuda.device(x.device))
         stack.enter_context(torch.cuda.stream(stream))

@@ -62,13 +62,16 @@ extern "C" {
 #define GEMM_LOSS_MAX_T       (1 << 24)
 #define GEMM_LOSS_MAX_V       (1 << 21)
 #define GEMM_LOSS_MAX_H       (1 << 20)
+#define GEMM_LOSS_MAX_TV      ((int64_t)1 << 37)   /* T * V: the tiles of one launch */
+#define GEMM_LOSS_MAX_TH      ((int64_t)1 << 37)   /* T * H                           */
 #define GEMM_LOSS_MAX_ENTRIES 1024
 
 /*
  * Arguments; zero-initialise, then fill what the call needs.
  *   x, w:      device, 16-byte aligned rows; ldx, ldw: elements between rows (0:
  *              packed; else at least the row's length, a multiple of 8, at most 2^21).
- *   T, V, H:   T >= 0, V >= 1, H a multiple of 8 >= 8; V a multiple of 8 for GEMM_B_KN.
+ *   T, V, H:   T >= 0, V >= 1, H a multiple of 8 >= 8; V a multiple of 8 for GEMM_B_KN;
+ *              at most GEMM_LOSS_MAX_*.
  *   layout:    GEMM_B_NK or GEMM_B_KN, combined with GEMM_BF16 or GEMM_FP16.
  *   kind:      GEMM_LOSS_XENT or GEMM_LOSS_DISTILL.
  *   target:    device int64 [T] (XENT).     ignore_index: the target of rows to leave out.

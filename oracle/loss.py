@@ -97,8 +97,11 @@ def forward(x, w, dtype, target=None, index=None, logits=None, tau=1.0, zeta=0.0
         for t in range(T):
             if on[t] and not bad[t]:
                 q[t, target[t]] = 1.0
-        loss = lse - (q * z).sum(axis=1) + (0.0 if mutation == 1 else zeta) * lse * lse
-        bound = el + ez + 8 * F32 * (np.abs(lse) + 2 * top) + zeta * (2 * np.abs(lse) * el + 4 * F32 * lse * lse)
+        at = np.where(q > 0, z, 0.0).sum(axis=1)   # a logit of -infinity elsewhere takes no part
+        loss = lse - at + (0.0 if mutation == 1 else zeta) * lse * lse
+        bound = el + ez + 8 * F32 * (np.abs(lse) + 2 * top)
+        if zeta:
+            bound = bound + zeta * (2 * np.abs(lse) * el + 4 * F32 * lse * lse)
     else:
         q, h, on, bad = teacher(index, logits, 1.0 if mutation == 2 else tau, V)
         loss = tau * tau * (h - (q * z).sum(axis=1) / tau + lse)

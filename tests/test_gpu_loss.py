@@ -74,8 +74,10 @@ SHAPES = [
     ("64x128", 100, 9001, 136, "bf16", "nk", dict(tile_v=64, tile_t=128)),
     ("128x128", 150, 20001, 136, "fp16", "nk", dict(tile_v=128, tile_t=128, dw_tile_p=128)),
     ("128x128 kn", 150, 20000, 136, "bf16", "kn", dict(tile_v=128, tile_t=128)),
-    ("256x256", 1000, 16000, 264, "bf16", "nk", dict(tile_v=256, tile_t=256, dw_tile_p=256)),
-    ("256x256 kn", 1000, 16000, 264, "fp16", "kn", dict(tile_v=256, tile_t=256, dw_tile_p=256)),
+    ("256x256", 1000, 16001, 1016, "bf16", "nk", dict(tile_v=256, tile_t=256, dw_tile_p=256)),
+    ("256x256 kn", 1000, 16000, 1016, "fp16", "kn", dict(tile_v=256, tile_t=256, dw_tile_p=256)),
+    ("256x256 dx", 2000, 16001, 2040, "bf16", "nk", dict(tile_v=256, dx_tile_h=256, dx_splits=4)),
+    ("256x256 dx, kn", 2000, 16000, 2040, "bf16", "kn", dict(tile_v=256, dx_tile_h=256, dx_splits=4)),
     ("dw in slices", 3000, 300, 136, "bf16", "nk", dict()),
     ("dw in slices, kn", 3000, 296, 136, "fp16", "kn", dict()),
     ("short vocabulary, long rows", 40, 100, 4096, "bf16", "nk", dict()),

@@ -139,6 +139,8 @@ def test_plans_cover_the_vocabulary_and_stay_small(dg):
     for _ in range(400):
         T, V, H = (int(np.exp(rng.uniform(0, np.log(m)))) for m in (1 << 20, 1 << 18, 1 << 10))
         V, H = max(V // 8 * 8, 8), 8 * max(H, 1)
+        if T * V > dg.GEMM_LOSS_MAX_TV:
+            continue
         layout = dg.GEMM_B_KN if rng.random() < 0.5 else dg.GEMM_B_NK
         kind = int(rng.random() < 0.3)
         entries = int(rng.integers(1, 200)) if kind else 0
@@ -217,6 +219,8 @@ REFUSED = [   # what, kind, backward too / only, expected status
     ("T too large", 0, change(T=(1 << 24) + 1), "both", "UNSUPPORTED"),
     ("V too large", 0, change(V=(1 << 21) + 8), "both", "UNSUPPORTED"),
     ("H too large", 0, change(H=(1 << 20) + 8), "both", "UNSUPPORTED"),
+    ("too many tiles", 0, change(T=1 << 20, V=1 << 18), "both", "UNSUPPORTED"),
+    ("too large a dx", 0, change(T=1 << 20, H=1 << 18), "both", "UNSUPPORTED"),
     ("ragged H", 0, change(H=36), "both", "UNSUPPORTED"),
     ("x rows overlap", 0, change(ldx=24), "both", "INVALID"),
     ("x rows unaligned", 0, change(ldx=36), "both", "UNSUPPORTED"),
