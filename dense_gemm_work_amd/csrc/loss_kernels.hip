@@ -431,7 +431,7 @@ __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
     load(p.P, p0, lds0);   // P's slab borrows the result's place
     load(p.Q, (int64_t)tq * 128, lds0 + OUT);
     wait_vm_lgkm<0>();
-    __builtin_amdgcn_s_barrier();
+    barrier();
     u32x4 pf[2][4];
 #pragma unroll
     for (int st = 0; st < 2; ++st)
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
         if (first) wait_vm_lgkm<0>();
         else wait_vm_lgkm<STORES>();
         first = false;
-        __builtin_amdgcn_s_barrier();
+        barrier();
         __builtin_amdgcn_sched_barrier(0);
         if (tq + step < p.g.tiles_q) load(p.Q, q0 + (int64_t)step * 128, lds0 + OUT + (buf ^ 1) * Op::SLAB);
         f32x4 acc[4][4];
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4));   // this wave's LDS writes; its loads go on
-        __builtin_amdgcn_s_barrier();
+        barrier();
         __builtin_amdgcn_sched_barrier(0);
         const int rows = (int)min((int64_t)128, p.Q.rows - q0);
         const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(

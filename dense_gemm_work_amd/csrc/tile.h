@@ -88,6 +88,13 @@ __device__ __forceinline__ void wait_vm_lgkm() {
     static_assert(N >= 0 && N < 64, "the counter holds 0..63");
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
 }
+// The workgroup's barrier without __syncthreads()' wait for loads in flight (the
+// callers wait for what they need); no memory access moves across it.
+__device__ __forceinline__ void barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 template <int PER>
 __device__ __forceinline__ void wait_stages(int stages) {
     switch (stages) {
@@ -376,7 +383,7 @@ struct Loop {
         if (n > NSP - 1) wait_vm_lgkm<LOADS + (NSP - 2) * OpP::LOADS>();
         else if (n > 1) wait_vm_lgkm<LOADS>();
         else wait_vm_lgkm<0>();
-        __builtin_amdgcn_s_barrier();
+        barrier();
         each(std::make_integer_sequence<int, reads(0)>(), [&](auto R) { read<0, 0, 0, decltype(R)::value>(p[0], q[0]); });
         // Iteration i (IT modulo ROUND): four half steps, each of which reads the next
         // one's fragments while it multiplies its own.  The last hands the stages
@@ -397,7 +404,7 @@ struct Loop {
                 __builtin_amdgcn_sched_barrier(0);
                 if (NSP > 2 && (steady || i + 2 < n)) wait_vm_lgkm<(NSP - 2) * OpP::LOADS>();
                 else wait_vm_lgkm<0>();
-                __builtin_amdgcn_s_barrier();
+                barrier();
                 __builtin_amdgcn_sched_barrier(0);
                 const bool more_p = steady || i + NSP < n, more_q = steady || i + NSQ < n;
                 products<1, BAR, NM, true, nit, 0, 0, true, RAGGED>(
@@ -416,7 +423,7 @@ struct Loop {
                 if (i + decltype(I)::value < n) iter(i + decltype(I)::value, I, std::false_type());
             });
         wait_vm_lgkm<0>();
-        __builtin_amdgcn_s_barrier();
+        barrier();
     }
     __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
                                             Acc &acc) {
@@ -524,7 +531,7 @@ struct ThinLoop {
             for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int i = 0; i < min(NS, n); ++i) load_all<RAGGED>(s0 + i, i);
         wait_stages<LOADS>(min(NS, n) - 1);
-        __builtin_amdgcn_s_barrier();
+        barrier();
         Frags f[2];
         read(f[0], 0);
         int st = 0;   // stage of iteration i
@@ -534,7 +541,7 @@ struct ThinLoop {
         auto iter = [&](int i, Frags &cur, Frags &next) {
             __builtin_amdgcn_sched_barrier(0);
             wait_stages<LOADS>(max(0, min(NS - 2, n - i - 2)));
-            __builtin_amdgcn_s_barrier();
+            barrier();
             __builtin_amdgcn_sched_barrier(0);
             if (i + NS < n) load_all<RAGGED>(s0 + i + NS, st);
             st = st + 1 == NS ? 0 : st + 1;
@@ -550,7 +557,7 @@ struct ThinLoop {
             if (i + 1 < n) iter(i + 1, f[1], f[0]);
         }
         wait_vm_lgkm<0>();
-        __builtin_amdgcn_s_barrier();
+        barrier();
         // a wave's gift to its partner, [wave][block][lane]
         f32x4 *buf = reinterpret_cast<f32x4 *>(lds_);
         const bool second = (threadIdx.x >> 6) & 1;

@@ -81,6 +81,11 @@ SHAPES = [
     ("dw in slices", 3000, 300, 136, "bf16", "nk", dict()),
     ("dw in slices, kn", 3000, 296, 136, "fp16", "kn", dict()),
     ("short vocabulary, long rows", 40, 100, 4096, "bf16", "nk", dict()),
+    ("one slab", 300, 3000, 8, "bf16", "nk", dict()),
+    ("one whole slab", 300, 3000, 64, "fp16", "kn", dict()),
+    ("two slabs, the second of 8", 700, 3000, 72, "fp16", "nk", dict()),
+    ("one slab, few rows", 20, 3001, 40, "bf16", "nk", dict()),
+    ("three slabs, few rows", 20, 3000, 136, "bf16", "kn", dict()),
 ]
 
 
