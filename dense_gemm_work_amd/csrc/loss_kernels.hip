@@ -749,39 +749,41 @@ __global__ __launch_bounds__(256) void loss_zero(char *out, int64_t rows, int64_
 // 128 x 128: four waves of 64 x 64, two workgroups a CU.
 // 256 x 256: eight waves of 128 x 64, one workgroup a CU.
 // A third stage of P (all of the LDS then) lets P's loads, most of which miss the
-// L2, travel for two iterations instead of one: 4096 x 131072 x 4096, logits and
-// dz 3 and 5 % faster, dx 2 %.  With both operands' rows contiguous (dw) its
-// registers spill (3.3 against 3.7 ms), and on 128 x 128 tiles it pays where both
-// have k contiguous (333 x 50001 x 2048: dz 95 against 107 us; dx 91 against 85).
-template <int TILE, int DT, bool PK, bool QK>
+// L2, travel for two iterations instead of one.  4096 x 131072 x 4096 on 256 x 256:
+// logits 2.995 against 3.071 ms, dz and dx 6.22 against 6.48 ms; with both
+// operands' rows contiguous (dw) its registers spill, dz and dw take 6.67 against
+// 6.35 ms.  On 128 x 128 tiles it pays for logits (333 x 50001 x 2048: 79.9 against
+// 84.3 us; w [H,V]: 80.7 against 88.3) and for products of operands with k
+// contiguous, not for the others (that shape's dz and dx: 168 against 164.5 us).
+template <int TILE, int DT, bool PK, bool QK, bool LOGITS = false>
 struct LoopOf;
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_128x128, DT, PK, QK> {
-    using type = Loop<DT, PK, QK, 128, 128, 2, 2, PK && QK ? 3 : 2, 2>;
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_128x128, DT, PK, QK, LOGITS> {
+    using type = Loop<DT, PK, QK, 128, 128, 2, 2, QK && (PK || LOGITS) ? 3 : 2, 2>;
 };
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_256x256, DT, PK, QK> {
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_256x256, DT, PK, QK, LOGITS> {
     using type = Loop<DT, PK, QK, 256, 256, 2, 4, PK || QK ? 3 : 2, 2>;
 };
 // Few rows: ThinLoop tiles, several workgroups a CU (48 to 80 KiB of LDS).
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_32x32, DT, PK, QK> {
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_32x32, DT, PK, QK, LOGITS> {
     using type = ThinLoop<DT, PK, QK, 32, 32, 6>;
 };
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_128x32, DT, PK, QK> {
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_128x32, DT, PK, QK, LOGITS> {
     using type = ThinLoop<DT, PK, QK, 128, 32, 4>;
 };
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_64x64, DT, PK, QK> {
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_64x64, DT, PK, QK, LOGITS> {
     using type = ThinLoop<DT, PK, QK, 64, 64, 5>;
 };
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_64x128, DT, PK, QK> {
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_64x128, DT, PK, QK, LOGITS> {
     using type = ThinLoop<DT, PK, QK, 64, 128, 3>;
 };
-template <int DT, bool PK, bool QK>
-struct LoopOf<LT_128x64, DT, PK, QK> {
+template <int DT, bool PK, bool QK, bool LOGITS>
+struct LoopOf<LT_128x64, DT, PK, QK, LOGITS> {
     using type = ThinLoop<DT, PK, QK, 128, 64, 3>;
 };
 template <int DT>
@@ -870,24 +872,25 @@ LossTileShape loss_tile_shape(int tile) {
 
 // f(loop type) for a tile, type and the operands' storage; an invalid value for
 // what no call asks for.
-template <int TILE, bool PK, bool QK, class F>
+template <int TILE, bool PK, bool QK, bool LOGITS, class F>
 static hipError_t with_type(int dtype, F &&f) {
-    return dtype == 0 ? f(Choice<typename LoopOf<TILE, 0, PK, QK>::type, 0>()) : f(Choice<typename LoopOf<TILE, 1, PK, QK>::type, 1>());
+    return dtype == 0 ? f(Choice<typename LoopOf<TILE, 0, PK, QK, LOGITS>::type, 0>())
+                      : f(Choice<typename LoopOf<TILE, 1, PK, QK, LOGITS>::type, 1>());
 }
-template <bool PK, bool QK, class F>
+template <bool PK, bool QK, bool LOGITS = false, class F>
 static hipError_t with_tile(int dtype, int tile, F &&f) {
     if constexpr (PK && QK) {   // their P slabs are too narrow for k-rows
-        if (tile == LT_32x32) return with_type<LT_32x32, PK, QK>(dtype, f);
-        if (tile == LT_64x64) return with_type<LT_64x64, PK, QK>(dtype, f);
-        if (tile == LT_64x128) return with_type<LT_64x128, PK, QK>(dtype, f);
+        if (tile == LT_32x32) return with_type<LT_32x32, PK, QK, LOGITS>(dtype, f);
+        if (tile == LT_64x64) return with_type<LT_64x64, PK, QK, LOGITS>(dtype, f);
+        if (tile == LT_64x128) return with_type<LT_64x128, PK, QK, LOGITS>(dtype, f);
     }
     if constexpr (QK) {
-        if (tile == LT_128x32) return with_type<LT_128x32, PK, QK>(dtype, f);
-        if (tile == LT_128x64) return with_type<LT_128x64, PK, QK>(dtype, f);
+        if (tile == LT_128x32) return with_type<LT_128x32, PK, QK, LOGITS>(dtype, f);
+        if (tile == LT_128x64) return with_type<LT_128x64, PK, QK, LOGITS>(dtype, f);
     }
     switch (tile) {
-    case LT_128x128: return with_type<LT_128x128, PK, QK>(dtype, f);
-    case LT_256x256: return with_type<LT_256x256, PK, QK>(dtype, f);
+    case LT_128x128: return with_type<LT_128x128, PK, QK, LOGITS>(dtype, f);
+    case LT_256x256: return with_type<LT_256x256, PK, QK, LOGITS>(dtype, f);
     default: return hipErrorInvalidValue;
     }
 }
@@ -895,7 +898,7 @@ static hipError_t with_tile(int dtype, int tile, F &&f) {
 hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const LossStats &s, hipStream_t stream) {
     auto run = [&](auto c) { return run_stats<typename decltype(c)::L>(p, s, stream); };
     if (!p.x.kc) return hipErrorInvalidValue;
-    return p.w.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
+    return p.w.kc ? with_tile<true, true, true>(dtype, tile, run) : with_tile<false, true, true>(dtype, tile, run);
 }
 
 hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz,
@@ -905,7 +908,7 @@ hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossR
         return run_dz<C::DT, typename C::L>(p, rows, scale, dz, ldd, stream);
     };
     if (!p.x.kc) return hipErrorInvalidValue;
-    return p.w.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
+    return p.w.kc ? with_tile<true, true, true>(dtype, tile, run) : with_tile<false, true, true>(dtype, tile, run);
 }
 
 hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStream_t stream) {
