@@ -17,6 +17,7 @@ using dgw::set_error;
 using dgw::set_hip_error;
 
 constexpr int64_t MAX_LD = int64_t(1) << 21;   // a tile's rows then stay within 32-bit byte offsets
+constexpr int MAX_CUS = 1 << 16;               // keeps a launch's workgroups within 32 bits
 constexpr int64_t PIECE_BYTES = int64_t(256) << 20;   // the logits' gradient of one piece
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
@@ -70,9 +71,12 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
     const int64_t ldx = or_packed(a.ldx, a.H), ldw = or_packed(a.ldw, row_of_w(a));
     if ((rc = check_ld(ldx, a.H, 8, "x")) != GEMM_OK || (rc = check_ld(ldw, row_of_w(a), 8, "w")) != GEMM_OK) return rc;
     if (a.kind == GEMM_LOSS_XENT && !(a.z_loss >= 0.0f && std::isfinite(a.z_loss))) return bad("z_loss must be finite and >= 0");
-    if (a.kind == GEMM_LOSS_DISTILL && !(a.temperature > 0.0f && std::isfinite(a.temperature)))
-        return bad("temperature must be finite and > 0");
-    if (a.num_cus < 0) return bad("num_cus must be >= 0");
+    if (a.kind == GEMM_LOSS_DISTILL) {
+        const float square = a.temperature * a.temperature;
+        if (!(a.temperature > 0.0f && square > 0.0f && std::isfinite(square)))
+            return bad("temperature and its square must be finite and > 0");
+    }
+    if (a.num_cus < 0 || a.num_cus > MAX_CUS) return bad("num_cus must be 0 .. 65536");
     const bool dw32 = a.dw_type != GEMM_LOSS_DW_SAME;
     const int64_t lddx = or_packed(a.lddx, a.H), lddw = or_packed(a.lddw, row_of_w(a));
     if (backward) {
@@ -89,6 +93,7 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
     if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
     if (!backward) {
         if (!a.loss) return bad("loss must be non-null");
+        if (overlap(a.loss, a.T * 4, a.lse, a.T * 4)) return bad("loss and lse must not overlap");
         return GEMM_OK;
     }
     if (!a.grad) return bad("grad must be non-null");
@@ -360,7 +365,7 @@ int backward(const gemm_loss_args_t &a) {
                 q.out = part<float>(c.ws, pl.at.dw);
                 q.out_kind = dgw::LO_SLOTS;
             }
-            if (pl.dw_outer) e = dgw::launch_loss_outer(c.dtype, q, 2 * std::min(c.cus, 1 << 16), c.stream);
+            if (pl.dw_outer) e = dgw::launch_loss_outer(c.dtype, q, 2 * c.cus, c.stream);
             else e = dgw::launch_loss_product(c.dtype, pl.dw, q, c.stream);
             if (e != hipSuccess) return set_hip_error(e, "launch dw");
             if (pl.dw_splits > 1 &&
@@ -384,7 +389,7 @@ extern "C" {
 int gemm_loss_plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out) {
     dgw::clear_error();
     if (!args || !out) return bad("args and out must be non-null");
-    if (num_cus < 1) return bad("num_cus must be >= 1");
+    if (num_cus < 1 || num_cus > MAX_CUS) return bad("num_cus must be 1 .. 65536");
     const int rc = check_sizes(*args);
     if (rc != GEMM_OK) return rc;
     std::memset(out, 0, sizeof *out);

@@ -14,13 +14,17 @@
 // slabs of k move from global memory straight into LDS (16 bytes a lane, no
 // registers) into NS stages; KC slabs are read with 128-bit LDS reads, RC slabs
 // with the transposing 64-bit read.  The XOR swizzles leave both free of bank
-// conflicts: 16 consecutive KC rows read at one chunk cover all 64 banks, and so
-// do the four k-rows that a transposing read touches.
+// conflicts: 16 consecutive KC rows read at one chunk cover all 64 banks (their
+// low three bits move the chunk), and so do the k-rows that a transposing read
+// touches (four consecutive ones per 16 lanes, those of neighbouring groups 8
+// apart: bits 0, 1 and 3 of k move the chunk).
 //
-// The products are 16x16x32 matrix instructions.  Under them the chip runs at its
-// power cap, and their accumulator traffic is half that of the 32x32x16 ones:
-// 4096 x 131072 x 4096 logits took 3.23 ms on those (1.36 PFLOP/s at 1.55 GHz, the
-// matrix cores busy 75 % of the time), 2.99 ms on these.
+// The products are 16x16x32 matrix instructions: on one card 4096 x 131072 x 4096
+// logits took 3.13 ms on them and 3.31 ms on 32x32x16 ones, and 3.0 to 3.05 ms
+// (1.44 to 1.47 PFLOP/s) since the products go back and forth along Q.  The chip
+// is at its power cap there: 1.6 to 1.7 GHz with the matrix cores busy 75 % of the
+// time.  Where it ran at 1.40 PFLOP/s, the same loop with every load answered by the
+// L2 ran at 1.55, and on operands of zeros, which cost the least power, at 1.65.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -332,9 +336,7 @@ struct Loop {
 
     // Products [M0, M1) of half HALF of a step, and evenly between them the reads of
     // the next half's fragments (half NH of step NSTEP of iteration NIT) when READ, and
-    // the loads of `issue` when LOAD: the matrix pipe keeps running while they go
-    // out.  Reads in one burst ahead of the products leave it idle while eight
-    // waves queue for the LDS.
+    // the loads of `issue` when LOAD: the matrix pipe keeps running while they go out.
     template <int HALF, int M0, int M1, bool READ, int NIT, int NSTEP, int NH, bool LOAD, bool RAGGED>
     __device__ __forceinline__ void products(const FragP &p, const FragQ &q, Acc &acc, FragP &np, FragQ &nq,
                                              const Issue &issue) const {

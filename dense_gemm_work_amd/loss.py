@@ -8,7 +8,10 @@ distillation over the logits ``x . w^T``, which are never kept.
 
 The torch-facing functions take their workspace from torch's allocator on the
 call's stream (so calls on different streams, and graphs captured separately, do
-not share one), unless ``workspace`` is given.
+not share one), unless ``workspace`` is given.  They record nothing for autograd:
+the backward calls are the gradients.  With ``stream`` given, the inputs must be
+ready on it and stay allocated until it has run the call (``record_stream`` on
+them says so to torch's allocator); results not given are allocated on it.
 """
 from __future__ import annotations
 
@@ -245,7 +248,8 @@ def linear_cross_entropy(x, w, target, *, b_layout: str = "nk", ignore_index: in
     that divisor's inverse in every row.
     x [T,H], w: bf16 or fp16 on one device, rows contiguous at any stride that
     is a multiple of 8 elements; target: int64 [T].  A target out of range makes
-    its row's loss NaN.  Enqueues on ``stream`` or torch's current stream;
+    its row's loss NaN.  Rows that are left out may hold anything finite: their
+    gradient is zero, and zero times infinity would be NaN in dw.  Enqueues on ``stream`` or torch's current stream;
     ``loss`` and ``lse`` may be given.
     """
     a = _product(x, w, b_layout)

@@ -79,15 +79,15 @@ extern "C" {
  *   entries:   K, 1 .. GEMM_LOSS_MAX_ENTRIES (DISTILL).
  *   teacher_index:  device int64 [T,K], packed (DISTILL).
  *   teacher_logits: device [T,K], packed, of teacher_type (DISTILL).
- *   temperature:    tau > 0 (DISTILL).
+ *   temperature:    tau > 0 (DISTILL); tau^2 must be a finite fp32 above 0 too.
  *   loss:      device fp32 [T], written by gemm_loss_forward.
- *   lse:       device fp32 [T], written by gemm_loss_forward, read by gemm_loss_backward.
+ *   lse:       device fp32 [T], written by gemm_loss_forward, read by gemm_loss_backward; must not overlap loss.
  *   grad:      device fp32 [T], the gradient g of each row's loss (backward).
  *   dx:        device [T,H] of the operands' type, lddx as ldx; NULL: not computed.
  *   dw:        device, w's layout, of dw_type, lddw as ldw (fp32: a multiple of 4); NULL: not computed.
  *   stream, workspace, workspace_bytes: as in gemm_args_t, except that the
  *              workspace need not be cleared; gemm_loss_plan_t.workspace_bytes is needed.
- *   num_cus:   plan for this many compute units (0: the device's).
+ *   num_cus:   plan for this many compute units, at most 65536 (0: the device's).
  */
 typedef struct gemm_loss_args_t {
     const void *x;
@@ -132,7 +132,7 @@ typedef struct gemm_loss_plan_t {
 } gemm_loss_plan_t;
 
 /* gemm_loss_plan -- plan the forward (backward = 0) or backward (1) call of `args`
- * for num_cus >= 1 compute units.  Reads sizes, layout, kind, entries, dx, dw and
+ * for num_cus compute units (1 .. 65536).  Reads sizes, layout, kind, entries, dx, dw and
  * dw_type only (the pointers for being NULL or not). */
 int gemm_loss_plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out);
 

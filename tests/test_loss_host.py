@@ -244,6 +244,9 @@ REFUSED = [   # what, kind, backward too / only, expected status
     ("temperature 0", 1, change(temperature=0.0), "both", "INVALID"),
     ("temperature NaN", 1, change(temperature=float("nan")), "both", "INVALID"),
     ("temperature inf", 1, change(temperature=float("inf")), "both", "INVALID"),
+    ("temperature squared inf", 1, change(temperature=1e20), "both", "INVALID"),
+    ("temperature squared 0", 1, change(temperature=1e-30), "both", "INVALID"),
+    ("loss over lse", 0, change(loss=4 * BASE + 60), "forward", "INVALID"),
     ("unknown dw type", 0, change(dw_type=3), "both", "INVALID"),
     ("dx unaligned", 0, change(dx=6 * BASE + 8), "backward", "UNSUPPORTED"),
     ("dw unaligned", 0, change(dw=7 * BASE + 4), "backward", "UNSUPPORTED"),
@@ -254,6 +257,7 @@ REFUSED = [   # what, kind, backward too / only, expected status
     ("dw over dx", 0, change(dw=6 * BASE + 512), "backward", "INVALID"),
     ("workspace unaligned", 0, change(workspace=11 * BASE + 16), "both", "INVALID"),
     ("negative num_cus", 0, change(num_cus=-1), "both", "INVALID"),
+    ("too many CUs", 0, change(num_cus=65537), "both", "INVALID"),
     ("workspace too small", 0, change(), "both", "WORKSPACE"),
     ("workspace too small", 1, change(), "both", "WORKSPACE"),
 ]
@@ -295,6 +299,8 @@ def test_null_arguments(dg):
     assert dg._lib.gemm_loss_plan(None, 0, 256, None) == dg.GEMM_ERR_INVALID
     with pytest.raises(dg.GemmError):
         dg.gemm_loss_plan(args_of(dg), False, 0)
+    with pytest.raises(dg.GemmError):
+        dg.gemm_loss_plan(args_of(dg), True, 65537)
 
 
 def test_tensor_checks(dg):
