@@ -10,6 +10,8 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -26,29 +28,32 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build the library)")
 
 
-def command(out: Path) -> list:
-    return [
-        hipcc(), f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
-        "-munsafe-fp-atomics",
-        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-        "-Wall", "-Wno-unused-function",
-        *[str(CSRC / s) for s in SOURCES],
-        "-o", str(out),
-    ]
+FLAGS = [
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-munsafe-fp-atomics",
+    "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    "-Wall", "-Wno-unused-function",
+]
 
 
 def build(verbose: bool = False) -> Path:
-    """Always recompiles (the driver's build check), then atomically replaces the library."""
-    tmp = LIB.with_name(LIB.name + f".tmp{os.getpid()}")
-    cmd = command(tmp)
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True, cwd=str(PKG))
-    if res.returncode != 0:
-        raise RuntimeError(f"HIP build failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stderr[-8000:]}")
-    noise = [ln for ln in res.stderr.splitlines() if "packed-fp32-ops" not in ln and ln.strip()]
-    if verbose and noise:
-        print("\n".join(noise[-40:]))
+    """Always recompiles, the sources side by side, then
+    links and atomically replaces the library."""
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        res = subprocess.run(cmd, capture_output=True, text=True, cwd=str(PKG))
+        if res.returncode != 0:
+            raise RuntimeError(f"HIP build failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stderr[-8000:]}")
+        noise = [ln for ln in res.stderr.splitlines() if "packed-fp32-ops" not in ln and ln.strip()]
+        if verbose and noise:
+            print("\n".join(noise[-40:]))
+
+    with tempfile.TemporaryDirectory(prefix="dgw_build_") as objects:
+        outs = [str(Path(objects) / (s + ".o")) for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(lambda s, o: run([hipcc(), *FLAGS, "-c", str(CSRC / s), "-o", o]), SOURCES, outs))
+        tmp = LIB.with_name(LIB.name + f".tmp{os.getpid()}")
+        run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *outs, "-o", str(tmp)])
     os.replace(tmp, LIB)
     build_example(verbose)
     return LIB
