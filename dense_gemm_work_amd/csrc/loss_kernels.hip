@@ -565,7 +565,10 @@ __device__ __forceinline__ float teacher_logit(const TeacherParams &p, int64_t a
 }
 
 // One wave per row: the softmax over its entries, then a counting sort of them
-// by bucket, entries of one bucket in the order they came.
+// by bucket, entries of one bucket in the order they came.  The row's maximum is
+// taken of the logits as they are and subtracted before the division by tau: a
+// finite logit stays finite at any tau (the lowest value over 0.5 would not), and
+// the largest entry's argument is 0.
 __global__ __launch_bounds__(256) void loss_teacher(TeacherParams p) {
     __shared__ int counts[4][LOSS_BUCKETS];
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -578,24 +581,24 @@ __global__ __launch_bounds__(256) void loss_teacher(TeacherParams p) {
     for (int k = lane; k < p.K; k += 64) {
         const int64_t i = p.index[base + k];
         if (i < 0) continue;
-        const float t = teacher_logit(p, base + k) * p.inv_tau;
+        const float t = teacher_logit(p, base + k);
         bad |= i >= p.V || t != t;
         m = fmaxf(m, t);
     }
     m = wave_max(m);
     bad = __any(bad);
     const bool none = m == -INF;
-    float total = 0.0f, dot = 0.0f;   // sum e, sum e (t - m)
+    float total = 0.0f, dot = 0.0f;   // sum e, sum e t
     for (int k = lane; k < p.K; k += 64) {
         if (none || p.index[base + k] < 0) continue;
-        const float t = teacher_logit(p, base + k) * p.inv_tau - m;
+        const float t = (teacher_logit(p, base + k) - m) * p.inv_tau;
         const float e = t == -INF ? 0.0f : expf(t);
         total += e;
         dot += e > 0.0f ? e * t : 0.0f;
     }
     total = wave_sum(total);
     dot = wave_sum(dot);
-    // sum q log q = sum e (t - m) / total - log total
+    // sum q log q = sum e t / total - log total
     if (lane == 0) p.entropy[row] = bad ? __builtin_nanf("") : none ? -INF : dot / total - logf(total);
 
     // each lane's bucket and its rank among the lanes of the same bucket (-1: no entry)
@@ -641,7 +644,7 @@ __global__ __launch_bounds__(256) void loss_teacher(TeacherParams p) {
         place(k, bucket, rank, last);
         if (rank >= 0) {
             const int at = count[bucket] + rank;
-            const float t = teacher_logit(p, base + k) * p.inv_tau - m;
+            const float t = (teacher_logit(p, base + k) - m) * p.inv_tau;
             const float q = t == -INF ? 0.0f : expf(t) / total;
             p.entries[base + at] = uint2{(uint32_t)p.index[base + k], __float_as_uint(q)};
         }
