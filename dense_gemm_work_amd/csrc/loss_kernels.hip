@@ -159,12 +159,15 @@ __global__ __launch_bounds__(L::NT, 2) void loss_stats(LogitParams p, LossStats 
                 for (int e = 0; e < 4; ++e) m = fmaxf(m, acc.v[i][j][e]);
             m = fmaxf(m, __shfl_xor(m, 16));
             m = fmaxf(m, __shfl_xor(m, 32));
-            const float base = m == -INF ? 0.0f : -m * p.c;   // a row of -infinity sums to 0
+            // the maximum is subtracted first, exactly: its own exponential is then 1, the
+            // sum at least 1 and no loss negative.  (z c - round(m c) would keep the
+            // rounding of m c, 1e-5 at logits of 250.)
+            const float top = m == -INF ? 0.0f : m;   // a row of -infinity sums to 0
             float se = 0.0f;
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) se += exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, base));
+                for (int e = 0; e < 4; ++e) se += exp2_fast((acc.v[i][j][e] - top) * p.c);
             float d = 0.0f;
             if (any_target<L::WAVE_P>(p.targets, range[j], first)) {
                 array.put(acc, j);
