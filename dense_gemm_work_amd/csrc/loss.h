@@ -50,7 +50,7 @@ struct LossStats {
 // What the rows' contributions to the logits' gradient follow from.
 struct LossRows {
     int64_t V;
-    float zeta, tau;
+    float zeta, tau, inv_tau;
     const int64_t *target;   // XENT
     int64_t ignore;
     const float *entropy;    // DISTILL

@@ -321,7 +321,8 @@ int backward(const gemm_loss_args_t &a) {
     if ((rc = begin(a, true, &c)) != GEMM_OK) return rc;
     const Plan &pl = c.plan;
     const bool xent = a.kind == GEMM_LOSS_XENT;
-    const dgw::LossRows rows{a.V, a.z_loss, xent ? 1.0f : a.temperature, xent ? a.target : nullptr, a.ignore_index,
+    const float tau = xent ? 1.0f : a.temperature;
+    const dgw::LossRows rows{a.V, a.z_loss, tau, 1.0f / tau, xent ? a.target : nullptr, a.ignore_index,
                              c.entropy, a.grad, a.lse};
     float *scale = c.dtype == 1 ? part<float>(c.ws, pl.at.scale) : nullptr;
     uint16_t *dz = part<uint16_t>(c.ws, pl.at.dz);

@@ -261,13 +261,13 @@ __device__ __forceinline__ void store16(const L &loop, const typename L::Acc &ac
 // What a row contributes to the logits' gradient, dz = a p - b q (0 when !on).
 // ---------------------------------------------------------------------------
 struct RowFactors {
-    float lse2;   // lse * log2 e
+    float lse;
     float a, b;
     bool on;
 };
 __device__ __forceinline__ RowFactors row_factors(const LossRows &p, int64_t row) {
     const float lse = p.lse[row], g = p.grad[row];
-    RowFactors r{lse * LOG2E, 0.0f, 0.0f, true};
+    RowFactors r{lse, 0.0f, 0.0f, true};
     if (p.target) {
         const int64_t y = p.target[row];
         const float bad = y < 0 || y >= p.V ? __builtin_nanf("") : 0.0f;
@@ -280,12 +280,14 @@ __device__ __forceinline__ RowFactors row_factors(const LossRows &p, int64_t row
         r.a = h != h ? h : g * p.tau;
         r.b = g * p.tau;
     }
-    if (!r.on) r.lse2 = r.a = r.b = 0.0f;
+    if (!r.on) r.lse = r.a = r.b = 0.0f;
     return r;
 }
 
 // ---------------------------------------------------------------------------
-// The logits' gradient of one tile: dz = a p - b q, p = exp2(z c - lse2).
+// The logits' gradient of one tile: dz = a p - b q, p = exp(z / tau - lse).  lse is
+// subtracted before the factor log2 e: at a sure row's target z / tau = lse, p = 1 and
+// dz = 0.  (z c - round(lse log2 e) left up to 1e-5 there at logits of 250.)
 // ---------------------------------------------------------------------------
 template <int DT, class L>
 __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, LossRows rows, const float *scale, uint16_t *dz,
@@ -298,7 +300,7 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, LossRows rows
     typename L::Acc acc;
     L::zero(acc);
     loop.run_any(p.w, p0, p.x, q0, p.H, 0, p.g.slabs, acc);
-    const float S = scale ? scale[0] : 1.0f;
+    const float S = scale ? scale[0] : 1.0f, inv_tau = rows.inv_tau;
     const int64_t first = p.v0 + p0 + loop.wp * L::WAVE_P;
     TargetRange range[L::CB];
 #pragma unroll
@@ -314,7 +316,7 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, LossRows rows
         for (int i = 0; i < L::RB; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                acc.v[i][j][e] = a * exp2_fast(__builtin_fmaf(acc.v[i][j][e], p.c, -r.lse2));
+                acc.v[i][j][e] = a * exp2_fast(__builtin_fmaf(acc.v[i][j][e], inv_tau, -r.lse) * LOG2E);
         if (any_target<L::WAVE_P>(p.targets, range[j], first)) {
             array.put(acc, j);
             for_targets<L::WAVE_P>(p.targets, range[j], first, loop.lane >> 4,

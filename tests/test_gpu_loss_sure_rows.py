@@ -2,11 +2,12 @@
 in the hundreds whose row has all of its mass on the target.  Operands are small
 integers, so every logit is exact whatever the order of its sum, and so are the
 expected values: the maximum's own exponential is 1, the sum of exponentials at
-least 1 and a sure row's loss 0."""
+least 1, a sure row's loss 0 and its gradient nothing but what the other entries
+hold."""
 import pytest
 import torch
 
-from loss_util import DTYPES, call_forward, say
+from loss_util import DTYPES, call_backward, call_forward, say, to_layout
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -75,6 +76,22 @@ def test_a_sure_rows_loss_is_zero(dg, size, kind, tau):
     # lse = m / tau: the division by tau as a product with its rounded inverse, two
     # roundings of half a step each
     assert float(((lse.double().cpu() - z / tau).abs() / (z / tau)).max()) <= 2 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("kind,tau", [("xent", 1.0), ("distill", 1.0), ("distill", 2.0)], ids=str)
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_a_sure_rows_gradient_is_that_of_the_others(dg, size, kind, tau):
+    # p of the target is exp(z - lse) with z = lse: 1, and dz there g - g = 0; the others
+    # have p below e^-34, so |dx| <= 1.5 tau 16500 e^-34 max|w| < 1e-10 and
+    # |dw| <= 1.5 tau T e^-34 256 < 1e-9
+    T, V, H, dtype, layout = size
+    d, z = sure(T, V, H, dtype, kind, layout)
+    say(f"  {kind} {size} tau={tau}")
+    loss, lse = call_forward(dg, d, layout, tau)
+    dw = torch.full(tuple(to_layout(d["w"], layout).shape), 7.0, device=DEV)
+    dx, dw = call_backward(dg, d, lse, layout, tau, dw=dw)
+    say(f"    |dx| <= {dx.abs().max().item():.3e}, |dw| <= {dw.abs().max().item():.3e}")
+    assert dx.abs().max().item() <= 1e-10 and dw.abs().max().item() <= 1e-9
 
 
 @pytest.mark.parametrize("T,V", [(5, 900), (40, 20001), (300, 5003)], ids=str)
