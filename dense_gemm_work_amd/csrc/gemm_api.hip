@@ -624,16 +624,18 @@ int current_device_cus(int *out) {
     return rc;
 }
 
-int library_workspace(int64_t bytes, hipStream_t stream, void **out) {
+int library_workspace(int64_t bytes, hipStream_t stream, void **out, std::unique_lock<std::mutex> *held) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
-    std::lock_guard<std::mutex> lock(g_mu);
+    std::unique_lock<std::mutex> lock(g_mu);
     DeviceState *ds = nullptr;
     int rc = device_state(dev, &ds);
     if (rc == GEMM_OK) rc = ensure_data(*ds, bytes, stream);
-    if (rc == GEMM_OK) *out = ds->data;
-    return rc;
+    if (rc != GEMM_OK) return rc;
+    *out = ds->data;
+    *held = std::move(lock);
+    return GEMM_OK;
 }
 
 }  // namespace dgw

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 #include <string>
 
 namespace dgw {
@@ -21,7 +22,9 @@ hipStream_t thread_stream();
 int current_device_cus(int *out);
 
 // At least `bytes` of the current device's library workspace.  Refused while
-// `stream` is being captured if the workspace would have to grow.
-int library_workspace(int64_t bytes, hipStream_t stream, void **out);
+// `stream` is being captured if the workspace would have to grow.  `lock` receives
+// the library's lock, which the caller keeps until its last kernel is enqueued:
+// until then no other thread's call uses the workspace, and gemm_release() waits.
+int library_workspace(int64_t bytes, hipStream_t stream, void **out, std::unique_lock<std::mutex> *lock);
 
 }  // namespace dgw

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 #include <string>
 
 #include "../../include/gemm_loss.h"
@@ -234,6 +235,7 @@ T *part(void *ws, int64_t at) {
 struct Call {
     hipStream_t stream;
     void *ws = nullptr;
+    std::unique_lock<std::mutex> lock;   // held for the whole call where ws is the library's
     int cus;
     int dtype;
     bool nk;
@@ -255,7 +257,7 @@ int begin(const gemm_loss_args_t &a, bool backward, Call *c) {
     if (a.workspace) {
         if ((int64_t)a.workspace_bytes < l.bytes)
             return set_error(GEMM_ERR_WORKSPACE, "caller workspace is smaller than plan.workspace_bytes (" + std::to_string(l.bytes) + ")");
-    } else if ((rc = dgw::library_workspace(l.bytes, c->stream, &c->ws)) != GEMM_OK) {
+    } else if ((rc = dgw::library_workspace(l.bytes, c->stream, &c->ws, &c->lock)) != GEMM_OK) {
         return rc;
     }
     if (a.kind == GEMM_LOSS_XENT) {
