@@ -46,6 +46,8 @@ GEMM_ERR_WORKSPACE = -3
 GEMM_ERR_HIP = -4
 GEMM_ERR_TIMEOUT = -5
 
+GEMM_NULL_STREAM = (1 << 8 * ctypes.sizeof(ctypes.c_void_p)) - 1   # HIP's null stream as an argument
+
 GEMM_B_KN = 0x00
 GEMM_B_NK = 0x01
 GEMM_BF16 = 0x00
@@ -293,6 +295,12 @@ def plan_dict(p: GemmPlan) -> dict:
     return d
 
 
+def stream_word(stream) -> int:
+    """A torch stream as a ``stream`` argument: the handle of torch's default stream is 0,
+    which the library would take for the thread's ``gemm_set_stream`` value."""
+    return stream.cuda_stream or GEMM_NULL_STREAM
+
+
 def layout_word(b_layout: str, dtype: str) -> int:
     lw = {"kn": GEMM_B_KN, "nk": GEMM_B_NK}[b_layout]
     return lw | {"bf16": GEMM_BF16, "fp16": GEMM_FP16}[dtype]
@@ -388,7 +396,7 @@ def gemm_tensors(a, b, c, b_layout: str = "kn", mode: str = "heuristic", splits:
         args.stride_a, args.stride_b, args.stride_c = sa, sb, (sc if sc else M * N)
     with torch.cuda.device(a.device):
         s = stream if stream is not None else torch.cuda.current_stream(a.device)
-        args.stream = s.cuda_stream
+        args.stream = stream_word(s)
         if unit_perm is not None:
             if unit_perm.dtype != torch.int32 or not unit_perm.is_cuda or not unit_perm.is_contiguous():
                 raise TypeError("unit_perm must be a contiguous int32 device tensor")
@@ -465,7 +473,7 @@ def gemm_grouped_tensors(problems, b_layout: str = "kn", mode: str = "heuristic"
     args.num_cus = num_cus
     with torch.cuda.device(a0.device):
         s = stream if stream is not None else torch.cuda.current_stream(a0.device)
-        args.stream = s.cuda_stream
+        args.stream = stream_word(s)
         if trace is not None:
             args.trace, args.trace_ints = trace.data_ptr(), trace.numel()
         if timing is not None:

@@ -322,7 +322,7 @@ int run(const gemm_args_t &a, bool noalloc = false, const gemm_group_t *groups =
         if (a.num_cus > 0 && p.workspace_bytes > (int64_t)GEMM_NOALLOC_MAX_BYTES) return scratch_too_small(p);
     }
 
-    hipStream_t stream = a.stream ? reinterpret_cast<hipStream_t>(a.stream) : g_stream;
+    hipStream_t stream = dgw::call_stream(a.stream);
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
@@ -611,7 +611,11 @@ namespace dgw {
 int set_error(int code, const std::string &msg) { return fail(code, msg); }
 int set_hip_error(hipError_t e, const char *what) { return fail_hip(e, what); }
 void clear_error() { g_err.clear(); }
-hipStream_t thread_stream() { return g_stream; }
+
+hipStream_t call_stream(void *stream) {
+    if (!stream) return g_stream;
+    return stream == GEMM_NULL_STREAM ? nullptr : reinterpret_cast<hipStream_t>(stream);
+}
 
 int current_device_cus(int *out) {
     int dev = 0;
@@ -698,12 +702,12 @@ int64_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t batch, uint
 }
 
 int gemm_set_stream(void *stream) {
-    g_stream = reinterpret_cast<hipStream_t>(stream);
+    g_stream = stream == GEMM_NULL_STREAM ? nullptr : reinterpret_cast<hipStream_t>(stream);
     return GEMM_OK;
 }
 
 int gemm_sync_status(void *stream) {
-    hipStream_t s = stream ? reinterpret_cast<hipStream_t>(stream) : g_stream;
+    hipStream_t s = dgw::call_stream(stream);
     hipError_t e = hipStreamSynchronize(s);
     if (e != hipSuccess) return fail_hip(e, "hipStreamSynchronize");
     int dev = 0;

@@ -15,8 +15,9 @@ int set_error(int code, const std::string &msg);
 int set_hip_error(hipError_t e, const char *what);
 void clear_error();
 
-// The calling thread's stream (gemm_set_stream).
-hipStream_t thread_stream();
+// The stream that a call's `stream` argument names: the calling thread's
+// (gemm_set_stream) for NULL, HIP's null stream for GEMM_NULL_STREAM.
+hipStream_t call_stream(void *stream);
 
 // Compute units of the current device.
 int current_device_cus(int *out);

@@ -245,7 +245,7 @@ struct Call {
 };
 
 int begin(const gemm_loss_args_t &a, bool backward, Call *c) {
-    c->stream = a.stream ? reinterpret_cast<hipStream_t>(a.stream) : dgw::thread_stream();
+    c->stream = dgw::call_stream(a.stream);
     c->dtype = (a.layout & 0xF0u) == GEMM_FP16 ? 1 : 0;
     c->nk = (a.layout & 0xFu) == GEMM_B_NK;
     int rc;
@@ -314,8 +314,7 @@ int backward(const gemm_loss_args_t &a) {
     hipError_t e;
     if (a.T == 0) {
         if (!a.dw || a.dw_type == GEMM_LOSS_DW_FP32_ADD) return GEMM_OK;
-        hipStream_t stream = a.stream ? reinterpret_cast<hipStream_t>(a.stream) : dgw::thread_stream();
-        if ((e = dgw::launch_loss_zero(a.dw, rows_of_w(a), row_of_w(a) * dw_size, lddw * dw_size, stream)) != hipSuccess)
+        if ((e = dgw::launch_loss_zero(a.dw, rows_of_w(a), row_of_w(a) * dw_size, lddw * dw_size, dgw::call_stream(a.stream))) != hipSuccess)
             return set_hip_error(e, "zero dw");
         return GEMM_OK;
     }

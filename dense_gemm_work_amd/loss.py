@@ -19,7 +19,7 @@ import contextlib
 import ctypes
 import functools
 
-from . import _check, _lib, layout_word
+from . import _check, _lib, layout_word, stream_word
 
 try:
     import torch
@@ -178,7 +178,7 @@ def _workspace_bytes(T, V, H, layout, kind, entries, dx, dw, dw_type, backward, 
 def _call(a, x, backward, workspace, outputs):
     """Runs the call on torch's current stream, its workspace torch's unless given."""
     device = x.device
-    a.stream = torch.cuda.current_stream(device).cuda_stream
+    a.stream = stream_word(torch.cuda.current_stream(device))
     if workspace is None:
         a.num_cus = cus = _cus(device.index)
         need = _workspace_bytes(a.T, a.V, a.H, a.layout, a.kind, a.entries, 1 if a.dx else 0, 1 if a.dw else 0,

@@ -238,10 +238,14 @@ typedef struct gemm_plan_t {
                              numbered batch entry after batch entry                        */
 } gemm_plan_t;
 
+/* HIP's null stream as an argument (its handle, NULL, asks for the thread's stream). */
+#define GEMM_NULL_STREAM ((void *)~(uintptr_t)0)
+
 /*
  * Extended arguments.  Zero-initialise, then fill what you need.
  *   A, B, C, M, N, K, layout, mode, splits: as for gemm().
- *   stream:   hipStream_t to enqueue on; NULL = the thread's gemm_set_stream value.
+ *   stream:   hipStream_t to enqueue on; NULL = the thread's gemm_set_stream value;
+ *             GEMM_NULL_STREAM = HIP's null stream, whatever the thread's is.
  *   workspace, workspace_bytes: caller-owned device memory of at least
  *             plan.workspace_bytes, zero-filled before its first use and used by
  *             one stream at a time; NULL = the library's per-device workspace.
@@ -461,7 +465,8 @@ int64_t gemm_workspace_size(int64_t M, int64_t N, int64_t K, int64_t batch, uint
  */
 int gemm_unit_range(const gemm_plan_t *plan, int64_t unit, int64_t *begin, int64_t *end);
 
-/* gemm_set_stream -- the calling thread's default stream (hipStream_t, may be NULL). */
+/* gemm_set_stream -- the calling thread's default stream (hipStream_t; NULL or
+ * GEMM_NULL_STREAM: HIP's null stream). */
 int gemm_set_stream(void *stream);
 
 /*

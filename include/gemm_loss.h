@@ -32,7 +32,8 @@
  * Every sum has a fixed order: the same call gives the same bits.
  *
  * Streams, errors and the library workspace are as in gemm.h: calls are
- * asynchronous on args.stream (else the thread's gemm_set_stream), return a
+ * asynchronous on args.stream (else the thread's gemm_set_stream; GEMM_NULL_STREAM:
+ * HIP's null stream), return a
  * GEMM_* status, launch nothing on a negative one, and gemm_last_error() says
  * why.  They enqueue kernels only and can be captured; with workspace = NULL the
  * library workspace must have been sized by an eager call before.

@@ -203,10 +203,58 @@ int two_threads() {
     return 0;
 }
 
+// Whether `call` launched something, all of it on `stream`.
+template <class F>
+bool runs_on(void *stream, F &&call) {
+    events.clear();
+    call();
+    bool any = false;
+    for (const Event &e : events)
+        if (e.what.rfind("launch", 0) == 0) {
+            any = true;
+            if (e.stream != stream) return false;
+        }
+    return any;
+}
+
+int streams() {
+    // NULL: the thread's stream; GEMM_NULL_STREAM: HIP's, whatever the thread's is
+    void *const own = at(100), *const given = at(101);
+    gemm_loss_args_t a = backward_args(), none = backward_args();
+    none.T = 0;   // dw is cleared
+    gemm_args_t g;
+    std::memset(&g, 0, sizeof g);
+    g.A = at(1), g.B = at(2), g.C = at<float>(40);
+    g.M = g.N = g.K = 256;
+    gemm_args_t common;
+    std::memset(&common, 0, sizeof common);
+    common.K = 256;
+    const gemm_group_t group = {at(1), at(2), at<float>(40), 256, 256};
+    for (void *thread : {static_cast<void *>(nullptr), own}) {
+        REQUIRE(gemm_set_stream(thread) == GEMM_OK);
+        struct {
+            void *argument, *want;
+        } const cases[] = {{nullptr, thread}, {given, given}, {GEMM_NULL_STREAM, nullptr}};
+        for (const auto &c : cases) {
+            a.stream = none.stream = g.stream = common.stream = c.argument;
+            REQUIRE(runs_on(c.want, [&] { REQUIRE(gemm_loss_forward(&a) == GEMM_OK); }));
+            REQUIRE(runs_on(c.want, [&] { REQUIRE(gemm_loss_backward(&a) == GEMM_OK); }));
+            REQUIRE(runs_on(c.want, [&] { REQUIRE(gemm_loss_backward(&none) == GEMM_OK); }));
+            REQUIRE(runs_on(c.want, [&] { REQUIRE(gemm_ex(&g) == GEMM_OK); }));
+            REQUIRE(runs_on(c.want, [&] { REQUIRE(gemm_grouped(&common, &group, 1) == GEMM_OK); }));
+        }
+        REQUIRE(runs_on(thread, [] { REQUIRE(gemm(at(1), at(2), at<float>(40), 256, 256, 256, 0, 0, 0) == GEMM_OK); }));
+    }
+    REQUIRE(gemm_set_stream(GEMM_NULL_STREAM) == GEMM_OK);
+    a.stream = nullptr;
+    REQUIRE(runs_on(nullptr, [&] { REQUIRE(gemm_loss_forward(&a) == GEMM_OK); }));
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
-    const std::map<std::string, int (*)()> scenarios = {{"release", release}, {"two_threads", two_threads}};
+    const std::map<std::string, int (*)()> scenarios = {{"release", release}, {"two_threads", two_threads}, {"streams", streams}};
     const auto s = scenarios.find(argc > 1 ? argv[1] : "");
     if (s == scenarios.end()) return 2;
     const int rc = s->second();

@@ -20,7 +20,19 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("scenario", ["release", "two_threads"])
+def test_torchs_default_stream_is_named_as_such():
+    import dense_gemm_work_amd as dg
+
+    class Stream:
+        cuda_stream = 0
+
+    assert dg.stream_word(Stream) == dg.GEMM_NULL_STREAM
+    assert dg.GemmLossArgs(stream=dg.stream_word(Stream)).stream == dg.GemmArgs(stream=2 ** 64 - 1).stream is not None
+    Stream.cuda_stream = 0x5000
+    assert dg.stream_word(Stream) == 0x5000
+
+
+@pytest.mark.parametrize("scenario", ["release", "two_threads", "streams"])
 def test_calls(program, scenario):
     res = subprocess.run([str(program), scenario], capture_output=True, text=True, timeout=60)
     assert res.returncode == 0 and res.stdout.split() == ["ok"], res.stdout + res.stderr
