@@ -57,13 +57,56 @@ int check_ld(int64_t ld, int64_t row, int64_t unit, const char *what) {
     return GEMM_OK;
 }
 
-bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a && b && a0 < b0 + (uintptr_t)bbytes && b0 < a0 + (uintptr_t)abytes;
+// A buffer of a call: `rows` rows of `row` bytes, `ld` bytes apart.
+struct Block {
+    const void *base;
+    int64_t rows, row, ld;
+    const char *name;
+    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(base); }
+    uintptr_t end() const { return begin() + (uintptr_t)((rows - 1) * ld + row); }
+};
+
+bool overlap(const Block &a, const Block &b) {
+    return a.base && b.base && a.rows > 0 && b.rows > 0 && a.begin() < b.end() && b.begin() < a.end();
 }
 
-int64_t span_bytes(int64_t rows, int64_t row, int64_t ld, int64_t size) {
-    return rows > 0 ? ((rows - 1) * ld + row) * size : 0;
+// The buffers of a call: first what it writes, then what it reads.
+struct Blocks {
+    Block b[8];
+    int written = 0, all = 0;
+    void add(const void *base, int64_t rows, int64_t row, int64_t ld, const char *name) { b[all++] = {base, rows, row, ld, name}; }
+};
+
+Blocks blocks_of(const gemm_loss_args_t &a, bool backward) {
+    Blocks s;
+    const int64_t t4 = a.T * 4, w_row = row_of_w(a) * 2, w_rows = rows_of_w(a);
+    const int64_t dw_size = a.dw_type != GEMM_LOSS_DW_SAME ? 4 : 2;
+    if (backward) {
+        s.add(a.dx, a.T, a.H * 2, or_packed(a.lddx, a.H) * 2, "dx");
+        s.add(a.dw, w_rows, row_of_w(a) * dw_size, or_packed(a.lddw, row_of_w(a)) * dw_size, "dw");
+    } else {
+        s.add(a.loss, 1, t4, t4, "loss");
+        s.add(a.lse, 1, t4, t4, "lse");
+    }
+    s.written = s.all;
+    s.add(a.x, a.T, a.H * 2, or_packed(a.ldx, a.H) * 2, "x");
+    s.add(a.w, w_rows, w_row, or_packed(a.ldw, row_of_w(a)) * 2, "w");
+    if (backward) {
+        s.add(a.lse, 1, t4, t4, "lse");
+        s.add(a.grad, 1, t4, t4, "grad");
+    }
+    if (a.kind == GEMM_LOSS_XENT) {
+        s.add(a.target, 1, a.T * 8, a.T * 8, "target");
+    } else {
+        const int64_t n = a.T * a.entries, size = a.teacher_type == GEMM_LOSS_FP32 ? 4 : 2;
+        s.add(a.teacher_index, 1, n * 8, n * 8, "teacher_index");
+        s.add(a.teacher_logits, 1, n * size, n * size, "teacher_logits");
+    }
+    return s;
+}
+
+int overlapping(const Block &a, const Block &b) {
+    return set_error(GEMM_ERR_INVALID, std::string(a.name) + " must not overlap " + b.name);
 }
 
 int check_args(const gemm_loss_args_t &a, bool backward) {
@@ -92,17 +135,12 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
     if (a.kind == GEMM_LOSS_XENT ? !a.target : !a.teacher_index || !a.teacher_logits)
         return bad("the loss's targets must be non-null");
     if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
-    if (!backward) {
-        if (!a.loss) return bad("loss must be non-null");
-        if (overlap(a.loss, a.T * 4, a.lse, a.T * 4)) return bad("loss and lse must not overlap");
-        return GEMM_OK;
-    }
-    if (!a.grad) return bad("grad must be non-null");
-    const int64_t xb = span_bytes(a.T, a.H, ldx, 2), wb = span_bytes(rows_of_w(a), row_of_w(a), ldw, 2);
-    const int64_t dxb = span_bytes(a.T, a.H, lddx, 2), dwb = span_bytes(rows_of_w(a), row_of_w(a), lddw, dw32 ? 4 : 2);
-    if (overlap(a.dx, dxb, a.x, xb) || overlap(a.dx, dxb, a.w, wb) || overlap(a.dw, dwb, a.x, xb) ||
-        overlap(a.dw, dwb, a.w, wb) || overlap(a.dx, dxb, a.dw, dwb))
-        return bad("dx and dw must not overlap x, w or each other");
+    if (!backward && !a.loss) return bad("loss must be non-null");
+    if (backward && !a.grad) return bad("grad must be non-null");
+    const Blocks s = blocks_of(a, backward);
+    for (int i = 0; i < s.written; ++i)
+        for (int j = i + 1; j < s.all; ++j)
+            if (overlap(s.b[i], s.b[j])) return overlapping(s.b[i], s.b[j]);
     return GEMM_OK;
 }
 
@@ -257,6 +295,10 @@ int begin(const gemm_loss_args_t &a, bool backward, Call *c) {
     if (a.workspace) {
         if ((int64_t)a.workspace_bytes < l.bytes)
             return set_error(GEMM_ERR_WORKSPACE, "caller workspace is smaller than plan.workspace_bytes (" + std::to_string(l.bytes) + ")");
+        const Blocks s = blocks_of(a, backward);
+        const Block ws{a.workspace, 1, l.bytes, l.bytes, "workspace"};
+        for (int i = 0; i < s.all; ++i)
+            if (overlap(ws, s.b[i])) return overlapping(ws, s.b[i]);
     } else if ((rc = dgw::library_workspace(l.bytes, c->stream, &c->ws, &c->lock)) != GEMM_OK) {
         return rc;
     }

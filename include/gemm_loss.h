@@ -31,6 +31,9 @@
  * at most 2^14, divided out of dx and dw), and accumulates dx and dw in fp32.
  * Every sum has a fixed order: the same call gives the same bits.
  *
+ * What a call writes (loss and lse; dx and dw; its workspace) must not overlap
+ * anything else that it takes; such calls are refused.
+ *
  * Streams, errors and the library workspace are as in gemm.h: calls are
  * asynchronous on args.stream (else the thread's gemm_set_stream; GEMM_NULL_STREAM:
  * HIP's null stream), return a
@@ -82,7 +85,7 @@ extern "C" {
  *   teacher_logits: device [T,K], packed, of teacher_type (DISTILL).
  *   temperature:    tau > 0 (DISTILL); tau^2 must be a finite fp32 above 0 too.
  *   loss:      device fp32 [T], written by gemm_loss_forward.
- *   lse:       device fp32 [T], written by gemm_loss_forward, read by gemm_loss_backward; must not overlap loss.
+ *   lse:       device fp32 [T], written by gemm_loss_forward, read by gemm_loss_backward.
  *   grad:      device fp32 [T], the gradient g of each row's loss (backward).
  *   dx:        device [T,H] of the operands' type, lddx as ldx; NULL: not computed.
  *   dw:        device, w's layout, of dw_type, lddw as ldw (fp32: a multiple of 4); NULL: not computed.
