@@ -67,7 +67,11 @@ struct Block {
 };
 
 bool overlap(const Block &a, const Block &b) {
-    return a.base && b.base && a.rows > 0 && b.rows > 0 && a.begin() < b.end() && b.begin() < a.end();
+    if (!a.base || !b.base || a.rows <= 0 || b.rows <= 0 || a.begin() >= b.end() || b.begin() >= a.end()) return false;
+    if (a.ld != b.ld || a.rows == 1 || b.rows == 1) return true;
+    // rows at one stride: each of a's begins `d` bytes behind where one of b's begins or would
+    const uintptr_t ld = (uintptr_t)a.ld, d = (a.begin() % ld + ld - b.begin() % ld) % ld;
+    return d < (uintptr_t)b.row || d + (uintptr_t)a.row > ld;
 }
 
 // The buffers of a call: first what it writes, then what it reads.

@@ -32,7 +32,8 @@
  * Every sum has a fixed order: the same call gives the same bits.
  *
  * What a call writes (loss and lse; dx and dw; its workspace) must not overlap
- * anything else that it takes; such calls are refused.
+ * anything else that it takes; such calls are refused.  (Rows of one matrix may lie
+ * between those of another at the same stride.)
  *
  * Streams, errors and the library workspace are as in gemm.h: calls are
  * asynchronous on args.stream (else the thread's gemm_set_stream; GEMM_NULL_STREAM:

@@ -101,3 +101,28 @@ def test_inputs_may_share_memory():
     a.grad = a.lse
     a.workspace_bytes = 0
     assert dg.gemm_loss_backward(a) == dg.GEMM_ERR_WORKSPACE, dg.gemm_last_error()
+
+
+def test_rows_that_lie_between_rows_do_not_overlap():
+    # x and dx as halves of one [T, 2H] buffer, w and dw of one [V, 3H]
+    import dense_gemm_work_amd as dg
+
+    def call(**kw):
+        a, _ = args(dg, 0, True)
+        a.ldx = a.lddx = 2 * H
+        a.ldw = a.lddw = 3 * H
+        a.dx, a.dw = a.x + 2 * H, a.w + 2 * 2 * H
+        a.workspace_bytes = 0
+        for k, v in kw.items():
+            setattr(a, k, v(a) if callable(v) else v)
+        return dg.gemm_loss_backward(a)
+
+    assert call() == dg.GEMM_ERR_WORKSPACE, dg.gemm_last_error()
+    assert call(dx=lambda a: a.x - 2 * H) == dg.GEMM_ERR_WORKSPACE, dg.gemm_last_error()
+    assert call(dw=lambda a: a.w + 2 * H + 3 * 2 * H * 5) == dg.GEMM_ERR_WORKSPACE, dg.gemm_last_error()
+    assert call(dx=lambda a: a.x + 2 * H - 16) == dg.GEMM_ERR_INVALID
+    assert call(dx=lambda a: a.x + 2 * H + 16) == dg.GEMM_ERR_INVALID
+    assert call(dw=lambda a: a.w + 2 * H - 16) == dg.GEMM_ERR_INVALID
+    assert call(dw=lambda a: a.w + 2 * 2 * H + 16) == dg.GEMM_ERR_INVALID
+    assert call(lddx=2 * H + 8) == dg.GEMM_ERR_INVALID                       # strides that drift apart
+    assert call(dw_type=dg.GEMM_LOSS_DW_FP32) == dg.GEMM_ERR_INVALID        # fp32 rows are twice as long
