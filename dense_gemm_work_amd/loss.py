@@ -9,7 +9,8 @@ distillation over the logits ``x . w^T``, which are never kept.
 The torch-facing functions take their workspace from torch's allocator on the
 call's stream (so calls on different streams, and graphs captured separately, do
 not share one), unless ``workspace`` is given.  They record nothing for autograd:
-the backward calls are the gradients.  With ``stream`` given, the inputs must be
+the backward calls are the gradients, and a forward call whose inputs require
+gradients while they are being recorded warns that its loss has none.  With ``stream`` given, the inputs must be
 ready on it and stay allocated until it has run the call (``record_stream`` on
 them says so to torch's allocator); results not given are allocated on it.
 """
@@ -18,6 +19,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import warnings
 
 from . import _check, _lib, layout_word, stream_word
 
@@ -145,6 +147,12 @@ def _product(x, w, b_layout):
     return a
 
 
+def _warn_of_no_graph(*inputs):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
+        warnings.warn("the loss is not recorded for autograd: its gradients come from the _backward call "
+                      "(pass detached tensors, or call under torch.no_grad())", stacklevel=3)
+
+
 def _xent(a, x, target, ignore_index, z_loss):
     a.kind = GEMM_LOSS_XENT
     a.target = _vector("target", target, (a.T,), torch.int64, x.device)
@@ -243,7 +251,7 @@ def linear_cross_entropy(x, w, target, *, b_layout: str = "nk", ignore_index: in
 
     ``loss[t] = lse[t] - logits[t, target[t]] + z_loss lse[t]^2``; rows whose
     target is ``ignore_index`` have loss 0.  Returns ``(loss, lse)``, fp32 [T];
-    ``lse`` is what the backward call needs.  A mean over the rows is
+    ``lse`` is what the backward call needs (neither is recorded for autograd).  A mean over the rows is
     ``loss.sum() / (target != ignore_index).sum()``, its backward call's ``grad``
     that divisor's inverse in every row.
     x [T,H], w: bf16 or fp16 on one device, rows contiguous at any stride that
@@ -252,6 +260,7 @@ def linear_cross_entropy(x, w, target, *, b_layout: str = "nk", ignore_index: in
     gradient is zero, and zero times infinity would be NaN in dw.  Enqueues on ``stream`` or torch's current stream;
     ``loss`` and ``lse`` may be given.
     """
+    _warn_of_no_graph(x, w)
     a = _product(x, w, b_layout)
     _xent(a, x, target, ignore_index, z_loss)
     return _forward(a, x, loss, lse, workspace, stream)
@@ -283,6 +292,7 @@ def linear_distill(x, w, teacher_index, teacher_logits, *, temperature: float = 
     have loss 0.  Returns ``(loss, lse)``, fp32 [T].  x, w and the rest as for
     ``linear_cross_entropy``.
     """
+    _warn_of_no_graph(x, w, teacher_logits)
     a = _product(x, w, b_layout)
     _distill(a, x, teacher_index, teacher_logits, temperature)
     return _forward(a, x, loss, lse, workspace, stream)
