@@ -430,11 +430,18 @@ int backward(const gemm_loss_args_t &a) {
     return GEMM_OK;
 }
 
-}  // namespace
+// No exception leaves a C call.  What can throw is the host's memory running out
+// (an error's text is allocated); this text is short enough not to be.
+template <class F>
+int guarded(F &&f) noexcept {
+    try {
+        return f();
+    } catch (...) {
+        return set_error(GEMM_ERR_WORKSPACE, "no host memory");
+    }
+}
 
-extern "C" {
-
-int gemm_loss_plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out) {
+int plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out) {
     dgw::clear_error();
     if (!args || !out) return bad("args and out must be non-null");
     if (num_cus < 1 || num_cus > MAX_CUS) return bad("num_cus must be 1 .. 65536");
@@ -460,14 +467,20 @@ int gemm_loss_plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_c
     return GEMM_OK;
 }
 
+}  // namespace
+
+extern "C" {
+
+int gemm_loss_plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out) {
+    return guarded([&] { return plan(args, backward, num_cus, out); });
+}
+
 int gemm_loss_forward(const gemm_loss_args_t *args) {
-    if (!args) return bad("args is null");
-    return forward(*args);
+    return guarded([&] { return args ? forward(*args) : bad("args is null"); });
 }
 
 int gemm_loss_backward(const gemm_loss_args_t *args) {
-    if (!args) return bad("args is null");
-    return backward(*args);
+    return guarded([&] { return args ? backward(*args) : bad("args is null"); });
 }
 
 }  // extern "C"

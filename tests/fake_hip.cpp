@@ -12,6 +12,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <new>
 #include <string>
 #include <thread>
 #include <vector>
@@ -21,6 +22,16 @@
 struct Dim {
     uint32_t x, y, z;
 };
+
+thread_local bool no_memory = false;   // operator new of this thread fails
+
+void *operator new(size_t n) {
+    void *p = no_memory ? nullptr : std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, size_t) noexcept { std::free(p); }
 
 namespace {
 
@@ -251,10 +262,35 @@ int streams() {
     return 0;
 }
 
+int no_exceptions() {
+    // without host memory for its message a refused call still returns, to C callers too
+    gemm_loss_args_t a = backward_args();
+    gemm_loss_plan_t plan;
+    a.temperature = -1.0f;
+    a.H = 36;
+    int rc[3] = {1, 1, 1};
+    try {
+        no_memory = true;
+        rc[0] = gemm_loss_forward(&a);
+        rc[1] = gemm_loss_backward(&a);
+        rc[2] = gemm_loss_plan(&a, 1, 256, &plan);
+        no_memory = false;
+    } catch (...) {
+        no_memory = false;
+        std::puts("an exception left a C call");
+        return 1;
+    }
+    for (int r : rc) REQUIRE(r < 0);
+    REQUIRE(std::strlen(gemm_last_error()) > 0);
+    a = backward_args();
+    REQUIRE(gemm_loss_forward(&a) == GEMM_OK && gemm_loss_backward(&a) == GEMM_OK);
+    return 0;
+}
+
 }  // namespace
 
 int main(int argc, char **argv) {
-    const std::map<std::string, int (*)()> scenarios = {{"release", release}, {"two_threads", two_threads}, {"streams", streams}};
+    const std::map<std::string, int (*)()> scenarios = {{"release", release}, {"two_threads", two_threads}, {"streams", streams}, {"no_exceptions", no_exceptions}};
     const auto s = scenarios.find(argc > 1 ? argv[1] : "");
     if (s == scenarios.end()) return 2;
     const int rc = s->second();

@@ -32,7 +32,7 @@ def test_torchs_default_stream_is_named_as_such():
     assert dg.stream_word(Stream) == 0x5000
 
 
-@pytest.mark.parametrize("scenario", ["release", "two_threads", "streams"])
+@pytest.mark.parametrize("scenario", ["release", "two_threads", "streams", "no_exceptions"])
 def test_calls(program, scenario):
     res = subprocess.run([str(program), scenario], capture_output=True, text=True, timeout=60)
     assert res.returncode == 0 and res.stdout.split() == ["ok"], res.stdout + res.stderr
