@@ -28,7 +28,9 @@
  * Arithmetic: logits, maxima, sums of exponentials and losses in fp32.  The
  * backward pass computes the logits again, rounds dz to the operands' type once
  * (fp16: after scaling by a power of two that brings the largest row factor to
- * at most 2^14, divided out of dx and dw), and accumulates dx and dw in fp32.
+ * at most 2^14, divided out of dx and dw: besides its rounding an entry of any row
+ * is off by at most 2^-38 of the call's largest factor), and accumulates dx and dw
+ * in fp32.
  * Every sum has a fixed order: the same call gives the same bits.
  *
  * What a call writes (loss and lse; dx and dw; its workspace) must not overlap
