@@ -25,7 +25,11 @@ struct LossMatrix {
     int64_t ld;
     int rows;
     bool kc;
+    int64_t part = 0;   // elements from the first 16-bit part to the second (0: one part)
 };
+
+// Up to this many rows dz is the sum of two 16-bit parts.
+constexpr int LOSS_FEW = 64;
 
 // The rows' sparse targets as the logits' epilogues read them.  XENT: the int64
 // target itself, weight 1.  DISTILL: a row's entries {index, probability} sorted
@@ -69,9 +73,10 @@ struct LossProblem {
 hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const LossStats &s, hipStream_t stream);
 
 // Logits again, as their gradient dz [T][ldd] (16 bits; ldd a multiple of 8,
-// zeros behind p.V), times *scale when scale != nullptr.
+// zeros behind p.V), times *scale when scale != nullptr.  The tiles of at most
+// LOSS_FEW rows write what the rounding left out, rounded too, `part` elements on.
 hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz,
-                          int64_t ldd, hipStream_t stream);
+                          int64_t ldd, int64_t part, hipStream_t stream);
 
 // out[q][p] = sum_k P[p][k] Q[q][k], times *unscale when unscale != nullptr.
 enum LossOut : int {
@@ -90,10 +95,12 @@ struct LossProduct {
     int64_t ldo;
     const float *unscale;   // not applied to slots
 };
+// The tiles of at most LOSS_FEW rows take a Q of two parts, the others one of one.
 hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStream_t stream);
 
-// The same for K <= 64 (one slab), both operands' rows contiguous and LO_16, on at
-// most about `workgroups` persistent workgroups (the splits and slots do not apply).
+// The same for K <= LOSS_FEW (one slab), both operands' rows contiguous and one of
+// them of two parts, on at most about `workgroups` persistent workgroups (the splits
+// and slots do not apply).
 hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream);
 
 // out from the slots of `splits` slices: out_kind LO_16, LO_F32 or LO_F32_ADD.

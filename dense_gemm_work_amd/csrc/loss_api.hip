@@ -153,7 +153,7 @@ struct Layout {
     int64_t entries = 0, starts = 0, entropy = 0;  // the teacher's entries
     int64_t stats = 0;                            // forward
     int64_t scale = 0, dz = 0, dx = 0, dw = 0;    // backward
-    int64_t ldd = 0;
+    int64_t ldd = 0, part = 0;                     // dz's rows, and from its first part to its second, in elements
     int64_t bytes = 0;
     int64_t take(int64_t n) {
         const int64_t at = bytes;
@@ -226,7 +226,7 @@ struct Plan {
     int logits = dgw::LT_128x128, dx = dgw::LT_128x128, dw = dgw::LT_128x128;   // tiles
     int64_t piece = 0;
     int pieces = 0, dx_splits = 1, dw_splits = 1;
-    bool dw_outer = false;   // dw by the kernel of at most 64 rows
+    bool dw_outer = false;   // dw by the kernel of few rows
     Layout at;
 };
 
@@ -243,11 +243,17 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
         l.stats = l.take(3 * ceil_div(a.V, dgw::loss_tile_shape(p.logits).p) * a.T * 4);
         return p;
     }
-    p.piece = std::min(round_up(a.V, 64), std::max<int64_t>(1024, PIECE_BYTES / 2 / std::max<int64_t>(a.T, 1) / 1024 * 1024));
+    const int64_t rows = std::max<int64_t>(a.T, 1), parts = a.T <= dgw::LOSS_FEW ? 2 : 1;   // of dz
+    p.piece = std::min(round_up(a.V, 64), std::max<int64_t>(1024, PIECE_BYTES / (2 * parts) / rows / 1024 * 1024));
+    // dw alone: dz is most of the workspace, and pieces cost it only launches.  Its
+    // second part stays within the 4 (T + 256)(H + 256) bytes that a slice of dx takes at
+    // most (64 x 50001 x 2048: pieces of 22528 entries, 110 us; T = 20: one piece, 80 us).
+    if (parts == 2 && !a.dx) p.piece = std::min(p.piece, std::max<int64_t>(1024, 2 * (rows + 256) * (a.H + 256) / rows / 1024 * 1024));
     p.pieces = (int)ceil_div(a.V, p.piece);
     l.ldd = p.piece;
     l.scale = l.take(8);
-    l.dz = l.take(a.T * l.ldd * 2);
+    l.dz = l.take(a.T * l.ldd * 2 * parts);
+    l.part = parts == 2 ? a.T * l.ldd : 0;
     const int64_t first = std::min(a.V, p.piece);
     p.logits = logits_tile(a, first, cus);
     if (a.dx) {
@@ -259,10 +265,12 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
     if (a.dw) {
         const bool nk = (a.layout & 0xFu) == GEMM_B_NK;
         const int64_t rp = nk ? a.H : first, rq = nk ? first : a.H;
-        const Choice c = choose(rp, rq, a.T, true, cus);
-        p.dw = c.tile;
-        p.dw_splits = c.splits;
-        p.dw_outer = a.T <= 64 && a.dw_type == GEMM_LOSS_DW_SAME;
+        p.dw_outer = parts == 2;
+        if (!p.dw_outer) {
+            const Choice c = choose(rp, rq, a.T, true, cus);
+            p.dw = c.tile;
+            p.dw_splits = c.splits;
+        }
         if (p.dw_splits > 1) l.dw = l.take(dgw::loss_slots_bytes(p.dw, rp, rq, p.dw_splits));
     }
     return p;
@@ -379,11 +387,11 @@ int backward(const gemm_loss_args_t &a) {
     for (int i = 0; i < pl.pieces; ++i) {
         const int64_t v0 = i * pl.piece, n = std::min(pl.piece, a.V - v0);
         const dgw::LossProblem p = problem(a, c, v0, n);
-        if ((e = dgw::launch_loss_dz(c.dtype, pl.logits, p, rows, scale, dz, pl.at.ldd, c.stream)) != hipSuccess)
+        if ((e = dgw::launch_loss_dz(c.dtype, pl.logits, p, rows, scale, dz, pl.at.ldd, pl.at.part, c.stream)) != hipSuccess)
             return set_hip_error(e, "launch the logits' gradient");
         if (a.dx) {   // dx[t][h] += sum_v w[v][h] dz[t][v]
             px.P = {p.w.base, ldw, (int)a.H, !c.nk};
-            px.Q = {dz, pl.at.ldd, (int)a.T, true};
+            px.Q = {dz, pl.at.ldd, (int)a.T, true, pl.at.part};
             px.K = (int)n;
             px.splits = pl.dx_splits;
             px.unscale = unscale;
@@ -398,7 +406,7 @@ int backward(const gemm_loss_args_t &a) {
         }
         if (a.dw) {   // dw[v][h] = sum_t x[t][h] dz[t][v], as stored
             const dgw::LossMatrix mx{static_cast<const uint16_t *>(a.x), or_packed(a.ldx, a.H), (int)a.H, false};
-            const dgw::LossMatrix mz{dz, pl.at.ldd, (int)n, false};
+            const dgw::LossMatrix mz{dz, pl.at.ldd, (int)n, false, pl.at.part};
             dgw::LossProduct q;
             q.P = c.nk ? mx : mz;
             q.Q = c.nk ? mz : mx;

@@ -224,6 +224,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
 }
 
+// v less its rounding to the type.
+template <int DT>
+__device__ __forceinline__ float remainder16(float v) {
+    if constexpr (DT == 0) return v - (float)(__bf16)v;
+    else return v - (float)(_Float16)v;
+}
+
 // The LDS must be free.  Chunks at or beyond cols8 (a multiple of 8) and rows at
 // or beyond rows_q are not stored.
 template <int DT, bool NT, class L>
@@ -288,10 +295,16 @@ __device__ __forceinline__ RowFactors row_factors(const LossRows &p, int64_t row
 // The logits' gradient of one tile: dz = a p - b q, p = exp(z / tau - lse).  lse is
 // subtracted before the factor log2 e: at a sure row's target z / tau = lse, p = 1 and
 // dz = 0.  (z c - round(lse log2 e) left up to 1e-5 there at logits of 250.)
+// dz is rounded to the operands' type, the matrix instructions' input: with many rows
+// dx and dw are then off by 0.0024 (bf16) or 0.0003 (fp16) of their size, rounded
+// themselves 0.0017 or 0.0002; a second part would cost each of their products
+// twice.  A row's gradient is mostly its target's entry, so with few rows nothing
+// averages (0.0042 at two rows), and there the streams of w and dw are the time: the
+// tiles of at most LOSS_FEW rows write the remainder too.
 // ---------------------------------------------------------------------------
 template <int DT, class L>
 __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, LossRows rows, const float *scale, uint16_t *dz,
-                                                 int64_t ldd) {
+                                                 int64_t ldd, int64_t part) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     int tp, tq, split;
     place(p.g, tp, tq, split);
@@ -336,6 +349,16 @@ __global__ __launch_bounds__(L::NT, 2) void loss_dz(LogitParams p, LossRows rows
     }
     __syncthreads();   // the lanes' arrays give way to the packed tile
     store16<DT, false>(loop, acc, lds, dz, ldd, p0, q0, ldd, p.T);
+    if constexpr (L::TQ <= LOSS_FEW) {
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < L::CB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc.v[i][j][e] = remainder16<DT>(acc.v[i][j][e]);
+        __syncthreads();
+        store16<DT, false>(loop, acc, lds, dz + part, ldd, p0, q0, ldd, p.T);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -360,7 +383,7 @@ __device__ __forceinline__ f32x4 *slot_base(float *slots, const Grid &g, int tp,
 }
 
 template <int DT, class L>
-__global__ __launch_bounds__(L::NT, 2) void loss_product(ProductParams p) {
+__global__ __launch_bounds__(L::NT, L::WAVES) void loss_product(ProductParams p) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     int tp, tq, split;
     place(p.g, tp, tq, split);
@@ -413,12 +436,19 @@ __global__ __launch_bounds__(L::NT, 2) void loss_product(ProductParams p) {
 // slab is on its way while this one is multiplied, and a tile's stores while the
 // next is.  64 x 50001 x 2048: 49 us with a workgroup per tile (each waits out its
 // slab's latency alone), 39 us this way (5.3 TB/s written).
+// One operand is dz in two parts.  As P both lie in registers; as Q they take two of
+// three places in LDS, so that two workgroups still fit a CU: the next tile's first
+// part goes into the third while this tile is multiplied, its second part into the
+// place that this tile's first part leaves.
 // ---------------------------------------------------------------------------
-template <int DT>
+template <int DT, int KIND, bool PARTS_P>
 __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
     using Op = Operand<false, 128, 4>;
-    constexpr int OUT = 128 * 128 * 2, CH = 16, STORES = 8;   // result tile bytes; chunks a row; stores a thread
-    __shared__ __attribute__((aligned(16))) char lds[OUT + 2 * Op::SLAB];
+    constexpr int PP = PARTS_P ? 2 : 1, PQ = 3 - PP;                    // parts of P and Q
+    constexpr int OUT = 128 * 128 * 2, CH = 16;                         // packed result tile in bytes; chunks a row
+    constexpr int STORES = KIND == LO_16 ? 8 : 16;                      // per thread
+    __shared__ __attribute__((aligned(16))) char lds[OUT + (PQ + 1) * Op::SLAB];
+    static_assert(PP * Op::SLAB <= OUT, "P's slabs borrow the result's place");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wp = wave & 1, wq = wave >> 1;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
@@ -426,81 +456,127 @@ __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
     const int tp = (int)blockIdx.x % p.g.tiles_p, step = (int)gridDim.x / p.g.tiles_p;
     int tq = (int)blockIdx.x / p.g.tiles_p;
     const int64_t p0 = (int64_t)tp * 128;
-    auto load = [&](const Matrix &m, int64_t row0, uint32_t dst) {
+    auto load = [&](const Matrix &m, int part, int64_t row0, uint32_t dst) {
         Op o;
         o.init(m, row0, p.K, wave, lane);
-        const i32x4 r = o.rsrc(0);
+        const i32x4 r = o.rsrc(0, part * 2 * m.part);
 #pragma unroll
         for (int x = 0; x < Op::LOADS; ++x) o.template load<false>(r, 0, x, dst + wave * Op::LOADS * 1024);
     };
-    load(p.P, p0, lds0);   // P's slab borrows the result's place
-    load(p.Q, (int64_t)tq * 128, lds0 + OUT);
+    uint32_t place[PQ], spare = lds0 + OUT + PQ * Op::SLAB;             // of this tile's parts of Q; free
+#pragma unroll
+    for (int x = 0; x < PP; ++x) load(p.P, x, p0, lds0 + x * Op::SLAB);
+#pragma unroll
+    for (int x = 0; x < PQ; ++x) load(p.Q, x, (int64_t)tq * 128, place[x] = lds0 + OUT + x * Op::SLAB);
     wait_vm_lgkm<0>();
     barrier();
-    u32x4 pf[2][4];
+    u32x4 pf[PP][2][4];
 #pragma unroll
-    for (int st = 0; st < 2; ++st)
+    for (int x = 0; x < PP; ++x)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pf[st][i] = Op::fragment(Op::address(lds0, wp * 64, lane, i) + Op::constant(0, st));
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pf[x][st][i] = Op::fragment(Op::address(lds0, wp * 64, lane, i) + x * Op::SLAB + Op::constant(0, st));
     uint32_t qa[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) qa[j] = Op::address(lds0 + OUT, wq * 64, lane, j);
+    for (int j = 0; j < 4; ++j) qa[j] = Op::address(0, wq * 64, lane, j);
     wait_vm_lgkm<0>();   // P's fragments are in registers before its place is written
     const float u = p.unscale ? *p.unscale : 1.0f;
     const int cols = (int)min((int64_t)128, ((p.P.rows + 7) & ~7) - p0);
     bool first = true;
-    for (int buf = 0; tq < p.g.tiles_q; tq += step, buf ^= 1) {
+    for (; tq < p.g.tiles_q; tq += step) {
         const int64_t q0 = (int64_t)tq * 128;
-        // This tile's slab is older than the last tile's stores, every one of which
+        const bool more = tq + step < p.g.tiles_q;
+        // This tile's slabs are older than the last tile's stores, every one of which
         // is issued whether it is inside the result or not.  After the barrier the
-        // other buffer and the result's place are free.
+        // spare place and the result's are free.
         __builtin_amdgcn_sched_barrier(0);
         if (first) wait_vm_lgkm<0>();
         else wait_vm_lgkm<STORES>();
         first = false;
         barrier();
         __builtin_amdgcn_sched_barrier(0);
-        if (tq + step < p.g.tiles_q) load(p.Q, q0 + (int64_t)step * 128, lds0 + OUT + (buf ^ 1) * Op::SLAB);
+        if (more) load(p.Q, 0, q0 + (int64_t)step * 128, spare);
         f32x4 acc[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            u32x4 qf[4];
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) qf[j] = Op::fragment(qa[j] + buf * Op::SLAB + Op::constant(0, st));
+            for (int y = PQ - 1; y >= 0; --y) {
+                u32x4 qf[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < 4; ++j) qf[j] = Op::fragment(place[y] + qa[j] + Op::constant(0, st));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = mfma<DT>(pf[st][i], qf[j], acc[i][j]);
-        }
-        // the packed tile, 16-byte chunk c of row r at c ^ r
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = wq * 64 + j * 16 + (lane & 15);
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = wp * 64 + i * 16 + 4 * (lane >> 4);
-                *reinterpret_cast<u32x2 *>(lds + r * 256 + (((c >> 3) ^ (r & (CH - 1))) << 4) + (c & 4) * 2) =
-                    u32x2{pack2<DT>(acc[i][j][0] * u, acc[i][j][1] * u), pack2<DT>(acc[i][j][2] * u, acc[i][j][3] * u)};
+                        for (int x = PP - 1; x >= 0; --x) acc[i][j] = mfma<DT>(pf[x][st][i], qf[j], acc[i][j]);
+            }
+        if constexpr (KIND == LO_16) {
+            // the packed tile, 16-byte chunk c of row r at c ^ r
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = wq * 64 + j * 16 + (lane & 15);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = wp * 64 + i * 16 + 4 * (lane >> 4);
+                    *reinterpret_cast<u32x2 *>(lds + r * 256 + (((c >> 3) ^ (r & (CH - 1))) << 4) + (c & 4) * 2) =
+                        u32x2{pack2<DT>(acc[i][j][0] * u, acc[i][j][1] * u), pack2<DT>(acc[i][j][2] * u, acc[i][j][3] * u)};
+                }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4));   // this wave's LDS writes; its loads go on
-        barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        const int rows = (int)min((int64_t)128, p.Q.rows - q0);
-        const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
-            static_cast<uint16_t *>(p.out) + q0 * p.ldo + p0, (short)0, (int)(((rows - 1) * p.ldo + cols) * 2), (int)RSRC_DW3);
-#pragma unroll
-        for (int x = 0; x < STORES; ++x) {
-            const int f = threadIdx.x + 256 * x, r = f / CH, c = f % CH;
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * 256 + ((c ^ (r & (CH - 1))) << 4));
-            const uint32_t off = r < rows && 8 * c < cols ? (uint32_t)(r * p.ldo + 8 * c) * 2 : OOB;
-            __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)off, 0, 2);   // non-temporal
+        if constexpr (KIND == LO_16 || PQ == 2) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4));   // this wave's LDS operations; its loads go on
+            barrier();
+            __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (PQ == 2) {
+            if (more) load(p.Q, 1, q0 + (int64_t)step * 128, place[0]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        const int rows = (int)min((int64_t)128, p.Q.rows - q0);
+        if constexpr (KIND == LO_16) {
+            const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+                static_cast<uint16_t *>(p.out) + q0 * p.ldo + p0, (short)0, (int)(((rows - 1) * p.ldo + cols) * 2), (int)RSRC_DW3);
+#pragma unroll
+            for (int x = 0; x < STORES; ++x) {
+                const int f = threadIdx.x + 256 * x, r = f / CH, c = f % CH;
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * 256 + ((c ^ (r & (CH - 1))) << 4));
+                const uint32_t off = r < rows && 8 * c < cols ? (uint32_t)(r * p.ldo + 8 * c) * 2 : OOB;
+                __builtin_amdgcn_raw_buffer_store_b128(v, out, (int)off, 0, 2);   // non-temporal
+            }
+        } else {   // four consecutive floats a lane; fp32 written through the caches (117 against 139 us for 64 x 32000 x 2048)
+            const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+                static_cast<float *>(p.out) + q0 * p.ldo + p0, (short)0, (int)(((rows - 1) * p.ldo + cols) * 4), (int)RSRC_DW3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = wq * 64 + j * 16 + (lane & 15);
+                uint32_t off[4];
+                u32x4 old[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = wp * 64 + i * 16 + 4 * (lane >> 4);
+                    off[i] = r < rows && c < cols ? (uint32_t)(r * p.ldo + c) * 4 : OOB;
+                    if constexpr (KIND == LO_F32_ADD) old[i] = __builtin_amdgcn_raw_buffer_load_b128(out, (int)off[i], 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4 v = acc[i][j] * u;
+                    if constexpr (KIND == LO_F32_ADD) v += __builtin_bit_cast(f32x4, old[i]);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), out, (int)off[i], 0, 0);
+                }
+            }
+        }
+        const uint32_t left = place[PQ - 1];   // the next tile's parts: in the spare place, and in the first one's
+        if constexpr (PQ == 2) place[1] = place[0];
+        place[0] = spare;
+        spare = left;
     }
 }
 
@@ -773,14 +849,15 @@ template <int DT, bool PK, bool QK, bool LOGITS>
 struct LoopOf<LT_256x256, DT, PK, QK, LOGITS> {
     using type = Loop<DT, PK, QK, 256, 256, 2, 4, PK || QK ? 3 : 2, 2>;
 };
-// Few rows: ThinLoop tiles, several workgroups a CU (48 to 80 KiB of LDS).
+// Few rows: ThinLoop tiles, several workgroups a CU for logits (48 to 80 KiB of LDS);
+// dx, whose Q is dz in two parts, runs one a CU (96 KiB).
 template <int DT, bool PK, bool QK, bool LOGITS>
 struct LoopOf<LT_32x32, DT, PK, QK, LOGITS> {
     using type = ThinLoop<DT, PK, QK, 32, 32, 6>;
 };
 template <int DT, bool PK, bool QK, bool LOGITS>
 struct LoopOf<LT_128x32, DT, PK, QK, LOGITS> {
-    using type = ThinLoop<DT, PK, QK, 128, 32, 4>;
+    using type = ThinLoop<DT, PK, QK, 128, 32, 4, LOGITS ? 1 : 2>;
 };
 template <int DT, bool PK, bool QK, bool LOGITS>
 struct LoopOf<LT_64x64, DT, PK, QK, LOGITS> {
@@ -792,17 +869,18 @@ struct LoopOf<LT_64x128, DT, PK, QK, LOGITS> {
 };
 template <int DT, bool PK, bool QK, bool LOGITS>
 struct LoopOf<LT_128x64, DT, PK, QK, LOGITS> {
-    using type = ThinLoop<DT, PK, QK, 128, 64, 3>;
+    using type = ThinLoop<DT, PK, QK, 128, 64, 3, LOGITS ? 1 : 2>;
 };
 template <int DT>
 using Loop128 = typename LoopOf<LT_128x128, DT, false, false>::type;
+bool few_rows(int tile) { return loss_tile_shape(tile).q <= LOSS_FEW; }
 template <class L_, int DT_>
 struct Choice {
     using L = L_;
     static constexpr int DT = DT_;
 };
 
-Matrix matrix(const LossMatrix &m) { return Matrix{m.base, m.ld, m.rows}; }
+Matrix matrix(const LossMatrix &m) { return Matrix{m.base, m.ld, m.rows, m.part}; }
 
 template <class L>
 Grid grid_of(int64_t rows_p, int64_t rows_q, int K, int splits) {
@@ -839,9 +917,10 @@ hipError_t run_stats(const LossProblem &p, const LossStats &s, hipStream_t strea
     return hipGetLastError();
 }
 template <int DT, class L>
-hipError_t run_dz(const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz, int64_t ldd, hipStream_t stream) {
+hipError_t run_dz(const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz, int64_t ldd, int64_t part,
+                  hipStream_t stream) {
     const LogitParams q = logit_params<L>(p);
-    hipLaunchKernelGGL((loss_dz<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q, rows, scale, dz, ldd);
+    hipLaunchKernelGGL((loss_dz<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q, rows, scale, dz, ldd, part);
     return hipGetLastError();
 }
 template <class L>
@@ -887,7 +966,7 @@ static hipError_t with_type(int dtype, F &&f) {
 }
 template <bool PK, bool QK, bool LOGITS = false, class F>
 static hipError_t with_tile(int dtype, int tile, F &&f) {
-    if constexpr (PK && QK) {   // their P slabs are too narrow for k-rows
+    if constexpr (PK && QK && LOGITS) {   // their P slabs are too narrow for k-rows
         if (tile == LT_32x32) return with_type<LT_32x32, PK, QK, LOGITS>(dtype, f);
         if (tile == LT_64x64) return with_type<LT_64x64, PK, QK, LOGITS>(dtype, f);
         if (tile == LT_64x128) return with_type<LT_64x128, PK, QK, LOGITS>(dtype, f);
@@ -910,12 +989,12 @@ hipError_t launch_loss_stats(int dtype, int tile, const LossProblem &p, const Lo
 }
 
 hipError_t launch_loss_dz(int dtype, int tile, const LossProblem &p, const LossRows &rows, const float *scale, uint16_t *dz,
-                          int64_t ldd, hipStream_t stream) {
+                          int64_t ldd, int64_t part, hipStream_t stream) {
     auto run = [&](auto c) {
         using C = decltype(c);
-        return run_dz<C::DT, typename C::L>(p, rows, scale, dz, ldd, stream);
+        return run_dz<C::DT, typename C::L>(p, rows, scale, dz, ldd, part, stream);
     };
-    if (!p.x.kc) return hipErrorInvalidValue;
+    if (!p.x.kc || few_rows(tile) != (part > 0)) return hipErrorInvalidValue;
     return p.w.kc ? with_tile<true, true, true>(dtype, tile, run) : with_tile<false, true, true>(dtype, tile, run);
 }
 
@@ -924,17 +1003,26 @@ hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStr
         using C = decltype(c);
         return run_product<C::DT, typename C::L>(p, stream);
     };
+    if (few_rows(tile) != (p.Q.part > 0) || p.P.part) return hipErrorInvalidValue;
     if (p.Q.kc) return p.P.kc ? with_tile<true, true>(dtype, tile, run) : with_tile<false, true>(dtype, tile, run);
     return p.P.kc ? hipErrorInvalidValue : with_tile<false, false>(dtype, tile, run);
 }
 
-hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream) {
-    if (p.P.kc || p.Q.kc || p.K > KB || p.out_kind != LO_16) return hipErrorInvalidValue;
-    ProductParams q = product_params<Loop128<0>>(p);
-    const int grid = std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;   // tiles_p < 2^14
-    if (dtype == 0) hipLaunchKernelGGL(loss_outer<0>, dim3(grid), dim3(256), 0, stream, q);
-    else hipLaunchKernelGGL(loss_outer<1>, dim3(grid), dim3(256), 0, stream, q);
+template <int DT, bool PARTS_P>
+static hipError_t run_outer(const ProductParams &q, int grid, hipStream_t stream) {
+    if (q.out_kind == LO_16) hipLaunchKernelGGL((loss_outer<DT, LO_16, PARTS_P>), dim3(grid), dim3(256), 0, stream, q);
+    else if (q.out_kind == LO_F32) hipLaunchKernelGGL((loss_outer<DT, LO_F32, PARTS_P>), dim3(grid), dim3(256), 0, stream, q);
+    else hipLaunchKernelGGL((loss_outer<DT, LO_F32_ADD, PARTS_P>), dim3(grid), dim3(256), 0, stream, q);
     return hipGetLastError();
+}
+
+hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream) {
+    if (p.P.kc || p.Q.kc || p.K > LOSS_FEW || p.out_kind > LO_F32_ADD || (p.P.part > 0) == (p.Q.part > 0)) return hipErrorInvalidValue;
+    static_assert(LOSS_FEW <= KB, "one slab of k");
+    const ProductParams q = product_params<Loop128<0>>(p);
+    const int grid = std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;   // tiles_p < 2^14
+    if (p.P.part) return dtype == 0 ? run_outer<0, true>(q, grid, stream) : run_outer<1, true>(q, grid, stream);
+    return dtype == 0 ? run_outer<0, false>(q, grid, stream) : run_outer<1, false>(q, grid, stream);
 }
 
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream) {

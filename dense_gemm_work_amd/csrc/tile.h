@@ -127,10 +127,13 @@ __device__ __forceinline__ u32x2 lds_tr16(uint32_t addr) {
 // base[row * ld + k] (KC) or base[k * ld + row] (RC), `rows` of them.  KC rows
 // are read in chunks of 8 k, RC k-rows in chunks of 8 rows: k (KC) or rows (RC)
 // rounded up to 8 must lie inside ld, and what lies there beyond k must be zero.
+// A matrix may be the sum of two 16-bit parts, the second `part` elements behind
+// the first; the loops that take such operands say so.
 struct Matrix {
     const uint16_t *base;
     int64_t ld;
     int rows;
+    int64_t part;
 };
 
 // One operand's slabs: R rows by 64 k, moved by NW waves.
@@ -178,14 +181,14 @@ struct Operand {
         }
     }
 
-    // Buffer of slab `slab`.
-    __device__ __forceinline__ i32x4 rsrc(int slab) const {
+    // Buffer of slab `slab`, `shift` bytes on.
+    __device__ __forceinline__ i32x4 rsrc(int slab, int64_t shift = 0) const {
         const int64_t kb = (int64_t)slab * KB;
-        if constexpr (KC) return make_rsrc(base + kb * 2, range - (uint32_t)kb * 2);
+        if constexpr (KC) return make_rsrc(base + shift + kb * 2, range - (uint32_t)kb * 2);
         // the range stops behind the last k-row's last chunk: width <= ld, so every
         // k-row beyond K starts outside it and reads zeros
         const int krows = (int)min((int64_t)KB, K - kb);
-        return make_rsrc(base + kb * ld * 2, (uint32_t)(((int64_t)(krows - 1) * ld + width) * 2));
+        return make_rsrc(base + shift + kb * ld * 2, (uint32_t)(((int64_t)(krows - 1) * ld + width) * 2));
     }
     template <bool RAGGED>
     __device__ __forceinline__ void load(i32x4 r, int slab, int x, uint32_t dst) const {
@@ -252,7 +255,7 @@ __device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &spli
 template <int DT, bool PK, bool QK, int TP_, int TQ_, int WP_, int WQ_, int NSP_, int NSQ_>
 struct Loop {
     static constexpr int TP = TP_, TQ = TQ_, WP = WP_, WQ = WQ_, NSP = NSP_, NSQ = NSQ_;
-    static constexpr int NW = WP * WQ, NT = 64 * NW;
+    static constexpr int NW = WP * WQ, NT = 64 * NW, WAVES = 2;   // waves resident per SIMD
     static constexpr int WAVE_P = TP / WP, WAVE_Q = TQ / WQ;
     static constexpr int RB = WAVE_P / 16, CB = WAVE_Q / 16;   // 16 x 16 blocks of a wave
     static constexpr int HB = RB / 2;                          // P blocks of half a step
@@ -447,8 +450,9 @@ struct Loop {
 // flight per CU.  After the loop the two waves of a half swap sums through LDS:
 // each then owns half of their blocks (of a 32-row tile, which has one block a
 // half, the wave of step 0 owns it and the other nothing), and the members below
-// describe that state, as Loop's do.
-template <int DT, bool PK, bool QK, int TP_, int TQ_, int NS_>
+// describe that state, as Loop's do.  PARTS = 2: Q is the sum of two parts, both
+// staged and multiplied with the same fragments of P.
+template <int DT, bool PK, bool QK, int TP_, int TQ_, int NS_, int PARTS = 1>
 struct ThinLoop {
     static constexpr int TP = TP_, TQ = TQ_, NS = NS_;
     static constexpr int NW = 4, NT = 256;
@@ -457,9 +461,9 @@ struct ThinLoop {
     static constexpr int WAVE_P = 16 * RB, WAVE_Q = TQ, WP = TP / WAVE_P, WQ = 1;
     using OpP = Operand<PK, TP, NW>;
     using OpQ = Operand<QK, TQ, NW>;
-    static constexpr int LOADS = OpP::LOADS + OpQ::LOADS;
-    static constexpr int STAGE = OpP::SLAB + OpQ::SLAB;
-    static constexpr int LDS_BYTES = NS * STAGE;
+    static constexpr int LOADS = OpP::LOADS + PARTS * OpQ::LOADS;
+    static constexpr int STAGE = OpP::SLAB + PARTS * OpQ::SLAB;
+    static constexpr int LDS_BYTES = NS * STAGE, WAVES = 2 * LDS_BYTES <= 160 * 1024 ? 2 : 1;
     static constexpr int PA = PK ? 1 : PB, QA = QK ? 1 : CB;
     static_assert(PB == 1 || PB == 2 || PB == 4, "32, 64 or 128 rows of P");
     static_assert(NS >= 2 && NS <= 8 && (NS - 1) * LOADS < 64, "the wait counter holds the loads in flight");
@@ -474,6 +478,7 @@ struct ThinLoop {
     char *lds_;
     OpP P;
     OpQ Q;
+    int64_t qpart;   // bytes from Q's first part to its second
     uint32_t pa[PA], qa[QA];
 
     __device__ __forceinline__ ThinLoop(char *lds) : lds_(lds) {
@@ -499,24 +504,31 @@ struct ThinLoop {
     }
 
     struct Frags {
-        u32x4 p[PB], q[CB];
+        u32x4 p[PB], q[PARTS][CB];
     };
     __device__ __forceinline__ void read(Frags &f, int st) const {
         const uint32_t o = st * STAGE;
 #pragma unroll
         for (int i = 0; i < PB; ++i) f.p[i] = OpP::fragment(pa[PK ? 0 : i] + o + (PK ? OpP::constant(i, 0) : 0));
 #pragma unroll
-        for (int j = 0; j < CB; ++j) f.q[j] = OpQ::fragment(qa[QK ? 0 : j] + o + (QK ? OpQ::constant(j, 0) : 0));
+        for (int x = 0; x < PARTS; ++x)
+#pragma unroll
+            for (int j = 0; j < CB; ++j)
+                f.q[x][j] = OpQ::fragment(qa[QK ? 0 : j] + o + x * OpQ::SLAB + (QK ? OpQ::constant(j, 0) : 0));
     }
     template <bool RAGGED>
     __device__ __forceinline__ void load_all(int slab, int st) const {
-        const i32x4 rp = P.rsrc(slab), rq = Q.rsrc(slab);
+        const i32x4 rp = P.rsrc(slab);
         const uint32_t dp = lds0 + st * STAGE + wave * OpP::LOADS * 1024;
         const uint32_t dq = lds0 + st * STAGE + OpP::SLAB + wave * OpQ::LOADS * 1024;
 #pragma unroll
         for (int x = 0; x < OpP::LOADS; ++x) P.template load<RAGGED>(rp, slab, x, dp);
 #pragma unroll
-        for (int x = 0; x < OpQ::LOADS; ++x) Q.template load<RAGGED>(rq, slab, x, dq);
+        for (int part = 0; part < PARTS; ++part) {
+            const i32x4 rq = Q.rsrc(slab, part * qpart);
+#pragma unroll
+            for (int x = 0; x < OpQ::LOADS; ++x) Q.template load<RAGGED>(rq, slab, x, dq + part * OpQ::SLAB);
+        }
     }
 
     template <bool RAGGED>
@@ -524,6 +536,7 @@ struct ThinLoop {
                                         Acc &out) {
         P.init(mp, p0, K, wave, lane);
         Q.init(mq, q0, K, wave, lane);
+        qpart = 2 * mq.part;
         const int n = s1 - s0;
         if (n <= 0) return;
         f32x4 acc[PB][CB];
@@ -551,7 +564,9 @@ struct ThinLoop {
 #pragma unroll
             for (int a = 0; a < PB; ++a)
 #pragma unroll
-                for (int b = 0; b < CB; ++b) acc[a][b] = mfma<DT>(cur.p[a], cur.q[b], acc[a][b]);
+                for (int b = 0; b < CB; ++b)
+#pragma unroll
+                    for (int x = PARTS - 1; x >= 0; --x) acc[a][b] = mfma<DT>(cur.p[a], cur.q[x][b], acc[a][b]);
             __builtin_amdgcn_sched_barrier(0);
         };
         for (int i = 0; i < n; i += 2) {

@@ -26,7 +26,8 @@
  * gradient is zero, and zero times infinity is not).
  *
  * Arithmetic: logits, maxima, sums of exponentials and losses in fp32.  The
- * backward pass computes the logits again, rounds dz to the operands' type once
+ * backward pass computes the logits again, rounds dz to the operands' type (up to
+ * 64 rows: to the sum of two such values) once
  * (fp16: after scaling by a power of two that brings the largest row factor to
  * at most 2^14, divided out of dx and dw: besides its rounding an entry of any row
  * is off by at most 2^-38 of the call's largest factor), and accumulates dx and dw

@@ -23,7 +23,9 @@ rounds dz and the results once:
 * the loss adds err(lse) and err(z), and a handful of roundings of its terms;
 * dz: |err dz| <= u |dz| + |a| p (err z / tau + err lse + (4 max|z| / tau + 8) f) + 4 f (|a| p + |b| q),
   in fp16 also half its smallest step, 2^-25, over the scale that brings the
-  largest |a| or |b| to at least 2^13;
+  largest |a| or |b| to at least 2^13.  A dz kept as the sum of two values of the
+  type (`parts` = 2) rounds the first one's remainder, at most u |dz|, instead:
+  u^2 |dz|;
 * dx: sum_v err dz |w| + 2 (V / 16 + 8 + parts) f sum_v |dz||w| + u |dx|; dw
   alike over rows (`parts`: slices and pieces that are added up, at most 64); a
   result below the type's normal range is off by half its smallest step.
@@ -117,8 +119,8 @@ def forward(x, w, dtype, target=None, index=None, logits=None, tau=1.0, zeta=0.0
     return Forward(loss, lse, np.where(on, bound, 0.0), el, z, ez, q, on, bad)
 
 
-def backward(f: Forward, x, w, dtype, grad, tau=1.0, zeta=0.0, distill=False, dw_type=None, mutation=0):
-    """(dx, dw, bounds of both) with dw [V,H]."""
+def backward(f: Forward, x, w, dtype, grad, tau=1.0, zeta=0.0, distill=False, dw_type=None, mutation=0, parts=1):
+    """(dx, dw, bounds of both) with dw [V,H]; `parts`: values of `dtype` whose sum holds an entry of dz."""
     u, small = HALF_STEP[dtype], SMALLEST[dtype]
     T, H = x.shape
     V = w.shape[0]
@@ -130,7 +132,7 @@ def backward(f: Forward, x, w, dtype, grad, tau=1.0, zeta=0.0, distill=False, dw
     dz[~f.on] = 0.0
     top = np.abs(f.z).max(axis=1) / tau
     ep = (f.z_bound / tau + f.lse_bound + (4 * top + 8) * F32)[:, None]
-    edz = u * np.abs(dz) + np.abs(a) * p * ep + (4 + 200 * distill) * F32 * (np.abs(a) * p + np.abs(b) * f.q)
+    edz = u ** parts * np.abs(dz) + np.abs(a) * p * ep + (4 + 200 * distill) * F32 * (np.abs(a) * p + np.abs(b) * f.q)
     if dtype == "fp16":
         edz += 2.0 ** -25 * max(np.abs(a).max(initial=0), np.abs(b).max(initial=0)) / 2.0 ** 13
     dx, dw = dz @ w, dz.T @ x
