@@ -214,8 +214,9 @@ int logits_tile(const gemm_loss_args_t &a, int64_t V, int cus) {
     return a.T <= 32 && V < 64 * (int64_t)cus ? dgw::LT_32x32 : dgw::LT_64x64;
 }
 
-// dx's tile and slices.  Few rows: one workgroup a CU (V = 32768, H = 2048, T = 2:
-// 16 slices 61 us for dz and dx together, 32 slices 68 us, which add up more).
+// dx's tile and slices.  Few rows: one workgroup a CU, which is what fits with dz in
+// two parts (with one part two fitted and were slower, their slices add up more: V =
+// 32768, H = 2048, T = 2: 16 slices 61 us for dz and dx together, 32 slices 68 us).
 Choice dx_choice(const gemm_loss_args_t &a, int64_t V, int cus) {
     if (a.T > 64) return choose(a.H, a.T, V, true, cus);
     const int tile = a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;

@@ -434,8 +434,10 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void loss_product(ProductParams p)
 // dw of at most 64 rows: one slab of k, so the stores are the cost.  A workgroup
 // keeps its 128 rows of P in registers and walks over tiles of Q: the next tile's
 // slab is on its way while this one is multiplied, and a tile's stores while the
-// next is.  64 x 50001 x 2048: 49 us with a workgroup per tile (each waits out its
-// slab's latency alone), 39 us this way (5.3 TB/s written).
+// next is.  64 x 50001 x 2048, dz in one part: 49 us with a workgroup per tile (each
+// waits out its slab's latency alone), 39 us this way (5.3 TB/s written); in two
+// parts 47.5 us (4.3 TB/s), in fp32 107 us, added to fp32 180 us (4.5 TB/s read and
+// written).  64 x 32000 x 2048, w [H,V]: 26.9 us (4.9 TB/s).
 // One operand is dz in two parts.  As P both lie in registers; as Q they take two of
 // three places in LDS, so that two workgroups still fit a CU: the next tile's first
 // part goes into the third while this tile is multiplied, its second part into the
@@ -835,10 +837,12 @@ __global__ __launch_bounds__(256) void loss_zero(char *out, int64_t rows, int64_
 // A third stage of P (all of the LDS then) lets P's loads, most of which miss the
 // L2, travel for two iterations instead of one.  4096 x 131072 x 4096 on 256 x 256:
 // logits 2.995 against 3.071 ms, dz and dx 6.22 against 6.48 ms; with both
-// operands' rows contiguous (dw) its registers spill, dz and dw take 6.67 against
-// 6.35 ms.  On 128 x 128 tiles it pays for logits (333 x 50001 x 2048: 79.9 against
-// 84.3 us; w [H,V]: 80.7 against 88.3) and for products of operands with k
-// contiguous, not for the others (that shape's dz and dx: 168 against 164.5 us).
+// operands' rows contiguous (dw) 29 registers a lane spill instead of 16, dz and dw
+// take 6.67 against 6.35 ms.  (Every 256 x 256 form spills some of its 256 registers:
+// logits 6, of w [H,V] 11, dz and dx 2.)  On 128 x 128 tiles it pays for logits
+// (333 x 50001 x 2048: 79.9 against 84.3 us; w [H,V]: 80.7 against 88.3) and for
+// products of operands with k contiguous, not for the others (that shape's dz and
+// dx: 168 against 164.5 us).
 template <int TILE, int DT, bool PK, bool QK, bool LOGITS = false>
 struct LoopOf;
 template <int DT, bool PK, bool QK, bool LOGITS>
