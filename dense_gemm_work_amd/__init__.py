@@ -33,6 +33,8 @@ __all__ = [
     "gemm_version", "gemm_tensors", "matmul", "plan_dict", "library_path",
     "GemmLossArgs", "GemmLossPlan", "gemm_loss_forward", "gemm_loss_backward", "gemm_loss_plan",
     "linear_cross_entropy", "linear_cross_entropy_backward", "linear_distill", "linear_distill_backward",
+    "GemmFfnArgs", "GemmFfnPlan", "gemm_ffn_forward", "gemm_ffn_backward", "gemm_ffn_plan",
+    "gated_ffn", "gated_ffn_backward",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -516,3 +518,7 @@ from .loss import (  # noqa: E402  (needs the loaded library)
     GEMM_LOSS_FP32, GEMM_LOSS_MAX_ENTRIES, GEMM_LOSS_MAX_H, GEMM_LOSS_MAX_T, GEMM_LOSS_MAX_TH, GEMM_LOSS_MAX_TV,
     GEMM_LOSS_MAX_V, GEMM_LOSS_XENT, GemmLossArgs, GemmLossPlan, gemm_loss_backward, gemm_loss_forward, gemm_loss_plan,
     linear_cross_entropy, linear_cross_entropy_backward, linear_distill, linear_distill_backward)
+from .ffn import (  # noqa: E402
+    GEMM_FFN_DW_FP32, GEMM_FFN_DW_FP32_ADD, GEMM_FFN_DW_SAME, GEMM_FFN_GELU, GEMM_FFN_MAX_F, GEMM_FFN_MAX_H,
+    GEMM_FFN_MAX_T, GEMM_FFN_MAX_TH, GEMM_FFN_RELU, GEMM_FFN_SILU, GemmFfnArgs, GemmFfnPlan, gated_ffn,
+    gated_ffn_backward, gemm_ffn_backward, gemm_ffn_forward, gemm_ffn_plan)

@@ -17,7 +17,8 @@ from pathlib import Path
 PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libdgw_gemm.so"
-SOURCES = ["gemm_kernels.hip", "gemm_api.hip", "plan.cpp", "loss_kernels.hip", "loss_api.hip"]
+SOURCES = ["gemm_kernels.hip", "gemm_api.hip", "plan.cpp", "loss_kernels.hip", "loss_api.hip", "ffn_kernels.hip",
+           "ffn_api.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,49 @@
+// ffn.h -- launch interface of the gated feed-forward kernels (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm_ffn.h"
+#include "loss.h"
+
+namespace dgw {
+
+// Tiles are named as the losses' (P x Q).  Of the forward kernel's P rows one half are
+// gate features, the other the same features of up.
+struct FfnGate {
+    int T, F, H;
+    LossMatrix gate, up, x;     // gate and up: F rows; x: k contiguous
+    uint32_t act;
+    uint16_t *h;                // [T][ldh], the product of the activation and up
+    int64_t ldh, part;          // tiles of at most LOSS_FEW rows write what the rounding left out `part` elements on
+    uint16_t *kept_gate, *kept_up;   // nullptr: not kept
+    int64_t ld_gate, ld_up;
+};
+hipError_t launch_ffn_gate(int dtype, int tile, const FfnGate &p, hipStream_t stream);
+
+// dh = dy . w_down, turned into dg, du and h where it stands.
+struct FfnSlope {
+    int T, F, H;
+    LossMatrix down, dy;        // down: F rows; dy: k contiguous
+    uint32_t act;
+    const uint16_t *gate, *up;
+    int64_t ld_gate, ld_up;
+    uint16_t *dg, *du, *h;      // [T][ld]
+    int64_t ld, part;           // as ldh and part above
+};
+hipError_t launch_ffn_slope(int dtype, int tile, const FfnSlope &p, hipStream_t stream);
+
+// out[q][p] = sum_f gate[p][f] dg[q][f] + up[p][f] du[q][f] in the operands' type, or
+// (splits > 1) the slices' slots as launch_loss_product writes them.  gate and up have
+// one ld, dg and du too.
+struct FfnSum {
+    LossMatrix gate, up, dg, du;
+    int F, splits;
+    void *out;
+    int64_t ldo;
+};
+hipError_t launch_ffn_sum(int dtype, int tile, const FfnSum &p, hipStream_t stream);
+
+}  // namespace dgw

@@ -1,0 +1,395 @@
+// ffn_kernels.hip -- gfx950 kernels of the gated feed-forward block (gemm_ffn.h).
+//
+// Forward: ffn_gate computes a tile of x . w_gate^T and the same tile of
+// x . w_up^T side by side (tile.h, PAIR), so a lane ends with both values of an
+// element and writes act(g) u in 16 bits; g and u reach memory only where the
+// caller keeps them.  Backward: ffn_slope computes a tile of dh = dy . w_down and
+// turns it into dg = dh u act'(g), du = dh act(g) and h = act(g) u.  The products
+// of h, dg and du with the weights and x are those of loss_kernels.hip.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "ffn.h"
+#include "tile.h"
+#include "tile_store.h"
+
+namespace dgw {
+
+using namespace tile;
+
+namespace {
+
+constexpr float LOG2E = 1.44269504088896340736f;
+
+// ---------------------------------------------------------------------------
+// act(g) and act'(g) in fp32, branch free.
+//   silu: g p, p = 1 / (1 + exp(-g));              p (1 + g (1 - p))
+//   gelu: g Phi(g);                                Phi(g) + g phi(g)
+//   relu: max(g, 0);                               [g > 0]
+// Phi is (1 + erf(g / sqrt 2)) / 2 with erfc from the rational approximation of
+// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (absolute error
+// 1.5e-7), the negative side from erfc itself, as the GEMM's epilogue does.
+// ---------------------------------------------------------------------------
+struct Act {
+    float value, slope;
+};
+template <uint32_t ACT>
+__device__ __forceinline__ Act activation(float g) {
+    if constexpr (ACT == GEMM_FFN_SILU) {
+        const float e = __builtin_amdgcn_exp2f(-g * LOG2E);
+        const float p = __builtin_amdgcn_rcpf(1.0f + e);
+        return {g * p, p * __builtin_fmaf(g, 1.0f - p, 1.0f)};
+    } else if constexpr (ACT == GEMM_FFN_GELU) {
+        const float x = fabsf(g) * 0.70710678118654752f, t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+        float poly = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+        poly = __builtin_fmaf(poly, t, 1.421413741f);
+        poly = __builtin_fmaf(poly, t, -0.284496736f);
+        poly = __builtin_fmaf(poly, t, 0.254829592f);
+        const float bell = __builtin_amdgcn_exp2f(g * g * (-0.5f * LOG2E));   // exp(-g^2 / 2)
+        const float q = 0.5f * poly * t * bell;
+        const float phi = g >= 0.0f ? 1.0f - q : q;
+        return {g * phi, __builtin_fmaf(g * bell, 0.39894228040143268f, phi)};
+    } else {
+        return {g > 0.0f ? g : 0.0f, g > 0.0f ? 1.0f : 0.0f};
+    }
+}
+
+// f(integral constant) for the activation: its branch is taken once, outside the loops.
+template <class F>
+__device__ __forceinline__ void with_act(uint32_t act, F &&f) {
+    if (act == GEMM_FFN_SILU) f(std::integral_constant<uint32_t, GEMM_FFN_SILU>());
+    else if (act == GEMM_FFN_GELU) f(std::integral_constant<uint32_t, GEMM_FFN_GELU>());
+    else f(std::integral_constant<uint32_t, GEMM_FFN_RELU>());
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b) {
+    if constexpr (DT == 0) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const f16x2 v = __builtin_bit_cast(f16x2, w);
+        a = (float)v[0];
+        b = (float)v[1];
+    }
+}
+template <int DT>
+__device__ __forceinline__ u32x2 pack4(f32x4 v) {
+    return u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+template <int DT>
+__device__ __forceinline__ f32x4 unpack4(u32x2 w) {
+    f32x4 v;
+    float a, b;
+    unpack2<DT>(w[0], a, b);
+    v[0] = a;
+    v[1] = b;
+    unpack2<DT>(w[1], a, b);
+    v[2] = a;
+    v[3] = b;
+    return v;
+}
+// v in 16 bits at `to` and, TWO, what that left out, rounded too, `part` elements on.
+// The rest is taken from the stored bits: the compiler may fold the multiplication that
+// made v into one of its conversions (v_fma_mixlo_f16) and not into another, and near a
+// tie the two then round apart.
+template <int DT, bool TWO>
+__device__ __forceinline__ void store4(uint16_t *to, int64_t part, f32x4 v) {
+    const u32x2 first = pack4<DT>(v);
+    *reinterpret_cast<u32x2 *>(to) = first;
+    if constexpr (TWO) *reinterpret_cast<u32x2 *>(to + part) = pack4<DT>(v - unpack4<DT>(first));
+}
+
+struct GateParams {
+    Matrix gate, up, x;
+    int T, F, H;
+    Grid g;
+    uint32_t act;
+    uint16_t *h, *kept_gate, *kept_up;
+    int64_t ldh, part, ld_gate, ld_up;
+};
+
+// One matrix's half of a paired tile, as store16 takes a tile.
+template <class L>
+struct Half {
+    static constexpr int TP = L::TP / 2, TQ = L::TQ, RB = L::RB / 2, CB = L::CB, NT = L::NT, LDS_BYTES = L::LDS_BYTES;
+    struct Acc {
+        f32x4 v[RB][CB];
+    };
+    const L &loop;
+    __device__ __forceinline__ bool active() const { return loop.active(); }
+    __device__ __forceinline__ int p_of(int i, int e) const { return loop.p_of(i, e); }
+    __device__ __forceinline__ int q_of(int j) const { return loop.q_of(j); }
+};
+
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT, 2) void ffn_gate(GateParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * (L::TP / 2), q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    loop.run_any(loop.pick(p.gate, p.up), p0, p.x, q0, p.H, 0, p.g.slabs, acc);
+    using V = Half<L>;
+    const V half{loop};
+    typename V::Acc out;
+    auto take = [&](int kind) {
+#pragma unroll
+        for (int i = 0; i < V::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < V::CB; ++j) out.v[i][j] = acc.v[2 * i + kind][j];
+    };
+    if (p.kept_gate) {
+        take(0);
+        store16<DT, true>(half, out, lds, p.kept_gate, p.ld_gate, p0, q0, p.F, p.T);
+        __syncthreads();
+        take(1);
+        store16<DT, true>(half, out, lds, p.kept_up, p.ld_up, p0, q0, p.F, p.T);
+        __syncthreads();
+    }
+    with_act(p.act, [&](auto A) {
+#pragma unroll
+        for (int i = 0; i < V::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < V::CB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    out.v[i][j][e] = activation<decltype(A)::value>(acc.v[2 * i][j][e]).value * acc.v[2 * i + 1][j][e];
+    });
+    store16<DT, false>(half, out, lds, p.h, p.ldh, p0, q0, p.F, p.T);
+}
+
+// Few rows: the halves' fp32 tiles meet in LDS ([row][TP + 4], 4 floats of padding
+// against bank conflicts).  h is the sum of two 16-bit parts: with few rows the
+// weights' stream is the time, and a second part costs it nothing.
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT, L::WAVES) void ffn_gate_few(GateParams p) {
+    constexpr int LD = L::TP + 4, QUADS = L::TP / 8;
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    static_assert(L::TQ * LD * 4 <= L::LDS_BYTES, "the tile fits");
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * (L::TP / 2), q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    loop.run_any(loop.pick(p.gate, p.up), p0, p.x, q0, p.H, 0, p.g.slabs, acc);
+    float *tile = reinterpret_cast<float *>(lds);
+    if (loop.active())
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < L::CB; ++j)
+                *reinterpret_cast<f32x4 *>(tile + loop.q_of(j) * LD + loop.p_of(i, 0)) = acc.v[i][j];
+    __syncthreads();
+    with_act(p.act, [&](auto A) {
+        for (int f = threadIdx.x; f < L::TQ * QUADS; f += L::NT) {
+            const int64_t row = q0 + f / QUADS, col = p0 + 4 * (f % QUADS);
+            if (row >= p.T || col >= p.F) continue;
+            const float *at = tile + f / QUADS * LD + 4 * (f % QUADS);
+            const f32x4 g = *reinterpret_cast<const f32x4 *>(at), u = *reinterpret_cast<const f32x4 *>(at + L::TP / 2);
+            f32x4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = activation<decltype(A)::value>(g[e]).value * u[e];
+            store4<DT, true>(p.h + row * p.ldh + col, p.part, h);
+            if (p.kept_gate) {
+                *reinterpret_cast<u32x2 *>(p.kept_gate + row * p.ld_gate + col) = pack4<DT>(g);
+                *reinterpret_cast<u32x2 *>(p.kept_up + row * p.ld_up + col) = pack4<DT>(u);
+            }
+        }
+    });
+}
+
+struct SlopeParams {
+    Matrix down, dy;
+    int T, F, H;
+    Grid g;
+    uint32_t act;
+    const uint16_t *gate, *up;
+    int64_t ld_gate, ld_up;
+    uint16_t *dg, *du, *h;
+    int64_t ld, part;
+};
+
+// A lane's four consecutive features are 8 bytes of gate, up and each result; the
+// four lanes of a row make 32 bytes, and the L2 joins those of neighbouring blocks.
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT, 2) void ffn_slope(SlopeParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    loop.run_any(p.down, p0, p.dy, q0, p.H, 0, p.g.slabs, acc);
+    if (!loop.active()) return;
+    with_act(p.act, [&](auto A) {
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j) {
+            const int64_t row = q0 + loop.q_of(j);
+            u32x2 g16[L::RB], u16[L::RB];
+#pragma unroll
+            for (int i = 0; i < L::RB; ++i) {
+                const int64_t col = p0 + loop.p_of(i, 0);
+                const bool in = row < p.T && col < p.F;
+                g16[i] = in ? *reinterpret_cast<const u32x2 *>(p.gate + row * p.ld_gate + col) : u32x2{0u, 0u};
+                u16[i] = in ? *reinterpret_cast<const u32x2 *>(p.up + row * p.ld_up + col) : u32x2{0u, 0u};
+            }
+#pragma unroll
+            for (int i = 0; i < L::RB; ++i) {
+                const int64_t col = p0 + loop.p_of(i, 0);
+                const f32x4 g = unpack4<DT>(g16[i]), u = unpack4<DT>(u16[i]);
+                f32x4 dg, du, h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Act a = activation<decltype(A)::value>(g[e]);
+                    dg[e] = acc.v[i][j][e] * u[e] * a.slope;
+                    du[e] = acc.v[i][j][e] * a.value;
+                    h[e] = u[e] * a.value;
+                }
+                if (row < p.T && col < p.F) {
+                    const int64_t at = row * p.ld + col;
+                    constexpr bool two = L::TQ <= LOSS_FEW;
+                    store4<DT, two>(p.dg + at, p.part, dg);
+                    store4<DT, two>(p.du + at, p.part, du);
+                    store4<DT, two>(p.h + at, p.part, h);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one block column's loads in flight: no more registers are free
+        }
+    });
+}
+
+// dx = dg . w_gate + du . w_up: one loop over both products' slabs, in `splits`
+// slices of them.
+struct SumParams {
+    Matrix gate, up, dg, du;
+    int F;
+    Grid g;
+    bool slots;
+    void *out;
+    int64_t ldo;
+};
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT, L::WAVES) void ffn_sum(SumParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    int tp, tq, split;
+    place(p.g, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    const int s0 = (int)((int64_t)p.g.slabs * split / p.g.splits), s1 = (int)((int64_t)p.g.slabs * (split + 1) / p.g.splits);
+    loop.also(p.up, p0, p.du, q0, p.F);
+    loop.run_any(p.gate, p0, p.dg, q0, p.F, s0, s1, acc);
+    if (!p.slots) {
+        store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, p.gate.rows, p.dg.rows);
+        return;
+    }
+    if (!loop.active()) return;
+    f32x4 *slot = slot_base<L>(static_cast<float *>(p.out), p.g, tp, tq, split, loop.wave, loop.lane);
+#pragma unroll
+    for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j) slot[(i * L::CB + j) * 64] = acc.v[i][j];
+}
+
+// ---------------------------------------------------------------------------
+// Dispatch
+// ---------------------------------------------------------------------------
+template <class L>
+hipError_t run_gate(const FfnGate &a, void (*kernel)(GateParams), hipStream_t stream) {
+    // a workgroup covers TP / 2 features: the grid is that of 2 F rows
+    const GateParams q{matrix(a.gate), matrix(a.up), matrix(a.x), a.T, a.F, a.H, grid_of<L>(2 * (int64_t)a.F, a.T, a.H, 1), a.act,
+                       a.h, a.kept_gate, a.kept_up, a.ldh, a.part, a.ld_gate, a.ld_up};
+    hipLaunchKernelGGL(kernel, dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q);
+    return hipGetLastError();
+}
+template <int DT, bool KC>
+hipError_t gate(int tile, const FfnGate &a, hipStream_t stream) {
+    using L128 = Loop<DT, KC, true, 128, 128, 2, 2, 3, 2, true>;
+    using L256 = Loop<DT, KC, true, 256, 256, 2, 4, 3, 2, true>;
+    using F128x32 = ThinLoop<DT, KC, true, 128, 32, 4, 1, true>;
+    using F128x64 = ThinLoop<DT, KC, true, 128, 64, 3, 1, true>;
+    switch (tile) {
+    case LT_128x128: return run_gate<L128>(a, ffn_gate<DT, L128>, stream);
+    case LT_256x256: return run_gate<L256>(a, ffn_gate<DT, L256>, stream);
+    case LT_128x32: return run_gate<F128x32>(a, ffn_gate_few<DT, F128x32>, stream);
+    case LT_128x64: return run_gate<F128x64>(a, ffn_gate_few<DT, F128x64>, stream);
+    default: break;
+    }
+    if constexpr (KC) {   // halves of fewer than 64 rows: k contiguous only
+        using F32 = ThinLoop<DT, true, true, 32, 32, 6, 1, true>;
+        using F64 = ThinLoop<DT, true, true, 64, 64, 5, 1, true>;
+        if (tile == LT_32x32) return run_gate<F32>(a, ffn_gate_few<DT, F32>, stream);
+        if (tile == LT_64x64) return run_gate<F64>(a, ffn_gate_few<DT, F64>, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int DT, class L>
+hipError_t run_slope(const FfnSlope &a, hipStream_t stream) {
+    const SlopeParams q{matrix(a.down), matrix(a.dy), a.T, a.F, a.H, grid_of<L>(a.F, a.T, a.H, 1), a.act, a.gate, a.up,
+                        a.ld_gate, a.ld_up, a.dg, a.du, a.h, a.ld, a.part};
+    hipLaunchKernelGGL((ffn_slope<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q);
+    return hipGetLastError();
+}
+template <int DT, bool KC>
+hipError_t slope(int tile, const FfnSlope &a, hipStream_t stream) {
+    switch (tile) {
+    case LT_128x128: return run_slope<DT, Loop<DT, KC, true, 128, 128, 2, 2, 3, 2>>(a, stream);
+    case LT_256x256: return run_slope<DT, Loop<DT, KC, true, 256, 256, 2, 4, 3, 2>>(a, stream);
+    case LT_64x64: return run_slope<DT, ThinLoop<DT, KC, true, 64, 64, 5>>(a, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+template <int DT, class L>
+hipError_t run_sum(const FfnSum &a, hipStream_t stream) {
+    SumParams q{matrix(a.gate), matrix(a.up), matrix(a.dg), matrix(a.du), a.F, grid_of<L>(a.gate.rows, a.dg.rows, a.F, a.splits),
+                a.splits > 1, a.out, a.ldo};
+    q.g.slabs *= 2;
+    hipLaunchKernelGGL((ffn_sum<DT, L>), dim3(blocks_of(q.g)), dim3(L::NT), 0, stream, q);
+    return hipGetLastError();
+}
+template <int DT, bool KC>
+hipError_t sum(int tile, const FfnSum &a, hipStream_t stream) {
+    switch (tile) {
+    case LT_128x128: return run_sum<DT, Loop<DT, KC, true, 128, 128, 2, 2, KC ? 3 : 2, 2, false, 2>>(a, stream);
+    case LT_256x256: return run_sum<DT, Loop<DT, KC, true, 256, 256, 2, 4, 3, 2, false, 2>>(a, stream);
+    case LT_128x32: return run_sum<DT, ThinLoop<DT, KC, true, 128, 32, 4, 2, false, 2>>(a, stream);
+    case LT_128x64: return run_sum<DT, ThinLoop<DT, KC, true, 128, 64, 3, 2, false, 2>>(a, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+bool few(int tile) { return loss_tile_shape(tile).q <= LOSS_FEW; }
+
+}  // namespace
+
+hipError_t launch_ffn_gate(int dtype, int tile, const FfnGate &p, hipStream_t stream) {
+    if (!p.x.kc || p.gate.kc != p.up.kc || few(tile) != (p.part > 0)) return hipErrorInvalidValue;
+    if (p.gate.kc) return dtype == 0 ? gate<0, true>(tile, p, stream) : gate<1, true>(tile, p, stream);
+    return dtype == 0 ? gate<0, false>(tile, p, stream) : gate<1, false>(tile, p, stream);
+}
+
+hipError_t launch_ffn_sum(int dtype, int tile, const FfnSum &p, hipStream_t stream) {
+    if (!p.dg.kc || !p.du.kc || p.gate.kc != p.up.kc || p.gate.ld != p.up.ld || p.dg.ld != p.du.ld || p.dg.part != p.du.part ||
+        few(tile) != (p.dg.part > 0))
+        return hipErrorInvalidValue;
+    if (p.gate.kc) return dtype == 0 ? sum<0, true>(tile, p, stream) : sum<1, true>(tile, p, stream);
+    return dtype == 0 ? sum<0, false>(tile, p, stream) : sum<1, false>(tile, p, stream);
+}
+
+hipError_t launch_ffn_slope(int dtype, int tile, const FfnSlope &p, hipStream_t stream) {
+    if (!p.dy.kc || few(tile) != (p.part > 0)) return hipErrorInvalidValue;
+    if (p.down.kc) return dtype == 0 ? slope<0, true>(tile, p, stream) : slope<1, true>(tile, p, stream);
+    return dtype == 0 ? slope<0, false>(tile, p, stream) : slope<1, false>(tile, p, stream);
+}
+
+}  // namespace dgw

@@ -21,10 +21,10 @@ LossTileShape loss_tile_shape(int tile);
 // An operand as it lies in memory: element (row, k) at base[row * ld + k]
 // (kc) or base[k * ld + row].
 struct LossMatrix {
-    const uint16_t *base;
-    int64_t ld;
-    int rows;
-    bool kc;
+    const uint16_t *base = nullptr;
+    int64_t ld = 0;
+    int rows = 0;
+    bool kc = false;
     int64_t part = 0;   // elements from the first 16-bit part to the second (0: one part)
 };
 

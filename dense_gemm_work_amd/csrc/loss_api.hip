@@ -9,26 +9,20 @@
 #include <string>
 
 #include "../../include/gemm_loss.h"
+#include "call.h"
 #include "internal.h"
 #include "loss.h"
 
 namespace {
 
+using namespace dgw::call;
 using dgw::set_error;
 using dgw::set_hip_error;
 
-constexpr int64_t MAX_LD = int64_t(1) << 21;   // a tile's rows then stay within 32-bit byte offsets
-constexpr int MAX_CUS = 1 << 16;               // keeps a launch's workgroups within 32 bits
 constexpr int64_t PIECE_BYTES = int64_t(256) << 20;   // the logits' gradient of one piece
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-int64_t ceil_div(int64_t v, int64_t m) { return (v + m - 1) / m; }
 
 int64_t row_of_w(const gemm_loss_args_t &a) { return (a.layout & 0xFu) == GEMM_B_NK ? a.H : a.V; }
 int64_t rows_of_w(const gemm_loss_args_t &a) { return (a.layout & 0xFu) == GEMM_B_NK ? a.V : a.H; }
-int64_t or_packed(int64_t ld, int64_t packed) { return ld ? ld : packed; }
-
-int bad(const char *msg) { return set_error(GEMM_ERR_INVALID, msg); }
 
 // What the host can tell from sizes, words and flags alone.
 int check_sizes(const gemm_loss_args_t &a) {
@@ -49,37 +43,6 @@ int check_sizes(const gemm_loss_args_t &a) {
     if (a.dw_type > GEMM_LOSS_DW_FP32_ADD) return bad("unknown dw_type");
     return GEMM_OK;
 }
-
-int check_ld(int64_t ld, int64_t row, int64_t unit, const char *what) {
-    if (ld < row) return set_error(GEMM_ERR_INVALID, std::string(what) + ": rows overlap");
-    if (ld % unit || ld > MAX_LD)
-        return set_error(GEMM_ERR_UNSUPPORTED, std::string(what) + ": rows must start at multiples of 16 bytes, at most 2^21 elements apart");
-    return GEMM_OK;
-}
-
-// A buffer of a call: `rows` rows of `row` bytes, `ld` bytes apart.
-struct Block {
-    const void *base;
-    int64_t rows, row, ld;
-    const char *name;
-    uintptr_t begin() const { return reinterpret_cast<uintptr_t>(base); }
-    uintptr_t end() const { return begin() + (uintptr_t)((rows - 1) * ld + row); }
-};
-
-bool overlap(const Block &a, const Block &b) {
-    if (!a.base || !b.base || a.rows <= 0 || b.rows <= 0 || a.begin() >= b.end() || b.begin() >= a.end()) return false;
-    if (a.ld != b.ld || a.rows == 1 || b.rows == 1) return true;
-    // rows at one stride: each of a's begins `d` bytes behind where one of b's begins or would
-    const uintptr_t ld = (uintptr_t)a.ld, d = (a.begin() % ld + ld - b.begin() % ld) % ld;
-    return d < (uintptr_t)b.row || d + (uintptr_t)a.row > ld;
-}
-
-// The buffers of a call: first what it writes, then what it reads.
-struct Blocks {
-    Block b[8];
-    int written = 0, all = 0;
-    void add(const void *base, int64_t rows, int64_t row, int64_t ld, const char *name) { b[all++] = {base, rows, row, ld, name}; }
-};
 
 Blocks blocks_of(const gemm_loss_args_t &a, bool backward) {
     Blocks s;
@@ -107,10 +70,6 @@ Blocks blocks_of(const gemm_loss_args_t &a, bool backward) {
         s.add(a.teacher_logits, 1, n * size, n * size, "teacher_logits");
     }
     return s;
-}
-
-int overlapping(const Block &a, const Block &b) {
-    return set_error(GEMM_ERR_INVALID, std::string(a.name) + " must not overlap " + b.name);
 }
 
 int check_args(const gemm_loss_args_t &a, bool backward) {
@@ -161,42 +120,6 @@ struct Layout {
         return at;
     }
 };
-
-// The tile of a product of rows_p x rows_q over k and, where its k may be sliced,
-// the slices (of at least 8 slabs): the cheapest by a model of the time in us,
-//   rounds of resident workgroups x (slabs x slab time + fixed time) + joining,
-// for 256 x 256 tiles, one a CU (1.53 us a slab, 8 us fixed), and 128 x 128 tiles,
-// two a CU (0.92 us a slab for the pair, 2.5 us fixed).  Model against measurement:
-// logits of 333 x 50001 x 2048: 114 / 96 us (measured 97-106 / 92-96), of
-// 200 x 50001 x 2048: 57 / 64 (58 / 67), of 777 x 50001 x 1536: 179 / 147 (150-166 /
-// 143), of 500 x 32768 x 4096: 106 / 123 (111 / 143); dw of 500 x 32768 x 4096: 162 /
-// 158 (154 / 158), of 2048 x 32768 x 2048: 228 / 255 (213 / 278); dx of
-// 500 x 32768 x 4096: 124 / 130 (124 / 147), of 200 x 50001 x 2048: 61 / 56 (73 / 64).
-// Joining takes a launch and reads the fp32 slices at 4.5 TB/s.
-struct Choice {
-    int tile, splits;
-};
-Choice choose(int64_t rows_p, int64_t rows_q, int64_t k, bool sliceable, int cus) {
-    Choice best{dgw::LT_128x128, 1};
-    double least = 0.0;
-    const int64_t slabs = ceil_div(k, 64);
-    auto consider = [&](int tile, double slab, double fixed) {
-        const dgw::LossTileShape s = dgw::loss_tile_shape(tile);
-        const int64_t tiles = ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q), slots = (int64_t)cus * s.per_cu;
-        const int64_t most = sliceable ? std::max<int64_t>(1, std::min<int64_t>(slots / tiles, slabs / 8)) : 1;
-        for (int64_t n = 1; n <= most; ++n) {
-            double us = (double)ceil_div(tiles * n, slots) * ((double)ceil_div(slabs, n) * slab + fixed);
-            if (n > 1) us += 3.0 + 4.0 * (double)n * (double)rows_p * (double)rows_q / 4.5e6;
-            if (least == 0.0 || us < least) {
-                least = us;
-                best = {tile, (int)n};
-            }
-        }
-    };
-    consider(dgw::LT_128x128, 0.92, 2.5);
-    consider(dgw::LT_256x256, 1.53, 8.0);
-    return best;
-}
 
 // The logits' tile.  Up to 64 rows the stream of w is the cost and thin tiles
 // keep more of it in flight (V = 32768, H = 2048, T = 32: 35 us on 64 x 64 tiles,
@@ -275,11 +198,6 @@ Plan make_plan(const gemm_loss_args_t &a, bool backward, int cus) {
         if (p.dw_splits > 1) l.dw = l.take(dgw::loss_slots_bytes(p.dw, rp, rq, p.dw_splits));
     }
     return p;
-}
-
-template <class T>
-T *part(void *ws, int64_t at) {
-    return reinterpret_cast<T *>(static_cast<char *>(ws) + at);
 }
 
 // The workspace, the stream and the teacher's entries of a call.
@@ -437,17 +355,6 @@ int backward(const gemm_loss_args_t &a) {
             return set_hip_error(e, "launch dx's join");
     }
     return GEMM_OK;
-}
-
-// No exception leaves a C call.  What can throw is the host's memory running out
-// (an error's text is allocated); this text is short enough not to be.
-template <class F>
-int guarded(F &&f) noexcept {
-    try {
-        return f();
-    } catch (...) {
-        return set_error(GEMM_ERR_WORKSPACE, "no host memory");
-    }
 }
 
 int plan(const gemm_loss_args_t *args, int32_t backward, int32_t num_cus, gemm_loss_plan_t *out) {

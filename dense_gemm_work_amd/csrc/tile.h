@@ -1,5 +1,5 @@
-// tile.h -- the product tiles of the vocabulary-loss kernels (device code,
-// internal to the library).
+// tile.h -- the product tiles of the kernels of the vocabulary losses, the gated
+// feed-forward block and the adapters (device code, internal to the library).
 //
 // One workgroup computes a TP x TQ block of sum_k P[p][k] Q[q][k] in fp32.  P is
 // the dimension that lies contiguous in the result's memory (vocabulary entries
@@ -52,7 +52,13 @@ constexpr uint32_t OOB = 0x7ffffff0u;         // beyond every buffer range used 
 constexpr uint32_t RSRC_DW3 = 0x00020000u;    // raw buffer, 32-bit data format
 
 __device__ __forceinline__ int swz_kc(int r) { return r & 7; }
-__device__ __forceinline__ int swz_rc(int k) { return ((k & 1) << 2) ^ ((k & 2) * 5) ^ ((k >> 2) & 2); }
+// k-rows of 8 chunks (R = 64): two of them cover the banks, bit 0 of k says which
+// half, and bits 1 and 3 move the pair of chunks that 4 lanes read.
+template <int R>
+__device__ __forceinline__ int swz_rc(int k) {
+    if constexpr (R == 64) return (k & 2) ^ ((k >> 1) & 4);
+    return ((k & 1) << 2) ^ ((k & 2) * 5) ^ ((k >> 2) & 2);
+}
 
 // D[row][col] += sum_k A[row][k] B[col][k]: lane l holds A row l % 16 and B column
 // l % 16 at k = 8 (l / 16) .. + 7, and D column l % 16, rows 4 (l / 16) .. + 3.
@@ -136,13 +142,21 @@ struct Matrix {
     int64_t part;
 };
 
-// One operand's slabs: R rows by 64 k, moved by NW waves.
-template <bool KC, int R, int NW>
+// Which of an operand's rows take part; the others are zeros, whatever they hold.
+struct AllRows {
+    __device__ __forceinline__ bool operator()(int64_t) const { return true; }
+};
+
+// One operand's slabs: R rows by 64 k, moved by NW waves.  SRC = 2: the slabs of a
+// second matrix of the same shape, ld and storage follow those of the first (the sum
+// of two products in one loop: as two loops one after the other, the accumulators
+// between them cost a thousand spilled registers).
+template <bool KC, int R, int NW, int SRC = 1>
 struct Operand {
     static constexpr int SLAB = R * KB * 2;          // bytes of one stage
     static constexpr int LOADS = R / 8 / NW;         // load instructions per wave and slab (1 KiB each)
     static_assert(LOADS >= 1 && LOADS * 8 * NW == R, "whole instructions per wave");
-    static_assert(KC || R >= 128, "the swizzle of k-rows needs 16 chunks");
+    static_assert(KC || R >= 64, "the swizzles of k-rows need 8 or 16 chunks");
 
     const char *base;
     int64_t ld;
@@ -151,8 +165,17 @@ struct Operand {
     int width;                     // RC: rows, rounded up to whole chunks
     uint32_t off[LOADS];           // the lane's byte offset at slab 0
     int kc;                        // KC: first k of the lane's chunk
+    const char *base2;             // SRC = 2
+    int turn;                      // its first slab
 
-    __device__ __forceinline__ void init(const Matrix &m, int64_t row0, int K_, int wave, int lane) {
+    __device__ __forceinline__ void also(const Matrix &m, int64_t row0, int slabs) {
+        base2 = reinterpret_cast<const char *>(KC ? m.base + row0 * m.ld : m.base + row0);
+        turn = slabs;
+    }
+    __device__ __forceinline__ int local(int slab) const { return SRC == 2 && slab >= turn ? slab - turn : slab; }
+
+    template <class Keep = AllRows>
+    __device__ __forceinline__ void init(const Matrix &m, int64_t row0, int K_, int wave, int lane, Keep keep = Keep()) {
         const int rows = (int)min((int64_t)R, m.rows - row0);
         ld = m.ld;
         K = K_;
@@ -164,7 +187,7 @@ struct Operand {
 #pragma unroll
             for (int x = 0; x < LOADS; ++x) {
                 const int r = 8 * (wave * LOADS + x) + (lane >> 3);
-                off[x] = r < rows ? (uint32_t)(r * ld + kc) * 2 : OOB;
+                off[x] = r < rows && keep(row0 + r) ? (uint32_t)(r * ld + kc) * 2 : OOB;
             }
         } else {
             constexpr int CH = R / 8;                // 16-byte chunks per k-row
@@ -175,7 +198,7 @@ struct Operand {
 #pragma unroll
             for (int x = 0; x < LOADS; ++x) {
                 const int k = (64 / CH) * (wave * LOADS + x) + lane / CH;
-                const int c = (lane % CH) ^ swz_rc(k);
+                const int c = (lane % CH) ^ swz_rc<R>(k);
                 off[x] = 8 * c < rows ? (uint32_t)(k * ld + 8 * c) * 2 : OOB;
             }
         }
@@ -183,7 +206,8 @@ struct Operand {
 
     // Buffer of slab `slab`, `shift` bytes on.
     __device__ __forceinline__ i32x4 rsrc(int slab, int64_t shift = 0) const {
-        const int64_t kb = (int64_t)slab * KB;
+        const char *base = SRC == 2 && slab >= turn ? base2 : this->base;
+        const int64_t kb = (int64_t)local(slab) * KB;
         if constexpr (KC) return make_rsrc(base + shift + kb * 2, range - (uint32_t)kb * 2);
         // the range stops behind the last k-row's last chunk: width <= ld, so every
         // k-row beyond K starts outside it and reads zeros
@@ -193,7 +217,7 @@ struct Operand {
     template <bool RAGGED>
     __device__ __forceinline__ void load(i32x4 r, int slab, int x, uint32_t dst) const {
         uint32_t o = off[x];
-        if constexpr (RAGGED && KC) o = slab * KB + kc < K ? o : OOB;
+        if constexpr (RAGGED && KC) o = local(slab) * KB + kc < K ? o : OOB;
         load_lds16(r, dst + x * 1024, o);
     }
 
@@ -213,7 +237,7 @@ struct Operand {
         } else {
             const int n = first + number * 16 + 4 * (lane & 3);
             const int k = 8 * group + ((lane & 15) >> 2);
-            return lds + k * (2 * R) + ((((n >> 3) ^ swz_rc(k)) & (R / 8 - 1)) << 4) + ((n & 7) << 1);
+            return lds + k * (2 * R) + ((((n >> 3) ^ swz_rc<R>(k)) & (R / 8 - 1)) << 4) + ((n & 7) << 1);
         }
     }
     // The fragment at `addr`: eight consecutive k of the lane's row.
@@ -251,20 +275,24 @@ __device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &spli
 }
 
 // The product loop of a TP x TQ tile on WP x WQ waves with NSP stages of P and NSQ
-// of Q (NSP >= NSQ).
-template <int DT, bool PK, bool QK, int TP_, int TQ_, int WP_, int WQ_, int NSP_, int NSQ_>
+// of Q (NSP >= NSQ).  PAIR: P's rows are TP / 2 rows each of two matrices, loaded by one
+// half of the waves each into one half of a stage; a wave's blocks alternate between
+// them, so a lane holds both products of a row in neighbouring blocks.
+template <int DT, bool PK, bool QK, int TP_, int TQ_, int WP_, int WQ_, int NSP_, int NSQ_, bool PAIR = false, int SRC = 1>
 struct Loop {
     static constexpr int TP = TP_, TQ = TQ_, WP = WP_, WQ = WQ_, NSP = NSP_, NSQ = NSQ_;
     static constexpr int NW = WP * WQ, NT = 64 * NW, WAVES = 2;   // waves resident per SIMD
     static constexpr int WAVE_P = TP / WP, WAVE_Q = TQ / WQ;
     static constexpr int RB = WAVE_P / 16, CB = WAVE_Q / 16;   // 16 x 16 blocks of a wave
     static constexpr int HB = RB / 2;                          // P blocks of half a step
-    using OpP = Operand<PK, TP, NW>;
-    using OpQ = Operand<QK, TQ, NW>;
+    static constexpr int KINDS = PAIR ? 2 : 1;                 // matrices of P
+    using OpP = Operand<PK, TP / KINDS, NW / KINDS, SRC>;
+    using OpQ = Operand<QK, TQ, NW, SRC>;
     static constexpr int LOADS = OpP::LOADS + OpQ::LOADS;      // per wave and slab
-    static constexpr int QREG = NSP * OpP::SLAB;               // Q's slabs lie behind P's
-    static constexpr int LDS_BYTES = NSP * OpP::SLAB + NSQ * OpQ::SLAB;
-    static constexpr int PA = OpP::template addresses<RB>(), QA = OpQ::template addresses<CB>();
+    static constexpr int SLAB_P = KINDS * OpP::SLAB;
+    static constexpr int QREG = NSP * SLAB_P;                  // Q's slabs lie behind P's
+    static constexpr int LDS_BYTES = NSP * SLAB_P + NSQ * OpQ::SLAB;
+    static constexpr int PA = OpP::template addresses<RB / KINDS>(), QA = OpQ::template addresses<CB>();
     static_assert(NSQ == 2 && (NSP == 2 || NSP == 3), "two stages, or three of P");
     static constexpr int ROUND = NSP == NSQ ? 2 : 6;           // iterations until the stages repeat
 
@@ -285,7 +313,7 @@ struct Loop {
         wq = wave / WP;
         lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
 #pragma unroll
-        for (int i = 0; i < PA; ++i) pa[i] = OpP::address(lds0, wp * WAVE_P, lane, i);
+        for (int i = 0; i < PA; ++i) pa[i] = OpP::address(lds0, wp * (WAVE_P / KINDS), lane, i);
 #pragma unroll
         for (int i = 0; i < QA; ++i) qa[i] = OpQ::address(lds0 + QREG, wq * WAVE_Q, lane, i);
     }
@@ -312,7 +340,8 @@ struct Loop {
             q.v[R - 1] = OpQ::fragment(qa[OpQ::which(R - 1, STEP)] + IT % NSQ * OpQ::SLAB + OpQ::constant(R - 1, STEP));
         } else {
             constexpr int i = HALF == 0 && R > 0 ? R - CB : R, b = HALF * HB + i;
-            p.v[i] = OpP::fragment(pa[OpP::which(b, STEP)] + IT % NSP * OpP::SLAB + OpP::constant(b, STEP));
+            p.v[i] = OpP::fragment(pa[OpP::which(b / KINDS, STEP)] + IT % NSP * SLAB_P + b % KINDS * OpP::SLAB +
+                                   OpP::constant(b / KINDS, STEP));
         }
     }
     static constexpr int reads(int half) { return half == 0 ? HB + CB : HB; }
@@ -325,7 +354,7 @@ struct Loop {
         bool p, q;   // whether there are such slabs
     };
     __device__ __forceinline__ Issue prepare(int sp, int stp, bool p, int sq, int stq, bool q) const {
-        return Issue{P.rsrc(sp), Q.rsrc(sq), lds0 + stp * OpP::SLAB + wave * OpP::LOADS * 1024,
+        return Issue{P.rsrc(sp), Q.rsrc(sq), lds0 + stp * SLAB_P + wave * OpP::LOADS * 1024,
                      lds0 + QREG + stq * OpQ::SLAB + wave * OpQ::LOADS * 1024, sp, sq, p, q};
     }
     template <bool RAGGED>
@@ -368,11 +397,11 @@ struct Loop {
 
     // acc += the products over slabs [s0, s1) of K.  Ends with a barrier: the LDS
     // is free on return.
-    template <bool RAGGED>
+    template <bool RAGGED, class Keep = AllRows>
     __device__ __forceinline__ void run(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
-                                        Acc &acc) {
-        P.init(mp, p0, K, wave, lane);
-        Q.init(mq, q0, K, wave, lane);
+                                        Acc &acc, Keep keep = Keep()) {
+        P.init(mp, p0, K, wave % (NW / KINDS), lane);
+        Q.init(mq, q0, K, wave, lane, keep);
         const int n = s1 - s0;
         if (n <= 0) return;
         FragP p[2];
@@ -430,16 +459,27 @@ struct Loop {
         wait_vm_lgkm<0>();
         barrier();
     }
+    template <class Keep = AllRows>
     __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
-                                            Acc &acc) {
-        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc);
-        else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
+                                            Acc &acc, Keep keep = Keep()) {
+        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc, keep);
+        else run<true>(mp, p0, mq, q0, K, s0, s1, acc, keep);
+    }
+    // SRC = 2, before run: the second product, over the same K (its slabs count on).
+    __device__ __forceinline__ void also(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K) {
+        P.also(mp, p0, (K + KB - 1) / KB);
+        Q.also(mq, q0, (K + KB - 1) / KB);
+    }
+    // PAIR: the one of P's matrices that this wave loads.
+    __device__ __forceinline__ const Matrix &pick(const Matrix &first, const Matrix &second) const {
+        return wave < NW / 2 ? first : second;
     }
 
     __device__ __forceinline__ bool active() const { return true; }
 
-    // Register e of block (i, j) is element (p, q) of the tile.
-    __device__ __forceinline__ int p_of(int i, int e) const { return wp * WAVE_P + i * 16 + 4 * (lane >> 4) + e; }
+    // Register e of block (i, j) is element (p, q) of the tile (PAIR: blocks 2 i and
+    // 2 i + 1 are element p_of(i, e) of either matrix).
+    __device__ __forceinline__ int p_of(int i, int e) const { return wp * (WAVE_P / KINDS) + i * 16 + 4 * (lane >> 4) + e; }
     __device__ __forceinline__ int q_of(int j) const { return wq * WAVE_Q + j * 16 + (lane & 15); }
 };
 
@@ -451,18 +491,20 @@ struct Loop {
 // each then owns half of their blocks (of a 32-row tile, which has one block a
 // half, the wave of step 0 owns it and the other nothing), and the members below
 // describe that state, as Loop's do.  PARTS = 2: Q is the sum of two parts, both
-// staged and multiplied with the same fragments of P.
-template <int DT, bool PK, bool QK, int TP_, int TQ_, int NS_, int PARTS = 1>
+// staged and multiplied with the same fragments of P.  PAIR: P's halves are TP / 2 rows
+// each of two matrices.
+template <int DT, bool PK, bool QK, int TP_, int TQ_, int NS_, int PARTS = 1, bool PAIR = false, int SRC = 1>
 struct ThinLoop {
     static constexpr int TP = TP_, TQ = TQ_, NS = NS_;
     static constexpr int NW = 4, NT = 256;
     static constexpr int PB = TP / 32;                         // P blocks of a wave during the loop
     static constexpr int RB = PB > 1 ? PB / 2 : 1, CB = TQ / 16;
     static constexpr int WAVE_P = 16 * RB, WAVE_Q = TQ, WP = TP / WAVE_P, WQ = 1;
-    using OpP = Operand<PK, TP, NW>;
-    using OpQ = Operand<QK, TQ, NW>;
+    static constexpr int KINDS = PAIR ? 2 : 1;                 // matrices of P
+    using OpP = Operand<PK, TP / KINDS, NW / KINDS, SRC>;
+    using OpQ = Operand<QK, TQ, NW, SRC>;
     static constexpr int LOADS = OpP::LOADS + PARTS * OpQ::LOADS;
-    static constexpr int STAGE = OpP::SLAB + PARTS * OpQ::SLAB;
+    static constexpr int SLAB_P = KINDS * OpP::SLAB, STAGE = SLAB_P + PARTS * OpQ::SLAB;
     static constexpr int LDS_BYTES = NS * STAGE, WAVES = 2 * LDS_BYTES <= 160 * 1024 ? 2 : 1;
     static constexpr int PA = PK ? 1 : PB, QA = QK ? 1 : CB;
     static_assert(PB == 1 || PB == 2 || PB == 4, "32, 64 or 128 rows of P");
@@ -490,10 +532,11 @@ struct ThinLoop {
         lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
 #pragma unroll
         for (int i = 0; i < PA; ++i)
-            pa[i] = OpP::address(lds0, (wave >> 1) * (TP / 2), lane, PK ? step : i) + (PK ? 0 : OpP::constant(0, step));
+            pa[i] = OpP::address(PAIR ? lds0 + (wave >> 1) * OpP::SLAB : lds0, PAIR ? 0 : (wave >> 1) * (TP / 2), lane,
+                                 PK ? step : i) + (PK ? 0 : OpP::constant(0, step));
 #pragma unroll
         for (int i = 0; i < QA; ++i)
-            qa[i] = OpQ::address(lds0 + OpP::SLAB, 0, lane, QK ? step : i) + (QK ? 0 : OpQ::constant(0, step));
+            qa[i] = OpQ::address(lds0 + SLAB_P, 0, lane, QK ? step : i) + (QK ? 0 : OpQ::constant(0, step));
     }
 
     static __device__ __forceinline__ void zero(Acc &a) {
@@ -520,7 +563,7 @@ struct ThinLoop {
     __device__ __forceinline__ void load_all(int slab, int st) const {
         const i32x4 rp = P.rsrc(slab);
         const uint32_t dp = lds0 + st * STAGE + wave * OpP::LOADS * 1024;
-        const uint32_t dq = lds0 + st * STAGE + OpP::SLAB + wave * OpQ::LOADS * 1024;
+        const uint32_t dq = lds0 + st * STAGE + SLAB_P + wave * OpQ::LOADS * 1024;
 #pragma unroll
         for (int x = 0; x < OpP::LOADS; ++x) P.template load<RAGGED>(rp, slab, x, dp);
 #pragma unroll
@@ -531,11 +574,11 @@ struct ThinLoop {
         }
     }
 
-    template <bool RAGGED>
+    template <bool RAGGED, class Keep = AllRows>
     __device__ __forceinline__ void run(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
-                                        Acc &out) {
-        P.init(mp, p0, K, wave, lane);
-        Q.init(mq, q0, K, wave, lane);
+                                        Acc &out, Keep keep = Keep()) {
+        P.init(mp, p0, K, wave % (NW / KINDS), lane);
+        Q.init(mq, q0, K, wave, lane, keep);
         qpart = 2 * mq.part;
         const int n = s1 - s0;
         if (n <= 0) return;
@@ -599,10 +642,18 @@ struct ThinLoop {
             for (int j = 0; j < CB; ++j) out.v[i][j] += buf[((wave ^ 1) * RB * CB + i * CB + j) * 64 + lane];
         __syncthreads();
     }
+    template <class Keep = AllRows>
     __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0,
-                                            int s1, Acc &acc) {
-        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc);
-        else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
+                                            int s1, Acc &acc, Keep keep = Keep()) {
+        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc, keep);
+        else run<true>(mp, p0, mq, q0, K, s0, s1, acc, keep);
+    }
+    __device__ __forceinline__ void also(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K) {
+        P.also(mp, p0, (K + KB - 1) / KB);
+        Q.also(mq, q0, (K + KB - 1) / KB);
+    }
+    __device__ __forceinline__ const Matrix &pick(const Matrix &first, const Matrix &second) const {
+        return wave < NW / 2 ? first : second;
     }
 
     __device__ __forceinline__ bool active() const { return PB > 1 || !(wave & 1); }

@@ -147,9 +147,9 @@ def _product(x, w, b_layout):
     return a
 
 
-def _warn_of_no_graph(*inputs):
+def _warn_of_no_graph(*inputs, what="the loss"):
     if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
-        warnings.warn("the loss is not recorded for autograd: its gradients come from the _backward call "
+        warnings.warn(f"{what} is not recorded for autograd: its gradients come from the _backward call "
                       "(pass detached tensors, or call under torch.no_grad())", stacklevel=3)
 
 
