@@ -35,6 +35,8 @@ __all__ = [
     "linear_cross_entropy", "linear_cross_entropy_backward", "linear_distill", "linear_distill_backward",
     "GemmFfnArgs", "GemmFfnPlan", "gemm_ffn_forward", "gemm_ffn_backward", "gemm_ffn_plan",
     "gated_ffn", "gated_ffn_backward",
+    "GemmLoraArgs", "GemmLoraPlan", "gemm_lora_forward", "gemm_lora_backward", "gemm_lora_plan",
+    "linear_lora", "linear_lora_backward",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -522,3 +524,7 @@ from .ffn import (  # noqa: E402
     GEMM_FFN_DW_FP32, GEMM_FFN_DW_FP32_ADD, GEMM_FFN_DW_SAME, GEMM_FFN_GELU, GEMM_FFN_MAX_F, GEMM_FFN_MAX_H,
     GEMM_FFN_MAX_T, GEMM_FFN_MAX_TH, GEMM_FFN_RELU, GEMM_FFN_SILU, GemmFfnArgs, GemmFfnPlan, gated_ffn,
     gated_ffn_backward, gemm_ffn_backward, gemm_ffn_forward, gemm_ffn_plan)
+from .lora import (  # noqa: E402
+    GEMM_LORA_DAB_FP32, GEMM_LORA_DAB_FP32_ADD, GEMM_LORA_DAB_SAME, GEMM_LORA_MAX_ADAPTERS, GEMM_LORA_MAX_H,
+    GEMM_LORA_MAX_LRH, GEMM_LORA_MAX_LT, GEMM_LORA_MAX_R, GEMM_LORA_MAX_T, GEMM_LORA_MAX_TH, GemmLoraArgs, GemmLoraPlan,
+    gemm_lora_backward, gemm_lora_forward, gemm_lora_plan, linear_lora, linear_lora_backward)

@@ -18,7 +18,7 @@ PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libdgw_gemm.so"
 SOURCES = ["gemm_kernels.hip", "gemm_api.hip", "plan.cpp", "loss_kernels.hip", "loss_api.hip", "ffn_kernels.hip",
-           "ffn_api.hip"]
+           "ffn_api.hip", "lora_kernels.hip", "lora_api.hip"]
 ARCH = "gfx950"
 
 

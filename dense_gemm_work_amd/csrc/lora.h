@@ -1,0 +1,82 @@
+// lora.h -- launch interface of the adapters' kernels (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gemm_lora.h"
+#include "loss.h"
+
+namespace dgw {
+
+// Each row's adapter: adapter[row] in 0 .. count - 1, none (negative) or out of range.
+struct LoraRows {
+    const int64_t *adapter;
+    int T;
+    int count;
+    const float *scale;   // per adapter, or nullptr: 1
+};
+
+// One low-rank side of every adapter: element (r, k) as in LossMatrix, the next
+// adapter `stride` elements on.
+struct LoraFactor {
+    LossMatrix first;   // R rows
+    int64_t stride;
+};
+
+// low[row][r] = scale sum_k x[row][k] f[r][k] with the row's own adapter's f, [T][R] in
+// the operands' type; rows without an adapter are left as they are.  `workgroups` of a
+// group of rows share its adapters (`lists`) and the k slabs (`splits`, through
+// `partial` [splits][T][R] fp32).
+struct LoraLow {
+    LoraRows rows;
+    LoraFactor f;
+    LossMatrix x;       // T rows, k contiguous
+    int R, K;
+    int lists, splits;
+    float *partial;
+    uint16_t *low;
+};
+enum LoraLowTile : int { LL_32x64 = 0, LL_64x64, LL_128x64 };   // R x rows; 32: k contiguous only
+int lora_low_tile(int R, bool kc);
+int lora_low_rows(int tile);    // R rows of a tile
+hipError_t launch_lora_low(int dtype, const LoraLow &p, hipStream_t stream);
+
+// out[q][p] = sum_k P[p][k] x[q][k] + sum_r f[p][r] low[q][r], f the row's adapter's; the
+// operands' type, or (splits > 1) slots as launch_loss_product writes them.  Rows whose
+// adapter is out of range are NaN.
+struct LoraProduct {
+    LoraRows rows;
+    LossMatrix P, x;
+    LoraFactor f;       // P.rows rows, stored as P is
+    const uint16_t *low;
+    int K, R, splits;
+    void *out;
+    int64_t ldo;
+};
+enum LoraTile : int { LP_128x128 = LT_128x128, LP_256x256 = LT_256x256, LP_64x64 = LT_64x64, LP_64x128 = LT_64x128, LP_64x32 = 100 };
+LossTileShape lora_tile_shape(int tile);
+int64_t lora_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits);
+hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, hipStream_t stream);
+hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, const float *slots, hipStream_t stream);
+
+// masks[a][slab]: which of rows 64 slab .. + 63 have adapter a.
+hipError_t launch_lora_masks(const LoraRows &rows, uint64_t *masks, hipStream_t stream);
+
+// out_a[q][p] = sum over the rows t of adapter a of P[t][p] Q[t][q], for every adapter.
+// One of P and Q is the narrow side (R wide, `narrow_p` says which).
+struct LoraOuter {
+    LossMatrix P, Q;    // rows contiguous
+    bool narrow_p;
+    int T, count;
+    const uint64_t *masks;
+    int splits;
+    float *partial;     // splits > 1: [splits][count][Q.rows][P.rows]
+    int out_kind;       // LO_16, LO_F32, LO_F32_ADD
+    void *out;          // [count][Q.rows][P.rows], rows ldo apart, adapters `stride`
+    int64_t ldo, stride;
+};
+hipError_t launch_lora_outer(int dtype, const LoraOuter &p, hipStream_t stream);
+
+}  // namespace dgw

@@ -1,0 +1,344 @@
+// lora_api.hip -- the C ABI declared in include/gemm_lora.h: argument checks,
+// planning, workspace layout and kernel launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+#include <string>
+
+#include "../../include/gemm_lora.h"
+#include "call.h"
+#include "internal.h"
+#include "lora.h"
+
+namespace {
+
+using namespace dgw::call;
+using dgw::set_error;
+using dgw::set_hip_error;
+
+bool is_nk(const gemm_lora_args_t &a) { return (a.layout & 0xFu) == GEMM_B_NK; }
+int64_t w_rows(const gemm_lora_args_t &a) { return is_nk(a) ? a.N : a.H; }
+int64_t w_row(const gemm_lora_args_t &a) { return is_nk(a) ? a.H : a.N; }
+int64_t stride_a(const gemm_lora_args_t &a) { return or_packed(a.stride_a, (int64_t)a.R * a.H); }
+int64_t stride_b(const gemm_lora_args_t &a) { return or_packed(a.stride_b, (int64_t)a.R * a.N); }
+int dab_size(const gemm_lora_args_t &a) { return a.dab_type == GEMM_LORA_DAB_SAME ? 2 : 4; }
+
+int check_sizes(const gemm_lora_args_t &a, bool backward) {
+    if (a.layout & ~0x1Fu || (a.layout & 0xEu)) return bad("layout word has unknown bits");
+    if (a.T < 0 || a.H < 1 || a.N < 1 || a.R < 1 || a.adapters < 1) return bad("T >= 0, H, N, R and adapters >= 1");
+    if (a.T > GEMM_LORA_MAX_T || a.H > GEMM_LORA_MAX_H || a.N > GEMM_LORA_MAX_H || a.R > GEMM_LORA_MAX_R ||
+        a.adapters > GEMM_LORA_MAX_ADAPTERS)
+        return set_error(GEMM_ERR_UNSUPPORTED, "T, H, N, R or adapters exceeds its GEMM_LORA_MAX_*");
+    if (a.T * a.H > GEMM_LORA_MAX_TH || a.T * a.N > GEMM_LORA_MAX_TH || a.H * a.N > GEMM_LORA_MAX_TH)
+        return set_error(GEMM_ERR_UNSUPPORTED, "T * H, T * N or H * N exceeds GEMM_LORA_MAX_TH");
+    if (a.adapters * (int64_t)a.R * std::max(a.H, a.N) > GEMM_LORA_MAX_LRH || (backward && a.adapters * a.T > GEMM_LORA_MAX_LT))
+        return set_error(GEMM_ERR_UNSUPPORTED, "adapters * R * H, adapters * R * N or adapters * T exceeds its GEMM_LORA_MAX_*");
+    if (a.H % 8 || a.N % 8 || a.R % 8) return set_error(GEMM_ERR_UNSUPPORTED, "H, N and R must be multiples of 8");
+    if (a.dab_type > GEMM_LORA_DAB_FP32_ADD) return bad("unknown dab_type");
+    return GEMM_OK;
+}
+
+Blocks blocks_of(const gemm_lora_args_t &a, bool backward) {
+    Blocks s;
+    auto rows16 = [&](const void *p, int64_t rows, int64_t row, int64_t ld, const char *name) {
+        s.add(p, rows, row * 2, or_packed(ld, row) * 2, name);
+    };
+    auto grad = [&](const void *p, int64_t n, const char *name) { s.add(p, 1, n * dab_size(a), n * dab_size(a), name); };
+    const int64_t ra = (int64_t)a.R * a.H, rb = (int64_t)a.R * a.N;
+    if (backward) {
+        rows16(a.dx, a.T, a.H, a.lddx, "dx");
+        grad(a.da, a.adapters * ra, "da");
+        grad(a.db, a.adapters * rb, "db");
+    } else {
+        rows16(a.y, a.T, a.N, a.ldy, "y");
+    }
+    s.written = s.all;
+    rows16(a.x, a.T, a.H, a.ldx, "x");
+    rows16(a.w, w_rows(a), w_row(a), a.ldw, "w");
+    rows16(a.a, a.adapters, ra, a.stride_a, "a");
+    rows16(a.b, a.adapters, rb, a.stride_b, "b");
+    if (backward) rows16(a.dy, a.T, a.N, a.lddy, "dy");
+    s.add(a.adapter, 1, a.T * 8, a.T * 8, "adapter");
+    s.add(a.scale, 1, a.adapters * 4, a.adapters * 4, "scale");
+    return s;
+}
+
+int check_args(const gemm_lora_args_t &a, bool backward) {
+    int rc = check_sizes(a, backward);
+    if (rc != GEMM_OK) return rc;
+    if (a.num_cus < 0 || a.num_cus > MAX_CUS) return bad("num_cus must be 0 .. 65536");
+    if ((rc = check_ld(or_packed(a.ldx, a.H), a.H, 8, "x")) != GEMM_OK) return rc;
+    if ((rc = check_ld(or_packed(a.ldw, w_row(a)), w_row(a), 8, "w")) != GEMM_OK) return rc;
+    if (stride_a(a) < a.R * a.H || stride_a(a) % 8 || stride_b(a) < a.R * a.N || stride_b(a) % 8)
+        return bad("stride_a and stride_b must be at least a matrix and multiples of 8");
+    if (!backward && (rc = check_ld(or_packed(a.ldy, a.N), a.N, 8, "y")) != GEMM_OK) return rc;
+    if (backward && ((rc = check_ld(or_packed(a.lddy, a.N), a.N, 8, "dy")) != GEMM_OK ||
+                     (rc = check_ld(or_packed(a.lddx, a.H), a.H, 8, "dx")) != GEMM_OK))
+        return rc;
+    const Blocks s = blocks_of(a, backward);
+    for (int i = 0; i < s.all; ++i) {
+        const bool words = s.b[i].base == a.adapter || s.b[i].base == a.scale;
+        if (s.b[i].begin() & (words ? 7 : 15) && s.b[i].base != a.scale)
+            return set_error(GEMM_ERR_UNSUPPORTED, std::string(s.b[i].name) + " must be " + (words ? "8" : "16") + "-byte aligned");
+    }
+    if (a.T == 0) return GEMM_OK;
+    if (!a.x || !a.w || !a.a || !a.b || !a.adapter) return bad("x, w, a, b and adapter must be non-null");
+    if (!backward && !a.y) return bad("y must be non-null");
+    if (backward && !a.dy) return bad("dy must be non-null");
+    if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
+    for (int i = 0; i < s.written; ++i)
+        for (int j = i + 1; j < s.all; ++j)
+            if (overlap(s.b[i], s.b[j])) return overlapping(s.b[i], s.b[j]);
+    return GEMM_OK;
+}
+
+// The narrow product's workgroups: over 64 rows, over the adapters among them and over
+// slices of k, about two a CU of those that find an adapter.
+struct Low {
+    int lists = 1, splits = 1;
+};
+Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
+    const int64_t groups = ceil_div(std::max<int64_t>(a.T, 1), 64) * ceil_div(a.R, dgw::lora_low_rows(dgw::lora_low_tile(a.R, kc)));
+    const int64_t most = std::min<int64_t>(a.adapters, std::min<int64_t>(std::max<int64_t>(a.T, 1), 64));
+    Low l;
+    l.lists = (int)std::max<int64_t>(1, std::min(most, 2 * cus / groups));
+    const int64_t busy = groups * (a.T <= 256 ? l.lists : std::min(l.lists, 2));
+    l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, 2 * cus / busy, (int64_t)16}));
+    return l;
+}
+
+// The wide product's tile and slices.
+Choice out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
+    if (a.T > 128) return choose(rows_p, a.T, k, true, cus);
+    const int tile = a.T <= 32 ? dgw::LP_64x32 : a.T <= 64 ? dgw::LP_64x64 : dgw::LP_64x128;
+    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(2 * cus / ceil_div(rows_p, 64), ceil_div(k, 64) / 4))};
+}
+
+int outer_splits(const gemm_lora_args_t &a, int64_t wide, int cus) {
+    const int64_t blocks = a.adapters * ceil_div(wide, 128) * ceil_div(a.R, 64);
+    return (int)std::max<int64_t>(1, std::min(2 * cus / blocks, ceil_div(a.T, 64) / 8));
+}
+
+struct Plan {
+    Low s, ds;
+    Choice out{dgw::LP_128x128, 1};
+    int da_splits = 1, db_splits = 1;
+    int64_t low = 0, dlow = 0, partial = 0, masks = 0;   // byte offsets
+    int64_t bytes = 0;
+    int64_t take(int64_t n) {
+        const int64_t at = bytes;
+        bytes += round_up(n, 256);
+        return at;
+    }
+};
+
+Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
+    Plan p;
+    const bool nk = is_nk(a);
+    int64_t partial = 0;   // one launch's after the other
+    auto need = [&](int64_t n) { partial = std::max(partial, n); };
+    auto low = [&](Low &l, int64_t k, bool kc, int64_t &at) {
+        l = low_plan(a, k, kc, cus);
+        at = p.take(a.T * a.R * 2);
+        if (l.splits > 1) need(l.splits * a.T * a.R * 4);
+    };
+    if (!backward || a.db) low(p.s, a.H, nk, p.low);
+    if (backward && (a.dx || a.da)) low(p.ds, a.N, !nk, p.dlow);
+    const int64_t wide = backward ? a.H : a.N;
+    if (!backward || a.dx) {
+        p.out = out_plan(a, wide, backward ? a.N : a.H, cus);
+        if (p.out.splits > 1) need(dgw::lora_slots_bytes(p.out.tile, wide, a.T, p.out.splits));
+    }
+    if (backward && (a.da || a.db)) {
+        p.masks = p.take(a.adapters * ceil_div(a.T, 64) * 8);
+        p.da_splits = outer_splits(a, a.H, cus);
+        p.db_splits = outer_splits(a, a.N, cus);
+        if (a.da && p.da_splits > 1) need(p.da_splits * (int64_t)a.adapters * a.R * a.H * 4);
+        if (a.db && p.db_splits > 1) need(p.db_splits * (int64_t)a.adapters * a.R * a.N * 4);
+    }
+    if (partial) p.partial = p.take(partial);
+    return p;
+}
+
+struct Call {
+    hipStream_t stream;
+    void *ws = nullptr;
+    std::unique_lock<std::mutex> lock;   // held for the whole call where ws is the library's
+    int cus;
+    int dtype;
+    bool nk;
+    Plan plan;
+    dgw::LoraRows rows;
+};
+
+int begin(const gemm_lora_args_t &a, bool backward, Call *c) {
+    c->stream = dgw::call_stream(a.stream);
+    c->dtype = (a.layout & 0xF0u) == GEMM_FP16 ? 1 : 0;
+    c->nk = is_nk(a);
+    int rc;
+    c->cus = a.num_cus;
+    if (!c->cus && (rc = dgw::current_device_cus(&c->cus)) != GEMM_OK) return rc;
+    c->plan = make_plan(a, backward, c->cus);
+    c->rows = {a.adapter, (int)a.T, a.adapters, a.scale};
+    c->ws = a.workspace;
+    if (!a.workspace) return dgw::library_workspace(c->plan.bytes, c->stream, &c->ws, &c->lock);
+    if ((int64_t)a.workspace_bytes < c->plan.bytes)
+        return set_error(GEMM_ERR_WORKSPACE, "caller workspace is smaller than plan.workspace_bytes (" + std::to_string(c->plan.bytes) + ")");
+    const Blocks s = blocks_of(a, backward);
+    const Block ws{a.workspace, 1, c->plan.bytes, c->plan.bytes, "workspace"};
+    for (int i = 0; i < s.all; ++i)
+        if (overlap(ws, s.b[i])) return overlapping(ws, s.b[i]);
+    return GEMM_OK;
+}
+
+dgw::LossMatrix matrix(const void *base, int64_t ld, int64_t packed, int64_t rows, bool kc) {
+    dgw::LossMatrix m;
+    m.base = static_cast<const uint16_t *>(base);
+    m.ld = or_packed(ld, packed);
+    m.rows = (int)rows;
+    m.kc = kc;
+    return m;
+}
+
+// a as `rows` x `k`: [R][H] (nk) or [H][R] (kn); b: [N][R] (nk) or [R][N] (kn).
+dgw::LoraFactor factor_a(const gemm_lora_args_t &a, bool rank_rows) {   // rows: the rank, or H
+    const bool nk = is_nk(a);
+    return {matrix(a.a, 0, nk ? a.H : a.R, rank_rows ? a.R : a.H, rank_rows == nk), stride_a(a)};
+}
+dgw::LoraFactor factor_b(const gemm_lora_args_t &a, bool rank_rows) {   // rows: the rank, or N
+    const bool nk = is_nk(a);
+    return {matrix(a.b, 0, nk ? a.R : a.N, rank_rows ? a.R : a.N, rank_rows != nk), stride_b(a)};
+}
+
+int narrow(const gemm_lora_args_t &a, const Call &c, const Low &l, const dgw::LoraFactor &f, const dgw::LossMatrix &x, int64_t k,
+           uint16_t *low) {
+    const dgw::LoraLow p{c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, c.plan.partial), low};
+    const hipError_t e = dgw::launch_lora_low(c.dtype, p, c.stream);
+    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the narrow product");
+}
+
+int wide(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &w, const dgw::LossMatrix &x, const dgw::LoraFactor &f,
+         const uint16_t *low, int64_t k, void *out, int64_t ldo) {
+    const Choice &how = c.plan.out;
+    float *slots = part<float>(c.ws, c.plan.partial);
+    dgw::LoraProduct p{c.rows, w, x, f, low, (int)k, a.R, how.splits, how.splits > 1 ? static_cast<void *>(slots) : out, ldo};
+    hipError_t e = dgw::launch_lora_product(c.dtype, how.tile, p, c.stream);
+    if (e == hipSuccess && how.splits > 1) {
+        p.out = out;
+        e = dgw::launch_lora_join(c.dtype, how.tile, p, slots, c.stream);
+    }
+    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the projection");
+}
+
+int forward(const gemm_lora_args_t &a) {
+    dgw::clear_error();
+    int rc = check_args(a, false);
+    if (rc != GEMM_OK || a.T == 0) return rc;
+    Call c;
+    if ((rc = begin(a, false, &c)) != GEMM_OK) return rc;
+    const dgw::LossMatrix x = matrix(a.x, a.ldx, a.H, a.T, true);
+    uint16_t *s = part<uint16_t>(c.ws, c.plan.low);
+    if ((rc = narrow(a, c, c.plan.s, factor_a(a, true), x, a.H, s)) != GEMM_OK) return rc;
+    return wide(a, c, matrix(a.w, a.ldw, w_row(a), a.N, c.nk), x, factor_b(a, false), s, a.H, a.y, or_packed(a.ldy, a.N));
+}
+
+// da or db: out[o][i] = sum over an adapter's rows of outs[t][o] ins[t][i] as "nk" stores
+// it; one of them holds the narrow rows.
+int outer(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &outs, const dgw::LossMatrix &ins, bool narrow_ins, int splits,
+          void *out, const char *what) {
+    dgw::LoraOuter p;
+    p.P = c.nk ? ins : outs;
+    p.Q = c.nk ? outs : ins;
+    p.narrow_p = narrow_ins == c.nk;
+    p.T = (int)a.T;
+    p.count = a.adapters;
+    p.masks = part<uint64_t>(c.ws, c.plan.masks);
+    p.splits = splits;
+    p.partial = part<float>(c.ws, c.plan.partial);
+    p.out_kind = a.dab_type == GEMM_LORA_DAB_SAME ? dgw::LO_16 : a.dab_type == GEMM_LORA_DAB_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
+    p.out = out;
+    p.ldo = p.P.rows;
+    p.stride = (int64_t)p.P.rows * p.Q.rows;
+    const hipError_t e = dgw::launch_lora_outer(c.dtype, p, c.stream);
+    return e == hipSuccess ? GEMM_OK : set_hip_error(e, what);
+}
+
+int backward(const gemm_lora_args_t &a) {
+    dgw::clear_error();
+    int rc = check_args(a, true);
+    if (rc != GEMM_OK || (!a.dx && !a.da && !a.db)) return rc;
+    hipError_t e;
+    if (a.T == 0) {
+        if (a.dab_type == GEMM_LORA_DAB_FP32_ADD) return GEMM_OK;
+        auto zero = [&](void *p, int64_t row) {
+            return p ? dgw::launch_loss_zero(p, (int64_t)a.adapters * a.R, row * dab_size(a), row * dab_size(a), dgw::call_stream(a.stream))
+                     : hipSuccess;
+        };
+        if ((e = zero(a.da, a.H)) != hipSuccess || (e = zero(a.db, a.N)) != hipSuccess) return set_hip_error(e, "zero da and db");
+        return GEMM_OK;
+    }
+    Call c;
+    if ((rc = begin(a, true, &c)) != GEMM_OK) return rc;
+    const Plan &pl = c.plan;
+    uint16_t *s = part<uint16_t>(c.ws, pl.low), *ds = part<uint16_t>(c.ws, pl.dlow);
+    const dgw::LossMatrix x = matrix(a.x, a.ldx, a.H, a.T, true), dy = matrix(a.dy, a.lddy, a.N, a.T, true);
+    if (a.db && (rc = narrow(a, c, pl.s, factor_a(a, true), x, a.H, s)) != GEMM_OK) return rc;
+    if ((a.dx || a.da) && (rc = narrow(a, c, pl.ds, factor_b(a, true), dy, a.N, ds)) != GEMM_OK) return rc;
+    if (a.dx && (rc = wide(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx,
+                           or_packed(a.lddx, a.H))) != GEMM_OK)
+        return rc;
+    if (!a.da && !a.db) return GEMM_OK;
+    if ((e = dgw::launch_lora_masks(c.rows, part<uint64_t>(c.ws, pl.masks), c.stream)) != hipSuccess)
+        return set_hip_error(e, "launch the rows' masks");
+    const dgw::LossMatrix ms = matrix(s, 0, a.R, a.R, false), mds = matrix(ds, 0, a.R, a.R, false);
+    const dgw::LossMatrix mx = matrix(a.x, a.ldx, a.H, a.H, false), mdy = matrix(a.dy, a.lddy, a.N, a.N, false);
+    if (a.da && (rc = outer(a, c, mds, mx, false, pl.da_splits, a.da, "launch da")) != GEMM_OK) return rc;
+    if (a.db && (rc = outer(a, c, mdy, ms, true, pl.db_splits, a.db, "launch db")) != GEMM_OK) return rc;
+    return GEMM_OK;
+}
+
+int plan(const gemm_lora_args_t *args, int32_t backward, int32_t num_cus, gemm_lora_plan_t *out) {
+    dgw::clear_error();
+    if (!args || !out) return bad("args and out must be non-null");
+    if (num_cus < 1 || num_cus > MAX_CUS) return bad("num_cus must be 1 .. 65536");
+    const int rc = check_sizes(*args, backward != 0);
+    if (rc != GEMM_OK) return rc;
+    std::memset(out, 0, sizeof *out);
+    const Plan p = make_plan(*args, backward != 0, num_cus);
+    const bool kc = is_nk(*args) == !backward;
+    const Low &l = backward ? p.ds : p.s;
+    const dgw::LossTileShape o = dgw::lora_tile_shape(p.out.tile);
+    out->num_cus = num_cus;
+    out->low_tile_r = dgw::lora_low_rows(dgw::lora_low_tile(args->R, kc));
+    out->low_splits = l.splits;
+    out->low_lists = l.lists;
+    out->out_tile_p = o.p;
+    out->out_tile_t = o.q;
+    out->out_splits = p.out.splits;
+    if (backward) {
+        out->da_splits = p.da_splits;
+        out->db_splits = p.db_splits;
+    }
+    out->workspace_bytes = p.bytes;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gemm_lora_plan(const gemm_lora_args_t *args, int32_t backward, int32_t num_cus, gemm_lora_plan_t *out) {
+    return guarded([&] { return plan(args, backward, num_cus, out); });
+}
+
+int gemm_lora_forward(const gemm_lora_args_t *args) {
+    return guarded([&] { return args ? forward(*args) : bad("args is null"); });
+}
+
+int gemm_lora_backward(const gemm_lora_args_t *args) {
+    return guarded([&] { return args ? backward(*args) : bad("args is null"); });
+}
+
+}  // extern "C"

@@ -142,9 +142,9 @@ struct Matrix {
     int64_t part;
 };
 
-// Which of an operand's rows take part; the others are zeros, whatever they hold.
+// Which rows of an operand's tile take part; the others are zeros, whatever they hold.
 struct AllRows {
-    __device__ __forceinline__ bool operator()(int64_t) const { return true; }
+    __device__ __forceinline__ bool operator()(int) const { return true; }
 };
 
 // One operand's slabs: R rows by 64 k, moved by NW waves.  SRC = 2: the slabs of a
@@ -187,7 +187,7 @@ struct Operand {
 #pragma unroll
             for (int x = 0; x < LOADS; ++x) {
                 const int r = 8 * (wave * LOADS + x) + (lane >> 3);
-                off[x] = r < rows && keep(row0 + r) ? (uint32_t)(r * ld + kc) * 2 : OOB;
+                off[x] = r < rows && keep(r) ? (uint32_t)(r * ld + kc) * 2 : OOB;
             }
         } else {
             constexpr int CH = R / 8;                // 16-byte chunks per k-row
@@ -397,11 +397,11 @@ struct Loop {
 
     // acc += the products over slabs [s0, s1) of K.  Ends with a barrier: the LDS
     // is free on return.
-    template <bool RAGGED, class Keep = AllRows>
+    template <bool RAGGED>
     __device__ __forceinline__ void run(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
-                                        Acc &acc, Keep keep = Keep()) {
+                                        Acc &acc) {
         P.init(mp, p0, K, wave % (NW / KINDS), lane);
-        Q.init(mq, q0, K, wave, lane, keep);
+        Q.init(mq, q0, K, wave, lane);
         const int n = s1 - s0;
         if (n <= 0) return;
         FragP p[2];
@@ -459,11 +459,10 @@ struct Loop {
         wait_vm_lgkm<0>();
         barrier();
     }
-    template <class Keep = AllRows>
     __device__ __forceinline__ void run_any(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K, int s0, int s1,
-                                            Acc &acc, Keep keep = Keep()) {
-        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc, keep);
-        else run<true>(mp, p0, mq, q0, K, s0, s1, acc, keep);
+                                            Acc &acc) {
+        if (K % KB == 0) run<false>(mp, p0, mq, q0, K, s0, s1, acc);
+        else run<true>(mp, p0, mq, q0, K, s0, s1, acc);
     }
     // SRC = 2, before run: the second product, over the same K (its slabs count on).
     __device__ __forceinline__ void also(const Matrix &mp, int64_t p0, const Matrix &mq, int64_t q0, int K) {

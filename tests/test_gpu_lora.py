@@ -1,0 +1,87 @@
+"""GPU parity of the projection with low-rank adapters with the 64-bit oracle, every element within its bound."""
+import pytest
+import torch
+
+from lora_util import call_backward, call_forward, make, oracle_backward, oracle_forward, ratio, stored
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dg():
+    import dense_gemm_work_amd as dg
+
+    assert torch.cuda.is_available(), "GPU test run without a visible GPU"
+    return dg
+
+
+def check_forward(dg, d, layout, dtype, **kw):
+    r = ratio(call_forward(dg, d, layout, **kw), oracle_forward(d, dtype))
+    print(f"    y {r:.3f}", flush=True)
+    assert r <= 1
+
+
+def check_backward(dg, d, layout, dtype, **kw):
+    got = call_backward(dg, d, layout, **kw)
+    want = oracle_backward(d, dtype, dab_type="fp32" if got[1].dtype == torch.float32 else None)
+    worst = {"dx": ratio(got[0], want["dx"])}
+    for name, t in zip(("da", "db"), got[1:]):
+        worst[name] = ratio(stored(t, layout), want[name])
+    print("   ", {k: round(v, 3) for k, v in worst.items()}, flush=True)
+    assert all(v <= 1 for v in worst.values()), worst
+
+
+SIZES = [   # T, H, N, L, R, dtype, layout, order
+    (1, 8, 8, 1, 8, "bf16", "nk", "one"),             # the smallest
+    (1, 72, 136, 3, 8, "fp16", "kn", "one"),
+    (1, 2048, 2048, 8, 16, "bf16", "nk", "one"),      # one token
+    (1, 256, 256, 8, 16, "bf16", "nk", "none"),
+    (2, 520, 264, 2, 24, "fp16", "nk", "mixed"),
+    (31, 264, 1000, 40, 16, "bf16", "kn", "mixed"),   # more adapters than rows
+    (33, 128, 520, 5, 64, "bf16", "nk", "mixed"),
+    (64, 1024, 264, 64, 8, "fp16", "nk", "mixed"),    # nearly a row each
+    (96, 512, 1032, 64, 16, "bf16", "nk", "mixed"),
+    (128, 200, 72, 4, 72, "bf16", "kn", "mixed"),     # a rank of two slabs
+    (129, 200, 72, 3, 136, "fp16", "nk", "packed"),   # a rank of three
+    (300, 136, 520, 7, 32, "bf16", "nk", "packed"),
+    (300, 136, 520, 300, 8, "bf16", "kn", "mixed"),   # many adapters in every tile
+    (777, 1032, 264, 5, 128, "fp16", "kn", "packed"),
+    (1000, 64, 64, 1, 8, "bf16", "nk", "one"),        # one adapter, many rows
+    (1030, 264, 2056, 9, 64, "bf16", "nk", "mixed"),
+    (4100, 72, 136, 2, 16, "fp16", "kn", "packed"),   # more rows than one word's slabs
+]
+
+
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_forward(dg, size):
+    T, H, N, L, R, dtype, layout, order = size
+    check_forward(dg, make(T, H, N, L, R, dtype, order, seed=T + N, dev="cuda"), layout, dtype)
+
+
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_backward(dg, size):
+    T, H, N, L, R, dtype, layout, order = size
+    check_backward(dg, make(T, H, N, L, R, dtype, order, seed=T + N, dev="cuda"), layout, dtype)
+
+
+# one case for each tile of the wide product (the plan's fields on 256 CUs)
+SHAPES = [
+    ("64x32", 20, 1032, 4104, "bf16", (64, 32)),
+    ("64x64", 50, 1032, 4104, "fp16", (64, 64)),
+    ("64x128", 100, 1032, 4104, "bf16", (64, 128)),
+    ("128x128", 400, 520, 4104, "fp16", (128, 128)),
+    ("256x256", 4000, 2000, 2056, "bf16", (256, 256)),
+    ("256x256, the other way", 4000, 2056, 2000, "fp16", None),   # dx on these tiles
+]
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: s[0])
+def test_every_tile(dg, shape, layout):
+    _, T, H, N, dtype, tile = shape
+    a = dg.GemmLoraArgs(T=T, H=H, N=N, R=16, adapters=6, layout=dg.layout_word(layout, dtype), dx=1)
+    plan = dg.gemm_lora_plan(a, tile is None, 256)
+    assert (plan.out_tile_p, plan.out_tile_t) == (tile or (256, 256))
+    d = make(T, H, N, 6, 16, dtype, "packed", seed=5, dev="cuda")
+    check_forward(dg, d, layout, dtype)
+    check_backward(dg, d, layout, dtype)
