@@ -25,32 +25,36 @@ struct LoraFactor {
     int64_t stride;
 };
 
-// low[row][r] = scale sum_k x[row][k] f[r][k] with the row's own adapter's f, [T][R] in
-// the operands' type; rows without an adapter are left as they are.  `workgroups` of a
-// group of rows share its adapters (`lists`) and the k slabs (`splits`, through
-// `partial` [splits][T][R] fp32).
+// partial[s][row][r] = sum over slice s of k of x[row][k] f[r][k] with the row's own
+// adapter's f, [splits][T][R] fp32, unscaled; rows without an adapter are left as they
+// are.  `lists` workgroups of a group of rows share its adapters.
 struct LoraLow {
     LoraRows rows;
     LoraFactor f;
     LossMatrix x;       // T rows, k contiguous
     int R, K;
     int lists, splits;
-    float *partial;
-    uint16_t *low;
+    float *partial;     // launch_lora_lows: nullptr leaves this product out
+    uint16_t *low;      // launch_lora_lows with masks: the scaled sums as the type holds them, [T][R]; nullptr: not kept
 };
 enum LoraLowTile : int { LL_32x64 = 0, LL_64x64, LL_128x64 };   // R x rows; 32: k contiguous only
 int lora_low_tile(int R, bool kc);
 int lora_low_rows(int tile);    // R rows of a tile
 hipError_t launch_lora_low(int dtype, const LoraLow &p, hipStream_t stream);
+// Both products of a backward call, one with a factor stored k contiguous and one not,
+// and, masks != nullptr, their low and masks[a][slab]: which of rows 64 slab .. + 63
+// have adapter a.
+hipError_t launch_lora_lows(int dtype, const LoraLow &s, const LoraLow &ds, uint64_t *masks, hipStream_t stream);
 
-// out[q][p] = sum_k P[p][k] x[q][k] + sum_r f[p][r] low[q][r], f the row's adapter's; the
-// operands' type, or (splits > 1) slots as launch_loss_product writes them.  Rows whose
+// out[q][p] = sum_k P[p][k] x[q][k] + sum_r f[p][r] low[q][r], f the row's adapter's and low its
+// scaled partial sums as the type holds them; the operands' type, or (splits > 1) slots as launch_loss_product writes them.  Rows whose
 // adapter is out of range are NaN.
 struct LoraProduct {
     LoraRows rows;
     LossMatrix P, x;
     LoraFactor f;       // P.rows rows, stored as P is
-    const uint16_t *low;
+    const float *partial;
+    int low_splits;
     int K, R, splits;
     void *out;
     int64_t ldo;
@@ -60,9 +64,6 @@ LossTileShape lora_tile_shape(int tile);
 int64_t lora_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits);
 hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, hipStream_t stream);
 hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, const float *slots, hipStream_t stream);
-
-// masks[a][slab]: which of rows 64 slab .. + 63 have adapter a.
-hipError_t launch_lora_masks(const LoraRows &rows, uint64_t *masks, hipStream_t stream);
 
 // out_a[q][p] = sum over the rows t of adapter a of P[t][p] Q[t][q], for every adapter.
 // One of P and Q is the narrow side (R wide, `narrow_p` says which).
@@ -74,9 +75,10 @@ struct LoraOuter {
     int splits;
     float *partial;     // splits > 1: [splits][count][Q.rows][P.rows]
     int out_kind;       // LO_16, LO_F32, LO_F32_ADD
-    void *out;          // [count][Q.rows][P.rows], rows ldo apart, adapters `stride`
+    void *out;          // [count][Q.rows][P.rows], rows ldo apart, adapters `stride`; nullptr: left out
     int64_t ldo, stride;
 };
-hipError_t launch_lora_outer(int dtype, const LoraOuter &p, hipStream_t stream);
+// da and db in one launch, one of them with a narrow P.
+hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, hipStream_t stream);
 
 }  // namespace dgw

@@ -105,7 +105,7 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     Low l;
     l.lists = (int)std::max<int64_t>(1, std::min(most, 2 * cus / groups));
     const int64_t busy = groups * (a.T <= 256 ? l.lists : std::min(l.lists, 2));
-    l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, 2 * cus / busy, (int64_t)16}));
+    l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, 2 * cus / busy, (int64_t)9}));
     return l;
 }
 
@@ -125,7 +125,8 @@ struct Plan {
     Low s, ds;
     Choice out{dgw::LP_128x128, 1};
     int da_splits = 1, db_splits = 1;
-    int64_t low = 0, dlow = 0, partial = 0, masks = 0;   // byte offsets
+    int64_t db_at = 0;   // db's slices behind da's
+    int64_t low = 0, dlow = 0, part_s = 0, part_ds = 0, partial = 0, masks = 0;   // byte offsets
     int64_t bytes = 0;
     int64_t take(int64_t n) {
         const int64_t at = bytes;
@@ -139,24 +140,29 @@ Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     const bool nk = is_nk(a);
     int64_t partial = 0;   // one launch's after the other
     auto need = [&](int64_t n) { partial = std::max(partial, n); };
-    auto low = [&](Low &l, int64_t k, bool kc, int64_t &at) {
+    const bool own = backward && (a.da || a.db);   // the adapters' gradients: s and ds in the type, too
+    auto low = [&](Low &l, int64_t k, bool kc, int64_t &slices, int64_t &at) {
         l = low_plan(a, k, kc, cus);
-        at = p.take(a.T * a.R * 2);
-        if (l.splits > 1) need(l.splits * a.T * a.R * 4);
+        slices = p.take(l.splits * a.T * a.R * 4);
+        if (own) at = p.take(a.T * a.R * 2);
     };
-    if (!backward || a.db) low(p.s, a.H, nk, p.low);
-    if (backward && (a.dx || a.da)) low(p.ds, a.N, !nk, p.dlow);
+    if (!backward || a.db) low(p.s, a.H, nk, p.part_s, p.low);
+    if (backward && (a.dx || a.da)) low(p.ds, a.N, !nk, p.part_ds, p.dlow);
     const int64_t wide = backward ? a.H : a.N;
     if (!backward || a.dx) {
         p.out = out_plan(a, wide, backward ? a.N : a.H, cus);
         if (p.out.splits > 1) need(dgw::lora_slots_bytes(p.out.tile, wide, a.T, p.out.splits));
     }
-    if (backward && (a.da || a.db)) {
+    if (own) {
         p.masks = p.take(a.adapters * ceil_div(a.T, 64) * 8);
         p.da_splits = outer_splits(a, a.H, cus);
         p.db_splits = outer_splits(a, a.N, cus);
-        if (a.da && p.da_splits > 1) need(p.da_splits * (int64_t)a.adapters * a.R * a.H * 4);
-        if (a.db && p.db_splits > 1) need(p.db_splits * (int64_t)a.adapters * a.R * a.N * 4);
+        // both at once
+        int64_t both = 0;
+        if (a.da && p.da_splits > 1) both += round_up(p.da_splits * (int64_t)a.adapters * a.R * a.H * 4, 256);
+        p.db_at = both;
+        if (a.db && p.db_splits > 1) both += p.db_splits * (int64_t)a.adapters * a.R * a.N * 4;
+        need(both);
     }
     if (partial) p.partial = p.take(partial);
     return p;
@@ -212,18 +218,17 @@ dgw::LoraFactor factor_b(const gemm_lora_args_t &a, bool rank_rows) {   // rows:
     return {matrix(a.b, 0, nk ? a.R : a.N, rank_rows ? a.R : a.N, rank_rows != nk), stride_b(a)};
 }
 
-int narrow(const gemm_lora_args_t &a, const Call &c, const Low &l, const dgw::LoraFactor &f, const dgw::LossMatrix &x, int64_t k,
-           uint16_t *low) {
-    const dgw::LoraLow p{c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, c.plan.partial), low};
-    const hipError_t e = dgw::launch_lora_low(c.dtype, p, c.stream);
-    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the narrow product");
+dgw::LoraLow narrow(const gemm_lora_args_t &a, const Call &c, const Low &l, const dgw::LoraFactor &f, const dgw::LossMatrix &x, int64_t k,
+                    int64_t slices) {
+    return {c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, slices), nullptr};
 }
 
 int wide(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &w, const dgw::LossMatrix &x, const dgw::LoraFactor &f,
-         const uint16_t *low, int64_t k, void *out, int64_t ldo) {
+         const dgw::LoraLow &low, int64_t k, void *out, int64_t ldo) {
     const Choice &how = c.plan.out;
     float *slots = part<float>(c.ws, c.plan.partial);
-    dgw::LoraProduct p{c.rows, w, x, f, low, (int)k, a.R, how.splits, how.splits > 1 ? static_cast<void *>(slots) : out, ldo};
+    dgw::LoraProduct p{c.rows, w, x, f, low.partial, low.splits, (int)k, a.R, how.splits,
+                       how.splits > 1 ? static_cast<void *>(slots) : out, ldo};
     hipError_t e = dgw::launch_lora_product(c.dtype, how.tile, p, c.stream);
     if (e == hipSuccess && how.splits > 1) {
         p.out = out;
@@ -239,15 +244,16 @@ int forward(const gemm_lora_args_t &a) {
     Call c;
     if ((rc = begin(a, false, &c)) != GEMM_OK) return rc;
     const dgw::LossMatrix x = matrix(a.x, a.ldx, a.H, a.T, true);
-    uint16_t *s = part<uint16_t>(c.ws, c.plan.low);
-    if ((rc = narrow(a, c, c.plan.s, factor_a(a, true), x, a.H, s)) != GEMM_OK) return rc;
+    const dgw::LoraLow s = narrow(a, c, c.plan.s, factor_a(a, true), x, a.H, c.plan.part_s);
+    const hipError_t e = dgw::launch_lora_low(c.dtype, s, c.stream);
+    if (e != hipSuccess) return set_hip_error(e, "launch the narrow product");
     return wide(a, c, matrix(a.w, a.ldw, w_row(a), a.N, c.nk), x, factor_b(a, false), s, a.H, a.y, or_packed(a.ldy, a.N));
 }
 
 // da or db: out[o][i] = sum over an adapter's rows of outs[t][o] ins[t][i] as "nk" stores
 // it; one of them holds the narrow rows.
-int outer(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &outs, const dgw::LossMatrix &ins, bool narrow_ins, int splits,
-          void *out, const char *what) {
+dgw::LoraOuter outer(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &outs, const dgw::LossMatrix &ins, bool narrow_ins,
+                     int splits, int64_t at, void *out) {
     dgw::LoraOuter p;
     p.P = c.nk ? ins : outs;
     p.Q = c.nk ? outs : ins;
@@ -256,13 +262,12 @@ int outer(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &outs,
     p.count = a.adapters;
     p.masks = part<uint64_t>(c.ws, c.plan.masks);
     p.splits = splits;
-    p.partial = part<float>(c.ws, c.plan.partial);
+    p.partial = part<float>(c.ws, c.plan.partial + at);
     p.out_kind = a.dab_type == GEMM_LORA_DAB_SAME ? dgw::LO_16 : a.dab_type == GEMM_LORA_DAB_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
     p.out = out;
     p.ldo = p.P.rows;
     p.stride = (int64_t)p.P.rows * p.Q.rows;
-    const hipError_t e = dgw::launch_lora_outer(c.dtype, p, c.stream);
-    return e == hipSuccess ? GEMM_OK : set_hip_error(e, what);
+    return p;
 }
 
 int backward(const gemm_lora_args_t &a) {
@@ -282,21 +287,25 @@ int backward(const gemm_lora_args_t &a) {
     Call c;
     if ((rc = begin(a, true, &c)) != GEMM_OK) return rc;
     const Plan &pl = c.plan;
-    uint16_t *s = part<uint16_t>(c.ws, pl.low), *ds = part<uint16_t>(c.ws, pl.dlow);
+    const bool own = a.da || a.db;
     const dgw::LossMatrix x = matrix(a.x, a.ldx, a.H, a.T, true), dy = matrix(a.dy, a.lddy, a.N, a.T, true);
-    if (a.db && (rc = narrow(a, c, pl.s, factor_a(a, true), x, a.H, s)) != GEMM_OK) return rc;
-    if ((a.dx || a.da) && (rc = narrow(a, c, pl.ds, factor_b(a, true), dy, a.N, ds)) != GEMM_OK) return rc;
+    dgw::LoraLow s = narrow(a, c, pl.s, factor_a(a, true), x, a.H, pl.part_s);
+    dgw::LoraLow ds = narrow(a, c, pl.ds, factor_b(a, true), dy, a.N, pl.part_ds);
+    s.low = part<uint16_t>(c.ws, pl.low);
+    ds.low = part<uint16_t>(c.ws, pl.dlow);
+    if (!a.db) s.partial = nullptr, s.low = nullptr;
+    if (!a.dx && !a.da) ds.partial = nullptr, ds.low = nullptr;
+    if ((e = dgw::launch_lora_lows(c.dtype, s, ds, own ? part<uint64_t>(c.ws, pl.masks) : nullptr, c.stream)) != hipSuccess)
+        return set_hip_error(e, "launch the narrow products");
     if (a.dx && (rc = wide(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx,
                            or_packed(a.lddx, a.H))) != GEMM_OK)
         return rc;
-    if (!a.da && !a.db) return GEMM_OK;
-    if ((e = dgw::launch_lora_masks(c.rows, part<uint64_t>(c.ws, pl.masks), c.stream)) != hipSuccess)
-        return set_hip_error(e, "launch the rows' masks");
-    const dgw::LossMatrix ms = matrix(s, 0, a.R, a.R, false), mds = matrix(ds, 0, a.R, a.R, false);
+    if (!own) return GEMM_OK;
+    const dgw::LossMatrix ms = matrix(s.low, 0, a.R, a.R, false), mds = matrix(ds.low, 0, a.R, a.R, false);
     const dgw::LossMatrix mx = matrix(a.x, a.ldx, a.H, a.H, false), mdy = matrix(a.dy, a.lddy, a.N, a.N, false);
-    if (a.da && (rc = outer(a, c, mds, mx, false, pl.da_splits, a.da, "launch da")) != GEMM_OK) return rc;
-    if (a.db && (rc = outer(a, c, mdy, ms, true, pl.db_splits, a.db, "launch db")) != GEMM_OK) return rc;
-    return GEMM_OK;
+    e = dgw::launch_lora_outers(c.dtype, outer(a, c, mds, mx, false, pl.da_splits, 0, a.da),
+                                outer(a, c, mdy, ms, true, pl.db_splits, pl.db_at, a.db), c.stream);
+    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch da and db");
 }
 
 int plan(const gemm_lora_args_t *args, int32_t backward, int32_t num_cus, gemm_lora_plan_t *out) {

@@ -35,30 +35,36 @@ __device__ __forceinline__ int adapter_of(const LoraRows &r, int64_t row) {
 // their first rows.
 template <int TQ>
 struct List {
-    int id[TQ], of[TQ], count[TQ / 32 + 1];
+    static constexpr int WORDS = (TQ + 63) / 64;
+    int id[TQ], of[TQ], count;
 
-    // Every thread of the workgroup calls this; it ends with a barrier.
-    __device__ __forceinline__ void fill(const LoraRows &r, int64_t q0) {
-        for (int t = threadIdx.x; t < TQ; t += blockDim.x) id[t] = adapter_of(r, q0 + t);
+    // Every thread of the workgroup calls this, thread t with the adapter of row t; it
+    // ends with a barrier.  One wave finds them, each step taking all rows of the first
+    // row left: as many steps as adapters.  (Each row compared with all before it took
+    // 6 us of a 128-row tile.)
+    __device__ __forceinline__ void fill(int mine) {
+        if (threadIdx.x < TQ) id[threadIdx.x] = mine;
         __syncthreads();
-        const int t = threadIdx.x, mine = t < TQ ? id[t] : NONE;
-        bool first = mine >= 0;
-        if (t < TQ)
-            for (int u = 0; u < t && first; ++u) first = id[u] != mine;
-        const uint64_t set = __ballot(first);
-        if (t < TQ && (t & 63) == 0) count[t >> 6] = __popcll(set);
-        __syncthreads();
-        int at = __popcll(set & ((1ull << (t & 63)) - 1)), all = 0;
-        for (int w = 0; w < (TQ + 63) / 64; ++w) {
-            if (w < t >> 6) at += count[w];
-            all += count[w];
+        if (threadIdx.x < 64) {
+            int v[WORDS];
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w) v[w] = 64 * w + threadIdx.x < TQ ? id[64 * w + threadIdx.x] : NONE;
+            int n = 0;
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w)
+                for (uint64_t left = __ballot(v[w] >= 0); left; left = __ballot(v[w] >= 0)) {
+                    const int a = __builtin_amdgcn_readlane(v[w], __builtin_ctzll(left));
+#pragma unroll
+                    for (int u = w; u < WORDS; ++u)
+                        if (v[u] == a) v[u] = NONE;
+                    if (threadIdx.x == 0) of[n] = a;
+                    ++n;
+                }
+            if (threadIdx.x == 0) count = n;
         }
-        if (first) of[at] = mine;
-        __syncthreads();
-        if (t == 0) count[TQ / 32] = all;
         __syncthreads();
     }
-    __device__ __forceinline__ int n() const { return __builtin_amdgcn_readfirstlane(count[TQ / 32]); }
+    __device__ __forceinline__ int n() const { return __builtin_amdgcn_readfirstlane(count); }
     __device__ __forceinline__ int adapter(int i) const { return __builtin_amdgcn_readfirstlane(of[i]); }
 };
 
@@ -66,31 +72,72 @@ __device__ __forceinline__ Matrix shifted(Matrix m, int64_t elements) {
     m.base += elements;
     return m;
 }
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4)); }   // loads go on
+
+// Sum over the slices of four values of a narrow row, in slice order, four loads in flight.
+__device__ __forceinline__ f32x4 sum_slices(const float *at, int64_t step, int splits) {
+    auto get = [&](int s) { return *reinterpret_cast<const f32x4 *>(at + s * step); };
+    f32x4 v = get(0);
+    int s = 1;
+    for (; s + 4 <= splits; s += 4) {
+        const f32x4 a = get(s), b = get(s + 1), c = get(s + 2), d = get(s + 3);
+        v = (((v + a) + b) + c) + d;
+    }
+    for (; s < splits; ++s) v += get(s);
+    return v;
+}
+
+// The same of eight.
+__device__ __forceinline__ void sum_slices(const float *at, int64_t step, int splits, f32x4 &u, f32x4 &v) {
+    auto get = [&](int s, int h) { return *reinterpret_cast<const f32x4 *>(at + s * step + 4 * h); };
+    u = get(0, 0);
+    v = get(0, 1);
+    int s = 1;
+    for (; s + 4 <= splits; s += 4) {
+        f32x4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = get(s + i, 0);
+            b[i] = get(s + i, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u += a[i];
+            v += b[i];
+        }
+    }
+    for (; s < splits; ++s) {
+        u += get(s, 0);
+        v += get(s, 1);
+    }
+}
 
 // ---------------------------------------------------------------------------
-// The narrow products.
+// The narrow products, unscaled, as fp32 slices [splits][T][R].  A workgroup takes
+// one slice of k of a group of rows, and of the group's adapters every `lists`-th:
+// those are the slowest part of its number, as most of them find no adapter and
+// would leave their XCDs idle (8192 x 4096, rank 64: 57 us with them fastest).
 // ---------------------------------------------------------------------------
 struct LowParams {
     LoraRows rows;
     Matrix f, x;
     int64_t stride;
     int R, K, slabs;
-    int tiles_r, lists, splits;
+    int tiles_r, groups, lists, splits;
+    int blocks;
     float *partial;
-    uint16_t *low;
+    uint16_t *low;   // lora_low_join
 };
 
-template <int DT, class L>
-__global__ __launch_bounds__(L::NT, L::WAVES) void lora_low(LowParams p) {
-    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
-    __shared__ List<L::TQ> list;
-    int id = (int)blockIdx.x;
+template <class L>
+__device__ __forceinline__ void low_block(const LowParams &p, int id, char *lds, List<L::TQ> &list) {
     const int split = id % p.splits;
     id /= p.splits;
-    const int first = id % p.lists;
-    id /= p.lists;
-    const int64_t p0 = (int64_t)(id % p.tiles_r) * L::TP, q0 = (int64_t)(id / p.tiles_r) * L::TQ;
-    list.fill(p.rows, q0);
+    const int64_t p0 = (int64_t)(id % p.tiles_r) * L::TP;
+    id /= p.tiles_r;
+    const int64_t q0 = (int64_t)(id % p.groups) * L::TQ;
+    const int first = id / p.groups;
+    list.fill(adapter_of(p.rows, threadIdx.x < L::TQ ? q0 + threadIdx.x : p.rows.T));
     const int s0 = (int)((int64_t)p.slabs * split / p.splits), s1 = (int)((int64_t)p.slabs * (split + 1) / p.splits);
     L loop(lds);
     for (int i = first; i < list.n(); i += p.lists) {
@@ -99,40 +146,70 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void lora_low(LowParams p) {
         L::zero(acc);
         loop.run_any(shifted(p.f, a * p.stride), p0, p.x, q0, p.K, s0, s1, acc, [&](int r) { return list.id[r] == a; });
         if (!loop.active()) continue;
-        const float scale = p.rows.scale ? p.rows.scale[a] : 1.0f;
 #pragma unroll
         for (int b = 0; b < L::RB; ++b)
 #pragma unroll
             for (int j = 0; j < L::CB; ++j) {
                 const int col = (int)p0 + loop.p_of(b, 0);
                 const int64_t row = q0 + loop.q_of(j);
-                if (col >= p.R || list.id[loop.q_of(j)] != a) continue;
-                const f32x4 v = acc.v[b][j];
-                if (p.splits > 1)
-                    *reinterpret_cast<f32x4 *>(p.partial + ((int64_t)split * p.rows.T + row) * p.R + col) = v;
-                else
-                    *reinterpret_cast<u32x2 *>(p.low + row * p.R + col) =
-                        u32x2{pack2<DT>(v[0] * scale, v[1] * scale), pack2<DT>(v[2] * scale, v[3] * scale)};
+                if (col < p.R && list.id[loop.q_of(j)] == a)
+                    *reinterpret_cast<f32x4 *>(p.partial + ((int64_t)split * p.rows.T + row) * p.R + col) = acc.v[b][j];
             }
     }
 }
 
-// The slices' sums, added in slice order, scaled and rounded: a thread per four values.
+template <class L>
+__global__ __launch_bounds__(L::NT, L::WAVES) void lora_low(LowParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    __shared__ List<L::TQ> list;
+    low_block<L>(p, (int)blockIdx.x, lds, list);
+}
+
+// Which rows of each 64 have which adapter: one wave per 64 rows.
+__device__ __forceinline__ void mask_block(const LoraRows &r, int id, uint64_t *masks) {
+    const int lane = threadIdx.x & 63, slabs = (r.T + 63) / 64;
+    const int slab = id * 4 + (threadIdx.x >> 6);
+    if (slab >= slabs) return;
+    const int mine = adapter_of(r, slab * (int64_t)64 + lane);
+    for (int a0 = 0; a0 < r.count; a0 += 64) {
+        uint64_t keep = 0;
+        for (int a = 0; a < min(64, r.count - a0); ++a) {
+            const uint64_t m = __ballot(mine == a0 + a);
+            if (lane == a) keep = m;
+        }
+        if (a0 + lane < r.count) masks[(int64_t)(a0 + lane) * slabs + slab] = keep;
+    }
+}
+
+// Backward: both narrow products (one factor has k contiguous, the other its rows) and
+// the rows' masks in one launch.
+template <class LK, class LR>
+__global__ __launch_bounds__(256, LK::WAVES < LR::WAVES ? LK::WAVES : LR::WAVES) void lora_lows(LowParams k, LowParams r, uint64_t *masks) {
+    __shared__ __attribute__((aligned(16))) char lds[LK::LDS_BYTES > LR::LDS_BYTES ? LK::LDS_BYTES : LR::LDS_BYTES];
+    __shared__ List<LK::TQ> list;
+    static_assert(LK::TQ == LR::TQ && LK::NT == 256 && LR::NT == 256, "one list, one size of workgroup");
+    const int id = (int)blockIdx.x;
+    if (id < k.blocks) low_block<LK>(k, id, lds, list);
+    else if (id < k.blocks + r.blocks) low_block<LR>(r, id - k.blocks, lds, list);
+    else mask_block(k.rows, id - k.blocks - r.blocks, masks);
+}
+
+// s and ds as the type holds them, for the adapters' gradients: a thread per four values.
 template <int DT>
-__global__ __launch_bounds__(256) void lora_low_join(LowParams p) {
-    const int quads = p.R / 4;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, row = id / quads;
-    if (row >= p.rows.T) return;
-    const int a = adapter_of(p.rows, row);
-    if (a < 0) return;
-    const int col = 4 * (int)(id % quads);
-    const f32x4 *at = reinterpret_cast<const f32x4 *>(p.partial + row * p.R + col);
-    const int64_t step = (int64_t)p.rows.T * quads;
-    f32x4 v = at[0];
-    for (int s = 1; s < p.splits; ++s) v += at[s * step];
-    const float scale = p.rows.scale ? p.rows.scale[a] : 1.0f;
-    *reinterpret_cast<u32x2 *>(p.low + row * p.R + col) =
-        u32x2{pack2<DT>(v[0] * scale, v[1] * scale), pack2<DT>(v[2] * scale, v[3] * scale)};
+__global__ __launch_bounds__(256) void lora_low_join(LowParams a, LowParams b) {
+    const int64_t each = (int64_t)a.rows.T * (a.R / 4);
+    int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const bool second = id >= each;
+    if (second) id -= each;
+    if (id >= each) return;
+    const int quads = a.R / 4, col = 4 * (int)(id % quads);
+    const int64_t row = id / quads;
+    const int l = adapter_of(a.rows, row);
+    uint16_t *low = second ? b.low : a.low;
+    if (l < 0 || !low) return;
+    const float scale = a.rows.scale ? a.rows.scale[l] : 1.0f;
+    const f32x4 v = sum_slices((second ? b.partial : a.partial) + row * a.R + col, (int64_t)a.rows.T * a.R, second ? b.splits : a.splits) * scale;
+    *reinterpret_cast<u32x2 *>(low + row * a.R + col) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
 }
 
 // ---------------------------------------------------------------------------
@@ -140,8 +217,10 @@ __global__ __launch_bounds__(256) void lora_low_join(LowParams p) {
 // ---------------------------------------------------------------------------
 struct WideParams {
     LoraRows rows;
-    Matrix P, x, f, low;
+    Matrix P, x, f;
     int64_t stride;
+    const float *partial;   // the narrow product's slices
+    int low_splits;
     int K, R;
     Grid g;
     bool slots;
@@ -150,108 +229,149 @@ struct WideParams {
 };
 
 // acc += the products of the adapters' slabs (list entries from, from + every, ...)
-// with the narrow rows, as a stream of (adapter, slab) items through NS stages.  Uses
-// the first BYTES bytes of the LDS, which must be free, and leaves them free.
+// with the narrow rows.  Those of the tile, 64 ranks at a time, are put together from
+// their slices, scaled, rounded and laid down in LDS, and stay in registers; the
+// adapters' slabs stream through NS stages, and each meets the 16-row blocks that hold
+// rows of its own, the others' rows masked to zero.  Uses the first BYTES bytes of the
+// LDS, which must be free, and leaves them free.
 template <int DT, class L, int NS>
 struct Extra {
     using OpP = typename L::OpP;
     using OpQ = typename L::OpQ;
-    static constexpr int STAGE = OpP::SLAB + OpQ::SLAB, BYTES = NS * STAGE, LOADS = OpP::LOADS + OpQ::LOADS;
-    static constexpr int PA = OpP::template addresses<L::RB>(), QA = OpQ::template addresses<L::CB>();
-    static_assert((NS - 1) * LOADS < 64, "the wait counter holds the loads in flight");
+    static constexpr int STAGE = OpP::SLAB, LOADS = OpP::LOADS, ROWS_AT = NS * STAGE, BYTES = ROWS_AT + L::TQ * 128;
+    static constexpr int PA = OpP::template addresses<L::RB>();
+    static_assert((NS - 1) * LOADS < 64 && NS <= 8, "the wait counter holds the loads in flight");
 
-    static __device__ __forceinline__ void run(const L &loop, const WideParams &p, int64_t p0, int64_t q0,
+    // Small tiles keep the narrow rows in registers and skip blocks without rows of the
+    // adapter; in the large ones either would spill the accumulators.
+    static constexpr bool HOLD = L::RB * L::CB <= 8;
+    static __device__ __forceinline__ u32x4 masked(u32x4 v, bool keep) {
+        return u32x4{keep ? v[0] : 0u, keep ? v[1] : 0u, keep ? v[2] : 0u, keep ? v[3] : 0u};
+    }
+
+    static __device__ __forceinline__ void run(const L &loop, char *lds, const WideParams &p, int64_t p0, int64_t q0,
                                                const List<L::TQ> &list, int from, int every, typename L::Acc &acc) {
         const int lane = loop.lane, wave = loop.wave, slabs = (p.R + KB - 1) / KB;
-        const int mine = list.n() > from ? (list.n() - from + every - 1) / every : 0, n = mine * slabs;
+        const int n = list.n() > from ? (list.n() - from + every - 1) / every : 0;
         if (!n) return;
         OpP P;
-        OpQ Q;
         P.init(p.f, p0, p.R, wave, lane);
-        Q.init(p.low, q0, p.R, wave, lane);
-        int id[OpQ::LOADS];   // the adapters of the rows that this lane loads
+        int id[L::CB];   // the adapters of the rows that this lane multiplies
 #pragma unroll
-        for (int x = 0; x < OpQ::LOADS; ++x) id[x] = list.id[8 * (wave * OpQ::LOADS + x) + (lane >> 3)];
-        uint32_t pa[PA], qa[QA];
+        for (int j = 0; j < L::CB; ++j) id[j] = list.id[loop.q_of(j)];
+        uint32_t pa[PA];
 #pragma unroll
         for (int i = 0; i < PA; ++i) pa[i] = OpP::address(loop.lds0, loop.wp * L::WAVE_P, lane, i);
+#pragma unroll 1
+        for (int slab = 0; slab < slabs; ++slab) {
+            auto issue = [&](int i, int stage) {
+                const i32x4 rp = P.rsrc(slab, list.adapter(from + i * every) * p.stride * 2);
 #pragma unroll
-        for (int i = 0; i < QA; ++i) qa[i] = OpQ::address(loop.lds0 + OpP::SLAB, loop.wq * L::WAVE_Q, lane, i);
-        int slab = 0, at = from;   // of the next item
-        auto issue = [&](int stage) {
-            const int a = list.adapter(at), s = slab;
-            const uint32_t dst = loop.lds0 + stage * STAGE;
-            const i32x4 rp = P.rsrc(s, a * p.stride * 2), rq = Q.rsrc(s);
-#pragma unroll
-            for (int x = 0; x < OpP::LOADS; ++x) P.template load<true>(rp, s, x, dst + wave * OpP::LOADS * 1024);
-            const bool in = s * KB + Q.kc < p.R;
-#pragma unroll
-            for (int x = 0; x < OpQ::LOADS; ++x)
-                load_lds16(rq, dst + OpP::SLAB + (wave * OpQ::LOADS + x) * 1024, in && id[x] == a ? Q.off[x] : OOB);
-            if (++slab == slabs) {
-                slab = 0;
-                at += every;
-            }
-        };
-        for (int i = 0; i < min(NS, n); ++i) issue(i);
-        int st = 0;
-        for (int i = 0; i < n; ++i) {
-            __builtin_amdgcn_sched_barrier(0);
-            wait_stages<LOADS>(min(NS, n - i) - 1);
-            barrier();
-            __builtin_amdgcn_sched_barrier(0);
-            const uint32_t o = st * STAGE;
-#pragma unroll
-            for (int step = 0; step < 2; ++step) {
-                u32x4 q[L::CB];
-#pragma unroll
-                for (int j = 0; j < L::CB; ++j) q[j] = OpQ::fragment(qa[OpQ::which(j, step)] + o + OpQ::constant(j, step));
-#pragma unroll
-                for (int b = 0; b < L::RB; ++b) {
-                    const u32x4 f = OpP::fragment(pa[OpP::which(b, step)] + o + OpP::constant(b, step));
-#pragma unroll
-                    for (int j = 0; j < L::CB; ++j) acc.v[b][j] = mfma<DT>(f, q[j], acc.v[b][j]);
+                for (int x = 0; x < LOADS; ++x) P.template load<true>(rp, slab, x, loop.lds0 + (stage * STAGE + wave * LOADS * 1024));
+            };
+            for (int i = 0; i < min(NS, n); ++i) issue(i, i);
+#pragma unroll 1
+            for (int f = threadIdx.x; f < L::TQ * 8; f += L::NT) {
+                const int r = f >> 3, c = f & 7, col = slab * KB + 8 * c, a = list.id[r];
+                u32x4 w = u32x4{0u, 0u, 0u, 0u};
+                if (a >= 0 && col < p.R) {
+                    const float *at = p.partial + (q0 + r) * p.R + col, scale = p.rows.scale ? p.rows.scale[a] : 1.0f;
+                    const int64_t step = (int64_t)p.rows.T * p.R;
+                    f32x4 u, v;
+                    sum_slices(at, step, p.low_splits, u, v);
+                    u *= scale;
+                    v *= scale;
+                    w = u32x4{pack2<DT>(u[0], u[1]), pack2<DT>(u[2], u[3]), pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
                 }
+                *reinterpret_cast<u32x4 *>(lds + ROWS_AT + r * 128 + ((c ^ swz_kc(r)) << 4)) = w;
             }
-            __builtin_amdgcn_sched_barrier(0);
-            wait_lds();
-            barrier();   // every wave has read the stage
-            __builtin_amdgcn_sched_barrier(0);
-            if (i + NS < n) issue(st);
-            st = st + 1 == NS ? 0 : st + 1;
+            __syncthreads();
+            auto narrow = [&](int step, int j) {
+                return *reinterpret_cast<const u32x4 *>(lds + ROWS_AT + loop.q_of(j) * 128 +
+                                                        (((4 * step + (lane >> 4)) ^ swz_kc(loop.q_of(j))) << 4));
+            };
+            u32x4 q[HOLD ? 2 : 1][L::CB];
+            if constexpr (HOLD)
+#pragma unroll
+                for (int step = 0; step < 2; ++step)
+#pragma unroll
+                    for (int j = 0; j < L::CB; ++j) q[step][j] = narrow(step, j);
+            int st = 0;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                __builtin_amdgcn_sched_barrier(0);
+                wait_stages<LOADS>(min(NS, n - i) - 1);
+                barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                const uint32_t o = st * STAGE;
+                const int a = list.adapter(from + i * every);
+#pragma unroll
+                for (int step = 0; step < 2; ++step) {
+                    if constexpr (HOLD) {
+                        u32x4 f[L::RB];
+#pragma unroll
+                        for (int b = 0; b < L::RB; ++b) f[b] = OpP::fragment(pa[OpP::which(b, step)] + o + OpP::constant(b, step));
+#pragma unroll
+                        for (int j = 0; j < L::CB; ++j) {
+                            if (!__any(id[j] == a)) continue;
+                            const u32x4 m = masked(q[step][j], id[j] == a);
+#pragma unroll
+                            for (int b = 0; b < L::RB; ++b) acc.v[b][j] = mfma<DT>(f[b], m, acc.v[b][j]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < L::CB; ++j) q[0][j] = masked(narrow(step, j), id[j] == a);
+#pragma unroll
+                        for (int b = 0; b < L::RB; ++b) {
+                            const u32x4 f = OpP::fragment(pa[OpP::which(b, step)] + o + OpP::constant(b, step));
+#pragma unroll
+                            for (int j = 0; j < L::CB; ++j) acc.v[b][j] = mfma<DT>(f, q[0][j], acc.v[b][j]);
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                wait_lds();
+                barrier();   // every wave has read the stage
+                __builtin_amdgcn_sched_barrier(0);
+                if (i + NS < n) issue(i + NS, st);
+                st = st + 1 == NS ? 0 : st + 1;
+            }
         }
         __syncthreads();
     }
-    // This wave's LDS operations; its loads go on.
-    static __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4)); }
 };
 
 template <int DT, class L, int NS>
 __global__ __launch_bounds__(L::NT, 2) void lora_product(WideParams p) {
     using X = Extra<DT, L, NS>;
-    constexpr int AT = (X::BYTES + 15) & ~15, NEED = AT + (int)sizeof(List<L::TQ>);
+    constexpr int NEED = X::BYTES + (int)sizeof(List<L::TQ>);
     constexpr int BYTES = NEED > L::LDS_BYTES ? NEED : L::LDS_BYTES;
     __shared__ __attribute__((aligned(16))) char lds[BYTES];
+    static_assert(L::NT >= L::TQ, "a thread for each row");
     int tp, tq, split;
     place(p.g, tp, tq, split);
     const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    const int mine = adapter_of(p.rows, threadIdx.x < L::TQ ? q0 + threadIdx.x : p.rows.T);
     L loop(lds);
     typename L::Acc acc;
     L::zero(acc);
     const int s0 = (int)((int64_t)p.g.slabs * split / p.g.splits), s1 = (int)((int64_t)p.g.slabs * (split + 1) / p.g.splits);
-    loop.run_any(p.P, p0, p.x, q0, p.K, s0, s1, acc);
-    List<L::TQ> &list = *reinterpret_cast<List<L::TQ> *>(lds + AT);
-    list.fill(p.rows, q0);
-    X::run(loop, p, p0, q0, list, split, p.g.splits, acc);
+    List<L::TQ> &list = *reinterpret_cast<List<L::TQ> *>(lds + X::BYTES);
+    // Small tiles: last, the rows' adapters on their way meanwhile.  Large ones: first, and
+    // one form of the loop for every K: what lives across their loop, or accumulators
+    // that meet two loops, spill hundreds of registers in its last iterations.
+    if constexpr (X::HOLD) loop.run_any(p.P, p0, p.x, q0, p.K, s0, s1, acc);
+    list.fill(mine);
+    X::run(loop, lds, p, p0, q0, list, split, p.g.splits, acc);
+    if constexpr (!X::HOLD) loop.template run<true>(p.P, p0, p.x, q0, p.K, s0, s1, acc);
 #pragma unroll
     for (int j = 0; j < L::CB; ++j)
-        if (list.id[loop.q_of(j)] == BAD)
+        if (adapter_of(p.rows, q0 + loop.q_of(j)) == BAD)
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc.v[i][j][e] = __builtin_nanf("");
     if (!p.slots) {
-        __syncthreads();
         store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, p.P.rows, p.x.rows);
         return;
     }
@@ -292,27 +412,12 @@ __global__ __launch_bounds__(256) void lora_join(WideParams p, const float *slot
 // ---------------------------------------------------------------------------
 // The adapters' own gradients.
 // ---------------------------------------------------------------------------
-// One wave per 64 rows.
-__global__ __launch_bounds__(256) void lora_masks(LoraRows r, int64_t slabs, uint64_t *masks) {
-    const int lane = threadIdx.x & 63;
-    const int64_t slab = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (slab >= slabs) return;
-    const int id = adapter_of(r, slab * 64 + lane);
-    for (int a0 = 0; a0 < r.count; a0 += 64) {
-        uint64_t keep = 0;
-        for (int a = 0; a < min(64, r.count - a0); ++a) {
-            const uint64_t m = __ballot(id == a0 + a);
-            if (lane == a) keep = m;
-        }
-        if (a0 + lane < r.count) masks[(int64_t)(a0 + lane) * slabs + slab] = keep;
-    }
-}
-
 struct OuterParams {
     Matrix P, Q;
     int T, slabs, count;
     const uint64_t *masks;
     int tiles_p, tiles_q, splits;
+    int blocks;
     float *partial;
     int out_kind;
     void *out;
@@ -346,17 +451,19 @@ struct Slabs {
     }
 };
 
+template <int TP, int TQ>
+constexpr int outer_lds() { return 3 * (TP + TQ) * KB * 2; }
+
 template <int DT, int TP, int TQ>
-__global__ __launch_bounds__(256) void lora_outer(OuterParams p) {
+__device__ __forceinline__ void outer_block(const OuterParams &p, int64_t id, char *lds) {
     constexpr int NS = 3, WP = TP / 32 > 2 ? 2 : 1, WQ = 4 / WP, RB = TP / WP / 16, CB = TQ / WQ / 16;
     using OpP = Operand<false, TP, 4>;
     using OpQ = Operand<false, TQ, 4>;
     constexpr int STAGE = OpP::SLAB + OpQ::SLAB, LOADS = OpP::LOADS + OpQ::LOADS;
-    __shared__ __attribute__((aligned(16))) char lds[NS * STAGE];
+    static_assert(NS * STAGE == outer_lds<TP, TQ>(), "the stages");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wp = wave % WP, wq = wave / WP;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
-    int64_t id = blockIdx.x;
     const int tp = (int)(id % p.tiles_p);
     id /= p.tiles_p;
     const int tq = (int)(id % p.tiles_q);
@@ -424,7 +531,7 @@ __global__ __launch_bounds__(256) void lora_outer(OuterParams p) {
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4));   // this wave's LDS operations; its loads go on
+        wait_lds();
         barrier();
         __builtin_amdgcn_sched_barrier(0);
         issue(st);
@@ -453,15 +560,22 @@ __global__ __launch_bounds__(256) void lora_outer(OuterParams p) {
         }
 }
 
+// da and db: the wide side contiguous in one, the narrow side in the other.
+template <int DT>
+__global__ __launch_bounds__(256, 2) void lora_outers(OuterParams wide, OuterParams narrow) {
+    __shared__ __attribute__((aligned(16))) char lds[outer_lds<128, 64>()];
+    const int64_t id = blockIdx.x;
+    if (id < wide.blocks) outer_block<DT, 128, 64>(wide, id, lds);
+    else outer_block<DT, 64, 128>(narrow, id - wide.blocks, lds);
+}
+
 template <int DT>
 __global__ __launch_bounds__(256) void lora_outer_join(OuterParams p) {
     const int64_t quads = p.P.rows / 4, all = (int64_t)p.count * p.Q.rows * quads;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (id >= all) return;
     const int64_t col = id % quads * 4, row = id / quads % p.Q.rows, a = id / quads / p.Q.rows;
-    const f32x4 *from = reinterpret_cast<const f32x4 *>(p.partial) + id;
-    f32x4 v = from[0];
-    for (int s = 1; s < p.splits; ++s) v += from[s * all];
+    f32x4 v = sum_slices(p.partial + id * 4, all * 4, p.splits);
     const int64_t at = a * p.stride + row * p.ldo + col;
     if (p.out_kind == LO_16) {
         *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.out) + at) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
@@ -475,37 +589,62 @@ __global__ __launch_bounds__(256) void lora_outer_join(OuterParams p) {
 // ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
-template <int DT, class L>
+template <class L>
+LowParams low_params(const LoraLow &a) {
+    LowParams q{a.rows, matrix(a.f.first), matrix(a.x), a.f.stride, a.R, a.K, (a.K + KB - 1) / KB, (a.R + L::TP - 1) / L::TP,
+                (int)(((int64_t)a.rows.T + L::TQ - 1) / L::TQ), a.lists, a.splits, 0, a.partial, a.low};
+    q.blocks = q.groups * q.tiles_r * q.lists * q.splits;
+    return q;
+}
+template <class L>
 hipError_t run_low(const LoraLow &a, hipStream_t stream) {
-    const LowParams q{a.rows, matrix(a.f.first), matrix(a.x), a.f.stride, a.R, a.K, (a.K + KB - 1) / KB,
-                      (a.R + L::TP - 1) / L::TP, a.lists, a.splits, a.partial, a.low};
-    const int64_t groups = ((int64_t)a.rows.T + L::TQ - 1) / L::TQ;
-    hipLaunchKernelGGL((lora_low<DT, L>), dim3((unsigned)(groups * q.tiles_r * a.lists * a.splits)), dim3(L::NT), 0, stream, q);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t quads = (int64_t)a.rows.T * (a.R / 4);
-    hipLaunchKernelGGL(lora_low_join<DT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, q);
+    const LowParams q = low_params<L>(a);
+    hipLaunchKernelGGL(lora_low<L>, dim3((unsigned)q.blocks), dim3(L::NT), 0, stream, q);
     return hipGetLastError();
 }
-template <int DT, bool KC>
-hipError_t low(const LoraLow &a, hipStream_t stream) {
-    switch (lora_low_tile(a.R, KC)) {
-    case LL_64x64: return run_low<DT, ThinLoop<DT, KC, true, 64, 64, 5>>(a, stream);
-    case LL_128x64: return run_low<DT, ThinLoop<DT, KC, true, 128, 64, 3>>(a, stream);
+
+// f(loop type) for a factor's storage and the rank.
+template <class L_>
+struct Narrow {
+    using L = L_;
+};
+template <int DT, bool KC, class F>
+hipError_t with_narrow(int R, F &&f) {
+    switch (lora_low_tile(R, KC)) {
+    case LL_64x64: return f(Narrow<ThinLoop<DT, KC, true, 64, 64, 5>>());
+    case LL_128x64: return f(Narrow<ThinLoop<DT, KC, true, 128, 64, 3>>());
     default: break;
     }
-    if constexpr (KC) return run_low<DT, ThinLoop<DT, true, true, 32, 64, 6>>(a, stream);
+    if constexpr (KC) return f(Narrow<ThinLoop<DT, true, true, 32, 64, 6>>());
     return hipErrorInvalidValue;
+}
+template <int DT>
+hipError_t run_lows(const LoraLow &k, const LoraLow &r, uint64_t *masks, hipStream_t stream) {
+    return with_narrow<DT, true>(k.R, [&](auto nk) {
+        return with_narrow<DT, false>(r.R, [&](auto nr) {
+            using LK = typename decltype(nk)::L;
+            using LR = typename decltype(nr)::L;
+            if constexpr (LK::TP == LR::TP || (LK::TP == 32 && LR::TP == 64)) {   // what one rank asks for
+                LowParams a = low_params<LK>(k), b = low_params<LR>(r);
+                if (!k.partial) a.blocks = 0;
+                if (!r.partial) b.blocks = 0;
+                const unsigned slabs = masks ? (unsigned)((k.rows.T + 255) / 256) : 0;
+                hipLaunchKernelGGL((lora_lows<LK, LR>), dim3((unsigned)(a.blocks + b.blocks) + slabs), dim3(256), 0, stream, a, b, masks);
+                hipError_t e = hipGetLastError();
+                if (e != hipSuccess || !masks) return e;
+                const int64_t quads = 2 * (int64_t)k.rows.T * (k.R / 4);
+                hipLaunchKernelGGL(lora_low_join<DT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, a, b);
+                return hipGetLastError();
+            } else {
+                return hipErrorInvalidValue;
+            }
+        });
+    });
 }
 
 template <class L>
 WideParams wide_params(const LoraProduct &a) {
-    LossMatrix low;
-    low.base = a.low;
-    low.ld = a.R;
-    low.rows = a.rows.T;
-    low.kc = true;
-    return WideParams{a.rows, matrix(a.P), matrix(a.x), matrix(a.f.first), matrix(low), a.f.stride, a.K, a.R,
+    return WideParams{a.rows, matrix(a.P), matrix(a.x), matrix(a.f.first), a.f.stride, a.partial, a.low_splits, a.K, a.R,
                       grid_of<L>(a.P.rows, a.x.rows, a.K, a.splits), a.splits > 1, a.out, a.ldo};
 }
 
@@ -518,11 +657,11 @@ struct Wide {
 template <int DT, bool KC, class F>
 hipError_t with_wide(int tile, F &&f) {
     switch (tile) {
-    case LP_128x128: return f(Wide<Loop<DT, KC, true, 128, 128, 2, 2, KC ? 3 : 2, 2>, DT, 2>());
-    case LP_256x256: return f(Wide<Loop<DT, KC, true, 256, 256, 2, 4, 3, 2>, DT, 2>());
-    case LP_64x32: return f(Wide<ThinLoop<DT, KC, true, 64, 32, 6>, DT, 6>());
-    case LP_64x64: return f(Wide<ThinLoop<DT, KC, true, 64, 64, 5>, DT, 4>());
-    case LP_64x128: return f(Wide<ThinLoop<DT, KC, true, 64, 128, 3>, DT, 3>());
+    case LP_128x128: return f(Wide<Loop<DT, KC, true, 128, 128, 2, 2, KC ? 3 : 2, 2>, DT, 3>());
+    case LP_256x256: return f(Wide<Loop<DT, KC, true, 256, 256, 2, 4, 3, 2>, DT, 3>());
+    case LP_64x32: return f(Wide<ThinLoop<DT, KC, true, 64, 32, 6>, DT, 7>());
+    case LP_64x64: return f(Wide<ThinLoop<DT, KC, true, 64, 64, 5>, DT, 6>());
+    case LP_64x128: return f(Wide<ThinLoop<DT, KC, true, 64, 128, 3>, DT, 6>());
     default: return hipErrorInvalidValue;
     }
 }
@@ -532,17 +671,25 @@ hipError_t with_wide(int dtype, int tile, bool kc, F &&f) {
     return dtype == 0 ? with_wide<0, false>(tile, f) : with_wide<1, false>(tile, f);
 }
 
-template <int DT, int TP, int TQ>
-hipError_t run_outer(const LoraOuter &a, hipStream_t stream) {
-    const OuterParams q{matrix(a.P), matrix(a.Q), a.T, (a.T + 63) / 64, a.count, a.masks, (a.P.rows + TP - 1) / TP,
-                        (a.Q.rows + TQ - 1) / TQ, a.splits, a.partial, a.out_kind, a.out, a.ldo, a.stride};
-    const int64_t blocks = (int64_t)a.count * q.tiles_p * q.tiles_q * a.splits;
-    hipLaunchKernelGGL((lora_outer<DT, TP, TQ>), dim3((unsigned)blocks), dim3(256), 0, stream, q);
+OuterParams outer_params(const LoraOuter &a) {
+    const int tp = a.narrow_p ? 64 : 128, tq = a.narrow_p ? 128 : 64;
+    OuterParams q{matrix(a.P), matrix(a.Q), a.T, (a.T + 63) / 64, a.count, a.masks, (a.P.rows + tp - 1) / tp,
+                  (a.Q.rows + tq - 1) / tq, a.splits, 0, a.partial, a.out_kind, a.out, a.ldo, a.stride};
+    q.blocks = a.out ? a.count * q.tiles_p * q.tiles_q * a.splits : 0;
+    return q;
+}
+template <int DT>
+hipError_t run_outers(const LoraOuter &wide, const LoraOuter &narrow, hipStream_t stream) {
+    const OuterParams w = outer_params(wide), n = outer_params(narrow);
+    hipLaunchKernelGGL(lora_outers<DT>, dim3((unsigned)(w.blocks + n.blocks)), dim3(256), 0, stream, w, n);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t quads = (int64_t)a.count * a.Q.rows * (a.P.rows / 4);
-    hipLaunchKernelGGL(lora_outer_join<DT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, q);
-    return hipGetLastError();
+    for (const OuterParams *q : {&w, &n}) {
+        if (e != hipSuccess || !q->out || q->splits == 1) continue;
+        const int64_t quads = (int64_t)q->count * q->Q.rows * (q->P.rows / 4);
+        hipLaunchKernelGGL(lora_outer_join<DT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, *q);
+        e = hipGetLastError();
+    }
+    return e;
 }
 
 }  // namespace
@@ -552,8 +699,14 @@ int lora_low_rows(int tile) { return tile == LL_32x64 ? 32 : tile == LL_64x64 ? 
 
 hipError_t launch_lora_low(int dtype, const LoraLow &p, hipStream_t stream) {
     if (!p.x.kc) return hipErrorInvalidValue;
-    if (p.f.first.kc) return dtype == 0 ? low<0, true>(p, stream) : low<1, true>(p, stream);
-    return dtype == 0 ? low<0, false>(p, stream) : low<1, false>(p, stream);
+    auto run = [&](auto n) { return run_low<typename decltype(n)::L>(p, stream); };
+    if (p.f.first.kc) return dtype == 0 ? with_narrow<0, true>(p.R, run) : with_narrow<1, true>(p.R, run);
+    return dtype == 0 ? with_narrow<0, false>(p.R, run) : with_narrow<1, false>(p.R, run);
+}
+hipError_t launch_lora_lows(int dtype, const LoraLow &s, const LoraLow &ds, uint64_t *masks, hipStream_t stream) {
+    const LoraLow &k = s.f.first.kc ? s : ds, &r = s.f.first.kc ? ds : s;
+    if (!s.x.kc || !ds.x.kc || !k.f.first.kc || r.f.first.kc || s.R != ds.R) return hipErrorInvalidValue;
+    return dtype == 0 ? run_lows<0>(k, r, masks, stream) : run_lows<1>(k, r, masks, stream);
 }
 
 LossTileShape lora_tile_shape(int tile) {
@@ -584,16 +737,10 @@ hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, const flo
     });
 }
 
-hipError_t launch_lora_masks(const LoraRows &rows, uint64_t *masks, hipStream_t stream) {
-    const int64_t slabs = ((int64_t)rows.T + 63) / 64;
-    hipLaunchKernelGGL(lora_masks, dim3((unsigned)((slabs + 3) / 4)), dim3(256), 0, stream, rows, slabs, masks);
-    return hipGetLastError();
-}
-
-hipError_t launch_lora_outer(int dtype, const LoraOuter &p, hipStream_t stream) {
-    if (p.P.kc || p.Q.kc) return hipErrorInvalidValue;
-    if (p.narrow_p) return dtype == 0 ? run_outer<0, 64, 128>(p, stream) : run_outer<1, 64, 128>(p, stream);
-    return dtype == 0 ? run_outer<0, 128, 64>(p, stream) : run_outer<1, 128, 64>(p, stream);
+hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, hipStream_t stream) {
+    const LoraOuter &w = da.narrow_p ? db : da, &n = da.narrow_p ? da : db;
+    if (w.P.kc || w.Q.kc || n.P.kc || n.Q.kc || w.narrow_p || !n.narrow_p) return hipErrorInvalidValue;
+    return dtype == 0 ? run_outers<0>(w, n, stream) : run_outers<1>(w, n, stream);
 }
 
 }  // namespace dgw
