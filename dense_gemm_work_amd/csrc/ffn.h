@@ -23,6 +23,11 @@ struct FfnGate {
 };
 hipError_t launch_ffn_gate(int dtype, int tile, const FfnGate &p, hipStream_t stream);
 
+// The whole forward call of at most FFN_VEC_T rows and weights with k contiguous: h [T][F]
+// is a workspace, fp32; p's own h is not used.
+constexpr int FFN_VEC_T = 4;
+hipError_t launch_ffn_vec(int dtype, const FfnGate &p, const LossMatrix &down, float *h, uint16_t *y, int64_t ldy, hipStream_t stream);
+
 // dh = dy . w_down, turned into dg, du and h where it stands.
 struct FfnSlope {
     int T, F, H;

@@ -133,6 +133,7 @@ Grad grad_plan(const gemm_ffn_args_t &a, const void *dw, Shape w, int cus) {
 }
 
 struct Plan {
+    bool vec = false;                       // forward, by the kernels of single rows
     int first = dgw::LT_128x128;
     Choice out{dgw::LT_128x128, 1};
     Grad gate, up, down;
@@ -156,7 +157,9 @@ Plan make_plan(const gemm_ffn_args_t &a, bool backward, int cus) {
     auto need = [&](const Choice &c, int64_t rows_p, int64_t rows_q) {
         if (c.splits > 1) slots = std::max(slots, dgw::loss_slots_bytes(c.tile, rows_p, rows_q, c.splits));
     };
-    p.h = p.take(hidden);
+    p.h = p.take(hidden);   // two parts are as large as fp32
+    p.vec = !backward && is_nk(a) && a.T <= dgw::FFN_VEC_T;
+    if (p.vec) return p;
     p.out = out_choice(a, cus);
     if (!backward) {
         p.first = gate_tile(a, cus);
@@ -242,8 +245,13 @@ int forward(const gemm_ffn_args_t &a) {
                          matrix(a.w_up, a.ldw_up, in.row, a.F, c.nk), matrix(a.x, a.ldx, a.H, a.T, true), a.act,
                          h, a.F, pl.part, static_cast<uint16_t *>(a.gate), static_cast<uint16_t *>(a.up),
                          or_packed(a.ldgate, a.F), or_packed(a.ldup, a.F)};
-    const hipError_t e = dgw::launch_ffn_gate(c.dtype, pl.first, g, c.stream);
-    if (e != hipSuccess) return set_hip_error(e, "launch the gated product");
+    hipError_t e;
+    if (pl.vec) {
+        e = dgw::launch_ffn_vec(c.dtype, g, matrix(a.w_down, a.ldw_down, down.row, a.H, true), part<float>(c.ws, pl.h),
+                                static_cast<uint16_t *>(a.y), or_packed(a.ldy, a.H), c.stream);
+        return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the block of single rows");
+    }
+    if ((e = dgw::launch_ffn_gate(c.dtype, pl.first, g, c.stream)) != hipSuccess) return set_hip_error(e, "launch the gated product");
     dgw::LossProduct y;   // y[t][o] = sum_f w_down[o][f] h[t][f]
     y.P = matrix(a.w_down, a.ldw_down, down.row, a.H, c.nk);
     y.Q = matrix(h, 0, a.F, a.T, true, pl.part);
@@ -353,6 +361,13 @@ int plan(const gemm_ffn_args_t *args, int32_t backward, int32_t num_cus, gemm_ff
     const Plan p = make_plan(*args, backward != 0, num_cus);
     const dgw::LossTileShape f = dgw::loss_tile_shape(p.first), o = dgw::loss_tile_shape(p.out.tile);
     out->num_cus = num_cus;
+    out->workspace_bytes = p.bytes;
+    if (p.vec) {   // four features or outputs a workgroup, every row; h in fp32
+        out->first_tile_f = out->out_tile_h = 4;
+        out->first_tile_t = out->out_tile_t = (int32_t)args->T;
+        out->out_splits = 1;
+        return GEMM_OK;
+    }
     out->parts = p.parts;
     out->first_tile_f = backward ? f.p : f.p / 2;
     out->first_tile_t = f.q;
@@ -365,7 +380,6 @@ int plan(const gemm_ffn_args_t *args, int32_t backward, int32_t num_cus, gemm_ff
         out->dw_tile_q = w.q;
         out->dw_splits = p.gate.c.splits;
     }
-    out->workspace_bytes = p.bytes;
     return GEMM_OK;
 }
 

@@ -14,6 +14,7 @@
 #include "ffn.h"
 #include "tile.h"
 #include "tile_store.h"
+#include "vec.h"
 
 namespace dgw {
 
@@ -64,33 +65,6 @@ __device__ __forceinline__ void with_act(uint32_t act, F &&f) {
     else f(std::integral_constant<uint32_t, GEMM_FFN_RELU>());
 }
 
-template <int DT>
-__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b) {
-    if constexpr (DT == 0) {
-        a = __uint_as_float(w << 16);
-        b = __uint_as_float(w & 0xffff0000u);
-    } else {
-        const f16x2 v = __builtin_bit_cast(f16x2, w);
-        a = (float)v[0];
-        b = (float)v[1];
-    }
-}
-template <int DT>
-__device__ __forceinline__ u32x2 pack4(f32x4 v) {
-    return u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-}
-template <int DT>
-__device__ __forceinline__ f32x4 unpack4(u32x2 w) {
-    f32x4 v;
-    float a, b;
-    unpack2<DT>(w[0], a, b);
-    v[0] = a;
-    v[1] = b;
-    unpack2<DT>(w[1], a, b);
-    v[2] = a;
-    v[3] = b;
-    return v;
-}
 // v in 16 bits at `to` and, TWO, what that left out, rounded too, `part` elements on.
 // The rest is taken from the stored bits: the compiler may fold the multiplication that
 // made v into one of its conversions (v_fma_mixlo_f16) and not into another, and near a
@@ -202,6 +176,39 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void ffn_gate_few(GateParams p) {
             }
         }
     });
+}
+
+// At most VEC_T rows: four features a workgroup; h stays fp32.
+template <int DT, int T>
+__global__ __launch_bounds__(256) void ffn_gate_vec(GateParams p, float *h) {
+    __shared__ float red[4][8][T];
+    const int64_t f0 = (int64_t)blockIdx.x * 4;
+    const uint16_t *w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = p.gate.base + (f0 + i) * p.gate.ld;
+        w[4 + i] = p.up.base + (f0 + i) * p.up.ld;
+    }
+    dot_rows<DT>(w, Rows16<DT>{p.x.base, p.x.ld}, p.T, p.H, red);
+    const int i = threadIdx.x & 3, t = threadIdx.x >> 2;
+    if (t >= T || t >= p.T) return;
+    const float g = joined(red, i, t), u = joined(red, 4 + i, t);
+    with_act(p.act, [&](auto A) { h[(int64_t)t * p.F + f0 + i] = activation<decltype(A)::value>(g).value * u; });
+    if (p.kept_gate) {
+        p.kept_gate[t * p.ld_gate + f0 + i] = (uint16_t)pack2<DT>(g, 0.0f);
+        p.kept_up[t * p.ld_up + f0 + i] = (uint16_t)pack2<DT>(u, 0.0f);
+    }
+}
+template <int DT, int T>
+__global__ __launch_bounds__(256) void ffn_down_vec(Matrix down, const float *h, int rows, int F, uint16_t *y, int64_t ldy) {
+    __shared__ float red[4][4][T];
+    const int64_t o0 = (int64_t)blockIdx.x * 4;
+    const uint16_t *w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = down.base + (o0 + i) * down.ld;
+    dot_rows<DT>(w, Rows32{h, F}, rows, F, red);
+    const int i = threadIdx.x & 3, t = threadIdx.x >> 2;
+    if (t < T && t < rows) y[t * ldy + o0 + i] = (uint16_t)pack2<DT>(joined(red, i, t), 0.0f);
 }
 
 struct SlopeParams {
@@ -368,6 +375,17 @@ hipError_t sum(int tile, const FfnSum &a, hipStream_t stream) {
     }
 }
 
+template <int DT, int T>
+hipError_t run_vec(const FfnGate &a, const LossMatrix &down, float *h, uint16_t *y, int64_t ldy, hipStream_t stream) {
+    const GateParams q{matrix(a.gate), matrix(a.up), matrix(a.x), a.T, a.F, a.H, Grid{}, a.act,
+                       nullptr, a.kept_gate, a.kept_up, 0, 0, a.ld_gate, a.ld_up};
+    hipLaunchKernelGGL((ffn_gate_vec<DT, T>), dim3((unsigned)(a.F / 4)), dim3(256), 0, stream, q, h);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ffn_down_vec<DT, T>), dim3((unsigned)(down.rows / 4)), dim3(256), 0, stream, matrix(down), h, a.T, a.F, y, ldy);
+    return hipGetLastError();
+}
+
 bool few(int tile) { return loss_tile_shape(tile).q <= LOSS_FEW; }
 
 }  // namespace
@@ -376,6 +394,13 @@ hipError_t launch_ffn_gate(int dtype, int tile, const FfnGate &p, hipStream_t st
     if (!p.x.kc || p.gate.kc != p.up.kc || few(tile) != (p.part > 0)) return hipErrorInvalidValue;
     if (p.gate.kc) return dtype == 0 ? gate<0, true>(tile, p, stream) : gate<1, true>(tile, p, stream);
     return dtype == 0 ? gate<0, false>(tile, p, stream) : gate<1, false>(tile, p, stream);
+}
+
+hipError_t launch_ffn_vec(int dtype, const FfnGate &p, const LossMatrix &down, float *h, uint16_t *y, int64_t ldy, hipStream_t stream) {
+    if (!p.gate.kc || !p.up.kc || !down.kc || p.T > VEC_T || p.F % 8 || p.H % 8 || down.rows % 8) return hipErrorInvalidValue;
+    if (p.T == 1) return dtype == 0 ? run_vec<0, 1>(p, down, h, y, ldy, stream) : run_vec<1, 1>(p, down, h, y, ldy, stream);
+    if (p.T == 2) return dtype == 0 ? run_vec<0, 2>(p, down, h, y, ldy, stream) : run_vec<1, 2>(p, down, h, y, ldy, stream);
+    return dtype == 0 ? run_vec<0, 4>(p, down, h, y, ldy, stream) : run_vec<1, 4>(p, down, h, y, ldy, stream);
 }
 
 hipError_t launch_ffn_sum(int dtype, int tile, const FfnSum &p, hipStream_t stream) {

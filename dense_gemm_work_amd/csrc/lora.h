@@ -63,6 +63,12 @@ enum LoraTile : int { LP_128x128 = LT_128x128, LP_256x256 = LT_256x256, LP_64x64
 LossTileShape lora_tile_shape(int tile);
 int64_t lora_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits);
 hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, hipStream_t stream);
+// Few rows (at most LORA_FEW_T rows, ranks of at most LORA_FEW_R): out and the narrow
+// product that it needs in two launches, always through `slots`; f's part is summed in
+// fp32 from unrounded narrow rows.
+constexpr int LORA_FEW_T = 128, LORA_FEW_R = 256;
+hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const LoraLow &low, float *slots, hipStream_t stream);
+
 hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, const float *slots, hipStream_t stream);
 
 // out_a[q][p] = sum over the rows t of adapter a of P[t][p] Q[t][q], for every adapter.

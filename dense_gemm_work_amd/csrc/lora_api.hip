@@ -113,8 +113,14 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
 Choice out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
     if (a.T > 128) return choose(rows_p, a.T, k, true, cus);
     const int tile = a.T <= 32 ? dgw::LP_64x32 : a.T <= 64 ? dgw::LP_64x64 : dgw::LP_64x128;
-    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(2 * cus / ceil_div(rows_p, 64), ceil_div(k, 64) / 4))};
+    // one workgroup a CU (96 x 4096 x 4096: 14.8 us, with two 16.2, and a shorter join)
+    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(rows_p, 64), ceil_div(k, 64) / 4))};
 }
+
+// Few rows of small ranks take the adapters in the join, where each row reads its own
+// adapter: no more than R elements of it a result, and only as long as that is little
+// beside w.
+bool few_rows(const gemm_lora_args_t &a) { return a.T <= dgw::LORA_FEW_T && a.R <= dgw::LORA_FEW_R && a.T * a.R <= 4096; }
 
 int outer_splits(const gemm_lora_args_t &a, int64_t wide, int cus) {
     const int64_t blocks = a.adapters * ceil_div(wide, 128) * ceil_div(a.R, 64);
@@ -124,6 +130,7 @@ int outer_splits(const gemm_lora_args_t &a, int64_t wide, int cus) {
 struct Plan {
     Low s, ds;
     Choice out{dgw::LP_128x128, 1};
+    bool few = false;
     int da_splits = 1, db_splits = 1;
     int64_t db_at = 0;   // db's slices behind da's
     int64_t low = 0, dlow = 0, part_s = 0, part_ds = 0, partial = 0, masks = 0;   // byte offsets
@@ -151,7 +158,8 @@ Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     const int64_t wide = backward ? a.H : a.N;
     if (!backward || a.dx) {
         p.out = out_plan(a, wide, backward ? a.N : a.H, cus);
-        if (p.out.splits > 1) need(dgw::lora_slots_bytes(p.out.tile, wide, a.T, p.out.splits));
+        p.few = !backward && few_rows(a);
+        if (p.out.splits > 1 || p.few) need(dgw::lora_slots_bytes(p.out.tile, wide, a.T, p.out.splits));
     }
     if (own) {
         p.masks = p.take(a.adapters * ceil_div(a.T, 64) * 8);
@@ -223,12 +231,16 @@ dgw::LoraLow narrow(const gemm_lora_args_t &a, const Call &c, const Low &l, cons
     return {c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, slices), nullptr};
 }
 
-int wide(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &w, const dgw::LossMatrix &x, const dgw::LoraFactor &f,
-         const dgw::LoraLow &low, int64_t k, void *out, int64_t ldo) {
+dgw::LoraProduct product(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &w, const dgw::LossMatrix &x,
+                         const dgw::LoraFactor &f, const dgw::LoraLow &low, int64_t k, void *out, int64_t ldo) {
+    return {c.rows, w, x, f, low.partial, low.splits, (int)k, a.R, c.plan.out.splits, out, ldo};
+}
+
+int wide(const Call &c, dgw::LoraProduct p) {
     const Choice &how = c.plan.out;
     float *slots = part<float>(c.ws, c.plan.partial);
-    dgw::LoraProduct p{c.rows, w, x, f, low.partial, low.splits, (int)k, a.R, how.splits,
-                       how.splits > 1 ? static_cast<void *>(slots) : out, ldo};
+    void *out = p.out;
+    if (how.splits > 1) p.out = slots;
     hipError_t e = dgw::launch_lora_product(c.dtype, how.tile, p, c.stream);
     if (e == hipSuccess && how.splits > 1) {
         p.out = out;
@@ -245,9 +257,15 @@ int forward(const gemm_lora_args_t &a) {
     if ((rc = begin(a, false, &c)) != GEMM_OK) return rc;
     const dgw::LossMatrix x = matrix(a.x, a.ldx, a.H, a.T, true);
     const dgw::LoraLow s = narrow(a, c, c.plan.s, factor_a(a, true), x, a.H, c.plan.part_s);
-    const hipError_t e = dgw::launch_lora_low(c.dtype, s, c.stream);
-    if (e != hipSuccess) return set_hip_error(e, "launch the narrow product");
-    return wide(a, c, matrix(a.w, a.ldw, w_row(a), a.N, c.nk), x, factor_b(a, false), s, a.H, a.y, or_packed(a.ldy, a.N));
+    const dgw::LoraProduct y = product(a, c, matrix(a.w, a.ldw, w_row(a), a.N, c.nk), x, factor_b(a, false), s, a.H, a.y,
+                                       or_packed(a.ldy, a.N));
+    hipError_t e;
+    if (c.plan.few) {
+        e = dgw::launch_lora_few(c.dtype, c.plan.out.tile, y, s, part<float>(c.ws, c.plan.partial), c.stream);
+        return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the projection of few rows");
+    }
+    if ((e = dgw::launch_lora_low(c.dtype, s, c.stream)) != hipSuccess) return set_hip_error(e, "launch the narrow product");
+    return wide(c, y);
 }
 
 // da or db: out[o][i] = sum over an adapter's rows of outs[t][o] ins[t][i] as "nk" stores
@@ -297,8 +315,8 @@ int backward(const gemm_lora_args_t &a) {
     if (!a.dx && !a.da) ds.partial = nullptr, ds.low = nullptr;
     if ((e = dgw::launch_lora_lows(c.dtype, s, ds, own ? part<uint64_t>(c.ws, pl.masks) : nullptr, c.stream)) != hipSuccess)
         return set_hip_error(e, "launch the narrow products");
-    if (a.dx && (rc = wide(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx,
-                           or_packed(a.lddx, a.H))) != GEMM_OK)
+    if (a.dx && (rc = wide(c, product(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx,
+                                      or_packed(a.lddx, a.H)))) != GEMM_OK)
         return rc;
     if (!own) return GEMM_OK;
     const dgw::LossMatrix ms = matrix(s.low, 0, a.R, a.R, false), mds = matrix(ds.low, 0, a.R, a.R, false);

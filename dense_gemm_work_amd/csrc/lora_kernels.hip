@@ -16,6 +16,7 @@
 #include "lora.h"
 #include "tile.h"
 #include "tile_store.h"
+#include "vec.h"
 
 namespace dgw {
 
@@ -410,6 +411,128 @@ __global__ __launch_bounds__(256) void lora_join(WideParams p, const float *slot
 }
 
 // ---------------------------------------------------------------------------
+// Few rows of small ranks, each perhaps with an adapter of its own: the wide and the
+// narrow product run side by side in one launch, and the join of the wide one's
+// slices adds the adapters' part, row by row, in fp32.  (96 x 4096 x 4096, 64 adapters
+// of rank 16: the adapters in the product's tiles cost it 12 us of 28, and waited for
+// the narrow product's launch.)
+// ---------------------------------------------------------------------------
+template <class L, class LN>
+__global__ __launch_bounds__(256, L::WAVES < LN::WAVES ? L::WAVES : LN::WAVES) void lora_few(WideParams w, LowParams n, int wide) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES > LN::LDS_BYTES ? L::LDS_BYTES : LN::LDS_BYTES];
+    __shared__ List<LN::TQ> list;
+    static_assert(L::NT == 256 && LN::NT == 256, "one size of workgroup");
+    if ((int)blockIdx.x >= wide) {
+        low_block<LN>(n, (int)blockIdx.x - wide, lds, list);
+        return;
+    }
+    int tp, tq, split;
+    place(w.g, wide, (int)blockIdx.x, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    const int s0 = (int)((int64_t)w.g.slabs * split / w.g.splits), s1 = (int)((int64_t)w.g.slabs * (split + 1) / w.g.splits);
+    loop.run_any(w.P, p0, w.x, q0, w.K, s0, s1, acc);
+    if (!loop.active()) return;
+    f32x4 *slot = slot_base<L>(static_cast<float *>(w.out), w.g, tp, tq, split, loop.wave, loop.lane);
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) {
+        if (q0 + 16 * j >= w.x.rows) break;   // blocks of rows that are not there
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i) slot[(i * L::CB + j) * 64] = acc.v[i][j];
+    }
+}
+
+// At most VEC_T rows of x and w with k contiguous: the wide product by dot_rows, eight
+// outputs a workgroup, into the slots of 64 x 32 tiles as one slice.
+template <int DT, int T, class L, class LN>
+__global__ __launch_bounds__(256) void lora_few_vec(WideParams w, LowParams n, int wide) {
+    __shared__ __attribute__((aligned(16))) char lds[LN::LDS_BYTES];
+    __shared__ List<LN::TQ> list;
+    __shared__ float red[4][8][T];
+    static_assert(LN::NT == 256 && L::TP == 64 && L::TQ == 32, "the join's tiles");
+    if ((int)blockIdx.x >= wide) {
+        low_block<LN>(n, (int)blockIdx.x - wide, lds, list);
+        return;
+    }
+    const int o0 = (int)blockIdx.x * 8;
+    const uint16_t *rows[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rows[i] = w.P.base + (int64_t)(o0 + i) * w.P.ld;
+    dot_rows<DT>(rows, Rows16<DT>{w.x.base, w.x.ld}, w.x.rows, w.K, red);
+    const int i = threadIdx.x & 7, t = threadIdx.x >> 3, o = o0 + i;
+    if (t >= T || t >= w.x.rows) return;
+    float *slot = static_cast<float *>(w.out) + (int64_t)(o >> 6) * (L::TP * L::TQ);
+    slot[((o >> 4) & 3) * L::CB * 256 + (t + 16 * ((o >> 2) & 3)) * 4 + (o & 3)] = joined(red, i, t);
+}
+
+// A workgroup: 16 rows (block j of a tile) by the tile's 64 columns.
+template <int DT, class L, bool KC>
+__global__ __launch_bounds__(256) void lora_few_join(WideParams p, const float *slots) {
+    static_assert(L::TP == 64 && L::RB == 1 && L::WP == 4, "a wave for each 16 columns");
+    __shared__ __attribute__((aligned(16))) float narrow[16 * (LORA_FEW_R + 4)];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = (int)blockIdx.x % L::CB, tile = (int)blockIdx.x / L::CB;
+    const int tp = tile % p.g.tiles_p, tq = tile / p.g.tiles_p;
+    const int64_t first = (int64_t)tq * L::TQ + 16 * j, row = first + (lane & 15);
+    const int64_t col = (int64_t)tp * 64 + 16 * wave + 4 * (lane >> 4);
+    if (first >= p.x.rows) return;
+    // the slices' sums first, whether or not their rows have adapters: no load waits for
+    // another
+    const int quads = p.R / 4, ld = p.R + 4;   // 4 floats of padding against bank conflicts
+    const bool in = row < p.x.rows && col < p.P.rows;
+    const int a = in ? adapter_of(p.rows, row) : NONE;
+    f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (in) {
+        const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * (L::TP * L::TQ);
+        v = sum_slices(slots + (int64_t)tile * (L::TP * L::TQ) + (wave * L::CB + j) * 256 + lane * 4, step, p.g.splits);
+    }
+    const float scale = a >= 0 && p.rows.scale ? p.rows.scale[a] : 1.0f;
+    for (int f = threadIdx.x; f < 16 * quads; f += 256) {
+        const int r = f / quads, q = f % quads;
+        if (first + r < p.x.rows)
+            *reinterpret_cast<f32x4 *>(narrow + r * ld + 4 * q) =
+                sum_slices(p.partial + (first + r) * p.R + 4 * q, (int64_t)p.rows.T * p.R, p.low_splits);
+    }
+    __syncthreads();
+    if (!in) return;
+    if (a >= 0) {
+        f32x4 sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const float *s = narrow + (lane & 15) * ld;
+        const uint16_t *f = p.f.base + a * p.stride;
+        if constexpr (KC) {   // four rows of the factor, which lie one after the other
+#pragma unroll 2
+            for (int r = 0; r < p.R; r += 8) {
+                const f32x4 s0 = *reinterpret_cast<const f32x4 *>(s + r), s1 = *reinterpret_cast<const f32x4 *>(s + r + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(f + (col + e) * p.f.ld + r);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        float lo, hi;
+                        unpack2<DT>(w[h], lo, hi);
+                        sum[e] = __builtin_fmaf(lo, h < 2 ? s0[2 * h] : s1[2 * h - 4], sum[e]);
+                        sum[e] = __builtin_fmaf(hi, h < 2 ? s0[2 * h + 1] : s1[2 * h - 3], sum[e]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll 8
+            for (int r = 0; r < p.R; ++r) {
+                const f32x4 w = unpack4<DT>(*reinterpret_cast<const u32x2 *>(f + r * p.f.ld + col));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[e] = __builtin_fmaf(w[e], s[r], sum[e]);
+            }
+        }
+        v += sum * scale;
+    } else if (a == BAD) {
+        v = f32x4{1.0f, 1.0f, 1.0f, 1.0f} * __builtin_nanf("");
+    }
+    *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.out) + row * p.ldo + col) =
+        u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+
+// ---------------------------------------------------------------------------
 // The adapters' own gradients.
 // ---------------------------------------------------------------------------
 struct OuterParams {
@@ -665,6 +788,50 @@ hipError_t with_wide(int tile, F &&f) {
     default: return hipErrorInvalidValue;
     }
 }
+// The few rows' two launches.
+template <int DT, bool KC, class L>
+hipError_t join_few(WideParams w, const float *slots, void *out, hipStream_t stream) {
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    w.out = out;
+    hipLaunchKernelGGL((lora_few_join<DT, L, KC>), dim3((unsigned)(w.g.tiles_p * w.g.tiles_q * L::CB)), dim3(256), 0, stream, w, slots);
+    return hipGetLastError();
+}
+template <int DT, bool KC, class L>
+hipError_t run_few(const LoraProduct &a, const LoraLow &low, float *slots, hipStream_t stream) {
+    // the wide product's factor is stored as P is, the narrow one's the other way (an
+    // input's side against an output's)
+    return with_narrow<DT, KC>(low.R, [&](auto n) {
+        using LN = typename decltype(n)::L;
+        WideParams w = wide_params<L>(a);
+        LowParams q = low_params<LN>(low);
+        void *out = w.out;
+        w.out = slots;
+        if constexpr (KC && L::TQ == 32) {
+            if (a.x.rows <= VEC_T) {
+                w.g.splits = 1;
+                const int wide = a.P.rows / 8;
+                const dim3 grid((unsigned)(wide + q.blocks));
+                if (a.x.rows == 1) hipLaunchKernelGGL((lora_few_vec<DT, 1, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
+                else if (a.x.rows == 2) hipLaunchKernelGGL((lora_few_vec<DT, 2, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
+                else hipLaunchKernelGGL((lora_few_vec<DT, 4, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
+                return join_few<DT, KC, L>(w, slots, out, stream);
+            }
+        }
+        const int wide = (int)blocks_of(w.g);
+        hipLaunchKernelGGL((lora_few<L, LN>), dim3((unsigned)(wide + q.blocks)), dim3(256), 0, stream, w, q, wide);
+        return join_few<DT, KC, L>(w, slots, out, stream);
+    });
+}
+template <int DT, bool KC>
+hipError_t few(int tile, const LoraProduct &a, const LoraLow &low, float *slots, hipStream_t stream) {
+    switch (tile) {
+    case LP_64x32: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 32, 6>>(a, low, slots, stream);
+    case LP_64x64: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 64, 5>>(a, low, slots, stream);
+    case LP_64x128: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 128, 3>>(a, low, slots, stream);
+    default: return hipErrorInvalidValue;
+    }
+}
 template <class F>
 hipError_t with_wide(int dtype, int tile, bool kc, F &&f) {
     if (kc) return dtype == 0 ? with_wide<0, true>(tile, f) : with_wide<1, true>(tile, f);
@@ -726,6 +893,12 @@ hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, hipStr
         hipLaunchKernelGGL((lora_product<W::DT, typename W::L, W::NS>), dim3(blocks_of(q.g)), dim3(W::L::NT), 0, stream, q);
         return hipGetLastError();
     });
+}
+hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const LoraLow &low, float *slots, hipStream_t stream) {
+    if (!p.x.kc || !low.x.kc || p.P.kc != p.f.first.kc || p.P.kc != low.f.first.kc || p.R > LORA_FEW_R || p.x.rows > LORA_FEW_T)
+        return hipErrorInvalidValue;
+    if (p.P.kc) return dtype == 0 ? few<0, true>(tile, p, low, slots, stream) : few<1, true>(tile, p, low, slots, stream);
+    return dtype == 0 ? few<0, false>(tile, p, low, slots, stream) : few<1, false>(tile, p, low, slots, stream);
 }
 hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, const float *slots, hipStream_t stream) {
     return with_wide(dtype, tile, true, [&](auto w) {   // the operands' storage does not matter here

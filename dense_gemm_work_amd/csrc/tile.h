@@ -260,8 +260,8 @@ struct Grid {
 // contiguous range of ids, and ids walk bands of `band` P tiles row by row of Q,
 // so the tiles that run at once on an XCD are a compact block that shares its
 // operands in the XCD's L2.
-__device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &split) {
-    const int n = (int)gridDim.x, b = (int)blockIdx.x, x = b & 7;
+__device__ __forceinline__ void place(const Grid &g, int n, int b, int &tp, int &tq, int &split) {
+    const int x = b & 7;
     int id = x * (n >> 3) + min(x, n & 7) + (b >> 3);
     const int tiles = g.tiles_p * g.tiles_q;
     split = id / tiles;
@@ -272,6 +272,10 @@ __device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &spli
     const int w = id - bnd * per;
     tq = w / rows;
     tp = bnd * g.band + (w - tq * rows);
+}
+
+__device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &split) {
+    place(g, (int)gridDim.x, (int)blockIdx.x, tp, tq, split);
 }
 
 // The product loop of a TP x TQ tile on WP x WQ waves with NSP stages of P and NSQ

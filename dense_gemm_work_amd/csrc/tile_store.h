@@ -26,6 +26,34 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, f16x2));
 }
 
+template <int DT>
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b) {
+    if constexpr (DT == 0) {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    } else {
+        const f16x2 v = __builtin_bit_cast(f16x2, w);
+        a = (float)v[0];
+        b = (float)v[1];
+    }
+}
+template <int DT>
+__device__ __forceinline__ u32x2 pack4(f32x4 v) {
+    return u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+template <int DT>
+__device__ __forceinline__ f32x4 unpack4(u32x2 w) {
+    f32x4 v;
+    float a, b;
+    unpack2<DT>(w[0], a, b);
+    v[0] = a;
+    v[1] = b;
+    unpack2<DT>(w[1], a, b);
+    v[2] = a;
+    v[3] = b;
+    return v;
+}
+
 // v less its rounding to the type.
 template <int DT>
 __device__ __forceinline__ float remainder16(float v) {

@@ -15,7 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import _check, _lib, layout_word, stream_word
+from . import _check, _lib, current_stream_word, layout_word
 from .loss import _cus, _on, _rows, _warn_of_no_graph
 
 try:
@@ -128,7 +128,7 @@ def _workspace_bytes(T, H, F, layout, ldw_gate, ldw_up, dx, dw_gate, dw_up, dw_d
 def _call(a, x, backward, workspace):
     """Runs the call on torch's current stream, its workspace torch's unless given."""
     device = x.device
-    a.stream = stream_word(torch.cuda.current_stream(device))
+    a.stream = current_stream_word(device.index)
     if workspace is None:
         a.num_cus = cus = _cus(device.index)
         need = _workspace_bytes(a.T, a.H, a.F, a.layout, a.ldw_gate, a.ldw_up, 1 if a.dx else 0, 1 if a.dw_gate else 0,
@@ -161,7 +161,7 @@ def gated_ffn(x, w_gate, w_up, w_down, *, activation: str = "silu", b_layout: st
         raise ValueError("gate and up are given both or neither")
     save = save or gate is not None
     with _on(x, stream):
-        y = torch.empty((a.T, a.H), dtype=x.dtype, device=x.device) if y is None else y
+        y = x.new_empty((a.T, a.H)) if y is None else y
         a.y, a.ldy = y.data_ptr(), _rows("y", y, a.T, a.H, x.dtype, x.device)
         if save:
             if gate is None:

@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from . import _check, _lib, layout_word, stream_word
+from . import _check, _lib, current_stream_word, layout_word
 from .loss import _cus, _on, _rows, _vector, _warn_of_no_graph
 
 try:
@@ -94,13 +94,16 @@ def _matrices(name, t, count, rows, cols, dtype, device):
         raise ValueError(f"{name} must be on {device}")
     if tuple(t.shape) != (count, rows, cols):
         raise ValueError(f"{name} must be [{count}, {rows}, {cols}]")
-    if cols > 1 and t.stride(2) != 1 or rows > 1 and t.stride(1) != cols:
+    if t.is_contiguous():
+        return 0
+    stride = t.stride()
+    if cols > 1 and stride[2] != 1 or rows > 1 and stride[1] != cols:
         raise ValueError(f"{name}: every adapter's matrix must be contiguous")
     if count <= 1:
         return 0
-    if t.stride(0) < rows * cols:   # an expanded tensor; 0 would mean packed
+    if stride[0] < rows * cols:   # an expanded tensor; 0 would mean packed
         raise ValueError(f"{name}: adapters overlap")
-    return t.stride(0)
+    return stride[0]
 
 
 def _projection(x, w, a, b, adapter, scale, b_layout):
@@ -139,7 +142,7 @@ def _workspace_bytes(T, H, N, R, adapters, layout, dx, da, db, dab_type, backwar
 def _call(p, x, backward, workspace):
     """Runs the call on torch's current stream, its workspace torch's unless given."""
     device = x.device
-    p.stream = stream_word(torch.cuda.current_stream(device))
+    p.stream = current_stream_word(device.index)
     if workspace is None:
         p.num_cus = cus = _cus(device.index)
         need = _workspace_bytes(p.T, p.H, p.N, p.R, p.adapters, p.layout, 1 if p.dx else 0, 1 if p.da else 0, 1 if p.db else 0,
@@ -169,7 +172,7 @@ def linear_lora(x, w, a, b, adapter, *, scale=None, b_layout: str = "nk", y=None
     _warn_of_no_graph(x, w, a, b, what="the projection")
     p = _projection(x, w, a, b, adapter, scale, b_layout)
     with _on(x, stream):
-        y = torch.empty((p.T, p.N), dtype=x.dtype, device=x.device) if y is None else y
+        y = x.new_empty((p.T, p.N)) if y is None else y
         p.y, p.ldy = y.data_ptr(), _rows("y", y, p.T, p.N, x.dtype, x.device)
         _call(p, x, False, workspace)
     return y

@@ -22,7 +22,7 @@
  * Arithmetic: products, activations and their slopes in fp32.  h, dg and du, the
  * operands of the next products, are rounded to the type once (up to 64 rows: to the
  * sum of two such values, as nothing averages there and the weights' streams are
- * the time); kept gate and up, y, dx and weight gradients of the type once each.
+ * the time; the forward call of up to 4 rows with GEMM_B_NK keeps h in fp32); kept gate and up, y, dx and weight gradients of the type once each.
  * fp16 values beyond its range become infinities, as everywhere.
  * Every sum has a fixed order: the same call gives the same bits.
  *
@@ -109,7 +109,7 @@ typedef struct gemm_ffn_args_t {
 /* How a call runs (host arithmetic only). */
 typedef struct gemm_ffn_plan_t {
     int32_t num_cus;
-    int32_t parts;                       /* 16-bit parts of h, dg and du                     */
+    int32_t parts;                       /* 16-bit parts of h, dg and du (0: h in fp32)      */
     int32_t first_tile_f, first_tile_t;  /* features x rows of the kernel that makes h (backward: dg, du and h) */
     int32_t out_tile_h, out_tile_t;      /* tile of y (backward: dx)                         */
     int32_t out_splits;                  /* slices of F summed apart                         */

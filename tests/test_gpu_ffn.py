@@ -43,6 +43,9 @@ SIZES = [   # T, H, F, dtype, layout, act
     (1, 8, 8, "fp16", "kn", "gelu"),
     (1, 520, 4096, "bf16", "nk", "silu"),      # one token
     (2, 72, 264, "fp16", "nk", "relu"),        # ragged everything
+    (3, 1032, 520, "bf16", "nk", "gelu"),
+    (4, 4104, 72, "fp16", "nk", "silu"),       # the last by the kernels of single rows
+    (5, 4104, 72, "bf16", "nk", "silu"),
     (31, 128, 1000, "bf16", "kn", "silu"),
     (33, 136, 8200, "fp16", "nk", "gelu"),     # 64 x 64 tiles
     (32, 64, 8216, "bf16", "nk", "silu"),      # many features, few rows

@@ -37,6 +37,9 @@ SIZES = [   # T, H, N, L, R, dtype, layout, order
     (1, 2048, 2048, 8, 16, "bf16", "nk", "one"),      # one token
     (1, 256, 256, 8, 16, "bf16", "nk", "none"),
     (2, 520, 264, 2, 24, "fp16", "nk", "mixed"),
+    (3, 2056, 72, 3, 40, "bf16", "nk", "mixed"),
+    (4, 264, 1032, 7, 256, "fp16", "nk", "mixed"),
+    (5, 264, 1032, 7, 16, "bf16", "nk", "mixed"),
     (31, 264, 1000, 40, 16, "bf16", "kn", "mixed"),   # more adapters than rows
     (33, 128, 520, 5, 64, "bf16", "nk", "mixed"),
     (64, 1024, 264, 64, 8, "fp16", "nk", "mixed"),    # nearly a row each
