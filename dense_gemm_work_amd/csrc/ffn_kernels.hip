@@ -222,8 +222,119 @@ struct SlopeParams {
     int64_t ld, part;
 };
 
-// A lane's four consecutive features are 8 bytes of gate, up and each result; the
-// four lanes of a row make 32 bytes, and the L2 joins those of neighbouring blocks.
+// dg, du and h of one element.
+struct Slopes {
+    f32x4 dg, du, h;
+};
+template <int DT, uint32_t ACT>
+__device__ __forceinline__ Slopes slopes(u32x2 gate, u32x2 up, f32x4 dh) {
+    const f32x4 g = unpack4<DT>(gate), u = unpack4<DT>(up);
+    Slopes s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const Act a = activation<ACT>(g[e]);
+        s.dg[e] = dh[e] * u[e] * a.slope;
+        s.du[e] = dh[e] * a.value;
+        s.h[e] = u[e] * a.value;
+    }
+    return s;
+}
+
+// The epilogue of large tiles.  gate and up come, and dg, du and h go, as whole rows of a
+// wave's part of the tile, 16 bytes a lane, by way of the wave's own share of the LDS
+// (16-byte chunk c of row r at c ^ r); no wave waits for another.  16 rows at a time, the
+// next 16 rows' gate and up on their way into the other of two buffers, dg and du over
+// what they were made of.  The buffer's stores are issued whether a lane's row and
+// chunk exist or not, so that the counts of what is in flight are known.  (8 bytes a
+// lane straight from and to memory: 8192 x 4096 x 12288 997 us, 585 of them the product.)
+template <int DT, uint32_t ACT, class L>
+__device__ __forceinline__ void slope_rows(const SlopeParams &p, const L &loop, const typename L::Acc &acc, char *lds, int64_t p0, int64_t q0) {
+    constexpr int ROW = 2 * L::WAVE_P, CH = ROW / 16, PART = 16 * ROW, N = PART / 1024;   // bytes a row and 16 rows; instructions
+    constexpr int SHARE = 5 * PART;   // two buffers of gate and up, one of h
+    static_assert(L::NW * SHARE <= L::LDS_BYTES && L::CB >= 2, "every wave's share fits");
+    char *own = lds + loop.wave * SHARE;
+    const uint32_t own0 = loop.lds0 + loop.wave * SHARE;
+    const int lane = loop.lane;
+    const int64_t pw = p0 + loop.wp * L::WAVE_P, qw = q0 + loop.wq * L::WAVE_Q;
+    const int rows = (int)max((int64_t)0, min((int64_t)L::WAVE_Q, p.T - qw)), cols = (int)max((int64_t)0, min((int64_t)L::WAVE_P, p.F - pw));
+    const bool any = rows > 0 && cols > 0;
+    auto reach = [&](int64_t ld) { return any ? (uint32_t)(((rows - 1) * ld + cols) * 2) : 0u; };
+    const i32x4 rg = make_rsrc(p.gate + (any ? qw * p.ld_gate + pw : 0), reach(p.ld_gate));
+    const i32x4 ru = make_rsrc(p.up + (any ? qw * p.ld_up + pw : 0), reach(p.ld_up));
+    // where lane's 16 bytes of instruction x lie: row of 16 and chunk
+    auto row_of = [&](int x) { return (x * 1024 + lane * 16) / ROW; };
+    auto chunk_of = [&](int x) { return ((x * 1024 + lane * 16) % ROW / 16) ^ (row_of(x) & (CH - 1)); };
+    auto offset = [&](int j, int x, int64_t ld) {
+        const int r = 16 * j + row_of(x), c = chunk_of(x);
+        return r < rows && 8 * c < cols ? (uint32_t)(r * ld + 8 * c) * 2 : OOB;
+    };
+    auto fetch = [&](int j) {
+        const uint32_t to = own0 + (j & 1) * 2 * PART;
+#pragma unroll
+        for (int x = 0; x < N; ++x) load_lds16(rg, to + x * 1024, offset(j, x, p.ld_gate));
+#pragma unroll
+        for (int x = 0; x < N; ++x) load_lds16(ru, to + PART + x * 1024, offset(j, x, p.ld_up));
+    };
+    auto send = [&](uint16_t *base, const char *from, int j) {
+        const __amdgpu_buffer_rsrc_t out =
+            __builtin_amdgcn_make_buffer_rsrc(base + (any ? qw * p.ld + pw : 0), (short)0, (int)reach(p.ld), (int)RSRC_DW3);
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+            __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const u32x4 *>(from + x * 1024 + lane * 16), out, (int)offset(j, x, p.ld), 0, 0);
+    };
+    fetch(0);
+    fetch(1);
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) {
+        __builtin_amdgcn_sched_barrier(0);
+        // behind this part's loads: the last one's stores and the next one's loads
+        if (j == 0) wait_vm_lgkm<2 * N>();
+        else if (j + 1 < L::CB) wait_vm_lgkm<5 * N>();
+        else wait_vm_lgkm<3 * N>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        char *g = own + (j & 1) * 2 * PART, *u = g + PART, *h = own + 4 * PART;
+        const int r = lane & 15;
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i) {
+            const int c = 16 * i + 4 * (lane >> 4), at = r * ROW + (((c >> 3) ^ (r & (CH - 1))) << 4) + (c & 4) * 2;
+            const Slopes s = slopes<DT, ACT>(*reinterpret_cast<const u32x2 *>(g + at), *reinterpret_cast<const u32x2 *>(u + at), acc.v[i][j]);
+            *reinterpret_cast<u32x2 *>(g + at) = pack4<DT>(s.dg);
+            *reinterpret_cast<u32x2 *>(u + at) = pack4<DT>(s.du);
+            *reinterpret_cast<u32x2 *>(h + at) = pack4<DT>(s.h);
+        }
+        asm volatile("" ::: "memory");
+        send(p.dg, g, j);
+        send(p.du, u, j);
+        send(p.h, h, j);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j + 2 < L::CB) {
+            __builtin_amdgcn_s_waitcnt((15 | (3 << 14)) | (7 << 4));   // this buffer has been read
+            fetch(j + 2);
+        }
+    }
+}
+
+// Few rows: a lane's four consecutive features are 8 bytes of gate, up and each result.
+template <int DT, uint32_t ACT, class L>
+__device__ __forceinline__ void slope_few(const SlopeParams &p, const L &loop, const typename L::Acc &acc, int64_t p0, int64_t q0) {
+#pragma unroll
+    for (int j = 0; j < L::CB; ++j) {
+        const int64_t row = q0 + loop.q_of(j);
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i) {
+            const int64_t col = p0 + loop.p_of(i, 0);
+            if (row >= p.T || col >= p.F) continue;
+            const Slopes s = slopes<DT, ACT>(*reinterpret_cast<const u32x2 *>(p.gate + row * p.ld_gate + col),
+                                             *reinterpret_cast<const u32x2 *>(p.up + row * p.ld_up + col), acc.v[i][j]);
+            const int64_t at = row * p.ld + col;
+            store4<DT, true>(p.dg + at, p.part, s.dg);
+            store4<DT, true>(p.du + at, p.part, s.du);
+            store4<DT, true>(p.h + at, p.part, s.h);
+        }
+    }
+}
+
 template <int DT, class L>
 __global__ __launch_bounds__(L::NT, 2) void ffn_slope(SlopeParams p) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
@@ -236,39 +347,8 @@ __global__ __launch_bounds__(L::NT, 2) void ffn_slope(SlopeParams p) {
     loop.run_any(p.down, p0, p.dy, q0, p.H, 0, p.g.slabs, acc);
     if (!loop.active()) return;
     with_act(p.act, [&](auto A) {
-#pragma unroll
-        for (int j = 0; j < L::CB; ++j) {
-            const int64_t row = q0 + loop.q_of(j);
-            u32x2 g16[L::RB], u16[L::RB];
-#pragma unroll
-            for (int i = 0; i < L::RB; ++i) {
-                const int64_t col = p0 + loop.p_of(i, 0);
-                const bool in = row < p.T && col < p.F;
-                g16[i] = in ? *reinterpret_cast<const u32x2 *>(p.gate + row * p.ld_gate + col) : u32x2{0u, 0u};
-                u16[i] = in ? *reinterpret_cast<const u32x2 *>(p.up + row * p.ld_up + col) : u32x2{0u, 0u};
-            }
-#pragma unroll
-            for (int i = 0; i < L::RB; ++i) {
-                const int64_t col = p0 + loop.p_of(i, 0);
-                const f32x4 g = unpack4<DT>(g16[i]), u = unpack4<DT>(u16[i]);
-                f32x4 dg, du, h;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Act a = activation<decltype(A)::value>(g[e]);
-                    dg[e] = acc.v[i][j][e] * u[e] * a.slope;
-                    du[e] = acc.v[i][j][e] * a.value;
-                    h[e] = u[e] * a.value;
-                }
-                if (row < p.T && col < p.F) {
-                    const int64_t at = row * p.ld + col;
-                    constexpr bool two = L::TQ <= LOSS_FEW;
-                    store4<DT, two>(p.dg + at, p.part, dg);
-                    store4<DT, two>(p.du + at, p.part, du);
-                    store4<DT, two>(p.h + at, p.part, h);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);   // one block column's loads in flight: no more registers are free
-        }
+        if constexpr (L::TQ <= LOSS_FEW) slope_few<DT, decltype(A)::value>(p, loop, acc, p0, q0);
+        else slope_rows<DT, decltype(A)::value>(p, loop, acc, lds, p0, q0);
     });
 }
 
