@@ -111,12 +111,12 @@ int slope_tile(const gemm_ffn_args_t &a, int cus) {
     return a.T > dgw::LOSS_FEW ? choose(a.F, a.T, a.H, false, cus).tile : dgw::LT_64x64;
 }
 
-// Tile and slices of y and dx, products over the F features.  Few rows: one workgroup
+// Tile and slices of y and dx, products over k = F and 2 F features.  Few rows: one workgroup
 // a CU, as two parts of h or dg leave room for.
-Choice out_choice(const gemm_ffn_args_t &a, int cus) {
-    if (a.T > dgw::LOSS_FEW) return choose(a.H, a.T, a.F, true, cus);
+Choice out_choice(const gemm_ffn_args_t &a, int64_t k, int cus) {
+    if (a.T > dgw::LOSS_FEW) return choose(a.H, a.T, k, true, cus);
     const int tile = a.T <= 32 ? dgw::LT_128x32 : dgw::LT_128x64;
-    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(a.H, 128), ceil_div(a.F, 64) / 8))};
+    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(a.H, 128), ceil_div(k, 64) / 8))};
 }
 
 // One weight gradient, out[q][p] = sum_t P[t][p] Q[t][q].
@@ -160,7 +160,7 @@ Plan make_plan(const gemm_ffn_args_t &a, bool backward, int cus) {
     p.h = p.take(hidden);   // two parts are as large as fp32
     p.vec = !backward && is_nk(a) && a.T <= dgw::FFN_VEC_T;
     if (p.vec) return p;
-    p.out = out_choice(a, cus);
+    p.out = out_choice(a, backward ? 2 * a.F : a.F, cus);
     if (!backward) {
         p.first = gate_tile(a, cus);
         need(p.out, a.H, a.T);
@@ -262,23 +262,51 @@ int forward(const gemm_ffn_args_t &a) {
     return product(c, pl.out, y, "launch y");
 }
 
-// dw = the product over the rows of two [T][...] matrices: `outs` holds the weight's
-// output features, `ins` its input features.
-int weight_gradient(const gemm_ffn_args_t &a, const Call &c, const Grad &g, void *dw, int64_t lddw, Shape w,
-                    const dgw::LossMatrix &outs, const dgw::LossMatrix &ins, const char *what) {
-    if (!g.wanted) return GEMM_OK;
-    dgw::LossProduct p;
-    p.P = c.nk ? ins : outs;
-    p.Q = c.nk ? outs : ins;
-    p.K = (int)a.T;
-    p.out = dw;
-    p.ldo = or_packed(lddw, w.row);
-    p.out_kind = a.dw_type == GEMM_FFN_DW_SAME ? dgw::LO_16 : a.dw_type == GEMM_FFN_DW_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
-    if (!g.outer) return product(c, g.c, p, what);
-    p.splits = 1;
-    p.unscale = nullptr;
-    const hipError_t e = dgw::launch_loss_outer(c.dtype, p, 2 * c.cus, c.stream);
-    return e == hipSuccess ? GEMM_OK : set_hip_error(e, what);
+// The weights' gradients: `outs` holds a weight's output features, `ins` its input ones.
+struct Weight {
+    const Grad &g;
+    void *dw;
+    int64_t ldo;
+    dgw::LossMatrix outs, ins;
+};
+int weight_gradients(const gemm_ffn_args_t &a, const Call &c, const Weight (&w)[3]) {
+    const int kind = a.dw_type == GEMM_FFN_DW_SAME ? dgw::LO_16 : a.dw_type == GEMM_FFN_DW_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
+    // one launch for those of whole products on one tile, else one each
+    int tile = -1;
+    bool together = a.T > dgw::LOSS_FEW;
+    for (const Weight &x : w)
+        if (x.dw) {
+            together = together && x.g.c.splits == 1 && (tile < 0 || tile == x.g.c.tile);
+            tile = x.g.c.tile;
+        }
+    if (together && tile >= 0) {
+        dgw::FfnWeights p;
+        p.T = (int)a.T;
+        p.out_kind = kind;
+        for (int i = 0; i < 3; ++i) p.one[i] = {c.nk ? w[i].ins : w[i].outs, c.nk ? w[i].outs : w[i].ins, w[i].dw, w[i].ldo};
+        const hipError_t e = dgw::launch_ffn_weights(c.dtype, tile, p, c.stream);
+        return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the weights' gradients");
+    }
+    for (const Weight &x : w) {
+        if (!x.dw) continue;
+        dgw::LossProduct p;
+        p.P = c.nk ? x.ins : x.outs;
+        p.Q = c.nk ? x.outs : x.ins;
+        p.K = (int)a.T;
+        p.out = x.dw;
+        p.ldo = x.ldo;
+        p.out_kind = kind;
+        if (!x.g.outer) {
+            const int rc = product(c, x.g.c, p, "launch a weight's gradient");
+            if (rc != GEMM_OK) return rc;
+            continue;
+        }
+        p.splits = 1;
+        p.unscale = nullptr;
+        const hipError_t e = dgw::launch_loss_outer(c.dtype, p, 2 * c.cus, c.stream);
+        if (e != hipSuccess) return set_hip_error(e, "launch a weight's gradient");
+    }
+    return GEMM_OK;
 }
 
 // dx[t][i] = sum_f w_gate[f][i] dg[t][f] + w_up[f][i] du[t][f].
@@ -346,9 +374,10 @@ int backward(const gemm_ffn_args_t &a) {
     const dgw::LossMatrix mx = matrix(a.x, a.ldx, a.H, a.H, false), mdy = matrix(a.dy, a.lddy, a.H, a.H, false);
     const dgw::LossMatrix mg = matrix(dg, 0, a.F, a.F, false, pl.part), mu = matrix(du, 0, a.F, a.F, false, pl.part),
                           mh = matrix(h, 0, a.F, a.F, false, pl.part);
-    if ((rc = weight_gradient(a, c, pl.gate, a.dw_gate, a.lddw_gate, in, mg, mx, "launch dw_gate")) != GEMM_OK) return rc;
-    if ((rc = weight_gradient(a, c, pl.up, a.dw_up, a.lddw_up, in, mu, mx, "launch dw_up")) != GEMM_OK) return rc;
-    return weight_gradient(a, c, pl.down, a.dw_down, a.lddw_down, down, mdy, mh, "launch dw_down");
+    const Weight w[3] = {{pl.gate, a.dw_gate, or_packed(a.lddw_gate, in.row), mg, mx},
+                         {pl.up, a.dw_up, or_packed(a.lddw_up, in.row), mu, mx},
+                         {pl.down, a.dw_down, or_packed(a.lddw_down, down.row), mdy, mh}};
+    return weight_gradients(a, c, w);
 }
 
 int plan(const gemm_ffn_args_t *args, int32_t backward, int32_t num_cus, gemm_ffn_plan_t *out) {

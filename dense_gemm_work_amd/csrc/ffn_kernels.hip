@@ -386,6 +386,51 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void ffn_sum(SumParams p) {
         for (int j = 0; j < L::CB; ++j) slot[(i * L::CB + j) * 64] = acc.v[i][j];
 }
 
+// The weights' gradients, each a product over the rows, in one launch: their tiles
+// together fill the last round of workgroups better than three launches' (331 x 1536 x
+// 4104: 31 us in three).
+struct WeightParams {
+    struct One {
+        Matrix P, Q;
+        Grid g;
+        void *out;
+        int64_t ldo;
+        int end;   // the launch's workgroups up to and with this gradient's
+    } one[3];
+    int count, T, out_kind;
+};
+template <int DT, class L>
+__global__ __launch_bounds__(L::NT, L::WAVES) void ffn_weights(WeightParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
+    int which = 0, start = 0;
+    while (which + 1 < p.count && (int)blockIdx.x >= p.one[which].end) start = p.one[which++].end;
+    const WeightParams::One &q = p.one[which];
+    int tp, tq, split;
+    place(q.g, q.end - start, (int)blockIdx.x - start, tp, tq, split);
+    const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
+    L loop(lds);
+    typename L::Acc acc;
+    L::zero(acc);
+    loop.run_any(q.P, p0, q.Q, q0, p.T, 0, q.g.slabs, acc);
+    if (p.out_kind == LO_16) {
+        store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(q.out), q.ldo, p0, q0, q.P.rows, q.Q.rows);
+        return;
+    }
+    const bool add = p.out_kind == LO_F32_ADD;
+#pragma unroll
+    for (int i = 0; i < L::RB; ++i) {
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j) {
+            const int64_t col = p0 + loop.p_of(i, 0), row = q0 + loop.q_of(j);
+            if (row < q.Q.rows && col < q.P.rows) {
+                f32x4 *at = reinterpret_cast<f32x4 *>(static_cast<float *>(q.out) + row * q.ldo + col);
+                *at = add ? acc.v[i][j] + *at : acc.v[i][j];
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);   // one block row's loads in flight: no more registers are free
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
@@ -466,6 +511,30 @@ hipError_t run_vec(const FfnGate &a, const LossMatrix &down, float *h, uint16_t 
     return hipGetLastError();
 }
 
+template <int DT, class L>
+hipError_t run_weights(const FfnWeights &a, hipStream_t stream) {
+    WeightParams q;
+    q.count = 0;
+    q.T = a.T;
+    q.out_kind = a.out_kind;
+    int end = 0;
+    for (const FfnWeights::One &w : a.one) {
+        if (!w.out) continue;
+        const Grid g = grid_of<L>(w.P.rows, w.Q.rows, a.T, 1);
+        end += (int)blocks_of(g);
+        q.one[q.count++] = {matrix(w.P), matrix(w.Q), g, w.out, w.ldo, end};
+    }
+    if (!end) return hipSuccess;
+    hipLaunchKernelGGL((ffn_weights<DT, L>), dim3((unsigned)end), dim3(L::NT), 0, stream, q);
+    return hipGetLastError();
+}
+template <int DT>
+hipError_t weights(int tile, const FfnWeights &a, hipStream_t stream) {
+    if (tile == LT_256x256) return run_weights<DT, Loop<DT, false, false, 256, 256, 2, 4, 2, 2>>(a, stream);
+    if (tile == LT_128x128) return run_weights<DT, Loop<DT, false, false, 128, 128, 2, 2, 2, 2>>(a, stream);
+    return hipErrorInvalidValue;
+}
+
 bool few(int tile) { return loss_tile_shape(tile).q <= LOSS_FEW; }
 
 }  // namespace
@@ -489,6 +558,12 @@ hipError_t launch_ffn_sum(int dtype, int tile, const FfnSum &p, hipStream_t stre
         return hipErrorInvalidValue;
     if (p.gate.kc) return dtype == 0 ? sum<0, true>(tile, p, stream) : sum<1, true>(tile, p, stream);
     return dtype == 0 ? sum<0, false>(tile, p, stream) : sum<1, false>(tile, p, stream);
+}
+
+hipError_t launch_ffn_weights(int dtype, int tile, const FfnWeights &p, hipStream_t stream) {
+    for (const FfnWeights::One &w : p.one)
+        if (w.out && (w.P.kc || w.Q.kc)) return hipErrorInvalidValue;
+    return dtype == 0 ? weights<0>(tile, p, stream) : weights<1>(tile, p, stream);
 }
 
 hipError_t launch_ffn_slope(int dtype, int tile, const FfnSlope &p, hipStream_t stream) {
