@@ -109,12 +109,55 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     return l;
 }
 
-// The wide product's tile and slices.
-Choice out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
-    if (a.T > 128) return choose(rows_p, a.T, k, true, cus);
-    const int tile = a.T <= 32 ? dgw::LP_64x32 : a.T <= 64 ? dgw::LP_64x64 : dgw::LP_64x128;
-    // one workgroup a CU (96 x 4096 x 4096: 14.8 us, with two 16.2, and a shorter join)
-    return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(rows_p, 64), ceil_div(k, 64) / 4))};
+// The wide product's tile, and which of its tiles are computed whole and in how many
+// slices the rest: the cheapest by choose()'s model of a tile's time (with 4 us more for the
+// adapters) and of the join, for slices of every tile and for whole rounds of workgroups
+// with slices of what is left over.  5000 x 4096 x 8192 on 256 CUs: 640 tiles of 256 x 256,
+// the last 128 in two slices, 293 us in the model; in three rounds of whole tiles 330.
+struct Wide {
+    int tile = dgw::LP_128x128, splits = 1;
+    int64_t whole = 0;   // tiles
+};
+int64_t tiles_of(int tile, int64_t rows_p, int64_t rows_q) {
+    const dgw::LossTileShape s = dgw::lora_tile_shape(tile);
+    return ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q);
+}
+Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
+    Wide best;
+    const int64_t slabs = ceil_div(k, 64);
+    if (a.T <= 128) {
+        best.tile = a.T <= 32 ? dgw::LP_64x32 : a.T <= 64 ? dgw::LP_64x64 : dgw::LP_64x128;
+        // one workgroup a CU (96 x 4096 x 4096: 14.8 us, with two 16.2, and a shorter join)
+        best.splits = (int)std::max<int64_t>(1, std::min(cus / ceil_div(rows_p, 64), slabs / 4));
+        best.whole = best.splits == 1 ? tiles_of(best.tile, rows_p, a.T) : 0;
+        return best;
+    }
+    double least = 0.0;
+    auto consider = [&](int tile, double pair, double lone, double fixed) {
+        const dgw::LossTileShape s = dgw::lora_tile_shape(tile);
+        const int64_t tiles = tiles_of(tile, rows_p, a.T), slots = (int64_t)cus * s.per_cu;
+        for (int64_t whole : {int64_t(0), tiles / slots * slots, tiles}) {
+            const int64_t rest = tiles - whole;
+            const int64_t most = rest ? std::max<int64_t>(1, std::min({slots / rest, slabs / 8, int64_t(16)})) : 1;
+            for (int64_t n = 1; n <= most; ++n) {
+                if (rest && whole && n == 1) continue;
+                // a workgroup alone on its CU gets through its slabs faster
+                const double slab = rest * n <= cus ? lone : pair;
+                double us = (double)ceil_div(whole, slots) * ((double)slabs * pair + fixed);
+                if (rest) us += (double)ceil_div(rest * n, slots) * ((double)ceil_div(slabs, n) * slab + fixed);
+                if (rest && n > 1) us += 3.0 + 4.0 * (double)n * (double)rest * (double)(s.p * s.q) / 4.5e6;
+                if (least == 0.0 || us < least) {
+                    least = us;
+                    best.tile = tile;
+                    best.splits = (int)n;
+                    best.whole = n == 1 ? tiles : whole;
+                }
+            }
+        }
+    };
+    consider(dgw::LP_128x128, 0.92, 0.6, 6.5);
+    consider(dgw::LP_256x256, 1.53, 1.53, 12.0);
+    return best;
 }
 
 // Few rows of small ranks take the adapters in the join, where each row reads its own
@@ -122,18 +165,20 @@ Choice out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
 // beside w.
 bool few_rows(const gemm_lora_args_t &a) { return a.T <= dgw::LORA_FEW_T && a.R <= dgw::LORA_FEW_R && a.T * a.R <= 4096; }
 
-int outer_splits(const gemm_lora_args_t &a, int64_t wide, int cus) {
-    const int64_t blocks = a.adapters * ceil_div(wide, 128) * ceil_div(a.R, 64);
-    return (int)std::max<int64_t>(1, std::min(2 * cus / blocks, ceil_div(a.T, 64) / 8));
+// Slices of the rows for da and db, which one launch computes.
+int outer_splits(const gemm_lora_args_t &a, int cus) {
+    const int64_t narrow = ceil_div(a.R, 64);
+    const int64_t blocks = a.adapters * narrow * ((a.da ? ceil_div(a.H, 128) : 0) + (a.db ? ceil_div(a.N, 128) : 0));
+    return (int)std::max<int64_t>(1, std::min(2 * cus / std::max<int64_t>(1, blocks), ceil_div(a.T, 64) / 8));
 }
 
 struct Plan {
     Low s, ds;
-    Choice out{dgw::LP_128x128, 1};
+    Wide out;
     bool few = false;
-    int da_splits = 1, db_splits = 1;
+    int dab_splits = 1;
     int64_t db_at = 0;   // db's slices behind da's
-    int64_t low = 0, dlow = 0, part_s = 0, part_ds = 0, partial = 0, masks = 0;   // byte offsets
+    int64_t low = 0, dlow = 0, part_s = 0, part_ds = 0, slots = 0, partial = 0, masks = 0;   // byte offsets
     int64_t bytes = 0;
     int64_t take(int64_t n) {
         const int64_t at = bytes;
@@ -145,8 +190,7 @@ struct Plan {
 Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     Plan p;
     const bool nk = is_nk(a);
-    int64_t partial = 0;   // one launch's after the other
-    auto need = [&](int64_t n) { partial = std::max(partial, n); };
+    int64_t slots = 0;
     const bool own = backward && (a.da || a.db);   // the adapters' gradients: s and ds in the type, too
     auto low = [&](Low &l, int64_t k, bool kc, int64_t &slices, int64_t &at) {
         l = low_plan(a, k, kc, cus);
@@ -159,20 +203,19 @@ Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     if (!backward || a.dx) {
         p.out = out_plan(a, wide, backward ? a.N : a.H, cus);
         p.few = !backward && few_rows(a);
-        if (p.out.splits > 1 || p.few) need(dgw::lora_slots_bytes(p.out.tile, wide, a.T, p.out.splits));
+        if (p.few) p.out.whole = 0;
+        const dgw::LossTileShape s = dgw::lora_tile_shape(p.out.tile);
+        slots = (tiles_of(p.out.tile, wide, a.T) - p.out.whole) * p.out.splits * s.p * s.q * 4;
     }
+    if (slots) p.slots = p.take(slots);
     if (own) {
         p.masks = p.take(a.adapters * ceil_div(a.T, 64) * 8);
-        p.da_splits = outer_splits(a, a.H, cus);
-        p.db_splits = outer_splits(a, a.N, cus);
-        // both at once
-        int64_t both = 0;
-        if (a.da && p.da_splits > 1) both += round_up(p.da_splits * (int64_t)a.adapters * a.R * a.H * 4, 256);
-        p.db_at = both;
-        if (a.db && p.db_splits > 1) both += p.db_splits * (int64_t)a.adapters * a.R * a.N * 4;
-        need(both);
+        p.dab_splits = outer_splits(a, cus);
+        if (p.dab_splits > 1) {
+            p.db_at = a.da ? round_up(p.dab_splits * (int64_t)a.adapters * a.R * a.H * 4, 256) : 0;
+            p.partial = p.take(p.db_at + (a.db ? p.dab_splits * (int64_t)a.adapters * a.R * a.N * 4 : 0));
+        }
     }
-    if (partial) p.partial = p.take(partial);
     return p;
 }
 
@@ -228,25 +271,15 @@ dgw::LoraFactor factor_b(const gemm_lora_args_t &a, bool rank_rows) {   // rows:
 
 dgw::LoraLow narrow(const gemm_lora_args_t &a, const Call &c, const Low &l, const dgw::LoraFactor &f, const dgw::LossMatrix &x, int64_t k,
                     int64_t slices) {
-    return {c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, slices), nullptr};
+    return {c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, slices)};
 }
 
 dgw::LoraProduct product(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &w, const dgw::LossMatrix &x,
                          const dgw::LoraFactor &f, const dgw::LoraLow &low, int64_t k, void *out, int64_t ldo) {
-    return {c.rows, w, x, f, low.partial, low.splits, (int)k, a.R, c.plan.out.splits, out, ldo};
-}
-
-int wide(const Call &c, dgw::LoraProduct p) {
-    const Choice &how = c.plan.out;
-    float *slots = part<float>(c.ws, c.plan.partial);
-    void *out = p.out;
-    if (how.splits > 1) p.out = slots;
-    hipError_t e = dgw::launch_lora_product(c.dtype, how.tile, p, c.stream);
-    if (e == hipSuccess && how.splits > 1) {
-        p.out = out;
-        e = dgw::launch_lora_join(c.dtype, how.tile, p, slots, c.stream);
-    }
-    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the projection");
+    const Wide &o = c.plan.out;
+    const bool sliced = o.splits > 1 || c.plan.few;
+    return {c.rows, w, x, f, low.partial, low.splits, (int)k, a.R, o.splits, (int)o.whole,
+            sliced ? part<float>(c.ws, c.plan.slots) : nullptr, out, ldo};
 }
 
 int forward(const gemm_lora_args_t &a) {
@@ -261,17 +294,19 @@ int forward(const gemm_lora_args_t &a) {
                                        or_packed(a.ldy, a.N));
     hipError_t e;
     if (c.plan.few) {
-        e = dgw::launch_lora_few(c.dtype, c.plan.out.tile, y, s, part<float>(c.ws, c.plan.partial), c.stream);
+        e = dgw::launch_lora_few(c.dtype, c.plan.out.tile, y, s, c.stream);
         return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the projection of few rows");
     }
     if ((e = dgw::launch_lora_low(c.dtype, s, c.stream)) != hipSuccess) return set_hip_error(e, "launch the narrow product");
-    return wide(c, y);
+    e = dgw::launch_lora_product(c.dtype, c.plan.out.tile, y, dgw::LoraLowJoin(), c.stream);
+    if (e == hipSuccess && y.splits > 1) e = dgw::launch_lora_join(c.dtype, c.plan.out.tile, y, c.stream);
+    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the projection");
 }
 
 // da or db: out[o][i] = sum over an adapter's rows of outs[t][o] ins[t][i] as "nk" stores
 // it; one of them holds the narrow rows.
 dgw::LoraOuter outer(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &outs, const dgw::LossMatrix &ins, bool narrow_ins,
-                     int splits, int64_t at, void *out) {
+                     int64_t at, void *out) {
     dgw::LoraOuter p;
     p.P = c.nk ? ins : outs;
     p.Q = c.nk ? outs : ins;
@@ -279,7 +314,7 @@ dgw::LoraOuter outer(const gemm_lora_args_t &a, const Call &c, const dgw::LossMa
     p.T = (int)a.T;
     p.count = a.adapters;
     p.masks = part<uint64_t>(c.ws, c.plan.masks);
-    p.splits = splits;
+    p.splits = c.plan.dab_splits;
     p.partial = part<float>(c.ws, c.plan.partial + at);
     p.out_kind = a.dab_type == GEMM_LORA_DAB_SAME ? dgw::LO_16 : a.dab_type == GEMM_LORA_DAB_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
     p.out = out;
@@ -309,20 +344,28 @@ int backward(const gemm_lora_args_t &a) {
     const dgw::LossMatrix x = matrix(a.x, a.ldx, a.H, a.T, true), dy = matrix(a.dy, a.lddy, a.N, a.T, true);
     dgw::LoraLow s = narrow(a, c, pl.s, factor_a(a, true), x, a.H, pl.part_s);
     dgw::LoraLow ds = narrow(a, c, pl.ds, factor_b(a, true), dy, a.N, pl.part_ds);
-    s.low = part<uint16_t>(c.ws, pl.low);
-    ds.low = part<uint16_t>(c.ws, pl.dlow);
-    if (!a.db) s.partial = nullptr, s.low = nullptr;
-    if (!a.dx && !a.da) ds.partial = nullptr, ds.low = nullptr;
+    if (!a.db) s.partial = nullptr;
+    if (!a.dx && !a.da) ds.partial = nullptr;
     if ((e = dgw::launch_lora_lows(c.dtype, s, ds, own ? part<uint64_t>(c.ws, pl.masks) : nullptr, c.stream)) != hipSuccess)
         return set_hip_error(e, "launch the narrow products");
-    if (a.dx && (rc = wide(c, product(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx,
-                                      or_packed(a.lddx, a.H)))) != GEMM_OK)
-        return rc;
+    dgw::LoraLowJoin join;
+    if (own)
+        join = {c.rows, a.R, s.partial, ds.partial, s.splits, ds.splits, s.partial ? part<uint16_t>(c.ws, pl.low) : nullptr,
+                ds.partial ? part<uint16_t>(c.ws, pl.dlow) : nullptr};
+    dgw::LoraProduct dx;
+    if (a.dx) {
+        dx = product(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx, or_packed(a.lddx, a.H));
+        e = dgw::launch_lora_product(c.dtype, pl.out.tile, dx, join, c.stream);
+        if (e == hipSuccess && dx.splits > 1 && !own) e = dgw::launch_lora_join(c.dtype, pl.out.tile, dx, c.stream);
+    } else {
+        e = dgw::launch_lora_low_join(c.dtype, join, c.stream);
+    }
+    if (e != hipSuccess) return set_hip_error(e, "launch dx");
     if (!own) return GEMM_OK;
-    const dgw::LossMatrix ms = matrix(s.low, 0, a.R, a.R, false), mds = matrix(ds.low, 0, a.R, a.R, false);
+    const dgw::LossMatrix ms = matrix(join.s_low, 0, a.R, a.R, false), mds = matrix(join.ds_low, 0, a.R, a.R, false);
     const dgw::LossMatrix mx = matrix(a.x, a.ldx, a.H, a.H, false), mdy = matrix(a.dy, a.lddy, a.N, a.N, false);
-    e = dgw::launch_lora_outers(c.dtype, outer(a, c, mds, mx, false, pl.da_splits, 0, a.da),
-                                outer(a, c, mdy, ms, true, pl.db_splits, pl.db_at, a.db), c.stream);
+    e = dgw::launch_lora_outers(c.dtype, outer(a, c, mds, mx, false, 0, a.da), outer(a, c, mdy, ms, true, pl.db_at, a.db),
+                                pl.out.tile, a.dx && dx.splits > 1 ? &dx : nullptr, c.stream);
     return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch da and db");
 }
 
@@ -344,10 +387,8 @@ int plan(const gemm_lora_args_t *args, int32_t backward, int32_t num_cus, gemm_l
     out->out_tile_p = o.p;
     out->out_tile_t = o.q;
     out->out_splits = p.out.splits;
-    if (backward) {
-        out->da_splits = p.da_splits;
-        out->db_splits = p.db_splits;
-    }
+    out->out_whole = p.out.whole;
+    if (backward) out->dab_splits = p.dab_splits;
     out->workspace_bytes = p.bytes;
     return GEMM_OK;
 }

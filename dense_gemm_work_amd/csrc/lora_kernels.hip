@@ -127,7 +127,6 @@ struct LowParams {
     int tiles_r, groups, lists, splits;
     int blocks;
     float *partial;
-    uint16_t *low;   // lora_low_join
 };
 
 template <class L>
@@ -195,22 +194,36 @@ __global__ __launch_bounds__(256, LK::WAVES < LR::WAVES ? LK::WAVES : LR::WAVES)
     else mask_block(k.rows, id - k.blocks - r.blocks, masks);
 }
 
-// s and ds as the type holds them, for the adapters' gradients: a thread per four values.
+// s and ds as the type holds them, for the adapters' gradients, [T][R]: a thread per
+// four values.  low == nullptr: not kept.
+struct LowJoin {
+    LoraRows rows;
+    int R;
+    struct One {
+        const float *partial;
+        int splits;
+        uint16_t *low;
+    } one[2];
+    int blocks;   // of 256 threads
+};
 template <int DT>
-__global__ __launch_bounds__(256) void lora_low_join(LowParams a, LowParams b) {
-    const int64_t each = (int64_t)a.rows.T * (a.R / 4);
-    int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__device__ __forceinline__ void join_block(const LowJoin &p, int64_t id) {
+    const int64_t each = (int64_t)p.rows.T * (p.R / 4);
     const bool second = id >= each;
     if (second) id -= each;
     if (id >= each) return;
-    const int quads = a.R / 4, col = 4 * (int)(id % quads);
+    const LowJoin::One q = second ? p.one[1] : p.one[0];
+    const int quads = p.R / 4, col = 4 * (int)(id % quads);
     const int64_t row = id / quads;
-    const int l = adapter_of(a.rows, row);
-    uint16_t *low = second ? b.low : a.low;
-    if (l < 0 || !low) return;
-    const float scale = a.rows.scale ? a.rows.scale[l] : 1.0f;
-    const f32x4 v = sum_slices((second ? b.partial : a.partial) + row * a.R + col, (int64_t)a.rows.T * a.R, second ? b.splits : a.splits) * scale;
-    *reinterpret_cast<u32x2 *>(low + row * a.R + col) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    const int a = adapter_of(p.rows, row);
+    if (a < 0 || !q.low) return;
+    const float scale = p.rows.scale ? p.rows.scale[a] : 1.0f;
+    const f32x4 v = sum_slices(q.partial + row * p.R + col, (int64_t)p.rows.T * p.R, q.splits) * scale;
+    *reinterpret_cast<u32x2 *>(q.low + row * p.R + col) = u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+template <int DT>
+__global__ __launch_bounds__(256) void lora_low_join(LowJoin p) {
+    join_block<DT>(p, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -223,11 +236,31 @@ struct WideParams {
     const float *partial;   // the narrow product's slices
     int low_splits;
     int K, R;
-    Grid g;
-    bool slots;
+    Grid g;       // splits: slices of each of the tail's tiles
+    int whole;    // tiles before the tail
+    float *slots;   // the tail's slices
     void *out;
     int64_t ldo;
+    LowJoin join;   // of the workgroups behind those of tiles
 };
+// Tiles that fill whole rounds of workgroups are computed whole, those of the last round
+// (the tail: ids from `whole` on) in slices, so that they fill it too.
+__host__ __device__ inline int wide_blocks(const Grid &g, int whole) { return whole + (g.tiles_p * g.tiles_q - whole) * g.splits; }
+// The workgroup's tile, slice and, of a tail tile, number in the tail (else -1).
+__device__ __forceinline__ int place_wide(const Grid &g, int whole, int b, int &tp, int &tq, int &split) {
+    const int rest = g.tiles_p * g.tiles_q - whole;
+    int id;
+    split = 0;
+    if (b < whole) {
+        id = spread(whole, b);
+    } else {
+        id = spread(rest * g.splits, b - whole);
+        split = id / rest;
+        id = whole + id - split * rest;
+    }
+    tile_of(g, id, tp, tq);
+    return b < whole ? -1 : id - whole;
+}
 
 // acc += the products of the adapters' slabs (list entries from, from + every, ...)
 // with the narrow rows.  Those of the tile, 64 ranks at a time, are put together from
@@ -342,6 +375,13 @@ struct Extra {
     }
 };
 
+// Slot of a tail tile's slice: a wave's blocks one after the other, each 64 float4.
+template <class L>
+__device__ __forceinline__ f32x4 *wide_slot(const WideParams &p, int tail, int split, int quad) {
+    const int64_t rest = p.g.tiles_p * p.g.tiles_q - p.whole;
+    return reinterpret_cast<f32x4 *>(p.slots) + (split * rest + tail) * (L::TP * L::TQ / 4) + quad;
+}
+
 template <int DT, class L, int NS>
 __global__ __launch_bounds__(L::NT, 2) void lora_product(WideParams p) {
     using X = Extra<DT, L, NS>;
@@ -349,21 +389,26 @@ __global__ __launch_bounds__(L::NT, 2) void lora_product(WideParams p) {
     constexpr int BYTES = NEED > L::LDS_BYTES ? NEED : L::LDS_BYTES;
     __shared__ __attribute__((aligned(16))) char lds[BYTES];
     static_assert(L::NT >= L::TQ, "a thread for each row");
+    const int wide = wide_blocks(p.g, p.whole);
+    if ((int)blockIdx.x >= wide) {
+        join_block<DT>(p.join, ((int64_t)blockIdx.x - wide) * L::NT + threadIdx.x);
+        return;
+    }
     int tp, tq, split;
-    place(p.g, tp, tq, split);
+    const int tail = place_wide(p.g, p.whole, (int)blockIdx.x, tp, tq, split), splits = tail < 0 ? 1 : p.g.splits;
     const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
     const int mine = adapter_of(p.rows, threadIdx.x < L::TQ ? q0 + threadIdx.x : p.rows.T);
     L loop(lds);
     typename L::Acc acc;
     L::zero(acc);
-    const int s0 = (int)((int64_t)p.g.slabs * split / p.g.splits), s1 = (int)((int64_t)p.g.slabs * (split + 1) / p.g.splits);
+    const int s0 = (int)((int64_t)p.g.slabs * split / splits), s1 = (int)((int64_t)p.g.slabs * (split + 1) / splits);
     List<L::TQ> &list = *reinterpret_cast<List<L::TQ> *>(lds + X::BYTES);
     // Small tiles: last, the rows' adapters on their way meanwhile.  Large ones: first, and
     // one form of the loop for every K: what lives across their loop, or accumulators
     // that meet two loops, spill hundreds of registers in its last iterations.
     if constexpr (X::HOLD) loop.run_any(p.P, p0, p.x, q0, p.K, s0, s1, acc);
     list.fill(mine);
-    X::run(loop, lds, p, p0, q0, list, split, p.g.splits, acc);
+    X::run(loop, lds, p, p0, q0, list, split, splits, acc);
     if constexpr (!X::HOLD) loop.template run<true>(p.P, p0, p.x, q0, p.K, s0, s1, acc);
 #pragma unroll
     for (int j = 0; j < L::CB; ++j)
@@ -372,42 +417,38 @@ __global__ __launch_bounds__(L::NT, 2) void lora_product(WideParams p) {
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc.v[i][j][e] = __builtin_nanf("");
-    if (!p.slots) {
+    if (splits == 1) {
         store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, p.P.rows, p.x.rows);
         return;
     }
     if (!loop.active()) return;
-    f32x4 *slot = slot_base<L>(static_cast<float *>(p.out), p.g, tp, tq, split, loop.wave, loop.lane);
+    f32x4 *slot = wide_slot<L>(p, tail, split, loop.wave * (L::RB * L::CB * 64) + loop.lane);
 #pragma unroll
     for (int i = 0; i < L::RB; ++i)
 #pragma unroll
         for (int j = 0; j < L::CB; ++j) slot[(i * L::CB + j) * 64] = acc.v[i][j];
 }
 
-// The slices' slots added in slice order.
+// The tail's slots added in slice order, 256 float4 a block.
 template <int DT, class L>
-__global__ __launch_bounds__(256) void lora_join(WideParams p, const float *slots) {
+__device__ __forceinline__ void tail_block(const WideParams &p, int64_t id) {
     constexpr int QUADS = L::TP * L::TQ / 4;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (id >= (int64_t)p.g.tiles_p * p.g.tiles_q * QUADS) return;
-    const int tile = (int)(id / QUADS), f = (int)(id % QUADS);
-    const int tp = tile % p.g.tiles_p, tq = tile / p.g.tiles_p;
+    const int64_t rest = p.g.tiles_p * p.g.tiles_q - p.whole;
+    const int tail = (int)(id / QUADS), f = (int)(id % QUADS);
+    int tp, tq;
+    tile_of(p.g, p.whole + tail, tp, tq);
     const int lane = f & 63, block = (f >> 6) % (L::RB * L::CB), wave = (f >> 6) / (L::RB * L::CB);
     const int i = block / L::CB, j = block % L::CB, wp = wave % L::WP, wq = wave / L::WP;
     const int64_t col = (int64_t)tp * L::TP + wp * L::WAVE_P + i * 16 + 4 * (lane >> 4);
     const int64_t row = (int64_t)tq * L::TQ + wq * L::WAVE_Q + j * 16 + (lane & 15);
     if (row >= p.x.rows || col >= p.P.rows) return;
-    const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * QUADS;
-    const f32x4 *at = reinterpret_cast<const f32x4 *>(slots) + id;
-    f32x4 v = at[0];
-    int s = 1;
-    for (; s + 4 <= p.g.splits; s += 4) {   // four loads in flight, added in order
-        const f32x4 a = at[s * step], b = at[(s + 1) * step], c = at[(s + 2) * step], d = at[(s + 3) * step];
-        v = (((v + a) + b) + c) + d;
-    }
-    for (; s < p.g.splits; ++s) v += at[s * step];
+    const f32x4 v = sum_slices(reinterpret_cast<const float *>(wide_slot<L>(p, tail, 0, f)), rest * (L::TP * L::TQ), p.g.splits);
     *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.out) + row * p.ldo + col) =
         u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+template <int DT, class L>
+__global__ __launch_bounds__(256) void lora_join(WideParams p) {
+    tail_block<DT, L>(p, (int64_t)blockIdx.x * 256 + threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -427,7 +468,7 @@ __global__ __launch_bounds__(256, L::WAVES < LN::WAVES ? L::WAVES : LN::WAVES) v
         return;
     }
     int tp, tq, split;
-    place(w.g, wide, (int)blockIdx.x, tp, tq, split);
+    const int tile = place_wide(w.g, 0, (int)blockIdx.x, tp, tq, split);   // every tile in slices
     const int64_t p0 = (int64_t)tp * L::TP, q0 = (int64_t)tq * L::TQ;
     L loop(lds);
     typename L::Acc acc;
@@ -435,7 +476,7 @@ __global__ __launch_bounds__(256, L::WAVES < LN::WAVES ? L::WAVES : LN::WAVES) v
     const int s0 = (int)((int64_t)w.g.slabs * split / w.g.splits), s1 = (int)((int64_t)w.g.slabs * (split + 1) / w.g.splits);
     loop.run_any(w.P, p0, w.x, q0, w.K, s0, s1, acc);
     if (!loop.active()) return;
-    f32x4 *slot = slot_base<L>(static_cast<float *>(w.out), w.g, tp, tq, split, loop.wave, loop.lane);
+    f32x4 *slot = wide_slot<L>(w, tile, split, loop.wave * (L::RB * L::CB * 64) + loop.lane);
 #pragma unroll
     for (int j = 0; j < L::CB; ++j) {
         if (q0 + 16 * j >= w.x.rows) break;   // blocks of rows that are not there
@@ -463,17 +504,19 @@ __global__ __launch_bounds__(256) void lora_few_vec(WideParams w, LowParams n, i
     dot_rows<DT>(rows, Rows16<DT>{w.x.base, w.x.ld}, w.x.rows, w.K, red);
     const int i = threadIdx.x & 7, t = threadIdx.x >> 3, o = o0 + i;
     if (t >= T || t >= w.x.rows) return;
-    float *slot = static_cast<float *>(w.out) + (int64_t)(o >> 6) * (L::TP * L::TQ);
+    // one tile of rows, so tile ids along P: tile_of's bands hold whole columns
+    float *slot = w.slots + (int64_t)(o >> 6) * (L::TP * L::TQ);
     slot[((o >> 4) & 3) * L::CB * 256 + (t + 16 * ((o >> 2) & 3)) * 4 + (o & 3)] = joined(red, i, t);
 }
 
 // A workgroup: 16 rows (block j of a tile) by the tile's 64 columns.
 template <int DT, class L, bool KC>
-__global__ __launch_bounds__(256) void lora_few_join(WideParams p, const float *slots) {
+__global__ __launch_bounds__(256) void lora_few_join(WideParams p) {
     static_assert(L::TP == 64 && L::RB == 1 && L::WP == 4, "a wave for each 16 columns");
     __shared__ __attribute__((aligned(16))) float narrow[16 * (LORA_FEW_R + 4)];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = (int)blockIdx.x % L::CB, tile = (int)blockIdx.x / L::CB;
-    const int tp = tile % p.g.tiles_p, tq = tile / p.g.tiles_p;
+    int tp, tq;
+    tile_of(p.g, tile, tp, tq);
     const int64_t first = (int64_t)tq * L::TQ + 16 * j, row = first + (lane & 15);
     const int64_t col = (int64_t)tp * 64 + 16 * wave + 4 * (lane >> 4);
     if (first >= p.x.rows) return;
@@ -485,7 +528,7 @@ __global__ __launch_bounds__(256) void lora_few_join(WideParams p, const float *
     f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (in) {
         const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * (L::TP * L::TQ);
-        v = sum_slices(slots + (int64_t)tile * (L::TP * L::TQ) + (wave * L::CB + j) * 256 + lane * 4, step, p.g.splits);
+        v = sum_slices(p.slots + (int64_t)tile * (L::TP * L::TQ) + (wave * L::CB + j) * 256 + lane * 4, step, p.g.splits);
     }
     const float scale = a >= 0 && p.rows.scale ? p.rows.scale[a] : 1.0f;
     for (int f = threadIdx.x; f < 16 * quads; f += 256) {
@@ -691,6 +734,15 @@ __global__ __launch_bounds__(256, 2) void lora_outers(OuterParams wide, OuterPar
     if (id < wide.blocks) outer_block<DT, 128, 64>(wide, id, lds);
     else outer_block<DT, 64, 128>(narrow, id - wide.blocks, lds);
 }
+// The same, with the blocks that join dx's tail behind them.
+template <int DT, class L>
+__global__ __launch_bounds__(256, 2) void lora_join_outers(WideParams p, OuterParams wide, OuterParams narrow) {
+    __shared__ __attribute__((aligned(16))) char lds[outer_lds<128, 64>()];
+    const int64_t id = (int64_t)blockIdx.x - wide.blocks - narrow.blocks;
+    if (id >= 0) tail_block<DT, L>(p, id * 256 + threadIdx.x);
+    else if ((int)blockIdx.x < wide.blocks) outer_block<DT, 128, 64>(wide, blockIdx.x, lds);
+    else outer_block<DT, 64, 128>(narrow, (int64_t)blockIdx.x - wide.blocks, lds);
+}
 
 template <int DT>
 __global__ __launch_bounds__(256) void lora_outer_join(OuterParams p) {
@@ -715,7 +767,7 @@ __global__ __launch_bounds__(256) void lora_outer_join(OuterParams p) {
 template <class L>
 LowParams low_params(const LoraLow &a) {
     LowParams q{a.rows, matrix(a.f.first), matrix(a.x), a.f.stride, a.R, a.K, (a.K + KB - 1) / KB, (a.R + L::TP - 1) / L::TP,
-                (int)(((int64_t)a.rows.T + L::TQ - 1) / L::TQ), a.lists, a.splits, 0, a.partial, a.low};
+                (int)(((int64_t)a.rows.T + L::TQ - 1) / L::TQ), a.lists, a.splits, 0, a.partial};
     q.blocks = q.groups * q.tiles_r * q.lists * q.splits;
     return q;
 }
@@ -753,10 +805,6 @@ hipError_t run_lows(const LoraLow &k, const LoraLow &r, uint64_t *masks, hipStre
                 if (!r.partial) b.blocks = 0;
                 const unsigned slabs = masks ? (unsigned)((k.rows.T + 255) / 256) : 0;
                 hipLaunchKernelGGL((lora_lows<LK, LR>), dim3((unsigned)(a.blocks + b.blocks) + slabs), dim3(256), 0, stream, a, b, masks);
-                hipError_t e = hipGetLastError();
-                if (e != hipSuccess || !masks) return e;
-                const int64_t quads = 2 * (int64_t)k.rows.T * (k.R / 4);
-                hipLaunchKernelGGL(lora_low_join<DT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, a, b);
                 return hipGetLastError();
             } else {
                 return hipErrorInvalidValue;
@@ -765,11 +813,18 @@ hipError_t run_lows(const LoraLow &k, const LoraLow &r, uint64_t *masks, hipStre
     });
 }
 
-template <class L>
-WideParams wide_params(const LoraProduct &a) {
-    return WideParams{a.rows, matrix(a.P), matrix(a.x), matrix(a.f.first), a.f.stride, a.partial, a.low_splits, a.K, a.R,
-                      grid_of<L>(a.P.rows, a.x.rows, a.K, a.splits), a.splits > 1, a.out, a.ldo};
+LowJoin low_join(const LoraLowJoin &a) {
+    LowJoin q{a.rows, a.R, {{a.s, a.s_splits, a.s_low}, {a.ds, a.ds_splits, a.ds_low}}, 0};
+    if (a.s_low || a.ds_low) q.blocks = (int)((2 * (int64_t)a.rows.T * (a.R / 4) + 255) / 256);
+    return q;
 }
+template <class L>
+WideParams wide_params(const LoraProduct &a, const LoraLowJoin &join = LoraLowJoin()) {
+    return WideParams{a.rows, matrix(a.P), matrix(a.x), matrix(a.f.first), a.f.stride, a.partial, a.low_splits, a.K, a.R,
+                      grid_of<L>(a.P.rows, a.x.rows, a.K, a.splits), a.whole, a.slots, a.out, a.ldo, low_join(join)};
+}
+template <class L>
+int64_t tail_blocks(const WideParams &p) { return (int64_t)(p.g.tiles_p * p.g.tiles_q - p.whole) * (L::TP * L::TQ / 4 / 256); }
 
 // f(loop type, stages of the adapters' slabs)
 template <class L_, int DT_, int NS_>
@@ -790,23 +845,20 @@ hipError_t with_wide(int tile, F &&f) {
 }
 // The few rows' two launches.
 template <int DT, bool KC, class L>
-hipError_t join_few(WideParams w, const float *slots, void *out, hipStream_t stream) {
+hipError_t join_few(const WideParams &w, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    w.out = out;
-    hipLaunchKernelGGL((lora_few_join<DT, L, KC>), dim3((unsigned)(w.g.tiles_p * w.g.tiles_q * L::CB)), dim3(256), 0, stream, w, slots);
+    hipLaunchKernelGGL((lora_few_join<DT, L, KC>), dim3((unsigned)(w.g.tiles_p * w.g.tiles_q * L::CB)), dim3(256), 0, stream, w);
     return hipGetLastError();
 }
 template <int DT, bool KC, class L>
-hipError_t run_few(const LoraProduct &a, const LoraLow &low, float *slots, hipStream_t stream) {
+hipError_t run_few(const LoraProduct &a, const LoraLow &low, hipStream_t stream) {
     // the wide product's factor is stored as P is, the narrow one's the other way (an
     // input's side against an output's)
     return with_narrow<DT, KC>(low.R, [&](auto n) {
         using LN = typename decltype(n)::L;
         WideParams w = wide_params<L>(a);
         LowParams q = low_params<LN>(low);
-        void *out = w.out;
-        w.out = slots;
         if constexpr (KC && L::TQ == 32) {
             if (a.x.rows <= VEC_T) {
                 w.g.splits = 1;
@@ -815,20 +867,20 @@ hipError_t run_few(const LoraProduct &a, const LoraLow &low, float *slots, hipSt
                 if (a.x.rows == 1) hipLaunchKernelGGL((lora_few_vec<DT, 1, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
                 else if (a.x.rows == 2) hipLaunchKernelGGL((lora_few_vec<DT, 2, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
                 else hipLaunchKernelGGL((lora_few_vec<DT, 4, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
-                return join_few<DT, KC, L>(w, slots, out, stream);
+                return join_few<DT, KC, L>(w, stream);
             }
         }
-        const int wide = (int)blocks_of(w.g);
+        const int wide = wide_blocks(w.g, 0);
         hipLaunchKernelGGL((lora_few<L, LN>), dim3((unsigned)(wide + q.blocks)), dim3(256), 0, stream, w, q, wide);
-        return join_few<DT, KC, L>(w, slots, out, stream);
+        return join_few<DT, KC, L>(w, stream);
     });
 }
 template <int DT, bool KC>
-hipError_t few(int tile, const LoraProduct &a, const LoraLow &low, float *slots, hipStream_t stream) {
+hipError_t few(int tile, const LoraProduct &a, const LoraLow &low, hipStream_t stream) {
     switch (tile) {
-    case LP_64x32: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 32, 6>>(a, low, slots, stream);
-    case LP_64x64: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 64, 5>>(a, low, slots, stream);
-    case LP_64x128: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 128, 3>>(a, low, slots, stream);
+    case LP_64x32: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 32, 6>>(a, low, stream);
+    case LP_64x64: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 64, 5>>(a, low, stream);
+    case LP_64x128: return run_few<DT, KC, ThinLoop<DT, KC, true, 64, 128, 3>>(a, low, stream);
     default: return hipErrorInvalidValue;
     }
 }
@@ -846,9 +898,7 @@ OuterParams outer_params(const LoraOuter &a) {
     return q;
 }
 template <int DT>
-hipError_t run_outers(const LoraOuter &wide, const LoraOuter &narrow, hipStream_t stream) {
-    const OuterParams w = outer_params(wide), n = outer_params(narrow);
-    hipLaunchKernelGGL(lora_outers<DT>, dim3((unsigned)(w.blocks + n.blocks)), dim3(256), 0, stream, w, n);
+hipError_t join_outers(const OuterParams &w, const OuterParams &n, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     for (const OuterParams *q : {&w, &n}) {
         if (e != hipSuccess || !q->out || q->splits == 1) continue;
@@ -880,40 +930,55 @@ LossTileShape lora_tile_shape(int tile) {
     if (tile == LP_64x32) return {64, 32, 2};
     return loss_tile_shape(tile);
 }
-int64_t lora_slots_bytes(int tile, int64_t rows_p, int64_t rows_q, int splits) {
-    const LossTileShape s = lora_tile_shape(tile);
-    return (rows_p + s.p - 1) / s.p * ((rows_q + s.q - 1) / s.q) * splits * (int64_t)s.p * s.q * 4;
-}
-
-hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, hipStream_t stream) {
-    if (!p.x.kc || p.P.kc != p.f.first.kc) return hipErrorInvalidValue;
+hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, const LoraLowJoin &join, hipStream_t stream) {
+    if (!p.x.kc || p.P.kc != p.f.first.kc || (p.splits == 1) != (p.slots == nullptr)) return hipErrorInvalidValue;
     return with_wide(dtype, tile, p.P.kc, [&](auto w) {
         using W = decltype(w);
-        const WideParams q = wide_params<typename W::L>(p);
-        hipLaunchKernelGGL((lora_product<W::DT, typename W::L, W::NS>), dim3(blocks_of(q.g)), dim3(W::L::NT), 0, stream, q);
+        using L = typename W::L;
+        const WideParams q = wide_params<L>(p, join);
+        const int joins = (q.join.blocks * 256 + L::NT - 1) / L::NT;
+        hipLaunchKernelGGL((lora_product<W::DT, L, W::NS>), dim3((unsigned)(wide_blocks(q.g, q.whole) + joins)), dim3(L::NT), 0, stream, q);
         return hipGetLastError();
     });
 }
-hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const LoraLow &low, float *slots, hipStream_t stream) {
+hipError_t launch_lora_low_join(int dtype, const LoraLowJoin &p, hipStream_t stream) {
+    const LowJoin q = low_join(p);
+    if (!q.blocks) return hipSuccess;
+    if (dtype == 0) hipLaunchKernelGGL(lora_low_join<0>, dim3((unsigned)q.blocks), dim3(256), 0, stream, q);
+    else hipLaunchKernelGGL(lora_low_join<1>, dim3((unsigned)q.blocks), dim3(256), 0, stream, q);
+    return hipGetLastError();
+}
+hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const LoraLow &low, hipStream_t stream) {
     if (!p.x.kc || !low.x.kc || p.P.kc != p.f.first.kc || p.P.kc != low.f.first.kc || p.R > LORA_FEW_R || p.x.rows > LORA_FEW_T)
         return hipErrorInvalidValue;
-    if (p.P.kc) return dtype == 0 ? few<0, true>(tile, p, low, slots, stream) : few<1, true>(tile, p, low, slots, stream);
-    return dtype == 0 ? few<0, false>(tile, p, low, slots, stream) : few<1, false>(tile, p, low, slots, stream);
+    if (p.P.kc) return dtype == 0 ? few<0, true>(tile, p, low, stream) : few<1, true>(tile, p, low, stream);
+    return dtype == 0 ? few<0, false>(tile, p, low, stream) : few<1, false>(tile, p, low, stream);
 }
-hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, const float *slots, hipStream_t stream) {
+hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, hipStream_t stream) {
     return with_wide(dtype, tile, true, [&](auto w) {   // the operands' storage does not matter here
         using W = decltype(w);
         const WideParams q = wide_params<typename W::L>(p);
-        const int64_t quads = (int64_t)q.g.tiles_p * q.g.tiles_q * (W::L::TP * W::L::TQ / 4);
-        hipLaunchKernelGGL((lora_join<W::DT, typename W::L>), dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, q, slots);
+        hipLaunchKernelGGL((lora_join<W::DT, typename W::L>), dim3((unsigned)tail_blocks<typename W::L>(q)), dim3(256), 0, stream, q);
         return hipGetLastError();
     });
 }
 
-hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, hipStream_t stream) {
+hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, int tile, const LoraProduct *tail, hipStream_t stream) {
     const LoraOuter &w = da.narrow_p ? db : da, &n = da.narrow_p ? da : db;
     if (w.P.kc || w.Q.kc || n.P.kc || n.Q.kc || w.narrow_p || !n.narrow_p) return hipErrorInvalidValue;
-    return dtype == 0 ? run_outers<0>(w, n, stream) : run_outers<1>(w, n, stream);
+    const OuterParams qw = outer_params(w), qn = outer_params(n);
+    if (!tail) {
+        if (dtype == 0) hipLaunchKernelGGL(lora_outers<0>, dim3((unsigned)(qw.blocks + qn.blocks)), dim3(256), 0, stream, qw, qn);
+        else hipLaunchKernelGGL(lora_outers<1>, dim3((unsigned)(qw.blocks + qn.blocks)), dim3(256), 0, stream, qw, qn);
+        return dtype == 0 ? join_outers<0>(qw, qn, stream) : join_outers<1>(qw, qn, stream);
+    }
+    return with_wide(dtype, tile, true, [&](auto x) {
+        using W = decltype(x);
+        const WideParams q = wide_params<typename W::L>(*tail);
+        const int64_t blocks = tail_blocks<typename W::L>(q) + qw.blocks + qn.blocks;
+        hipLaunchKernelGGL((lora_join_outers<W::DT, typename W::L>), dim3((unsigned)blocks), dim3(256), 0, stream, q, qw, qn);
+        return join_outers<W::DT>(qw, qn, stream);
+    });
 }
 
 }  // namespace dgw

@@ -256,16 +256,14 @@ struct Grid {
     int slabs;               // slabs of k
 };
 
-// The workgroup's tile and slice.  Workgroup b runs on XCD b % 8; each XCD gets a
-// contiguous range of ids, and ids walk bands of `band` P tiles row by row of Q,
-// so the tiles that run at once on an XCD are a compact block that shares its
-// operands in the XCD's L2.
-__device__ __forceinline__ void place(const Grid &g, int n, int b, int &tp, int &tq, int &split) {
+// Workgroup b of n runs on XCD b % 8; each XCD gets a contiguous range of ids.
+__device__ __forceinline__ int spread(int n, int b) {
     const int x = b & 7;
-    int id = x * (n >> 3) + min(x, n & 7) + (b >> 3);
-    const int tiles = g.tiles_p * g.tiles_q;
-    split = id / tiles;
-    id -= split * tiles;
+    return x * (n >> 3) + min(x, n & 7) + (b >> 3);
+}
+// Ids of tiles walk bands of `band` P tiles row by row of Q, so the tiles that run at
+// once on an XCD are a compact block that shares its operands in the XCD's L2.
+__device__ __forceinline__ void tile_of(const Grid &g, int id, int &tp, int &tq) {
     const int per = g.band * g.tiles_q;
     const int bnd = id / per;
     const int rows = min(g.band, g.tiles_p - bnd * g.band);
@@ -273,7 +271,12 @@ __device__ __forceinline__ void place(const Grid &g, int n, int b, int &tp, int 
     tq = w / rows;
     tp = bnd * g.band + (w - tq * rows);
 }
-
+// The workgroup's tile and slice.
+__device__ __forceinline__ void place(const Grid &g, int n, int b, int &tp, int &tq, int &split) {
+    const int id = spread(n, b), tiles = g.tiles_p * g.tiles_q;
+    split = id / tiles;
+    tile_of(g, id - split * tiles, tp, tq);
+}
 __device__ __forceinline__ void place(const Grid &g, int &tp, int &tq, int &split) {
     place(g, (int)gridDim.x, (int)blockIdx.x, tp, tq, split);
 }

@@ -56,8 +56,7 @@ class GemmLoraPlan(ctypes.Structure):
         ("num_cus", ctypes.c_int32),
         ("low_tile_r", ctypes.c_int32), ("low_splits", ctypes.c_int32), ("low_lists", ctypes.c_int32),
         ("out_tile_p", ctypes.c_int32), ("out_tile_t", ctypes.c_int32), ("out_splits", ctypes.c_int32),
-        ("da_splits", ctypes.c_int32), ("db_splits", ctypes.c_int32),
-        ("workspace_bytes", ctypes.c_int64),
+        ("dab_splits", ctypes.c_int32), ("out_whole", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64),
     ]
 
 

@@ -67,24 +67,33 @@ def test_backward(dg, size):
     check_backward(dg, make(T, H, N, L, R, dtype, order, seed=T + N, dev="cuda"), layout, dtype)
 
 
-# one case for each tile of the wide product (the plan's fields on 256 CUs)
-SHAPES = [
-    ("64x32", 20, 1032, 4104, "bf16", (64, 32)),
-    ("64x64", 50, 1032, 4104, "fp16", (64, 64)),
-    ("64x128", 100, 1032, 4104, "bf16", (64, 128)),
-    ("128x128", 400, 520, 4104, "fp16", (128, 128)),
-    ("256x256", 4000, 2000, 2056, "bf16", (256, 256)),
-    ("256x256, the other way", 4000, 2056, 2000, "fp16", None),   # dx on these tiles
+# one case for each tile of the wide product and each way its tiles are computed (the plan's fields on 256 CUs):
+# all in slices, all whole, and whole but for the last ones
+SHAPES = [   # T, H, N, R, dtype, backward, tile, how
+    (20, 1032, 4104, 256, "bf16", False, (64, 32), "sliced"),
+    (50, 1032, 4104, 128, "fp16", False, (64, 64), "sliced"),
+    (100, 1032, 4104, 64, "bf16", False, (64, 128), "sliced"),
+    (100, 136, 30000, 64, "fp16", False, (64, 128), "whole"),
+    (1000, 2056, 1032, 16, "bf16", False, (128, 128), "sliced"),
+    (1000, 1032, 8200, 16, "fp16", False, (128, 128), "tail"),
+    (1000, 1032, 1032, 16, "bf16", True, (128, 128), "whole"),
+    (4000, 2056, 1032, 16, "fp16", True, (128, 128), "tail"),
+    (1000, 4096, 4104, 16, "bf16", False, (256, 256), "sliced"),
+    (2000, 2056, 4096, 16, "fp16", True, (256, 256), "sliced"),
+    (8192, 1032, 1032, 16, "bf16", False, (256, 256), "whole"),
+    (5000, 2056, 4096, 72, "bf16", False, (256, 256), "tail"),
+    (5000, 4096, 2056, 16, "fp16", True, (256, 256), "tail"),
 ]
 
 
 @pytest.mark.parametrize("layout", ["nk", "kn"])
-@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: s[0])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[6][0]}x{s[6][1]}-{s[7]}-{s[0]}x{s[1]}x{s[2]}-{'bwd' if s[5] else 'fwd'}")
 def test_every_tile(dg, shape, layout):
-    _, T, H, N, dtype, tile = shape
-    a = dg.GemmLoraArgs(T=T, H=H, N=N, R=16, adapters=6, layout=dg.layout_word(layout, dtype), dx=1)
-    plan = dg.gemm_lora_plan(a, tile is None, 256)
-    assert (plan.out_tile_p, plan.out_tile_t) == (tile or (256, 256))
-    d = make(T, H, N, 6, 16, dtype, "packed", seed=5, dev="cuda")
-    check_forward(dg, d, layout, dtype)
-    check_backward(dg, d, layout, dtype)
+    T, H, N, R, dtype, backward, tile, how = shape
+    a = dg.GemmLoraArgs(T=T, H=H, N=N, R=R, adapters=6, layout=dg.layout_word(layout, dtype), dx=1, da=1, db=1)
+    plan = dg.gemm_lora_plan(a, backward, 256)
+    tiles = -(-(H if backward else N) // plan.out_tile_p) * -(-T // plan.out_tile_t)
+    assert (plan.out_tile_p, plan.out_tile_t) == tile
+    assert how == ("whole" if plan.out_whole == tiles else "tail" if plan.out_whole else "sliced")
+    d = make(T, H, N, 6, R, dtype, "packed", seed=5, dev="cuda")
+    (check_backward if backward else check_forward)(dg, d, layout, dtype)
