@@ -31,7 +31,7 @@ GEMM_LORA_MAX_R = 1024
 GEMM_LORA_MAX_ADAPTERS = 1 << 16
 GEMM_LORA_MAX_TH = 1 << 37
 GEMM_LORA_MAX_LT = 1 << 34
-GEMM_LORA_MAX_LRH = 1 << 40
+GEMM_LORA_MAX_LRH = 1 << 38
 
 
 class GemmLoraArgs(ctypes.Structure):

@@ -58,7 +58,7 @@ extern "C" {
 #define GEMM_LORA_MAX_ADAPTERS (1 << 16)
 #define GEMM_LORA_MAX_TH       ((int64_t)1 << 37)   /* T * H, T * N and H * N      */
 #define GEMM_LORA_MAX_LT       ((int64_t)1 << 34)   /* L * T (backward)            */
-#define GEMM_LORA_MAX_LRH      ((int64_t)1 << 40)   /* L * R * H and L * R * N     */
+#define GEMM_LORA_MAX_LRH      ((int64_t)1 << 38)   /* L * R * H and L * R * N     */
 
 /*
  * Arguments; zero-initialise, then fill what the call needs.
