@@ -165,7 +165,7 @@ def gated_ffn(x, w_gate, w_up, w_down, *, activation: str = "silu", b_layout: st
         a.y, a.ldy = y.data_ptr(), _rows("y", y, a.T, a.H, x.dtype, x.device)
         if save:
             if gate is None:
-                gate = torch.empty((a.T, a.F), dtype=x.dtype, device=x.device)
+                gate = x.new_empty((a.T, a.F))
                 up = torch.empty_like(gate)
             _hidden(a, x, gate, up)
         _call(a, x, False, workspace)
@@ -194,16 +194,16 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, *, activation: str
         raise ValueError("accumulate_dw needs fp32 gradients to add to")
     with _on(x, stream):
         if need_dx:
-            dx = torch.empty((a.T, a.H), dtype=x.dtype, device=x.device) if dx is None else dx
+            dx = torch.empty_like(x) if dx is None else dx
             a.dx, a.lddx = dx.data_ptr(), _rows("dx", dx, a.T, a.H, x.dtype, x.device)
         if need_dw:
             if not given:
-                dw_gate, dw_up, dw_down = (torch.empty(tuple(w.shape), dtype=x.dtype, device=x.device)
-                                           for w in (w_gate, w_up, w_down))
+                dw_gate, dw_up, dw_down = torch.empty_like(w_gate), torch.empty_like(w_up), torch.empty_like(w_down)
             fp32 = dw_gate.dtype == torch.float32
-            for name, t, w in (("dw_gate", dw_gate, w_gate), ("dw_up", dw_up, w_up), ("dw_down", dw_down, w_down)):
-                setattr(a, name, t.data_ptr())
-                setattr(a, "ld" + name, _rows(name, t, *w.shape, torch.float32 if fp32 else x.dtype, x.device))
+            dtype = torch.float32 if fp32 else x.dtype
+            a.dw_gate, a.lddw_gate = dw_gate.data_ptr(), _rows("dw_gate", dw_gate, *w_gate.shape, dtype, x.device)
+            a.dw_up, a.lddw_up = dw_up.data_ptr(), _rows("dw_up", dw_up, *w_up.shape, dtype, x.device)
+            a.dw_down, a.lddw_down = dw_down.data_ptr(), _rows("dw_down", dw_down, *w_down.shape, dtype, x.device)
             if fp32:
                 a.dw_type = GEMM_FFN_DW_FP32_ADD if accumulate_dw else GEMM_FFN_DW_FP32
         _call(a, x, True, workspace)

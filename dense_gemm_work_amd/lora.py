@@ -91,7 +91,7 @@ def _matrices(name, t, count, rows, cols, dtype, device):
         raise TypeError(f"{name} must be {dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != (count, rows, cols):
+    if t.shape != (count, rows, cols):
         raise ValueError(f"{name} must be [{count}, {rows}, {cols}]")
     if t.is_contiguous():
         return 0
@@ -197,11 +197,11 @@ def linear_lora_backward(dy, x, w, a, b, adapter, *, scale=None, b_layout: str =
         raise ValueError("accumulate_dab needs fp32 gradients to add to")
     with _on(x, stream):
         if need_dx:
-            dx = torch.empty((p.T, p.H), dtype=x.dtype, device=x.device) if dx is None else dx
+            dx = torch.empty_like(x) if dx is None else dx
             p.dx, p.lddx = dx.data_ptr(), _rows("dx", dx, p.T, p.H, x.dtype, x.device)
         if need_dab:
             if da is None:
-                da, db = (torch.empty(tuple(t.shape), dtype=x.dtype, device=x.device) for t in (a, b))
+                da, db = a.new_empty(a.shape), b.new_empty(b.shape)   # packed, as a and b need not be
             dtype = torch.float32 if da.dtype == torch.float32 else x.dtype
             p.da, p.db = _vector("da", da, a.shape, dtype, x.device), _vector("db", db, b.shape, dtype, x.device)
             if dtype == torch.float32:

@@ -107,15 +107,16 @@ def _rows(name, t, rows, cols, dtype, device):
         raise TypeError(f"{name} must be {dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}]")
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
+    step, unit = t.stride()
+    if unit != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name}: every row must be contiguous")
     if rows <= 1:
         return 0
-    if t.stride(0) < cols:   # an expanded tensor; 0 would mean packed
+    if step < cols:   # an expanded tensor; 0 would mean packed
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return step
 
 
 def _vector(name, t, shape, dtypes, device):
@@ -123,7 +124,7 @@ def _vector(name, t, shape, dtypes, device):
         raise TypeError(f"{name} must be {dtypes}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)}")
     return t.data_ptr()
 
