@@ -51,15 +51,18 @@ struct FfnSum {
 };
 hipError_t launch_ffn_sum(int dtype, int tile, const FfnSum &p, hipStream_t stream);
 
-// out[q][p] = sum over T rows of P[t][p] Q[t][q], for up to three weights in one launch;
-// out_kind LO_16, LO_F32 or LO_F32_ADD.
+// out[q][p] = sum over T rows of P[t][p] Q[t][q], for up to three weights in one launch,
+// and one that joins where the rows are cut into `splits` slices (by way of `slots`,
+// loss_slots_bytes() for each weight, one behind the other); out_kind LO_16, LO_F32 or
+// LO_F32_ADD.
 struct FfnWeights {
     struct One {
         LossMatrix P, Q;   // rows contiguous
         void *out;         // nullptr: left out
         int64_t ldo;
     } one[3];
-    int T, out_kind;
+    int T, out_kind, splits;
+    float *slots;   // nullptr: splits is 1
 };
 hipError_t launch_ffn_weights(int dtype, int tile, const FfnWeights &p, hipStream_t stream);
 

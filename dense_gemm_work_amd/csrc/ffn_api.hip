@@ -119,24 +119,21 @@ Choice out_choice(const gemm_ffn_args_t &a, int64_t k, int cus) {
     return {tile, (int)std::max<int64_t>(1, std::min<int64_t>(cus / ceil_div(a.H, 128), ceil_div(k, 64) / 8))};
 }
 
-// One weight gradient, out[q][p] = sum_t P[t][p] Q[t][q].
-struct Grad {
-    bool wanted = false, outer = false;
-    Choice c{dgw::LT_128x128, 1};
-};
-Grad grad_plan(const gemm_ffn_args_t &a, const void *dw, Shape w, int cus) {
-    Grad g;
-    g.wanted = dw != nullptr;
-    g.outer = a.T <= dgw::LOSS_FEW;
-    if (!g.outer) g.c = choose(w.row, w.rows, std::max<int64_t>(a.T, 1), true, cus);
-    return g;
+// Tile and slices of the rows of the weights' gradients, which one launch computes: by
+// choose()'s model for their tiles together.
+Choice weights_choice(const gemm_ffn_args_t &a, int cus) {
+    const int64_t k = std::max<int64_t>(a.T, 1), each = (a.dw_gate ? 1 : 0) + (a.dw_up ? 1 : 0) + (a.dw_down ? 1 : 0);
+    if (!each) return {dgw::LT_128x128, 1};
+    // as one weight of `each` times the features: the tiles' number is all that counts
+    return choose(a.H, each * round_up(a.F, 256), k, true, cus);
 }
 
 struct Plan {
     bool vec = false;                       // forward, by the kernels of single rows
     int first = dgw::LT_128x128;
     Choice out{dgw::LT_128x128, 1};
-    Grad gate, up, down;
+    bool outer = false;      // the weights' gradients by the kernel of few rows
+    Choice weights{dgw::LT_128x128, 1};
     int parts = 1;
     int64_t part = 0;                       // elements from a first part to its second
     int64_t h = 0, dg = 0, du = 0, slots = 0;   // byte offsets
@@ -168,17 +165,25 @@ Plan make_plan(const gemm_ffn_args_t &a, bool backward, int cus) {
         p.first = slope_tile(a, cus);
         p.dg = p.take(hidden);
         p.du = p.take(hidden);
-        const Shape in = shape_in(a), down = shape_down(a);
-        p.gate = grad_plan(a, a.dw_gate, in, cus);
-        p.up = grad_plan(a, a.dw_up, in, cus);
-        p.down = grad_plan(a, a.dw_down, down, cus);
+        p.outer = a.T <= dgw::LOSS_FEW;
+        if (!p.outer) {
+            p.weights = weights_choice(a, cus);
+            if (p.weights.splits > 1) {
+                const Shape in = shape_in(a), down = shape_down(a);
+                auto add = [&](const void *dw, Shape w) {
+                    if (dw) slots += dgw::loss_slots_bytes(p.weights.tile, w.row, w.rows, p.weights.splits);
+                };
+                add(a.dw_gate, in);
+                add(a.dw_up, in);
+                add(a.dw_down, down);
+            }
+        }
         if (a.dx) {
             need(p.out, a.H, a.T);
             const int64_t packed = shape_in(a).row;
-            if (or_packed(a.ldw_gate, packed) != or_packed(a.ldw_up, packed)) slots = dgw::loss_slots_bytes(p.out.tile, a.H, a.T, p.out.splits);
+            if (or_packed(a.ldw_gate, packed) != or_packed(a.ldw_up, packed))
+                slots = std::max(slots, dgw::loss_slots_bytes(p.out.tile, a.H, a.T, p.out.splits));
         }
-        if (p.gate.wanted || p.up.wanted) need(p.gate.c, in.row, in.rows);
-        if (p.down.wanted) need(p.down.c, down.row, down.rows);
     }
     if (slots) p.slots = p.take(slots);   // one product after the other
     return p;
@@ -264,27 +269,22 @@ int forward(const gemm_ffn_args_t &a) {
 
 // The weights' gradients: `outs` holds a weight's output features, `ins` its input ones.
 struct Weight {
-    const Grad &g;
     void *dw;
     int64_t ldo;
     dgw::LossMatrix outs, ins;
 };
 int weight_gradients(const gemm_ffn_args_t &a, const Call &c, const Weight (&w)[3]) {
     const int kind = a.dw_type == GEMM_FFN_DW_SAME ? dgw::LO_16 : a.dw_type == GEMM_FFN_DW_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
-    // one launch for those of whole products on one tile, else one each
-    int tile = -1;
-    bool together = a.T > dgw::LOSS_FEW;
-    for (const Weight &x : w)
-        if (x.dw) {
-            together = together && x.g.c.splits == 1 && (tile < 0 || tile == x.g.c.tile);
-            tile = x.g.c.tile;
-        }
-    if (together && tile >= 0) {
+    hipError_t e = hipSuccess;
+    if (!c.plan.outer) {
+        const Choice &how = c.plan.weights;
         dgw::FfnWeights p;
         p.T = (int)a.T;
         p.out_kind = kind;
+        p.splits = how.splits;
+        p.slots = how.splits > 1 ? part<float>(c.ws, c.plan.slots) : nullptr;
         for (int i = 0; i < 3; ++i) p.one[i] = {c.nk ? w[i].ins : w[i].outs, c.nk ? w[i].outs : w[i].ins, w[i].dw, w[i].ldo};
-        const hipError_t e = dgw::launch_ffn_weights(c.dtype, tile, p, c.stream);
+        e = dgw::launch_ffn_weights(c.dtype, how.tile, p, c.stream);
         return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the weights' gradients");
     }
     for (const Weight &x : w) {
@@ -293,18 +293,12 @@ int weight_gradients(const gemm_ffn_args_t &a, const Call &c, const Weight (&w)[
         p.P = c.nk ? x.ins : x.outs;
         p.Q = c.nk ? x.outs : x.ins;
         p.K = (int)a.T;
+        p.splits = 1;
+        p.unscale = nullptr;
         p.out = x.dw;
         p.ldo = x.ldo;
         p.out_kind = kind;
-        if (!x.g.outer) {
-            const int rc = product(c, x.g.c, p, "launch a weight's gradient");
-            if (rc != GEMM_OK) return rc;
-            continue;
-        }
-        p.splits = 1;
-        p.unscale = nullptr;
-        const hipError_t e = dgw::launch_loss_outer(c.dtype, p, 2 * c.cus, c.stream);
-        if (e != hipSuccess) return set_hip_error(e, "launch a weight's gradient");
+        if ((e = dgw::launch_loss_outer(c.dtype, p, 2 * c.cus, c.stream)) != hipSuccess) return set_hip_error(e, "launch a weight's gradient");
     }
     return GEMM_OK;
 }
@@ -374,9 +368,9 @@ int backward(const gemm_ffn_args_t &a) {
     const dgw::LossMatrix mx = matrix(a.x, a.ldx, a.H, a.H, false), mdy = matrix(a.dy, a.lddy, a.H, a.H, false);
     const dgw::LossMatrix mg = matrix(dg, 0, a.F, a.F, false, pl.part), mu = matrix(du, 0, a.F, a.F, false, pl.part),
                           mh = matrix(h, 0, a.F, a.F, false, pl.part);
-    const Weight w[3] = {{pl.gate, a.dw_gate, or_packed(a.lddw_gate, in.row), mg, mx},
-                         {pl.up, a.dw_up, or_packed(a.lddw_up, in.row), mu, mx},
-                         {pl.down, a.dw_down, or_packed(a.lddw_down, down.row), mdy, mh}};
+    const Weight w[3] = {{a.dw_gate, or_packed(a.lddw_gate, in.row), mg, mx},
+                         {a.dw_up, or_packed(a.lddw_up, in.row), mu, mx},
+                         {a.dw_down, or_packed(a.lddw_down, down.row), mdy, mh}};
     return weight_gradients(a, c, w);
 }
 
@@ -404,10 +398,10 @@ int plan(const gemm_ffn_args_t *args, int32_t backward, int32_t num_cus, gemm_ff
     out->out_tile_t = o.q;
     out->out_splits = p.out.splits;
     if (backward) {
-        const dgw::LossTileShape w = dgw::loss_tile_shape(p.gate.c.tile);
+        const dgw::LossTileShape w = dgw::loss_tile_shape(p.weights.tile);
         out->dw_tile_p = w.p;
         out->dw_tile_q = w.q;
-        out->dw_splits = p.gate.c.splits;
+        out->dw_splits = p.weights.splits;
     }
     return GEMM_OK;
 }

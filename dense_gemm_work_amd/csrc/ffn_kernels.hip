@@ -395,7 +395,8 @@ struct WeightParams {
         Grid g;
         void *out;
         int64_t ldo;
-        int end;   // the launch's workgroups up to and with this gradient's
+        float *slots;   // g.splits > 1
+        int end;        // the launch's workgroups up to and with this gradient's
     } one[3];
     int count, T, out_kind;
 };
@@ -411,7 +412,16 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void ffn_weights(WeightParams p) {
     L loop(lds);
     typename L::Acc acc;
     L::zero(acc);
-    loop.run_any(q.P, p0, q.Q, q0, p.T, 0, q.g.slabs, acc);
+    const int s0 = (int)((int64_t)q.g.slabs * split / q.g.splits), s1 = (int)((int64_t)q.g.slabs * (split + 1) / q.g.splits);
+    loop.run_any(q.P, p0, q.Q, q0, p.T, s0, s1, acc);
+    if (q.g.splits > 1) {
+        f32x4 *slot = slot_base<L>(q.slots, q.g, tp, tq, split, loop.wave, loop.lane);
+#pragma unroll
+        for (int i = 0; i < L::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < L::CB; ++j) slot[(i * L::CB + j) * 64] = acc.v[i][j];
+        return;
+    }
     if (p.out_kind == LO_16) {
         store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(q.out), q.ldo, p0, q0, q.P.rows, q.Q.rows);
         return;
@@ -429,6 +439,39 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void ffn_weights(WeightParams p) {
         }
         __builtin_amdgcn_sched_barrier(0);   // one block row's loads in flight: no more registers are free
     }
+}
+
+// The slices' slots added in slice order; `end` counts blocks of 256 float4 here.
+template <int DT, class L>
+__global__ __launch_bounds__(256) void ffn_weights_join(WeightParams p) {
+    constexpr int QUADS = L::TP * L::TQ / 4;
+    int which = 0, start = 0;
+    while (which + 1 < p.count && (int)blockIdx.x >= p.one[which].end) start = p.one[which++].end;
+    const WeightParams::One &q = p.one[which];
+    const int64_t id = ((int64_t)blockIdx.x - start) * 256 + threadIdx.x;
+    const int tile = (int)(id / QUADS), f = (int)(id % QUADS);
+    const int tp = tile % q.g.tiles_p, tq = tile / q.g.tiles_p;
+    const int lane = f & 63, block = (f >> 6) % (L::RB * L::CB), wave = (f >> 6) / (L::RB * L::CB);
+    const int i = block / L::CB, j = block % L::CB, wp = wave % L::WP, wq = wave / L::WP;
+    const int64_t col = (int64_t)tp * L::TP + wp * L::WAVE_P + i * 16 + 4 * (lane >> 4);
+    const int64_t row = (int64_t)tq * L::TQ + wq * L::WAVE_Q + j * 16 + (lane & 15);
+    if (row >= q.Q.rows || col >= q.P.rows) return;
+    const int64_t step = (int64_t)q.g.tiles_p * q.g.tiles_q * QUADS;
+    const f32x4 *at = reinterpret_cast<const f32x4 *>(q.slots) + id;
+    f32x4 v = at[0];
+    int s = 1;
+    for (; s + 4 <= q.g.splits; s += 4) {   // four loads in flight, added in order
+        const f32x4 a = at[s * step], b = at[(s + 1) * step], c = at[(s + 2) * step], d = at[(s + 3) * step];
+        v = (((v + a) + b) + c) + d;
+    }
+    for (; s < q.g.splits; ++s) v += at[s * step];
+    const int64_t to = row * q.ldo + col;
+    if (p.out_kind == LO_16) {
+        *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(q.out) + to) = pack4<DT>(v);
+        return;
+    }
+    f32x4 *out = reinterpret_cast<f32x4 *>(static_cast<float *>(q.out) + to);
+    *out = p.out_kind == LO_F32_ADD ? v + *out : v;
 }
 
 // ---------------------------------------------------------------------------
@@ -518,14 +561,21 @@ hipError_t run_weights(const FfnWeights &a, hipStream_t stream) {
     q.T = a.T;
     q.out_kind = a.out_kind;
     int end = 0;
+    float *slots = a.slots;
     for (const FfnWeights::One &w : a.one) {
         if (!w.out) continue;
-        const Grid g = grid_of<L>(w.P.rows, w.Q.rows, a.T, 1);
+        const Grid g = grid_of<L>(w.P.rows, w.Q.rows, a.T, a.splits);
         end += (int)blocks_of(g);
-        q.one[q.count++] = {matrix(w.P), matrix(w.Q), g, w.out, w.ldo, end};
+        q.one[q.count++] = {matrix(w.P), matrix(w.Q), g, w.out, w.ldo, slots, end};
+        if (slots) slots += (int64_t)blocks_of(g) * (L::TP * L::TQ);
     }
     if (!end) return hipSuccess;
     hipLaunchKernelGGL((ffn_weights<DT, L>), dim3((unsigned)end), dim3(L::NT), 0, stream, q);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    end = 0;
+    for (int i = 0; i < q.count; ++i) q.one[i].end = end += q.one[i].g.tiles_p * q.one[i].g.tiles_q * (L::TP * L::TQ / 4 / 256);
+    hipLaunchKernelGGL((ffn_weights_join<DT, L>), dim3((unsigned)end), dim3(256), 0, stream, q);
     return hipGetLastError();
 }
 template <int DT>
@@ -561,6 +611,7 @@ hipError_t launch_ffn_sum(int dtype, int tile, const FfnSum &p, hipStream_t stre
 }
 
 hipError_t launch_ffn_weights(int dtype, int tile, const FfnWeights &p, hipStream_t stream) {
+    if ((p.splits == 1) != (p.slots == nullptr)) return hipErrorInvalidValue;
     for (const FfnWeights::One &w : p.one)
         if (w.out && (w.P.kc || w.Q.kc)) return hipErrorInvalidValue;
     return dtype == 0 ? weights<0>(tile, p, stream) : weights<1>(tile, p, stream);

@@ -78,7 +78,7 @@ hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, hipStream
 // Few rows (at most LORA_FEW_T rows, ranks of at most LORA_FEW_R): out and the narrow
 // product that it needs in two launches, every tile through `slots` (whole is 0); f's part
 // is summed in fp32 from unrounded narrow rows.
-constexpr int LORA_FEW_T = 128, LORA_FEW_R = 256;
+constexpr int LORA_FEW_T = 256, LORA_FEW_R = 256;
 hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const LoraLow &low, hipStream_t stream);
 
 // out_a[q][p] = sum over the rows t of adapter a of P[t][p] Q[t][q], for every adapter.

@@ -131,13 +131,13 @@ int64_t tiles_of(int tile, int64_t rows_p, int64_t rows_q) {
     const dgw::LossTileShape s = dgw::lora_tile_shape(tile);
     return ceil_div(rows_p, s.p) * ceil_div(rows_q, s.q);
 }
-Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
+Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, bool few, int cus) {
     Wide best;
     const int64_t slabs = ceil_div(k, 64);
-    if (a.T <= 128) {
+    if (a.T <= 128 || few) {
         best.tile = a.T <= 32 ? dgw::LP_64x32 : a.T <= 64 ? dgw::LP_64x64 : dgw::LP_64x128;
         // one workgroup a CU (96 x 4096 x 4096: 14.8 us, with two 16.2, and a shorter join)
-        best.splits = (int)std::max<int64_t>(1, std::min(cus / ceil_div(rows_p, 64), slabs / 4));
+        best.splits = (int)std::max<int64_t>(1, std::min(cus / (ceil_div(rows_p, 64) * std::max<int64_t>(1, ceil_div(a.T, 128))), slabs / 4));
         best.whole = best.splits == 1 ? tiles_of(best.tile, rows_p, a.T) : 0;
         return best;
     }
@@ -169,10 +169,16 @@ Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, int cus) {
     return best;
 }
 
-// Few rows of small ranks take the adapters in the join, where each row reads its own
-// adapter: no more than R elements of it a result, and only as long as that is little
-// beside w.
-bool few_rows(const gemm_lora_args_t &a) { return a.T <= dgw::LORA_FEW_T && a.R <= dgw::LORA_FEW_R && a.T * a.R <= 4096; }
+// Few rows of small ranks may take the adapters in the join, where each row reads its own
+// adapter (R N elements) whatever the other rows read; in the product's tiles each
+// adapter costs about half a microsecond, and there are min(adapters, T) at most.  In the
+// join, 238 x 296 x 6400 with 63 adapters of rank 24: FEW_A us, in the tiles 69; 256 x 8192
+// x 8192 with two of rank 32: FEW_B us, in the tiles FEW_C.
+bool few_rows(const gemm_lora_args_t &a) {
+    if (a.T > dgw::LORA_FEW_T || a.R > dgw::LORA_FEW_R) return false;
+    const double join = (double)(a.T * a.R) * (double)a.N * 2.0 / 8e6;
+    return join < 6.0 + 0.5 * (double)std::min<int64_t>(a.adapters, a.T);
+}
 
 // Slices of the rows for da and db, which one launch computes.
 int outer_splits(const gemm_lora_args_t &a, int cus) {
@@ -210,8 +216,8 @@ Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     if (backward && (a.dx || a.da)) low(p.ds, a.N, !nk, p.part_ds, p.dlow);
     const int64_t wide = backward ? a.H : a.N;
     if (!backward || a.dx) {
-        p.out = out_plan(a, wide, backward ? a.N : a.H, cus);
         p.few = !backward && few_rows(a);
+        p.out = out_plan(a, wide, backward ? a.N : a.H, p.few, cus);
         if (p.few) p.out.whole = 0;
         const dgw::LossTileShape s = dgw::lora_tile_shape(p.out.tile);
         slots = (tiles_of(p.out.tile, wide, a.T) - p.out.whole) * p.out.splits * s.p * s.q * 4;

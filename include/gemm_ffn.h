@@ -113,7 +113,7 @@ typedef struct gemm_ffn_plan_t {
     int32_t first_tile_f, first_tile_t;  /* features x rows of the kernel that makes h (backward: dg, du and h) */
     int32_t out_tile_h, out_tile_t;      /* tile of y (backward: dx)                         */
     int32_t out_splits;                  /* slices of F summed apart                         */
-    int32_t dw_tile_p, dw_tile_q;        /* backward: tile of dw_gate and dw_up (columns x rows as stored) */
+    int32_t dw_tile_p, dw_tile_q;        /* backward: tile of the weights' gradients (columns x rows as stored) */
     int32_t dw_splits;                   /* backward: slices of the rows summed apart        */
     int64_t workspace_bytes;
 } gemm_ffn_plan_t;
