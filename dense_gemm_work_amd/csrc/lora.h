@@ -62,7 +62,7 @@ struct LoraProduct {
     LoraRows rows;
     LossMatrix P, x;
     LoraFactor f;       // P.rows rows, stored as P is
-    const float *partial;
+    const float *partial;   // nullptr: without the adapters' part, which the join of few rows adds (whole is 0)
     int low_splits;
     int K, R, splits, whole;
     float *slots;       // nullptr: splits is 1
@@ -80,6 +80,8 @@ hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, hipStream
 // is summed in fp32 from unrounded narrow rows.
 constexpr int LORA_FEW_T = 256, LORA_FEW_R = 256;
 hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const LoraLow &low, hipStream_t stream);
+// The second of them, after launch_lora_product without partial.
+hipError_t launch_lora_few_join(int dtype, int tile, const LoraProduct &p, const LoraLow &low, hipStream_t stream);
 
 // out_a[q][p] = sum over the rows t of adapter a of P[t][p] Q[t][q], for every adapter.
 // One of P and Q is the narrow side (R wide, `narrow_p` says which).
@@ -95,7 +97,8 @@ struct LoraOuter {
     int64_t ldo, stride;
 };
 // da and db in one launch, one of them with a narrow P, and the join of a product's tail
-// (of tiles `tile`) unless that is nullptr.
-hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, int tile, const LoraProduct *tail, hipStream_t stream);
+// (of tiles `tile`) unless that is nullptr; with `few`, that of few rows.
+hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, int tile, const LoraProduct *tail, const LoraLow *few,
+                              hipStream_t stream);
 
 }  // namespace dgw

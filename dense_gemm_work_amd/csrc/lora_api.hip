@@ -170,13 +170,13 @@ Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, bool few, in
 }
 
 // Few rows of small ranks may take the adapters in the join, where each row reads its own
-// adapter (R N elements) whatever the other rows read; in the product's tiles each
+// adapter (R elements a result) whatever the other rows read; in the product's tiles each
 // adapter costs about half a microsecond, and there are min(adapters, T) at most.  In the
-// join, 238 x 296 x 6400 with 63 adapters of rank 24: FEW_A us, in the tiles 69; 256 x 8192
-// x 8192 with two of rank 32: FEW_B us, in the tiles FEW_C.
-bool few_rows(const gemm_lora_args_t &a) {
+// join, 238 x 296 x 6400 with 63 adapters of rank 24: 42 us, in the tiles 69; 256 x 8192
+// x 8192 with two of rank 32: 72 us, in the tiles 59.
+bool few_rows(const gemm_lora_args_t &a, int64_t wide) {
     if (a.T > dgw::LORA_FEW_T || a.R > dgw::LORA_FEW_R) return false;
-    const double join = (double)(a.T * a.R) * (double)a.N * 2.0 / 8e6;
+    const double join = (double)(a.T * a.R) * (double)wide * 2.0 / 8e6;
     return join < 6.0 + 0.5 * (double)std::min<int64_t>(a.adapters, a.T);
 }
 
@@ -216,7 +216,7 @@ Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     if (backward && (a.dx || a.da)) low(p.ds, a.N, !nk, p.part_ds, p.dlow);
     const int64_t wide = backward ? a.H : a.N;
     if (!backward || a.dx) {
-        p.few = !backward && few_rows(a);
+        p.few = few_rows(a, wide);
         p.out = out_plan(a, wide, backward ? a.N : a.H, p.few, cus);
         if (p.few) p.out.whole = 0;
         const dgw::LossTileShape s = dgw::lora_tile_shape(p.out.tile);
@@ -370,8 +370,10 @@ int backward(const gemm_lora_args_t &a) {
     dgw::LoraProduct dx;
     if (a.dx) {
         dx = product(a, c, matrix(a.w, a.ldw, w_row(a), a.H, !c.nk), dy, factor_a(a, false), ds, a.N, a.dx, or_packed(a.lddx, a.H));
+        if (pl.few) dx.partial = nullptr;
         e = dgw::launch_lora_product(c.dtype, pl.out.tile, dx, join, c.stream);
-        if (e == hipSuccess && dx.splits > 1 && !own) e = dgw::launch_lora_join(c.dtype, pl.out.tile, dx, c.stream);
+        if (e == hipSuccess && !own && pl.few) e = dgw::launch_lora_few_join(c.dtype, pl.out.tile, dx, ds, c.stream);
+        else if (e == hipSuccess && !own && dx.splits > 1) e = dgw::launch_lora_join(c.dtype, pl.out.tile, dx, c.stream);
     } else {
         e = dgw::launch_lora_low_join(c.dtype, join, c.stream);
     }
@@ -380,7 +382,7 @@ int backward(const gemm_lora_args_t &a) {
     const dgw::LossMatrix ms = matrix(join.s_low, 0, a.R, a.R, false), mds = matrix(join.ds_low, 0, a.R, a.R, false);
     const dgw::LossMatrix mx = matrix(a.x, a.ldx, a.H, a.H, false), mdy = matrix(a.dy, a.lddy, a.N, a.N, false);
     e = dgw::launch_lora_outers(c.dtype, outer(a, c, mds, mx, false, 0, a.da), outer(a, c, mdy, ms, true, pl.db_at, a.db),
-                                pl.out.tile, a.dx && dx.splits > 1 ? &dx : nullptr, c.stream);
+                                pl.out.tile, a.dx && (dx.splits > 1 || pl.few) ? &dx : nullptr, pl.few ? &ds : nullptr, c.stream);
     return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch da and db");
 }
 

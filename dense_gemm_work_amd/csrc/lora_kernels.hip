@@ -407,17 +407,19 @@ __global__ __launch_bounds__(L::NT, 2) void lora_product(WideParams p) {
     // one form of the loop for every K: what lives across their loop, or accumulators
     // that meet two loops, spill hundreds of registers in its last iterations.
     if constexpr (X::HOLD) loop.run_any(p.P, p0, p.x, q0, p.K, s0, s1, acc);
-    list.fill(mine);
-    X::run(loop, lds, p, p0, q0, list, split, splits, acc);
+    if (p.partial) {   // else the join adds the adapters
+        list.fill(mine);
+        X::run(loop, lds, p, p0, q0, list, split, splits, acc);
+    }
     if constexpr (!X::HOLD) loop.template run<true>(p.P, p0, p.x, q0, p.K, s0, s1, acc);
 #pragma unroll
     for (int j = 0; j < L::CB; ++j)
-        if (adapter_of(p.rows, q0 + loop.q_of(j)) == BAD)
+        if (p.partial && adapter_of(p.rows, q0 + loop.q_of(j)) == BAD)
 #pragma unroll
             for (int i = 0; i < L::RB; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc.v[i][j][e] = __builtin_nanf("");
-    if (splits == 1) {
+    if (tail < 0) {
         store16<DT, true>(loop, acc, lds, static_cast<uint16_t *>(p.out), p.ldo, p0, q0, p.P.rows, p.x.rows);
         return;
     }
@@ -509,15 +511,15 @@ __global__ __launch_bounds__(256) void lora_few_vec(WideParams w, LowParams n, i
     slot[((o >> 4) & 3) * L::CB * 256 + (t + 16 * ((o >> 2) & 3)) * 4 + (o & 3)] = joined(red, i, t);
 }
 
-// A workgroup: 16 rows (block j of a tile) by the tile's 64 columns.
-template <int DT, class L, bool KC>
-__global__ __launch_bounds__(256) void lora_few_join(WideParams p) {
-    static_assert(L::TP == 64 && L::RB == 1 && L::WP == 4, "a wave for each 16 columns");
-    __shared__ __attribute__((aligned(16))) float narrow[16 * (LORA_FEW_R + 4)];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = (int)blockIdx.x % L::CB, tile = (int)blockIdx.x / L::CB;
+// A workgroup: 16 rows (block j of a tile of 64 x 16 cb) by the tile's 64 columns, a wave
+// for each 16 of them.
+constexpr int FEW_LDS = 16 * (LORA_FEW_R + 4);   // floats
+template <int DT, bool KC>
+__device__ __forceinline__ void few_join_block(const WideParams &p, int cb, int id, float *narrow) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = id % cb, tile = id / cb, floats_of_tile = 64 * 16 * cb;
     int tp, tq;
     tile_of(p.g, tile, tp, tq);
-    const int64_t first = (int64_t)tq * L::TQ + 16 * j, row = first + (lane & 15);
+    const int64_t first = (int64_t)tq * 16 * cb + 16 * j, row = first + (lane & 15);
     const int64_t col = (int64_t)tp * 64 + 16 * wave + 4 * (lane >> 4);
     if (first >= p.x.rows) return;
     // the slices' sums first, whether or not their rows have adapters: no load waits for
@@ -527,8 +529,8 @@ __global__ __launch_bounds__(256) void lora_few_join(WideParams p) {
     const int a = in ? adapter_of(p.rows, row) : NONE;
     f32x4 v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (in) {
-        const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * (L::TP * L::TQ);
-        v = sum_slices(p.slots + (int64_t)tile * (L::TP * L::TQ) + (wave * L::CB + j) * 256 + lane * 4, step, p.g.splits);
+        const int64_t step = (int64_t)p.g.tiles_p * p.g.tiles_q * floats_of_tile;
+        v = sum_slices(p.slots + tile * (int64_t)floats_of_tile + (wave * cb + j) * 256 + lane * 4, step, p.g.splits);
     }
     const float scale = a >= 0 && p.rows.scale ? p.rows.scale[a] : 1.0f;
     for (int f = threadIdx.x; f < 16 * quads; f += 256) {
@@ -573,6 +575,12 @@ __global__ __launch_bounds__(256) void lora_few_join(WideParams p) {
     }
     *reinterpret_cast<u32x2 *>(static_cast<uint16_t *>(p.out) + row * p.ldo + col) =
         u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+
+template <int DT, bool KC>
+__global__ __launch_bounds__(256) void lora_few_join(WideParams p, int cb) {
+    __shared__ __attribute__((aligned(16))) float narrow[FEW_LDS];
+    few_join_block<DT, KC>(p, cb, (int)blockIdx.x, narrow);
 }
 
 // ---------------------------------------------------------------------------
@@ -761,6 +769,17 @@ __global__ __launch_bounds__(256) void lora_outer_join(OuterParams p) {
     *to = v;
 }
 
+// The same, with the blocks that join few rows' dx behind them.
+template <int DT, bool KC>
+__global__ __launch_bounds__(256, 2) void lora_few_join_outers(WideParams p, int cb, OuterParams wide, OuterParams narrow) {
+    __shared__ __attribute__((aligned(16))) char lds[outer_lds<128, 64>()];
+    static_assert(FEW_LDS * 4 <= outer_lds<128, 64>(), "the narrow rows fit");
+    const int id = (int)blockIdx.x - wide.blocks - narrow.blocks;
+    if (id >= 0) few_join_block<DT, KC>(p, cb, id, reinterpret_cast<float *>(lds));
+    else if ((int)blockIdx.x < wide.blocks) outer_block<DT, 128, 64>(wide, blockIdx.x, lds);
+    else outer_block<DT, 64, 128>(narrow, (int64_t)blockIdx.x - wide.blocks, lds);
+}
+
 // ---------------------------------------------------------------------------
 // Dispatch
 // ---------------------------------------------------------------------------
@@ -844,11 +863,12 @@ hipError_t with_wide(int tile, F &&f) {
     }
 }
 // The few rows' two launches.
-template <int DT, bool KC, class L>
-hipError_t join_few(const WideParams &w, hipStream_t stream) {
+unsigned few_blocks(const Grid &g, int cb) { return (unsigned)(g.tiles_p * g.tiles_q * cb); }
+template <int DT, bool KC>
+hipError_t join_few(const WideParams &w, int cb, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((lora_few_join<DT, L, KC>), dim3((unsigned)(w.g.tiles_p * w.g.tiles_q * L::CB)), dim3(256), 0, stream, w);
+    hipLaunchKernelGGL((lora_few_join<DT, KC>), dim3(few_blocks(w.g, cb)), dim3(256), 0, stream, w, cb);
     return hipGetLastError();
 }
 template <int DT, bool KC, class L>
@@ -867,12 +887,12 @@ hipError_t run_few(const LoraProduct &a, const LoraLow &low, hipStream_t stream)
                 if (a.x.rows == 1) hipLaunchKernelGGL((lora_few_vec<DT, 1, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
                 else if (a.x.rows == 2) hipLaunchKernelGGL((lora_few_vec<DT, 2, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
                 else hipLaunchKernelGGL((lora_few_vec<DT, 4, L, LN>), grid, dim3(256), 0, stream, w, q, wide);
-                return join_few<DT, KC, L>(w, stream);
+                return join_few<DT, KC>(w, L::CB, stream);
             }
         }
         const int wide = wide_blocks(w.g, 0);
         hipLaunchKernelGGL((lora_few<L, LN>), dim3((unsigned)(wide + q.blocks)), dim3(256), 0, stream, w, q, wide);
-        return join_few<DT, KC, L>(w, stream);
+        return join_few<DT, KC>(w, L::CB, stream);
     });
 }
 template <int DT, bool KC>
@@ -931,7 +951,7 @@ LossTileShape lora_tile_shape(int tile) {
     return loss_tile_shape(tile);
 }
 hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, const LoraLowJoin &join, hipStream_t stream) {
-    if (!p.x.kc || p.P.kc != p.f.first.kc || (p.splits == 1) != (p.slots == nullptr)) return hipErrorInvalidValue;
+    if (!p.x.kc || p.P.kc != p.f.first.kc || (p.splits > 1 && !p.slots) || (!p.partial && !p.slots)) return hipErrorInvalidValue;
     return with_wide(dtype, tile, p.P.kc, [&](auto w) {
         using W = decltype(w);
         using L = typename W::L;
@@ -940,6 +960,15 @@ hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, const 
         hipLaunchKernelGGL((lora_product<W::DT, L, W::NS>), dim3((unsigned)(wide_blocks(q.g, q.whole) + joins)), dim3(L::NT), 0, stream, q);
         return hipGetLastError();
     });
+}
+hipError_t launch_lora_few_join(int dtype, int tile, const LoraProduct &p, const LoraLow &low, hipStream_t stream) {
+    WideParams q = wide_params<ThinLoop<0, true, true, 64, 32, 6>>(p);   // every tile of few rows has 64 columns
+    const int cb = lora_tile_shape(tile).q / 16;
+    q.g.tiles_q = (int)((p.x.rows + 16 * cb - 1) / (16 * cb));
+    q.partial = low.partial;
+    q.low_splits = low.splits;
+    if (p.P.kc) return dtype == 0 ? join_few<0, true>(q, cb, stream) : join_few<1, true>(q, cb, stream);
+    return dtype == 0 ? join_few<0, false>(q, cb, stream) : join_few<1, false>(q, cb, stream);
 }
 hipError_t launch_lora_low_join(int dtype, const LoraLowJoin &p, hipStream_t stream) {
     const LowJoin q = low_join(p);
@@ -963,10 +992,23 @@ hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, hipStream
     });
 }
 
-hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, int tile, const LoraProduct *tail, hipStream_t stream) {
+hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &db, int tile, const LoraProduct *tail, const LoraLow *few,
+                              hipStream_t stream) {
     const LoraOuter &w = da.narrow_p ? db : da, &n = da.narrow_p ? da : db;
     if (w.P.kc || w.Q.kc || n.P.kc || n.Q.kc || w.narrow_p || !n.narrow_p) return hipErrorInvalidValue;
     const OuterParams qw = outer_params(w), qn = outer_params(n);
+    if (tail && few) {
+        WideParams q = wide_params<ThinLoop<0, true, true, 64, 32, 6>>(*tail);   // every tile of few rows has 64 columns
+        const int cb = lora_tile_shape(tile).q / 16;
+        q.g.tiles_q = (int)((tail->x.rows + 16 * cb - 1) / (16 * cb));
+        q.partial = few->partial;
+        q.low_splits = few->splits;
+        const dim3 grid(few_blocks(q.g, cb) + (unsigned)(qw.blocks + qn.blocks));
+        auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, q, cb, qw, qn); };
+        if (tail->P.kc) dtype == 0 ? run(lora_few_join_outers<0, true>) : run(lora_few_join_outers<1, true>);
+        else dtype == 0 ? run(lora_few_join_outers<0, false>) : run(lora_few_join_outers<1, false>);
+        return hipGetLastError();
+    }
     if (!tail) {
         if (dtype == 0) hipLaunchKernelGGL(lora_outers<0>, dim3((unsigned)(qw.blocks + qn.blocks)), dim3(256), 0, stream, qw, qn);
         else hipLaunchKernelGGL(lora_outers<1>, dim3((unsigned)(qw.blocks + qn.blocks)), dim3(256), 0, stream, qw, qn);
