@@ -15,7 +15,9 @@ returns a new fp32 tensor): it checks the
 tensors' device, dtype, shape and contiguity on the host, passes their data
 pointers and torch's current HIP stream, and raises ``GemmError`` on a
 negative status.  The vocabulary losses (``linear_cross_entropy``,
-``linear_distill`` and their backward calls) are in ``loss.py`` and offered here
+``linear_distill`` and their backward calls) are in ``loss.py``, the gated
+feed-forward block (``gated_ffn``) in ``ffn.py`` and projections with adapters
+(``linear_lora``) in ``lora.py``, and offered here
 too.  Importing this module fails loudly when the library has not
 been built; there is no fallback path.
 """
