@@ -287,7 +287,10 @@ struct Extra {
                                                const List<L::TQ> &list, int from, int every, typename L::Acc &acc) {
         const int lane = loop.lane, wave = loop.wave, slabs = (p.R + KB - 1) / KB;
         const int n = list.n() > from ? (list.n() - from + every - 1) / every : 0;
-        if (!n) return;
+        if (!n) {
+            __syncthreads();   // the list is read: its LDS is free, too
+            return;
+        }
         OpP P;
         P.init(p.f, p0, p.R, wave, lane);
         int id[L::CB];   // the adapters of the rows that this lane multiplies
@@ -1007,7 +1010,7 @@ hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &d
         auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, q, cb, qw, qn); };
         if (tail->P.kc) dtype == 0 ? run(lora_few_join_outers<0, true>) : run(lora_few_join_outers<1, true>);
         else dtype == 0 ? run(lora_few_join_outers<0, false>) : run(lora_few_join_outers<1, false>);
-        return hipGetLastError();
+        return dtype == 0 ? join_outers<0>(qw, qn, stream) : join_outers<1>(qw, qn, stream);
     }
     if (!tail) {
         if (dtype == 0) hipLaunchKernelGGL(lora_outers<0>, dim3((unsigned)(qw.blocks + qn.blocks)), dim3(256), 0, stream, qw, qn);
