@@ -53,7 +53,7 @@ __device__ __forceinline__ Act activation(float g) {
         const float phi = g >= 0.0f ? 1.0f - q : q;
         return {g * phi, __builtin_fmaf(g * bell, 0.39894228040143268f, phi)};
     } else {
-        return {g > 0.0f ? g : 0.0f, g > 0.0f ? 1.0f : 0.0f};
+        return {g <= 0.0f ? 0.0f : g, g <= 0.0f ? 0.0f : 1.0f};   // NaN stays
     }
 }
 
@@ -65,7 +65,8 @@ __device__ __forceinline__ void with_act(uint32_t act, F &&f) {
     else f(std::integral_constant<uint32_t, GEMM_FFN_RELU>());
 }
 
-// v in 16 bits at `to` and, TWO, what that left out, rounded too, `part` elements on.
+// v in 16 bits at `to` and, TWO, what that left out, rounded too, `part` elements on
+// (nothing where the first is infinite: infinity less infinity would make it NaN).
 // The rest is taken from the stored bits: the compiler may fold the multiplication that
 // made v into one of its conversions (v_fma_mixlo_f16) and not into another, and near a
 // tie the two then round apart.
@@ -73,7 +74,13 @@ template <int DT, bool TWO>
 __device__ __forceinline__ void store4(uint16_t *to, int64_t part, f32x4 v) {
     const u32x2 first = pack4<DT>(v);
     *reinterpret_cast<u32x2 *>(to) = first;
-    if constexpr (TWO) *reinterpret_cast<u32x2 *>(to + part) = pack4<DT>(v - unpack4<DT>(first));
+    if constexpr (TWO) {
+        const f32x4 f = unpack4<DT>(first);
+        f32x4 rest;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rest[e] = __builtin_isinf(f[e]) ? 0.0f : v[e] - f[e];
+        *reinterpret_cast<u32x2 *>(to + part) = pack4<DT>(rest);
+    }
 }
 
 struct GateParams {

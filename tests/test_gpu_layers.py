@@ -228,6 +228,36 @@ def test_large_gates(dg):
         assert all(fu.ratio(t, want[k]) <= 1 for k, t in zip(("y", "gate", "up"), got)), act
 
 
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("T", [2, 5, 40, 65, 700])
+def test_hidden_values_beyond_fp16(dg, layout, T):
+    # h, dg and du overflow to infinities and every weight is positive: y and dx are infinite, not NaN (h stays
+    # fp32 up to 4 rows of "nk": 128 features of 256 * 512 / 2^14 each are 1024 there, exactly)
+    H, F = 64, 128
+    one = lambda *s: torch.ones(*s, dtype=torch.float16, device=DEV)
+    x, wg, wu, wd = one(T, H), one(F, H) * 4, one(F, H) * 8, one(H, F) * 2.0 ** -14
+    stored = [fu.stored(w, layout) for w in (wg, wu, wd)]
+    y, gate, up = dg.gated_ffn(x, *stored, activation="relu", b_layout=layout, save=True)
+    assert bool((gate == 256).all()) and bool((up == 512).all())
+    whole = layout == "nk" and T <= 4
+    assert bool((y == (1024 if whole else math.inf)).all())
+    dy = one(T, H) * 2.0 ** 13                                    # dh = 2^13 * 64 / 2^14 = 32; dg, du = 2^14, 2^13: in range
+    dx, _, _, _ = dg.gated_ffn_backward(dy, x, *stored, gate, up, activation="relu", b_layout=layout)
+    assert bool((dx == math.inf).all())                           # 128 * (2^14 * 4 + 2^13 * 8) in fp16
+    dx, dwg, dwu, dwd = dg.gated_ffn_backward(dy * 4, x, *stored, gate, up * 2, activation="relu", b_layout=layout)
+    assert all(bool((t == math.inf).all()) for t in (dx, dwg, dwd))   # dg = 2^17, h = 2^18; du = 2^15 is in range
+    assert not bool(dwu.isnan().any())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_nan_gates_stay_nan(dg, act, T):
+    d = fu.make(T, 64, 64, "bf16", seed=1, dev=DEV)
+    d["w_gate"][5] = float("nan")
+    d["w_down"][:, 5] = 1.0
+    assert bool(fu.call_forward(dg, d, act=act).isnan().all())
+
+
 # ---- streams, graphs, workspaces ---------------------------------------------------------------------
 def everything(dg, d, e, **kw):
     return [*fu.call_forward(dg, d, save=True, **kw), *fu.call_backward(dg, d, **kw), lu.call_forward(dg, e, **kw),
