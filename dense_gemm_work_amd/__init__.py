@@ -539,5 +539,6 @@ from .ffn import (  # noqa: E402
     gated_ffn_backward, gemm_ffn_backward, gemm_ffn_forward, gemm_ffn_plan)
 from .lora import (  # noqa: E402
     GEMM_LORA_DAB_FP32, GEMM_LORA_DAB_FP32_ADD, GEMM_LORA_DAB_SAME, GEMM_LORA_MAX_ADAPTERS, GEMM_LORA_MAX_H,
-    GEMM_LORA_MAX_LRH, GEMM_LORA_MAX_LT, GEMM_LORA_MAX_R, GEMM_LORA_MAX_T, GEMM_LORA_MAX_TH, GemmLoraArgs, GemmLoraPlan,
+    GEMM_LORA_MAX_LRH, GEMM_LORA_MAX_LT, GEMM_LORA_MAX_R, GEMM_LORA_MAX_STRIDE, GEMM_LORA_MAX_T, GEMM_LORA_MAX_TH,
+    GEMM_LORA_MAX_TILES, GEMM_LORA_MAX_TR, GemmLoraArgs, GemmLoraPlan,
     gemm_lora_backward, gemm_lora_forward, gemm_lora_plan, linear_lora, linear_lora_backward)

@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <utility>
 
 #include "../../include/gemm_lora.h"
 #include "call.h"
@@ -25,6 +26,11 @@ int64_t stride_a(const gemm_lora_args_t &a) { return or_packed(a.stride_a, (int6
 int64_t stride_b(const gemm_lora_args_t &a) { return or_packed(a.stride_b, (int64_t)a.R * a.N); }
 int dab_size(const gemm_lora_args_t &a) { return a.dab_type == GEMM_LORA_DAB_SAME ? 2 : 4; }
 
+// Tiles of da and db: 64 of the rank by 128, for each adapter.
+int64_t outer_tiles(const gemm_lora_args_t &a) {
+    return a.adapters * ceil_div(a.R, 64) * ((a.da ? ceil_div(a.H, 128) : 0) + (a.db ? ceil_div(a.N, 128) : 0));
+}
+
 int check_sizes(const gemm_lora_args_t &a, bool backward) {
     if (a.layout & ~0x1Fu || (a.layout & 0xEu)) return bad("layout word has unknown bits");
     if (a.T < 0 || a.H < 1 || a.N < 1 || a.R < 1 || a.adapters < 1) return bad("T >= 0, H, N, R and adapters >= 1");
@@ -33,8 +39,11 @@ int check_sizes(const gemm_lora_args_t &a, bool backward) {
         return set_error(GEMM_ERR_UNSUPPORTED, "T, H, N, R or adapters exceeds its GEMM_LORA_MAX_*");
     if (a.T * a.H > GEMM_LORA_MAX_TH || a.T * a.N > GEMM_LORA_MAX_TH || a.H * a.N > GEMM_LORA_MAX_TH)
         return set_error(GEMM_ERR_UNSUPPORTED, "T * H, T * N or H * N exceeds GEMM_LORA_MAX_TH");
-    if (a.adapters * (int64_t)a.R * std::max(a.H, a.N) > GEMM_LORA_MAX_LRH || (backward && a.adapters * a.T > GEMM_LORA_MAX_LT))
-        return set_error(GEMM_ERR_UNSUPPORTED, "adapters * R * H, adapters * R * N or adapters * T exceeds its GEMM_LORA_MAX_*");
+    if (a.adapters * (int64_t)a.R * std::max(a.H, a.N) > GEMM_LORA_MAX_LRH || (backward && a.adapters * a.T > GEMM_LORA_MAX_LT) ||
+        a.T * a.R > GEMM_LORA_MAX_TR)
+        return set_error(GEMM_ERR_UNSUPPORTED, "adapters * R * H, adapters * R * N, adapters * T or T * R exceeds its GEMM_LORA_MAX_*");
+    if (backward && outer_tiles(a) > GEMM_LORA_MAX_TILES)
+        return set_error(GEMM_ERR_UNSUPPORTED, "da and db have more than GEMM_LORA_MAX_TILES tiles; ask for them in two calls, or for fewer adapters");
     if (a.H % 8 || a.N % 8 || a.R % 8) return set_error(GEMM_ERR_UNSUPPORTED, "H, N and R must be multiples of 8");
     if (a.dab_type > GEMM_LORA_DAB_FP32_ADD) return bad("unknown dab_type");
     return GEMM_OK;
@@ -71,17 +80,18 @@ int check_args(const gemm_lora_args_t &a, bool backward) {
     if (a.num_cus < 0 || a.num_cus > MAX_CUS) return bad("num_cus must be 0 .. 65536");
     if ((rc = check_ld(or_packed(a.ldx, a.H), a.H, 8, "x")) != GEMM_OK) return rc;
     if ((rc = check_ld(or_packed(a.ldw, w_row(a)), w_row(a), 8, "w")) != GEMM_OK) return rc;
-    if (stride_a(a) < a.R * a.H || stride_a(a) % 8 || stride_b(a) < a.R * a.N || stride_b(a) % 8)
-        return bad("stride_a and stride_b must be at least a matrix and multiples of 8");
+    for (const auto &[stride, least] : {std::pair{stride_a(a), a.R * a.H}, std::pair{stride_b(a), a.R * a.N}})
+        if (stride < least || stride % 8 || stride > GEMM_LORA_MAX_STRIDE)
+            return bad("stride_a and stride_b must be at least a matrix, multiples of 8 and at most GEMM_LORA_MAX_STRIDE");
     if (!backward && (rc = check_ld(or_packed(a.ldy, a.N), a.N, 8, "y")) != GEMM_OK) return rc;
     if (backward && ((rc = check_ld(or_packed(a.lddy, a.N), a.N, 8, "dy")) != GEMM_OK ||
                      (rc = check_ld(or_packed(a.lddx, a.H), a.H, 8, "dx")) != GEMM_OK))
         return rc;
     const Blocks s = blocks_of(a, backward);
     for (int i = 0; i < s.all; ++i) {
-        const bool words = s.b[i].base == a.adapter || s.b[i].base == a.scale;
-        if (s.b[i].begin() & (words ? 7 : 15) && s.b[i].base != a.scale)
-            return set_error(GEMM_ERR_UNSUPPORTED, std::string(s.b[i].name) + " must be " + (words ? "8" : "16") + "-byte aligned");
+        const uintptr_t unit = i == s.all - 1 ? 4 : i == s.all - 2 ? 8 : 16;   // scale, adapter, the matrices
+        if (s.b[i].begin() & (unit - 1))
+            return set_error(GEMM_ERR_UNSUPPORTED, std::string(s.b[i].name) + " must be " + std::to_string(unit) + "-byte aligned");
     }
     if (a.T == 0) return GEMM_OK;
     if (!a.x || !a.w || !a.a || !a.b || !a.adapter) return bad("x, w, a, b and adapter must be non-null");
@@ -182,9 +192,7 @@ bool few_rows(const gemm_lora_args_t &a, int64_t wide) {
 
 // Slices of the rows for da and db, which one launch computes.
 int outer_splits(const gemm_lora_args_t &a, int cus) {
-    const int64_t narrow = ceil_div(a.R, 64);
-    const int64_t blocks = a.adapters * narrow * ((a.da ? ceil_div(a.H, 128) : 0) + (a.db ? ceil_div(a.N, 128) : 0));
-    return (int)std::max<int64_t>(1, std::min(2 * cus / std::max<int64_t>(1, blocks), ceil_div(a.T, 64) / 8));
+    return (int)std::max<int64_t>(1, std::min(2 * cus / std::max<int64_t>(1, outer_tiles(a)), ceil_div(a.T, 64) / 8));
 }
 
 struct Plan {

@@ -32,6 +32,9 @@ GEMM_LORA_MAX_ADAPTERS = 1 << 16
 GEMM_LORA_MAX_TH = 1 << 37
 GEMM_LORA_MAX_LT = 1 << 34
 GEMM_LORA_MAX_LRH = 1 << 38
+GEMM_LORA_MAX_TR = 1 << 31
+GEMM_LORA_MAX_TILES = 1 << 23
+GEMM_LORA_MAX_STRIDE = 1 << 40
 
 
 class GemmLoraArgs(ctypes.Structure):

@@ -23,7 +23,8 @@
  * zero).  What x, dy hold in one row never reaches another row or another adapter.
  *
  * Arithmetic: products in fp32.  s and ds, the operands of the next products, are
- * rounded to the type once, after the scale, as tensors of the type would be; y, dx,
+ * rounded to the type once, after the scale, as tensors of the type would be (up to 256
+ * rows y and dx may be made from them unrounded); y, dx,
  * and da and db of the type once each; y's and dx's two parts are one fp32 sum.
  * fp16 values beyond its range become infinities, as everywhere.
  * Every sum has a fixed order: the same call gives the same bits.
@@ -59,6 +60,9 @@ extern "C" {
 #define GEMM_LORA_MAX_TH       ((int64_t)1 << 37)   /* T * H, T * N and H * N      */
 #define GEMM_LORA_MAX_LT       ((int64_t)1 << 34)   /* L * T (backward)            */
 #define GEMM_LORA_MAX_LRH      ((int64_t)1 << 38)   /* L * R * H and L * R * N     */
+#define GEMM_LORA_MAX_TR       ((int64_t)1 << 31)   /* T * R                       */
+#define GEMM_LORA_MAX_TILES    ((int64_t)1 << 23)   /* backward: L ceil(R / 64) (ceil(H / 128) if da + ceil(N / 128) if db) */
+#define GEMM_LORA_MAX_STRIDE   ((int64_t)1 << 40)   /* stride_a, stride_b          */
 
 /*
  * Arguments; zero-initialise, then fill what the call needs.
@@ -66,7 +70,7 @@ extern "C" {
  *              packed; else at least the row's length, a multiple of 8, at most 2^21).
  *   a, b:      device, 16-byte aligned, each adapter's matrix packed; stride_a,
  *              stride_b: elements between adapters (0: packed; else at least a matrix,
- *              a multiple of 8).
+ *              a multiple of 8, at most GEMM_LORA_MAX_STRIDE).
  *   T, H, N, R, adapters: T >= 0; H, N and R multiples of 8 >= 8; adapters (L) >= 1; at
  *              most GEMM_LORA_MAX_*.
  *   layout:    GEMM_B_NK or GEMM_B_KN, combined with GEMM_BF16 or GEMM_FP16.

@@ -97,3 +97,24 @@ def test_every_tile(dg, shape, layout):
     assert how == ("whole" if plan.out_whole == tiles else "tail" if plan.out_whole else "sliced")
     d = make(T, H, N, 6, R, dtype, "packed", seed=5, dev="cuda")
     (check_backward if backward else check_forward)(dg, d, layout, dtype)
+
+
+EDGES = [   # T, H, N, L, R, dtype, layout, order: both sides of what few rows take, the largest rank
+    (256, 264, 1032, 70, 16, "bf16", "nk", "mixed"),
+    (257, 264, 1032, 70, 16, "bf16", "nk", "mixed"),
+    (256, 264, 520, 300, 24, "fp16", "kn", "mixed"),
+    (40, 136, 264, 40, 256, "bf16", "nk", "mixed"),
+    (40, 136, 264, 40, 264, "bf16", "nk", "mixed"),
+    (2, 136, 264, 2, 1024, "fp16", "nk", "mixed"),
+    (60, 136, 264, 3, 1024, "bf16", "kn", "mixed"),
+    (300, 264, 136, 3, 1024, "bf16", "nk", "mixed"),
+    (5000, 1032, 2056, 5, 40, "bf16", "nk", "none"),      # large tiles without an adapter
+]
+
+
+@pytest.mark.parametrize("size", EDGES, ids=lambda s: "x".join(map(str, s)))
+def test_edges(dg, size):
+    T, H, N, L, R, dtype, layout, order = size
+    d = make(T, H, N, L, R, dtype, order, seed=T + R, dev="cuda")
+    check_forward(dg, d, layout, dtype)
+    check_backward(dg, d, layout, dtype)

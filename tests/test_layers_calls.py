@@ -196,6 +196,11 @@ REFUSED = [   # kind, what, where, status
     (Lora, change(adapters=1 << 16, R=1024, H=1 << 20), "both", "UNSUPPORTED"),
     (Lora, change(T=1 << 20, N=1 << 18), "both", "UNSUPPORTED"),
     (Lora, change(T=1 << 20, adapters=1 << 15), "backward", "UNSUPPORTED"),
+    (Lora, change(T=1 << 22, R=1024), "both", "UNSUPPORTED"),
+    (Lora, change(adapters=1 << 16, H=1 << 14, stride_a=0, ldx=0, ldw=0, lddx=0), "backward", "UNSUPPORTED"),
+    (Lora, change(stride_a=(1 << 40) + 8), "both", "INVALID"),
+    (Lora, change(stride_b=1 << 62), "both", "INVALID"),
+    (Lora, change(scale=6 * BASE + 2), "both", "UNSUPPORTED"),
     (Lora, change(dab_type=3), "both", "INVALID"),
     (Lora, change(stride_a=R * H - 8), "both", "INVALID"),
     (Lora, change(stride_b=N * R + 4), "both", "INVALID"),
