@@ -114,16 +114,14 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     const int64_t most = std::min<int64_t>(a.adapters, std::min<int64_t>(std::max<int64_t>(a.T, 1), 64));
     Low l;
     l.lists = (int)std::max<int64_t>(1, std::min(most, 2 * cus / groups));
-    // A group of rows of few requests has one or two adapters, and the workgroups that
-    // find none cost about what they wait for: four share many groups' adapters, and
-    // those take two slices (8192 x 4096, rank 64: 41 us, in four slices 46, one 62; 5000 x
-    // 4096: 18 us, six in three slices 24).
-    const int64_t found = a.T <= 256 ? l.lists : std::min(l.lists, 2);
-    int64_t most_splits = 9;
-    if (groups >= 64) {
-        l.lists = std::min(l.lists, 4);
-        most_splits = 2;
-    }
+    // Beyond few rows a group has the one or two adapters of its requests, and the
+    // workgroups that find none cost about what they wait for: at most four share a group's
+    // adapters (the gradients' call for 1327 x 2536 x 5288 with 47 adapters of rank 8: 99 us, with 24
+    // lists 136; 1000 x 2048 x 4096 with 64 mixed row by row: 254 us, eight lists 263, 24 lists
+    // 328, two 273), and many groups take two slices (8192 x 4096, rank 64: 41 us, in four
+    // slices 46, one 62).
+    if (a.T > 256) l.lists = std::min(l.lists, 4);
+    const int64_t found = a.T <= 256 ? l.lists : std::min(l.lists, 2), most_splits = groups >= 64 ? 2 : 9;
     l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, 2 * cus / (groups * found), most_splits}));
     return l;
 }

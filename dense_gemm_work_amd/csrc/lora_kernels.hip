@@ -755,10 +755,14 @@ __global__ __launch_bounds__(256, 2) void lora_join_outers(WideParams p, OuterPa
     else outer_block<DT, 64, 128>(narrow, (int64_t)blockIdx.x - wide.blocks, lds);
 }
 
+// The slices of da and db added in slice order, a thread per four values: the first
+// `wide_blocks` workgroups those of one, the others those of the other.
 template <int DT>
-__global__ __launch_bounds__(256) void lora_outer_join(OuterParams p) {
+__global__ __launch_bounds__(256) void lora_outer_join(OuterParams wide, OuterParams narrow, int wide_blocks) {
+    const bool first = (int)blockIdx.x < wide_blocks;
+    const OuterParams &p = first ? wide : narrow;
     const int64_t quads = p.P.rows / 4, all = (int64_t)p.count * p.Q.rows * quads;
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t id = (int64_t)(blockIdx.x - (first ? 0 : wide_blocks)) * 256 + threadIdx.x;
     if (id >= all) return;
     const int64_t col = id % quads * 4, row = id / quads % p.Q.rows, a = id / quads / p.Q.rows;
     f32x4 v = sum_slices(p.partial + id * 4, all * 4, p.splits);
@@ -922,14 +926,12 @@ OuterParams outer_params(const LoraOuter &a) {
 }
 template <int DT>
 hipError_t join_outers(const OuterParams &w, const OuterParams &n, hipStream_t stream) {
-    hipError_t e = hipGetLastError();
-    for (const OuterParams *q : {&w, &n}) {
-        if (e != hipSuccess || !q->out || q->splits == 1) continue;
-        const int64_t quads = (int64_t)q->count * q->Q.rows * (q->P.rows / 4);
-        hipLaunchKernelGGL(lora_outer_join<DT>, dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream, *q);
-        e = hipGetLastError();
-    }
-    return e;
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || w.splits == 1) return e;
+    auto blocks = [](const OuterParams &q) { return q.out ? (int)(((int64_t)q.count * q.Q.rows * (q.P.rows / 4) + 255) / 256) : 0; };
+    const int first = blocks(w);
+    hipLaunchKernelGGL(lora_outer_join<DT>, dim3((unsigned)(first + blocks(n))), dim3(256), 0, stream, w, n, first);
+    return hipGetLastError();
 }
 
 }  // namespace
