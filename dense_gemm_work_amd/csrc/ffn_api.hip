@@ -275,7 +275,7 @@ struct Weight {
 };
 int weight_gradients(const gemm_ffn_args_t &a, const Call &c, const Weight (&w)[3]) {
     const int kind = a.dw_type == GEMM_FFN_DW_SAME ? dgw::LO_16 : a.dw_type == GEMM_FFN_DW_FP32 ? dgw::LO_F32 : dgw::LO_F32_ADD;
-    hipError_t e = hipSuccess;
+    hipError_t e;
     if (!c.plan.outer) {
         const Choice &how = c.plan.weights;
         dgw::FfnWeights p;
@@ -287,20 +287,19 @@ int weight_gradients(const gemm_ffn_args_t &a, const Call &c, const Weight (&w)[
         e = dgw::launch_ffn_weights(c.dtype, how.tile, p, c.stream);
         return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the weights' gradients");
     }
-    for (const Weight &x : w) {
-        if (!x.dw) continue;
-        dgw::LossProduct p;
-        p.P = c.nk ? x.ins : x.outs;
-        p.Q = c.nk ? x.outs : x.ins;
-        p.K = (int)a.T;
-        p.splits = 1;
-        p.unscale = nullptr;
-        p.out = x.dw;
-        p.ldo = x.ldo;
-        p.out_kind = kind;
-        if ((e = dgw::launch_loss_outer(c.dtype, p, 2 * c.cus, c.stream)) != hipSuccess) return set_hip_error(e, "launch a weight's gradient");
+    dgw::LossProduct p[3];
+    for (int i = 0; i < 3; ++i) {
+        p[i].P = c.nk ? w[i].ins : w[i].outs;
+        p[i].Q = c.nk ? w[i].outs : w[i].ins;
+        p[i].K = (int)a.T;
+        p[i].splits = 1;
+        p[i].unscale = nullptr;
+        p[i].out = w[i].dw;
+        p[i].ldo = w[i].ldo;
+        p[i].out_kind = kind;
     }
-    return GEMM_OK;
+    e = dgw::launch_loss_outers(c.dtype, p, 2 * c.cus, c.stream);
+    return e == hipSuccess ? GEMM_OK : set_hip_error(e, "launch the weights' gradients");
 }
 
 // dx[t][i] = sum_f w_gate[f][i] dg[t][f] + w_up[f][i] du[t][f].

@@ -102,6 +102,9 @@ hipError_t launch_loss_product(int dtype, int tile, const LossProduct &p, hipStr
 // them of two parts, on at most about `workgroups` persistent workgroups (the splits
 // and slots do not apply).
 hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream);
+// Three of them in one launch, of one out_kind (out == nullptr: left out); the first two's
+// operand of two parts is P or Q, the third's the other.
+hipError_t launch_loss_outers(int dtype, const LossProduct (&p)[3], int workgroups, hipStream_t stream);
 
 // out from the slots of `splits` slices: out_kind LO_16, LO_F32 or LO_F32_ADD.
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream);

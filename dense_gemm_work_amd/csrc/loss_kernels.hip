@@ -381,20 +381,24 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void loss_product(ProductParams p)
 // part goes into the third while this tile is multiplied, its second part into the
 // place that this tile's first part leaves.
 // ---------------------------------------------------------------------------
+constexpr int OUTER_OUT = 128 * 128 * 2;   // packed result tile in bytes
+template <bool PARTS_P>
+constexpr int outer_lds() { return OUTER_OUT + (PARTS_P ? 2 : 3) * Operand<false, 128, 4>::SLAB; }
+
+// Workgroup `block` of `blocks`.
 template <int DT, int KIND, bool PARTS_P>
-__global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
+__device__ __forceinline__ void outer_tiles(const ProductParams &p, int block, int blocks, char *lds) {
     using Op = Operand<false, 128, 4>;
     constexpr int PP = PARTS_P ? 2 : 1, PQ = 3 - PP;                    // parts of P and Q
-    constexpr int OUT = 128 * 128 * 2, CH = 16;                         // packed result tile in bytes; chunks a row
+    constexpr int OUT = OUTER_OUT, CH = 16;                             // chunks a row
     constexpr int STORES = KIND == LO_16 ? 8 : 16;                      // per thread
-    __shared__ __attribute__((aligned(16))) char lds[OUT + (PQ + 1) * Op::SLAB];
-    static_assert(PP * Op::SLAB <= OUT, "P's slabs borrow the result's place");
+    static_assert(PP * Op::SLAB <= OUT && outer_lds<PARTS_P>() == OUT + (PQ + 1) * Op::SLAB, "P's slabs borrow the result's place");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wp = wave & 1, wq = wave >> 1;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
     // the grid is a multiple of tiles_p: a workgroup stays with its tile of P
-    const int tp = (int)blockIdx.x % p.g.tiles_p, step = (int)gridDim.x / p.g.tiles_p;
-    int tq = (int)blockIdx.x / p.g.tiles_p;
+    const int tp = block % p.g.tiles_p, step = blocks / p.g.tiles_p;
+    int tq = block / p.g.tiles_p;
     const int64_t p0 = (int64_t)tp * 128;
     auto load = [&](const Matrix &m, int part, int64_t row0, uint32_t dst) {
         Op o;
@@ -518,6 +522,22 @@ __global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
         place[0] = spare;
         spare = left;
     }
+}
+
+template <int DT, int KIND, bool PARTS_P>
+__global__ __launch_bounds__(256, 2) void loss_outer(ProductParams p) {
+    __shared__ __attribute__((aligned(16))) char lds[outer_lds<PARTS_P>()];
+    outer_tiles<DT, KIND, PARTS_P>(p, (int)blockIdx.x, (int)gridDim.x, lds);
+}
+
+// Three of them side by side (a or b or c workgroups each, zero: none), the first two's
+// parts in one operand, the third's in the other.
+template <int DT, int KIND, bool PARTS_P>
+__global__ __launch_bounds__(256, 2) void loss_outers(ProductParams pa, ProductParams pb, ProductParams pc, int a, int b, int c) {
+    __shared__ __attribute__((aligned(16))) char lds[outer_lds<false>()];
+    const int id = (int)blockIdx.x;
+    if (id < a + b) outer_tiles<DT, KIND, PARTS_P>(id < a ? pa : pb, id < a ? id : id - a, id < a ? a : b, lds);
+    else outer_tiles<DT, KIND, !PARTS_P>(pc, id - a - b, c, lds);
 }
 
 // The slices' slots added in slice order.  One thread per float4 of a slot.
@@ -943,13 +963,46 @@ static hipError_t run_outer(const ProductParams &q, int grid, hipStream_t stream
     return hipGetLastError();
 }
 
+static int outer_grid(const ProductParams &q, int workgroups) {
+    return std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;   // tiles_p < 2^14
+}
+
 hipError_t launch_loss_outer(int dtype, const LossProduct &p, int workgroups, hipStream_t stream) {
     if (p.P.kc || p.Q.kc || p.K > LOSS_FEW || p.out_kind > LO_F32_ADD || (p.P.part > 0) == (p.Q.part > 0)) return hipErrorInvalidValue;
     static_assert(LOSS_FEW <= KB, "one slab of k");
     const ProductParams q = product_params<Loop128<0>>(p);
-    const int grid = std::min(std::max(1, workgroups / q.g.tiles_p), q.g.tiles_q) * q.g.tiles_p;   // tiles_p < 2^14
+    const int grid = outer_grid(q, workgroups);
     if (p.P.part) return dtype == 0 ? run_outer<0, true>(q, grid, stream) : run_outer<1, true>(q, grid, stream);
     return dtype == 0 ? run_outer<0, false>(q, grid, stream) : run_outer<1, false>(q, grid, stream);
+}
+
+template <int DT, bool PARTS_P>
+static hipError_t run_outers(const ProductParams (&q)[3], const int (&grid)[3], hipStream_t stream) {
+    auto run = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(grid[0] + grid[1] + grid[2]), dim3(256), 0, stream, q[0], q[1], q[2], grid[0], grid[1], grid[2]);
+    };
+    if (q[0].out_kind == LO_16) run(loss_outers<DT, LO_16, PARTS_P>);
+    else if (q[0].out_kind == LO_F32) run(loss_outers<DT, LO_F32, PARTS_P>);
+    else run(loss_outers<DT, LO_F32_ADD, PARTS_P>);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_outers(int dtype, const LossProduct (&p)[3], int workgroups, hipStream_t stream) {
+    ProductParams q[3];
+    int grid[3], products = 0;
+    for (const LossProduct &x : p) products += x.out != nullptr;
+    if (!products) return hipSuccess;
+    const bool parts_p = p[0].P.part > 0;
+    for (int i = 0; i < 3; ++i) {
+        const LossProduct &x = p[i];
+        if (x.P.kc || x.Q.kc || x.K > LOSS_FEW || x.out_kind != p[0].out_kind || x.out_kind > LO_F32_ADD ||
+            (x.P.part > 0) == (x.Q.part > 0) || (x.P.part > 0) != (i < 2 ? parts_p : !parts_p))
+            return hipErrorInvalidValue;
+        q[i] = product_params<Loop128<0>>(x);
+        grid[i] = x.out ? outer_grid(q[i], workgroups / products) : 0;
+    }
+    if (parts_p) return dtype == 0 ? run_outers<0, true>(q, grid, stream) : run_outers<1, true>(q, grid, stream);
+    return dtype == 0 ? run_outers<0, false>(q, grid, stream) : run_outers<1, false>(q, grid, stream);
 }
 
 hipError_t launch_loss_join(int dtype, int tile, const LossProduct &p, const float *slots, hipStream_t stream) {
