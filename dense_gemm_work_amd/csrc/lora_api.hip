@@ -105,15 +105,18 @@ int check_args(const gemm_lora_args_t &a, bool backward) {
 }
 
 // The narrow product's workgroups: over 64 rows, over the adapters among them and over
-// slices of k, about two a CU of those that find an adapter.
+// slices of k.
 struct Low {
     int lists = 1, splits = 1;
 };
 Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     const int64_t groups = ceil_div(std::max<int64_t>(a.T, 1), 64) * ceil_div(a.R, dgw::lora_low_rows(dgw::lora_low_tile(a.R, kc)));
     const int64_t most = std::min<int64_t>(a.adapters, std::min<int64_t>(std::max<int64_t>(a.T, 1), 64));
+    // Few rows': one a CU, as the wide product's run beside them (96 x 4096 x 4096, 64 adapters
+    // of rank 16: 24.9 us, with two 28.5).
+    const int64_t budget = a.T <= 256 ? cus : 2 * cus;
     Low l;
-    l.lists = (int)std::max<int64_t>(1, std::min(most, 2 * cus / groups));
+    l.lists = (int)std::max<int64_t>(1, std::min(most, budget / groups));
     // Beyond few rows a group has the one or two adapters of its requests, and the
     // workgroups that find none cost about what they wait for: at most four share a group's
     // adapters (the gradients' call for 1327 x 2536 x 5288 with 47 adapters of rank 8: 99 us, with 24
@@ -122,7 +125,7 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     // slices 46, one 62).
     if (a.T > 256) l.lists = std::min(l.lists, 4);
     const int64_t found = a.T <= 256 ? l.lists : std::min(l.lists, 2), most_splits = groups >= 64 ? 2 : 9;
-    l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, 2 * cus / (groups * found), most_splits}));
+    l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, budget / (groups * found), most_splits}));
     return l;
 }
 
