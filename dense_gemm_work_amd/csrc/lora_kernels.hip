@@ -628,16 +628,19 @@ struct Slabs {
     }
 };
 
-template <int TP, int TQ>
-constexpr int outer_lds() { return 3 * (TP + TQ) * KB * 2; }
+template <int TP, int TQ, int NS = 3>
+constexpr int outer_lds() { return NS * (TP + TQ) * KB * 2; }
 
-template <int DT, int TP, int TQ>
+// NS: stages.  Few rows have one or two slabs for each of their adapters: one stage, so that
+// six workgroups fit a CU (96 x 4096 x 4096, 64 adapters of rank 16, with dx's join: 24 us, in
+// three stages 31).
+template <int DT, int TP, int TQ, int NS = 3>
 __device__ __forceinline__ void outer_block(const OuterParams &p, int64_t id, char *lds) {
-    constexpr int NS = 3, WP = TP / 32 > 2 ? 2 : 1, WQ = 4 / WP, RB = TP / WP / 16, CB = TQ / WQ / 16;
+    constexpr int WP = TP / 32 > 2 ? 2 : 1, WQ = 4 / WP, RB = TP / WP / 16, CB = TQ / WQ / 16;
     using OpP = Operand<false, TP, 4>;
     using OpQ = Operand<false, TQ, 4>;
     constexpr int STAGE = OpP::SLAB + OpQ::SLAB, LOADS = OpP::LOADS + OpQ::LOADS;
-    static_assert(NS * STAGE == outer_lds<TP, TQ>(), "the stages");
+    static_assert(NS * STAGE == outer_lds<TP, TQ, NS>(), "the stages");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wp = wave % WP, wq = wave / WP;
     const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((const lds_void *)lds);
@@ -778,13 +781,13 @@ __global__ __launch_bounds__(256) void lora_outer_join(OuterParams wide, OuterPa
 
 // The same, with the blocks that join few rows' dx behind them.
 template <int DT, bool KC>
-__global__ __launch_bounds__(256, 2) void lora_few_join_outers(WideParams p, int cb, OuterParams wide, OuterParams narrow) {
-    __shared__ __attribute__((aligned(16))) char lds[outer_lds<128, 64>()];
-    static_assert(FEW_LDS * 4 <= outer_lds<128, 64>(), "the narrow rows fit");
+__global__ __launch_bounds__(256, 4) void lora_few_join_outers(WideParams p, int cb, OuterParams wide, OuterParams narrow) {
+    __shared__ __attribute__((aligned(16))) char lds[outer_lds<128, 64, 1>()];
+    static_assert(FEW_LDS * 4 <= outer_lds<128, 64, 1>(), "the narrow rows fit");
     const int id = (int)blockIdx.x - wide.blocks - narrow.blocks;
     if (id >= 0) few_join_block<DT, KC>(p, cb, id, reinterpret_cast<float *>(lds));
-    else if ((int)blockIdx.x < wide.blocks) outer_block<DT, 128, 64>(wide, blockIdx.x, lds);
-    else outer_block<DT, 64, 128>(narrow, (int64_t)blockIdx.x - wide.blocks, lds);
+    else if ((int)blockIdx.x < wide.blocks) outer_block<DT, 128, 64, 1>(wide, blockIdx.x, lds);
+    else outer_block<DT, 64, 128, 1>(narrow, (int64_t)blockIdx.x - wide.blocks, lds);
 }
 
 // ---------------------------------------------------------------------------
