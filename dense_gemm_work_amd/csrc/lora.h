@@ -35,6 +35,7 @@ struct LoraLow {
     int R, K;
     int lists, splits;
     float *partial;     // launch_lora_lows: nullptr leaves this product out
+    bool by_rows;       // launch_lora_few, launch_lora_lows: a workgroup for a row and eight ranks, splits is 1
 };
 enum LoraLowTile : int { LL_32x64 = 0, LL_64x64, LL_128x64 };   // R x rows; 32: k contiguous only
 int lora_low_tile(int R, bool kc);

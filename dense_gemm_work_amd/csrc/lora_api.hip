@@ -104,6 +104,16 @@ int check_args(const gemm_lora_args_t &a, bool backward) {
     return GEMM_OK;
 }
 
+// Few rows of small ranks with an adapter for at least every fourth of them: the narrow products
+// row by row, as a tile of 64 rows would be read for one or two.  The gradients' call
+// for 96 x 4096 x 4096, 64 adapters of rank 16: 46 us, on tiles 64; 200 x 2048 x 4096, 50
+// of rank 32: 64 us, 77; its forward call 32 both ways; 250 x 4096 x 4096 with two of
+// rank 16, which stays with the tiles: 25 us, row by row 27.5; 96 x 4096 x 4096 with 96 of
+// rank 64, which does too: 97 and 122 us (gradients).
+bool low_by_rows(const gemm_lora_args_t &a) {
+    return a.T <= dgw::LORA_FEW_T && a.R <= 32 && 4 * std::min<int64_t>(a.adapters, a.T) >= a.T;
+}
+
 // The narrow product's workgroups: over 64 rows, over the adapters among them and over
 // slices of k.
 struct Low {
@@ -112,8 +122,8 @@ struct Low {
 Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     const int64_t groups = ceil_div(std::max<int64_t>(a.T, 1), 64) * ceil_div(a.R, dgw::lora_low_rows(dgw::lora_low_tile(a.R, kc)));
     const int64_t most = std::min<int64_t>(a.adapters, std::min<int64_t>(std::max<int64_t>(a.T, 1), 64));
-    // Few rows': one a CU, as the wide product's run beside them (96 x 4096 x 4096, 64 adapters
-    // of rank 16: 24.9 us, with two 28.5).
+    // Few rows': one a CU, as the wide product's run beside them (96 x 4096 x 4096, 20 adapters
+    // of rank 16: 19 us, with two 23; 96 of rank 64: 51 and 57).
     const int64_t budget = a.T <= 256 ? cus : 2 * cus;
     Low l;
     l.lists = (int)std::max<int64_t>(1, std::min(most, budget / groups));
@@ -199,7 +209,7 @@ int outer_splits(const gemm_lora_args_t &a, int cus) {
 struct Plan {
     Low s, ds;
     Wide out;
-    bool few = false;
+    bool few = false, by_rows = false;
     int dab_splits = 1;
     int64_t db_at = 0;   // db's slices behind da's
     int64_t low = 0, dlow = 0, part_s = 0, part_ds = 0, slots = 0, partial = 0, masks = 0;   // byte offsets
@@ -217,15 +227,16 @@ Plan make_plan(const gemm_lora_args_t &a, bool backward, int cus) {
     int64_t slots = 0;
     const bool own = backward && (a.da || a.db);   // the adapters' gradients: s and ds in the type, too
     auto low = [&](Low &l, int64_t k, bool kc, int64_t &slices, int64_t &at) {
-        l = low_plan(a, k, kc, cus);
+        if (!p.by_rows) l = low_plan(a, k, kc, cus);
         slices = p.take(l.splits * a.T * a.R * 4);
         if (own) at = p.take(a.T * a.R * 2);
     };
+    const int64_t wide = backward ? a.H : a.N;
+    p.few = (!backward || a.dx) && few_rows(a, wide);
+    p.by_rows = (backward || p.few) && low_by_rows(a);
     if (!backward || a.db) low(p.s, a.H, nk, p.part_s, p.low);
     if (backward && (a.dx || a.da)) low(p.ds, a.N, !nk, p.part_ds, p.dlow);
-    const int64_t wide = backward ? a.H : a.N;
     if (!backward || a.dx) {
-        p.few = few_rows(a, wide);
         p.out = out_plan(a, wide, backward ? a.N : a.H, p.few, cus);
         if (p.few) p.out.whole = 0;
         const dgw::LossTileShape s = dgw::lora_tile_shape(p.out.tile);
@@ -295,7 +306,7 @@ dgw::LoraFactor factor_b(const gemm_lora_args_t &a, bool rank_rows) {   // rows:
 
 dgw::LoraLow narrow(const gemm_lora_args_t &a, const Call &c, const Low &l, const dgw::LoraFactor &f, const dgw::LossMatrix &x, int64_t k,
                     int64_t slices) {
-    return {c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, slices)};
+    return {c.rows, f, x, a.R, (int)k, l.lists, l.splits, part<float>(c.ws, slices), c.plan.by_rows};
 }
 
 dgw::LoraProduct product(const gemm_lora_args_t &a, const Call &c, const dgw::LossMatrix &w, const dgw::LossMatrix &x,
@@ -407,7 +418,7 @@ int plan(const gemm_lora_args_t *args, int32_t backward, int32_t num_cus, gemm_l
     const Low &l = backward ? p.ds : p.s;
     const dgw::LossTileShape o = dgw::lora_tile_shape(p.out.tile);
     out->num_cus = num_cus;
-    out->low_tile_r = dgw::lora_low_rows(dgw::lora_low_tile(args->R, kc));
+    out->low_tile_r = p.by_rows ? 8 : dgw::lora_low_rows(dgw::lora_low_tile(args->R, kc));
     out->low_splits = l.splits;
     out->low_lists = l.lists;
     out->out_tile_p = o.p;

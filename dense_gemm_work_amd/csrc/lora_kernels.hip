@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "lora.h"
 #include "tile.h"
@@ -165,6 +166,58 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void lora_low(LowParams p) {
     low_block<L>(p, (int)blockIdx.x, lds, list);
 }
 
+// Few rows, many of them with an adapter of their own: a workgroup for a row and eight
+// ranks, straight from memory, as one slice.  (Where the factor's rows are contiguous a
+// wave reads 16 bytes of each: with up to 64 bytes, and as many fewer workgroups, the
+// gradients' call for 96 x 4096 x 4096 with 64 adapters of rank 16 takes 54 us, not 46.)
+template <int DT_, bool KC>
+struct RowLow {
+    static constexpr int DT = DT_, TP = 8, TQ = 64, NT = 256, WAVES = 2, LDS_BYTES = 4 * 8 * 4;
+};
+template <class L>
+struct IsRowLow : std::false_type {};
+template <int DT, bool KC>
+struct IsRowLow<RowLow<DT, KC>> : std::true_type {};
+
+template <int DT, bool KC>
+__device__ __forceinline__ void row_block(const LowParams &p, int id, char *lds, RowLow<DT, KC>) {
+    const int64_t t = id / p.tiles_r;
+    const int r0 = id % p.tiles_r * 8, a = adapter_of(p.rows, t);
+    if (a < 0) return;
+    const uint16_t *f = p.f.base + a * p.stride, *x = p.x.base + t * p.x.ld;
+    float(&red)[4][8][1] = *reinterpret_cast<float(*)[4][8][1]>(lds);
+    if constexpr (KC) {
+        const uint16_t *w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = f + (r0 + i) * p.f.ld;
+        dot_rows<DT>(w, Rows16<DT>{x, 0}, 1, p.K, red);
+    } else {
+        float acc[8] = {};
+#pragma unroll 4
+        for (int k = threadIdx.x; k < p.K; k += 256) {
+            const f32x8 v = unpack8<DT>(*reinterpret_cast<const u32x4 *>(f + k * p.f.ld + r0));
+            float lo, hi;
+            unpack2<DT>(x[k], lo, hi);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(v.v[e], lo, acc[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+            for (int o = 32; o; o >>= 1) acc[e] += __shfl_xor(acc[e], o);
+            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6][e][0] = acc[e];
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x < 8) p.partial[t * p.R + r0 + threadIdx.x] = joined(red, threadIdx.x, 0);
+}
+
+template <class L>
+__device__ __forceinline__ void narrow_block(const LowParams &p, int id, char *lds, List<L::TQ> &list) {
+    if constexpr (IsRowLow<L>::value) row_block(p, id, lds, L());
+    else low_block<L>(p, id, lds, list);
+}
+
 // Which rows of each 64 have which adapter: one wave per 64 rows.
 __device__ __forceinline__ void mask_block(const LoraRows &r, int id, uint64_t *masks) {
     const int lane = threadIdx.x & 63, slabs = (r.T + 63) / 64;
@@ -189,8 +242,8 @@ __global__ __launch_bounds__(256, LK::WAVES < LR::WAVES ? LK::WAVES : LR::WAVES)
     __shared__ List<LK::TQ> list;
     static_assert(LK::TQ == LR::TQ && LK::NT == 256 && LR::NT == 256, "one list, one size of workgroup");
     const int id = (int)blockIdx.x;
-    if (id < k.blocks) low_block<LK>(k, id, lds, list);
-    else if (id < k.blocks + r.blocks) low_block<LR>(r, id - k.blocks, lds, list);
+    if (id < k.blocks) narrow_block<LK>(k, id, lds, list);
+    else if (id < k.blocks + r.blocks) narrow_block<LR>(r, id - k.blocks, lds, list);
     else mask_block(k.rows, id - k.blocks - r.blocks, masks);
 }
 
@@ -469,7 +522,7 @@ __global__ __launch_bounds__(256, L::WAVES < LN::WAVES ? L::WAVES : LN::WAVES) v
     __shared__ List<LN::TQ> list;
     static_assert(L::NT == 256 && LN::NT == 256, "one size of workgroup");
     if ((int)blockIdx.x >= wide) {
-        low_block<LN>(n, (int)blockIdx.x - wide, lds, list);
+        narrow_block<LN>(n, (int)blockIdx.x - wide, lds, list);
         return;
     }
     int tp, tq, split;
@@ -499,7 +552,7 @@ __global__ __launch_bounds__(256) void lora_few_vec(WideParams w, LowParams n, i
     __shared__ float red[4][8][T];
     static_assert(LN::NT == 256 && L::TP == 64 && L::TQ == 32, "the join's tiles");
     if ((int)blockIdx.x >= wide) {
-        low_block<LN>(n, (int)blockIdx.x - wide, lds, list);
+        narrow_block<LN>(n, (int)blockIdx.x - wide, lds, list);
         return;
     }
     const int o0 = (int)blockIdx.x * 8;
@@ -797,7 +850,7 @@ template <class L>
 LowParams low_params(const LoraLow &a) {
     LowParams q{a.rows, matrix(a.f.first), matrix(a.x), a.f.stride, a.R, a.K, (a.K + KB - 1) / KB, (a.R + L::TP - 1) / L::TP,
                 (int)(((int64_t)a.rows.T + L::TQ - 1) / L::TQ), a.lists, a.splits, 0, a.partial};
-    q.blocks = q.groups * q.tiles_r * q.lists * q.splits;
+    q.blocks = IsRowLow<L>::value ? a.rows.T * q.tiles_r : q.groups * q.tiles_r * q.lists * q.splits;
     return q;
 }
 template <class L>
@@ -813,8 +866,9 @@ struct Narrow {
     using L = L_;
 };
 template <int DT, bool KC, class F>
-hipError_t with_narrow(int R, F &&f) {
-    switch (lora_low_tile(R, KC)) {
+hipError_t with_narrow(const LoraLow &p, F &&f) {
+    if (p.by_rows) return f(Narrow<RowLow<DT, KC>>());
+    switch (lora_low_tile(p.R, KC)) {
     case LL_64x64: return f(Narrow<ThinLoop<DT, KC, true, 64, 64, 5>>());
     case LL_128x64: return f(Narrow<ThinLoop<DT, KC, true, 128, 64, 3>>());
     default: break;
@@ -824,11 +878,11 @@ hipError_t with_narrow(int R, F &&f) {
 }
 template <int DT>
 hipError_t run_lows(const LoraLow &k, const LoraLow &r, uint64_t *masks, hipStream_t stream) {
-    return with_narrow<DT, true>(k.R, [&](auto nk) {
-        return with_narrow<DT, false>(r.R, [&](auto nr) {
+    return with_narrow<DT, true>(k, [&](auto nk) {
+        return with_narrow<DT, false>(r, [&](auto nr) {
             using LK = typename decltype(nk)::L;
             using LR = typename decltype(nr)::L;
-            if constexpr (LK::TP == LR::TP || (LK::TP == 32 && LR::TP == 64)) {   // what one rank asks for
+            if constexpr (LK::TP == LR::TP || (LK::TP == 32 && LR::TP == 64)) {   // what one rank and number of rows ask for
                 LowParams a = low_params<LK>(k), b = low_params<LR>(r);
                 if (!k.partial) a.blocks = 0;
                 if (!r.partial) b.blocks = 0;
@@ -885,7 +939,7 @@ template <int DT, bool KC, class L>
 hipError_t run_few(const LoraProduct &a, const LoraLow &low, hipStream_t stream) {
     // the wide product's factor is stored as P is, the narrow one's the other way (an
     // input's side against an output's)
-    return with_narrow<DT, KC>(low.R, [&](auto n) {
+    return with_narrow<DT, KC>(low, [&](auto n) {
         using LN = typename decltype(n)::L;
         WideParams w = wide_params<L>(a);
         LowParams q = low_params<LN>(low);
@@ -943,14 +997,18 @@ int lora_low_tile(int R, bool kc) { return R <= 32 && kc ? LL_32x64 : R <= 64 ? 
 int lora_low_rows(int tile) { return tile == LL_32x64 ? 32 : tile == LL_64x64 ? 64 : 128; }
 
 hipError_t launch_lora_low(int dtype, const LoraLow &p, hipStream_t stream) {
-    if (!p.x.kc) return hipErrorInvalidValue;
-    auto run = [&](auto n) { return run_low<typename decltype(n)::L>(p, stream); };
-    if (p.f.first.kc) return dtype == 0 ? with_narrow<0, true>(p.R, run) : with_narrow<1, true>(p.R, run);
-    return dtype == 0 ? with_narrow<0, false>(p.R, run) : with_narrow<1, false>(p.R, run);
+    if (!p.x.kc || p.by_rows) return hipErrorInvalidValue;
+    auto run = [&](auto n) {
+        using L = typename decltype(n)::L;
+        if constexpr (IsRowLow<L>::value) return hipErrorInvalidValue;   // few rows' launch makes theirs
+        else return run_low<L>(p, stream);
+    };
+    if (p.f.first.kc) return dtype == 0 ? with_narrow<0, true>(p, run) : with_narrow<1, true>(p, run);
+    return dtype == 0 ? with_narrow<0, false>(p, run) : with_narrow<1, false>(p, run);
 }
 hipError_t launch_lora_lows(int dtype, const LoraLow &s, const LoraLow &ds, uint64_t *masks, hipStream_t stream) {
     const LoraLow &k = s.f.first.kc ? s : ds, &r = s.f.first.kc ? ds : s;
-    if (!s.x.kc || !ds.x.kc || !k.f.first.kc || r.f.first.kc || s.R != ds.R) return hipErrorInvalidValue;
+    if (!s.x.kc || !ds.x.kc || !k.f.first.kc || r.f.first.kc || s.R != ds.R || s.by_rows != ds.by_rows) return hipErrorInvalidValue;
     return dtype == 0 ? run_lows<0>(k, r, masks, stream) : run_lows<1>(k, r, masks, stream);
 }
 

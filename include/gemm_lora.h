@@ -112,7 +112,7 @@ typedef struct gemm_lora_args_t {
 /* How a call runs (host arithmetic only). */
 typedef struct gemm_lora_plan_t {
     int32_t num_cus;
-    int32_t low_tile_r, low_splits, low_lists;   /* s (backward: ds): rank x 64 rows; slices of k; workgroups over a tile's adapters */
+    int32_t low_tile_r, low_splits, low_lists;   /* s (backward: ds): rank x 64 rows (8: a row by itself); slices of k; workgroups over a tile's adapters */
     int32_t out_tile_p, out_tile_t;              /* tile of y (backward: dx)                  */
     int32_t out_splits;                          /* slices of k of the tiles behind the first out_whole */
     int32_t dab_splits;                          /* backward: slices of the rows for da and db */

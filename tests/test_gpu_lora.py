@@ -118,3 +118,18 @@ def test_edges(dg, size):
     d = make(T, H, N, L, R, dtype, order, seed=T + R, dev="cuda")
     check_forward(dg, d, layout, dtype)
     check_backward(dg, d, layout, dtype)
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("size", [(1, 4104, 72, 1, 8), (7, 72, 4104, 2, 32), (100, 520, 264, 25, 24), (256, 264, 1032, 64, 32)], ids=str)
+def test_narrow_products_row_by_row(dg, size, layout):
+    T, H, N, L, R = size
+    for backward in (False, True):   # an adapter for every fourth row, ranks up to 32
+        a = dg.GemmLoraArgs(T=T, H=H, N=N, R=R, adapters=L, layout=dg.layout_word(layout, "fp16"), dx=1, da=1, db=1)
+        assert dg.gemm_lora_plan(a, backward, 256).low_tile_r == 8
+        a.R = 40
+        assert dg.gemm_lora_plan(a, backward, 256).low_tile_r > 8
+    d = make(T, H, N, L, R, "fp16", "mixed", seed=T + R, dev="cuda")
+    d["adapter"][T // 2] = -1 if T > 1 else 0
+    check_forward(dg, d, layout, "fp16")
+    check_backward(dg, d, layout, "fp16")
