@@ -193,8 +193,9 @@ Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, bool few, in
 // Few rows of small ranks may take the adapters in the join, where each row reads its own
 // adapter (R elements a result) whatever the other rows read; in the product's tiles each
 // adapter costs about half a microsecond, and there are min(adapters, T) at most.  In the
-// join, 238 x 296 x 6400 with 63 adapters of rank 24: 42 us, in the tiles 69; 256 x 8192
-// x 8192 with two of rank 32: 72 us, in the tiles 59.
+// join, 238 x 296 x 6400 with 63 adapters of rank 24: 34 us, in the tiles 61; 96 x 4096 x
+// 4096 with 64 of rank 16: 21 and 46; 256 x 8192 x 8192 with two of rank 32: 73 us, in the
+// tiles 63.
 bool few_rows(const gemm_lora_args_t &a, int64_t wide) {
     if (a.T > dgw::LORA_FEW_T || a.R > dgw::LORA_FEW_R) return false;
     const double join = (double)(a.T * a.R) * (double)wide * 2.0 / 8e6;
