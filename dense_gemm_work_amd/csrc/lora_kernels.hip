@@ -319,7 +319,7 @@ __device__ __forceinline__ int place_wide(const Grid &g, int whole, int b, int &
 // with the narrow rows.  Those of the tile, 64 ranks at a time, are put together from
 // their slices, scaled, rounded and laid down in LDS, and stay in registers; the
 // adapters' slabs stream through NS stages, and each meets the 16-row blocks that hold
-// rows of its own, the others' rows masked to zero.  Uses the first BYTES bytes of the
+// rows of its own; what it holds reaches no other row.  Uses the first BYTES bytes of the
 // LDS, which must be free, and leaves them free.
 template <int DT, class L, int NS>
 struct Extra {
@@ -329,15 +329,87 @@ struct Extra {
     static constexpr int PA = OpP::template addresses<L::RB>();
     static_assert((NS - 1) * LOADS < 64 && NS <= 8, "the wait counter holds the loads in flight");
 
-    // Small tiles keep the narrow rows in registers and skip blocks without rows of the
-    // adapter; in the large ones either would spill the accumulators.
-    static constexpr bool HOLD = L::RB * L::CB <= 8;
+    // Small tiles keep the narrow rows in registers, skip blocks without rows of the adapter
+    // and keep a product for the rows of the adapter alone.  In the large ones any of these
+    // spills accumulators (the last 100 to 180 registers of 256 x 256), and the others' rows
+    // are multiplied as zeros, which an infinity or NaN of the adapter would carry into them:
+    // where the sums hold one, they are made again with `scrub`, the finite part as before and
+    // the rest added to the adapter's own rows.  (That the sums are looked at: 331.5 us instead
+    // of 331 at 5000 x 4096 x 8192, 24 of rank 64; 118.6 instead of 113.9 at 1000 x 2048 x 4096
+    // with 64 of rank 16 mixed row by row.)
+    static constexpr bool HOLD = L::RB * L::CB <= 8, KC = OpP::which(1, 0) == 0;
+    static __device__ __forceinline__ bool nonfinite(uint32_t v) {
+        constexpr uint32_t EXPONENT = DT == 0 ? 0x7f80u : 0x7c00u;
+        return (v & EXPONENT) == EXPONENT;
+    }
     static __device__ __forceinline__ u32x4 masked(u32x4 v, bool keep) {
         return u32x4{keep ? v[0] : 0u, keep ? v[1] : 0u, keep ? v[2] : 0u, keep ? v[3] : 0u};
     }
+    // scrub: an adapter's slab without its infinities and NaN.  Between barriers.
+    static __device__ __forceinline__ void clear_nonfinite(char *stage) {
+        for (int f = threadIdx.x; f < STAGE / 16; f += L::NT) {
+            u32x4 v = *reinterpret_cast<u32x4 *>(stage + 16 * f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] &= (nonfinite(v[i]) ? 0u : 0xffffu) | (nonfinite(v[i] >> 16) ? 0u : 0xffff0000u);
+            *reinterpret_cast<u32x4 *>(stage + 16 * f) = v;
+        }
+        __syncthreads();
+    }
+    // scrub: what the slab's infinities and NaN add to the rows of their own adapter (a slice
+    // adds those of every adapter: twice is the same).
+    static __device__ __forceinline__ void add_nonfinite(const L &loop, const char *rows, const WideParams &p, int64_t p0, int slab,
+                                                         const int (&id)[L::CB], typename L::Acc &acc) {
+        const int ranks = min(KB, p.R - slab * KB);
+#pragma unroll
+        for (int j = 0; j < L::CB; ++j) {
+            if (id[j] < 0) continue;
+            const uint16_t *f = p.f.base + id[j] * p.stride + (KC ? p0 * p.f.ld : p0) + (int64_t)slab * KB * (KC ? 1 : p.f.ld);
+            const char *own = rows + loop.q_of(j) * 128;
+#pragma unroll 1
+            for (int r = 0; r < ranks; ++r) {
+                const uint32_t word = *reinterpret_cast<const uint16_t *>(own + (((r >> 3) ^ swz_kc(loop.q_of(j))) << 4) + (r & 7) * 2);
+                float s, none;
+                unpack2<DT>(word, s, none);
+                int ld = (int)p.f.ld;
+                asm volatile("" : "+s"(ld));   // or the offsets of every block would be kept in registers
+#pragma unroll
+                for (int b = 0; b < L::RB; ++b) {
+                    const int row = loop.p_of(b, 0);
+                    if (p0 + row < p.f.rows)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = f[KC ? (row + e) * ld : row + e];
+                            float v;
+                            unpack2<DT>(w, v, none);
+                            if (nonfinite(w)) acc.v[b][j][e] = __builtin_fmaf(v, s, acc.v[b][j][e]);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                f += KC ? 1 : ld;
+            }
+        }
+    }
+    // Whether a sum of the workgroup's is infinite or NaN.  The LDS is free, before and after.
+    static __device__ __forceinline__ bool any_nonfinite(const typename L::Acc &acc, char *lds) {
+        float zero = 0.0f;
+#pragma unroll
+        for (int b = 0; b < L::RB; ++b)
+#pragma unroll
+            for (int j = 0; j < L::CB; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) zero = __builtin_fmaf(acc.v[b][j][e], 0.0f, zero);
+        int *flag = reinterpret_cast<int *>(lds);
+        if (threadIdx.x == 0) *flag = 0;
+        __syncthreads();
+        if (zero != 0.0f) *flag = 1;
+        __syncthreads();
+        const bool any = __builtin_amdgcn_readfirstlane(*flag);
+        __syncthreads();
+        return any;
+    }
 
     static __device__ __forceinline__ void run(const L &loop, char *lds, const WideParams &p, int64_t p0, int64_t q0,
-                                               const List<L::TQ> &list, int from, int every, typename L::Acc &acc) {
+                                               const List<L::TQ> &list, int from, int every, bool scrub, typename L::Acc &acc) {
         const int lane = loop.lane, wave = loop.wave, slabs = (p.R + KB - 1) / KB;
         const int n = list.n() > from ? (list.n() - from + every - 1) / every : 0;
         if (!n) {
@@ -395,20 +467,25 @@ struct Extra {
                 __builtin_amdgcn_sched_barrier(0);
                 const uint32_t o = st * STAGE;
                 const int a = list.adapter(from + i * every);
+                if constexpr (HOLD) {
+                    u32x4 f[2][L::RB];
 #pragma unroll
-                for (int step = 0; step < 2; ++step) {
-                    if constexpr (HOLD) {
-                        u32x4 f[L::RB];
+                    for (int step = 0; step < 2; ++step)
 #pragma unroll
-                        for (int b = 0; b < L::RB; ++b) f[b] = OpP::fragment(pa[OpP::which(b, step)] + o + OpP::constant(b, step));
+                        for (int b = 0; b < L::RB; ++b) f[step][b] = OpP::fragment(pa[OpP::which(b, step)] + o + OpP::constant(b, step));
 #pragma unroll
-                        for (int j = 0; j < L::CB; ++j) {
-                            if (!__any(id[j] == a)) continue;
-                            const u32x4 m = masked(q[step][j], id[j] == a);
+                    for (int j = 0; j < L::CB; ++j) {
+                        if (!__any(id[j] == a)) continue;
 #pragma unroll
-                            for (int b = 0; b < L::RB; ++b) acc.v[b][j] = mfma<DT>(f[b], m, acc.v[b][j]);
+                        for (int b = 0; b < L::RB; ++b) {
+                            const f32x4 v = mfma<DT>(f[1][b], q[1][j], mfma<DT>(f[0][b], q[0][j], acc.v[b][j]));
+                            acc.v[b][j] = id[j] == a ? v : acc.v[b][j];
                         }
-                    } else {
+                    }
+                } else {
+                    if (scrub) clear_nonfinite(lds + o);
+#pragma unroll
+                    for (int step = 0; step < 2; ++step) {
 #pragma unroll
                         for (int j = 0; j < L::CB; ++j) q[0][j] = masked(narrow(step, j), id[j] == a);
 #pragma unroll
@@ -426,6 +503,11 @@ struct Extra {
                 if (i + NS < n) issue(i + NS, st);
                 st = st + 1 == NS ? 0 : st + 1;
             }
+            if constexpr (!HOLD)
+                if (scrub) {
+                    add_nonfinite(loop, lds + ROWS_AT, p, p0, slab, id, acc);
+                    __syncthreads();   // the rows have been read
+                }
         }
         __syncthreads();
     }
@@ -465,7 +547,12 @@ __global__ __launch_bounds__(L::NT, 2) void lora_product(WideParams p) {
     if constexpr (X::HOLD) loop.run_any(p.P, p0, p.x, q0, p.K, s0, s1, acc);
     if (p.partial) {   // else the join adds the adapters
         list.fill(mine);
-        X::run(loop, lds, p, p0, q0, list, split, splits, acc);
+        X::run(loop, lds, p, p0, q0, list, split, splits, false, acc);
+        if constexpr (!X::HOLD)
+            if (list.n() > 0 && X::any_nonfinite(acc, lds)) {
+                L::zero(acc);
+                X::run(loop, lds, p, p0, q0, list, split, splits, true, acc);
+            }
     }
     if constexpr (!X::HOLD) loop.template run<true>(p.P, p0, p.x, q0, p.K, s0, s1, acc);
 #pragma unroll

@@ -167,7 +167,7 @@ def linear_lora(x, w, a, b, adapter, *, scale=None, b_layout: str = "nk", y=None
     at any stride that is a multiple of 8 elements, adapters packed; H, N and R
     multiples of 8.  adapter: int64 [T], negative: none; rows of one request lie
     best together.  scale: fp32 [L].  A row whose adapter is L or more is NaN.
-    Adapters must be finite: a row of another request may meet them times zero.
+    What an adapter holds, an infinity or NaN too, reaches the rows that name it alone.
     Nothing is recorded for autograd.  Enqueues on ``stream`` or torch's current
     stream.
     """

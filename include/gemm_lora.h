@@ -18,9 +18,9 @@
  * as a product tile goes over every adapter that occurs among its rows.  An adapter
  * that no row names is not read, and its da and db are zero.  A row whose adapter is
  * >= L has y and dx of NaN and no part in da and db: nothing is read out of range.
- * Adapters and w must be finite, also for the sake of other requests' rows (a row is
- * multiplied by zero with other adapters of its tile, and zero times infinity is not
- * zero).  What x, dy hold in one row never reaches another row or another adapter.
+ * What x and dy hold in one row, infinities and NaN too, never reaches another row or
+ * another adapter's da and db, and what an adapter holds reaches the rows that name it
+ * and no others.
  *
  * Arithmetic: products in fp32.  s and ds, the operands of the next products, are
  * rounded to the type once, after the scale, as tensors of the type would be (up to 256
