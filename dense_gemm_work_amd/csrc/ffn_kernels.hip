@@ -496,20 +496,18 @@ template <int DT, bool KC>
 hipError_t gate(int tile, const FfnGate &a, hipStream_t stream) {
     using L128 = Loop<DT, KC, true, 128, 128, 2, 2, 3, 2, true>;
     using L256 = Loop<DT, KC, true, 256, 256, 2, 4, 3, 2, true>;
-    using F128x32 = ThinLoop<DT, KC, true, 128, 32, 4, 1, true>;
-    using F128x64 = ThinLoop<DT, KC, true, 128, 64, 3, 1, true>;
-    switch (tile) {
-    case LT_128x128: return run_gate<L128>(a, ffn_gate<DT, L128>, stream);
-    case LT_256x256: return run_gate<L256>(a, ffn_gate<DT, L256>, stream);
-    case LT_128x32: return run_gate<F128x32>(a, ffn_gate_few<DT, F128x32>, stream);
-    case LT_128x64: return run_gate<F128x64>(a, ffn_gate_few<DT, F128x64>, stream);
-    default: break;
-    }
+    if (tile == LT_128x128) return run_gate<L128>(a, ffn_gate<DT, L128>, stream);
+    if (tile == LT_256x256) return run_gate<L256>(a, ffn_gate<DT, L256>, stream);
     if constexpr (KC) {   // halves of fewer than 64 rows: k contiguous only
         using F32 = ThinLoop<DT, true, true, 32, 32, 6, 1, true>;
         using F64 = ThinLoop<DT, true, true, 64, 64, 5, 1, true>;
         if (tile == LT_32x32) return run_gate<F32>(a, ffn_gate_few<DT, F32>, stream);
         if (tile == LT_64x64) return run_gate<F64>(a, ffn_gate_few<DT, F64>, stream);
+    } else {
+        using F128x32 = ThinLoop<DT, false, true, 128, 32, 4, 1, true>;
+        using F128x64 = ThinLoop<DT, false, true, 128, 64, 3, 1, true>;
+        if (tile == LT_128x32) return run_gate<F128x32>(a, ffn_gate_few<DT, F128x32>, stream);
+        if (tile == LT_128x64) return run_gate<F128x64>(a, ffn_gate_few<DT, F128x64>, stream);
     }
     return hipErrorInvalidValue;
 }

@@ -1029,7 +1029,7 @@ hipError_t run_few(const LoraProduct &a, const LoraLow &low, hipStream_t stream)
         using LN = typename decltype(n)::L;
         WideParams w = wide_params<L>(a);
         LowParams q = low_params<LN>(low);
-        if constexpr (KC && L::TQ == 32) {
+        if constexpr (KC && L::TQ == 32 && LN::TP != 32) {   // up to 32 ranks, so few rows' narrow products are made row by row
             if (a.x.rows <= VEC_T) {
                 w.g.splits = 1;
                 const int wide = a.P.rows / 8;
@@ -1054,10 +1054,10 @@ hipError_t few(int tile, const LoraProduct &a, const LoraLow &low, hipStream_t s
     default: return hipErrorInvalidValue;
     }
 }
+// The same where the operands' storage does not matter.
 template <class F>
-hipError_t with_wide(int dtype, int tile, bool kc, F &&f) {
-    if (kc) return dtype == 0 ? with_wide<0, true>(tile, f) : with_wide<1, true>(tile, f);
-    return dtype == 0 ? with_wide<0, false>(tile, f) : with_wide<1, false>(tile, f);
+hipError_t with_tile(int dtype, int tile, F &&f) {
+    return dtype == 0 ? with_wide<0, true>(tile, f) : with_wide<1, true>(tile, f);
 }
 
 OuterParams outer_params(const LoraOuter &a) {
@@ -1104,14 +1104,16 @@ LossTileShape lora_tile_shape(int tile) {
 }
 hipError_t launch_lora_product(int dtype, int tile, const LoraProduct &p, const LoraLowJoin &join, hipStream_t stream) {
     if (!p.x.kc || p.P.kc != p.f.first.kc || (p.splits > 1 && !p.slots) || (!p.partial && !p.slots)) return hipErrorInvalidValue;
-    return with_wide(dtype, tile, p.P.kc, [&](auto w) {
+    auto run = [&](auto w) {
         using W = decltype(w);
         using L = typename W::L;
         const WideParams q = wide_params<L>(p, join);
         const int joins = (q.join.blocks * 256 + L::NT - 1) / L::NT;
         hipLaunchKernelGGL((lora_product<W::DT, L, W::NS>), dim3((unsigned)(wide_blocks(q.g, q.whole) + joins)), dim3(L::NT), 0, stream, q);
         return hipGetLastError();
-    });
+    };
+    if (!p.P.kc) return dtype == 0 ? with_wide<0, false>(tile, run) : with_wide<1, false>(tile, run);
+    return with_tile(dtype, tile, run);
 }
 hipError_t launch_lora_few_join(int dtype, int tile, const LoraProduct &p, const LoraLow &low, hipStream_t stream) {
     WideParams q = wide_params<ThinLoop<0, true, true, 64, 32, 6>>(p);   // every tile of few rows has 64 columns
@@ -1136,7 +1138,7 @@ hipError_t launch_lora_few(int dtype, int tile, const LoraProduct &p, const Lora
     return dtype == 0 ? few<0, false>(tile, p, low, stream) : few<1, false>(tile, p, low, stream);
 }
 hipError_t launch_lora_join(int dtype, int tile, const LoraProduct &p, hipStream_t stream) {
-    return with_wide(dtype, tile, true, [&](auto w) {   // the operands' storage does not matter here
+    return with_tile(dtype, tile, [&](auto w) {
         using W = decltype(w);
         const WideParams q = wide_params<typename W::L>(p);
         hipLaunchKernelGGL((lora_join<W::DT, typename W::L>), dim3((unsigned)tail_blocks<typename W::L>(q)), dim3(256), 0, stream, q);
@@ -1166,7 +1168,7 @@ hipError_t launch_lora_outers(int dtype, const LoraOuter &da, const LoraOuter &d
         else hipLaunchKernelGGL(lora_outers<1>, dim3((unsigned)(qw.blocks + qn.blocks)), dim3(256), 0, stream, qw, qn);
         return dtype == 0 ? join_outers<0>(qw, qn, stream) : join_outers<1>(qw, qn, stream);
     }
-    return with_wide(dtype, tile, true, [&](auto x) {
+    return with_tile(dtype, tile, [&](auto x) {
         using W = decltype(x);
         const WideParams q = wide_params<typename W::L>(*tail);
         const int64_t blocks = tail_blocks<typename W::L>(q) + qw.blocks + qn.blocks;
