@@ -58,6 +58,14 @@ inline int overlapping(const Block &a, const Block &b) {
     return set_error(GEMM_ERR_INVALID, std::string(a.name) + " must not overlap " + b.name);
 }
 
+// What a call writes is apart from all else that it takes.
+inline int apart(const Blocks &s) {
+    for (int i = 0; i < s.written; ++i)
+        for (int j = i + 1; j < s.all; ++j)
+            if (overlap(s.b[i], s.b[j])) return overlapping(s.b[i], s.b[j]);
+    return GEMM_OK;
+}
+
 // The tile of a product of rows_p x rows_q over k and, where its k may be sliced,
 // the slices (of at least 8 slabs): the cheapest by a model of the time in us,
 //   rounds of resident workgroups x (slabs x slab time + fixed time) + joining,

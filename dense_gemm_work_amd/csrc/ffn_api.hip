@@ -88,16 +88,13 @@ int check_args(const gemm_ffn_args_t &a, bool backward) {
         if ((rc = check_ld(b.ld / size, b.row / size, fp32 ? unit32 : 8, b.name)) != GEMM_OK) return rc;
         if (b.begin() & 15) return set_error(GEMM_ERR_UNSUPPORTED, std::string(b.name) + " must be 16-byte aligned");
     }
-    if (a.T == 0) return GEMM_OK;
+    if (a.T == 0) return apart(s);   // a gradient of no rows is cleared
     if (!a.x || !a.w_gate || !a.w_up || !a.w_down) return bad("x, w_gate, w_up and w_down must be non-null");
     if (!backward && !a.y) return bad("y must be non-null");
     if (!backward && !a.gate != !a.up) return bad("gate and up are kept both or neither");
     if (backward && (!a.dy || !a.gate || !a.up)) return bad("dy, gate and up must be non-null");
     if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
-    for (int i = 0; i < s.written; ++i)
-        for (int j = i + 1; j < s.all; ++j)
-            if (overlap(s.b[i], s.b[j])) return overlapping(s.b[i], s.b[j]);
-    return GEMM_OK;
+    return apart(s);
 }
 
 // Tile of the kernel that makes h from x.  Its P rows are both matrices' features.

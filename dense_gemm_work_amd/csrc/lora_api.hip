@@ -93,15 +93,12 @@ int check_args(const gemm_lora_args_t &a, bool backward) {
         if (s.b[i].begin() & (unit - 1))
             return set_error(GEMM_ERR_UNSUPPORTED, std::string(s.b[i].name) + " must be " + std::to_string(unit) + "-byte aligned");
     }
-    if (a.T == 0) return GEMM_OK;
+    if (a.T == 0) return apart(s);   // a gradient of no rows is cleared
     if (!a.x || !a.w || !a.a || !a.b || !a.adapter) return bad("x, w, a, b and adapter must be non-null");
     if (!backward && !a.y) return bad("y must be non-null");
     if (backward && !a.dy) return bad("dy must be non-null");
     if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
-    for (int i = 0; i < s.written; ++i)
-        for (int j = i + 1; j < s.all; ++j)
-            if (overlap(s.b[i], s.b[j])) return overlapping(s.b[i], s.b[j]);
-    return GEMM_OK;
+    return apart(s);
 }
 
 // Few rows of small ranks with an adapter for at least every fourth of them: the narrow products

@@ -91,7 +91,7 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
         if (a.dw && (rc = check_ld(lddw, row_of_w(a), dw32 ? 4 : 8, "dw")) != GEMM_OK) return rc;
         if (a.dw && (reinterpret_cast<uintptr_t>(a.dw) & 15)) return set_error(GEMM_ERR_UNSUPPORTED, "dw must be 16-byte aligned");
     }
-    if (a.T == 0) return GEMM_OK;
+    if (a.T == 0) return apart(blocks_of(a, backward));   // a gradient of no rows is cleared
     if (!a.x || !a.w || !a.lse) return bad("x, w and lse must be non-null");
     if ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w) | reinterpret_cast<uintptr_t>(a.dx)) & 15)
         return set_error(GEMM_ERR_UNSUPPORTED, "x, w and dx must be 16-byte aligned");
@@ -100,11 +100,7 @@ int check_args(const gemm_loss_args_t &a, bool backward) {
     if (a.workspace && reinterpret_cast<uintptr_t>(a.workspace) & 255) return bad("a caller workspace must be 256-byte aligned");
     if (!backward && !a.loss) return bad("loss must be non-null");
     if (backward && !a.grad) return bad("grad must be non-null");
-    const Blocks s = blocks_of(a, backward);
-    for (int i = 0; i < s.written; ++i)
-        for (int j = i + 1; j < s.all; ++j)
-            if (overlap(s.b[i], s.b[j])) return overlapping(s.b[i], s.b[j]);
-    return GEMM_OK;
+    return apart(blocks_of(a, backward));
 }
 
 // Byte offsets of a call's parts in its workspace.
