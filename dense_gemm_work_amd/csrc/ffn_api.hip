@@ -45,11 +45,13 @@ int dw_size(const gemm_ffn_args_t &a) { return a.dw_type == GEMM_FFN_DW_SAME ? 2
 Blocks blocks_of(const gemm_ffn_args_t &a, bool backward) {
     Blocks s;
     const Shape in = shape_in(a), down = shape_down(a);
+    // strides that check_ld refuses stay so in bytes, which could pass 64 bits
+    auto stride = [](int64_t ld, int64_t row) { return std::clamp(or_packed(ld, row), int64_t(-1), MAX_LD + 1); };
     auto rows16 = [&](const void *p, int64_t rows, int64_t row, int64_t ld, const char *name) {
-        s.add(p, rows, row * 2, or_packed(ld, row) * 2, name);
+        s.add(p, rows, row * 2, stride(ld, row) * 2, name);
     };
     auto grad = [&](const void *p, Shape w, int64_t ld, const char *name) {
-        s.add(p, w.rows, w.row * dw_size(a), or_packed(ld, w.row) * dw_size(a), name);
+        s.add(p, w.rows, w.row * dw_size(a), stride(ld, w.row) * dw_size(a), name);
     };
     if (backward) {
         rows16(a.dx, a.T, a.H, a.lddx, "dx");
