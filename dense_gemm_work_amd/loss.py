@@ -25,6 +25,7 @@ from . import _check, _lib, layout_word, stream_word
 
 try:
     import torch
+    from torch.autograd import forward_ad
 except ImportError:   # the C entry points need no torch
     torch = None
 
@@ -152,6 +153,8 @@ def _warn_of_no_graph(*inputs, what="the loss"):
     if torch.is_grad_enabled() and any(t.requires_grad for t in inputs):
         warnings.warn(f"{what} is not recorded for autograd: its gradients come from the _backward call "
                       "(pass detached tensors, or call under torch.no_grad())", stacklevel=3)
+    if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in inputs):
+        warnings.warn(f"{what} has no forward-mode derivative: the tangents of its inputs are dropped", stacklevel=3)
 
 
 def _xent(a, x, target, ignore_index, z_loss):
