@@ -120,7 +120,8 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     const int64_t groups = ceil_div(std::max<int64_t>(a.T, 1), 64) * ceil_div(a.R, dgw::lora_low_rows(dgw::lora_low_tile(a.R, kc)));
     const int64_t most = std::min<int64_t>(a.adapters, std::min<int64_t>(std::max<int64_t>(a.T, 1), 64));
     // Few rows': one a CU, as the wide product's run beside them (96 x 4096 x 4096, 20 adapters
-    // of rank 16: 19 us, with two 23; 96 of rank 64: 51 and 57).
+    // of rank 16: 19 us, with two 23; 96 of rank 64: 51 and 57).  More rows': two, of which
+    // tiles of 64 ranks run one after the other, as one fits beside its list.
     const int64_t budget = a.T <= 256 ? cus : 2 * cus;
     Low l;
     l.lists = (int)std::max<int64_t>(1, std::min(most, budget / groups));

@@ -159,8 +159,12 @@ __device__ __forceinline__ void low_block(const LowParams &p, int id, char *lds,
     }
 }
 
+// Waves resident per SIMD of a workgroup of four with `bytes` of LDS for its tiles and a list.
+// The list makes 64 x 64 tiles of five stages, half of a CU's LDS, one workgroup a CU.
+constexpr int waves_with_list(int bytes) { return 2 * (bytes + (int)sizeof(List<64>)) <= 160 * 1024 ? 2 : 1; }
+
 template <class L>
-__global__ __launch_bounds__(L::NT, L::WAVES) void lora_low(LowParams p) {
+__global__ __launch_bounds__(L::NT, waves_with_list(L::LDS_BYTES)) void lora_low(LowParams p) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES];
     __shared__ List<L::TQ> list;
     low_block<L>(p, (int)blockIdx.x, lds, list);
@@ -172,7 +176,7 @@ __global__ __launch_bounds__(L::NT, L::WAVES) void lora_low(LowParams p) {
 // gradients' call for 96 x 4096 x 4096 with 64 adapters of rank 16 takes 54 us, not 46.)
 template <int DT_, bool KC>
 struct RowLow {
-    static constexpr int DT = DT_, TP = 8, TQ = 64, NT = 256, WAVES = 2, LDS_BYTES = 4 * 8 * 4;
+    static constexpr int DT = DT_, TP = 8, TQ = 64, NT = 256, LDS_BYTES = 4 * 8 * 4;
 };
 template <class L>
 struct IsRowLow : std::false_type {};
@@ -237,7 +241,7 @@ __device__ __forceinline__ void mask_block(const LoraRows &r, int id, uint64_t *
 // Backward: both narrow products (one factor has k contiguous, the other its rows) and
 // the rows' masks in one launch.
 template <class LK, class LR>
-__global__ __launch_bounds__(256, LK::WAVES < LR::WAVES ? LK::WAVES : LR::WAVES) void lora_lows(LowParams k, LowParams r, uint64_t *masks) {
+__global__ __launch_bounds__(256, waves_with_list(LK::LDS_BYTES > LR::LDS_BYTES ? LK::LDS_BYTES : LR::LDS_BYTES)) void lora_lows(LowParams k, LowParams r, uint64_t *masks) {
     __shared__ __attribute__((aligned(16))) char lds[LK::LDS_BYTES > LR::LDS_BYTES ? LK::LDS_BYTES : LR::LDS_BYTES];
     __shared__ List<LK::TQ> list;
     static_assert(LK::TQ == LR::TQ && LK::NT == 256 && LR::NT == 256, "one list, one size of workgroup");
@@ -603,7 +607,7 @@ __global__ __launch_bounds__(256) void lora_join(WideParams p) {
 // of rank 16: 21 us; the adapters in the product's tiles, after the narrow product's launch: 46.)
 // ---------------------------------------------------------------------------
 template <class L, class LN>
-__global__ __launch_bounds__(256, L::WAVES < LN::WAVES ? L::WAVES : LN::WAVES) void lora_few(WideParams w, LowParams n, int wide) {
+__global__ __launch_bounds__(256, waves_with_list(L::LDS_BYTES > LN::LDS_BYTES ? L::LDS_BYTES : LN::LDS_BYTES)) void lora_few(WideParams w, LowParams n, int wide) {
     __shared__ __attribute__((aligned(16))) char lds[L::LDS_BYTES > LN::LDS_BYTES ? L::LDS_BYTES : LN::LDS_BYTES];
     __shared__ List<LN::TQ> list;
     static_assert(L::NT == 256 && LN::NT == 256, "one size of workgroup");
