@@ -106,7 +106,10 @@ int check_args(const gemm_lora_args_t &a, bool backward) {
 // for 96 x 4096 x 4096, 64 adapters of rank 16: 46 us, on tiles 64; 200 x 2048 x 4096, 50
 // of rank 32: 64 us, 77; its forward call 32 both ways; 250 x 4096 x 4096 with two of
 // rank 16, which stays with the tiles: 25 us, row by row 27.5; 96 x 4096 x 4096 with 96 of
-// rank 64, which does too: 97 and 122 us (gradients).
+// rank 64, which does too: 97 and 122 us (gradients).  The pool's size stands for the
+// adapters that the rows name, which the host does not know; a pool of 64 that rows name
+// one of loses nothing by it: 200 x 4096 x 4096, rank 16, 26 us row by row and 30 on tiles
+// (gradients 41 and 57; a pool of that one: 23 and 34).
 bool low_by_rows(const gemm_lora_args_t &a) {
     return a.T <= dgw::LORA_FEW_T && a.R <= 32 && 4 * std::min<int64_t>(a.adapters, a.T) >= a.T;
 }
@@ -129,8 +132,13 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
     // workgroups that find none cost about what they wait for: at most four share a group's
     // adapters (the gradients' call for 1327 x 2536 x 5288 with 47 adapters of rank 8: 99 us, with 24
     // lists 136; 1000 x 2048 x 4096 with 64 mixed row by row: 254 us, eight lists 263, 24 lists
-    // 328, two 273), and many groups take two slices (8192 x 4096, rank 64: 41 us, in four
-    // slices 46, one 62).
+    // 328, two 273).  On both sides of few rows, x 4096 x 4096, rank 40, forward: 256 rows,
+    // 64 mixed 61 us, with 24 lists 79, with four 258; 16 packed 32 from two lists on; 257 rows,
+    // 64 mixed 83 in four and in 24 lists, 73 in six, 190 in one; 16 packed 36, in 24 lists 37.
+    // Up to nine slices fill the CUs that few groups leave idle (x 4096 x 4096, four of rank 64:
+    // 512 rows 41 us, in one slice 53, four 43, 16 46; gradients of 1024 rows 80, in one 87, four
+    // 78, 16 91); many groups take two (gradients of 4096 rows 150, in one 154, four 161, nine
+    // 182; of 8192 rows 283, 274, 303, 343; between them 2048 rows 106 in eight, 95 in two).
     if (a.T > 256) l.lists = std::min(l.lists, 4);
     const int64_t found = a.T <= 256 ? l.lists : std::min(l.lists, 2), most_splits = groups >= 64 ? 2 : 9;
     l.splits = (int)std::max<int64_t>(1, std::min({ceil_div(k, 64) / 2, budget / (groups * found), most_splits}));
@@ -141,7 +149,7 @@ Low low_plan(const gemm_lora_args_t &a, int64_t k, bool kc, int cus) {
 // slices the rest: the cheapest by choose()'s model of a tile's time (with 4 us more for the
 // adapters) and of the join, for slices of every tile and for whole rounds of workgroups
 // with slices of what is left over.  5000 x 4096 x 8192 on 256 CUs: 640 tiles of 256 x 256,
-// the last 128 in two slices, 293 us in the model; in three rounds of whole tiles 330.
+// the last 128 in two slices, 299 us in the model; in three rounds of whole tiles 330.
 struct Wide {
     int tile = dgw::LP_128x128, splits = 1;
     int64_t whole = 0;   // tiles
@@ -193,7 +201,8 @@ Wide out_plan(const gemm_lora_args_t &a, int64_t rows_p, int64_t k, bool few, in
 // adapter costs about half a microsecond, and there are min(adapters, T) at most.  In the
 // join, 238 x 296 x 6400 with 63 adapters of rank 24: 34 us, in the tiles 61; 96 x 4096 x
 // 4096 with 64 of rank 16: 21 and 46; 256 x 8192 x 8192 with two of rank 32: 73 us, in the
-// tiles 63.
+// tiles 63.  Of a pool of 64 that the rows name one of (see low_by_rows): 200 x 4096 x 4096,
+// rank 16, 26 us, in the tiles 40.
 bool few_rows(const gemm_lora_args_t &a, int64_t wide) {
     if (a.T > dgw::LORA_FEW_T || a.R > dgw::LORA_FEW_R) return false;
     const double join = (double)(a.T * a.R) * (double)wide * 2.0 / 8e6;
