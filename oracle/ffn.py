@@ -14,7 +14,10 @@ or du), each the roundings of a straightforward fp32 evaluation that rounds h, d
 du and the results once:
 
 * a product over K is a chain of K / 16 matrix instructions, each of which rounds
-  its sum of 16 products and the running value, and of at most 64 slices:
+  its sum of 16 products and the running value.  Cut into S slices of at least 128
+  of K each, it is a chain of K / (16 S) and S sums, with S <= K / 128 never more
+  than K / 16 + 8.  64 more cover the fixed parts: halves of a chain that are joined,
+  eight products a lane and the lanes' sums where rows are multiplied one by one:
   2 (K / 16 + 8 + 64) f sum |a||b|;
 * act: silu's exponential has an argument of up to |g| log2 e, rounded twice (a
   relative error of 2 |g| f), and a handful of roundings follow: (8 + 2 |g|) f |act|,
@@ -38,13 +41,13 @@ import torch
 F32 = 2.0 ** -24
 HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": F32}
 SMALLEST = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}   # half the smallest step
-SLICES = 64
+FIXED = 64
 STEEPEST = 1.13   # the largest slope: gelu's, 1.1290
 
 
 def product_error(a, b_t, K):
     """Bound of a . b_t accumulated in fp32."""
-    return 2.0 * (K / 16 + 8 + SLICES) * F32 * (a.abs() @ b_t.abs())
+    return 2.0 * (K / 16 + 8 + FIXED) * F32 * (a.abs() @ b_t.abs())
 
 
 def activation(g, act):

@@ -12,7 +12,10 @@ f = 2^-24: half a step of fp32), each the roundings of a straightforward fp32
 evaluation that rounds s, ds and the results once:
 
 * a product over K is a chain of K / 16 matrix instructions, each of which rounds
-  its sum of 16 products and the running value, and of at most 64 slices:
+  its sum of 16 products and the running value.  Cut into S slices of at least 128
+  of K each, it is a chain of K / (16 S) and S sums, with S <= K / 128 never more
+  than K / 16 + 8.  64 more cover the fixed parts: halves of a chain that are joined,
+  eight products a lane and the lanes' sums where rows are multiplied one by one:
   2 (K / 16 + 8 + 64) f sum |a||b|.  Zeros from other rows or adapters add nothing;
   a row's sum passes one instruction pair more for each adapter of its tile, at
   most 256 of ranks of at most 64 slabs, that add zero and round nothing.
@@ -28,12 +31,12 @@ import torch
 F32 = 2.0 ** -24
 HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": F32}
 SMALLEST = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}   # half the smallest step
-SLICES = 64
+FIXED = 64
 
 
 def product(a, b):
     """a . b and the bound of its fp32 evaluation's error."""
-    return a @ b, 2.0 * (a.shape[1] / 16 + 8 + SLICES) * F32 * (a.abs() @ b.abs())
+    return a @ b, 2.0 * (a.shape[1] / 16 + 8 + FIXED) * F32 * (a.abs() @ b.abs())
 
 
 def narrow(x, factor, c, dtype):
