@@ -5,7 +5,7 @@
 // slices and joins cost is latency.  Four waves share a few rows of the weights, a
 // quarter of k each: 16 bytes a lane straight into registers, fp32 multiply-adds, one
 // reduction at the end.  Every load of a workgroup is in flight at once, and the
-// result needs no second launch.  (One token, 1536 x 4096: gate and up 8.3 us on 32 x 32
+// result needs no launch that joins slices.  (One token, 1536 x 4096: gate and up 8.3 us on 32 x 32
 // tiles.)
 #pragma once
 
