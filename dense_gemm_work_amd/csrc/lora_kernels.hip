@@ -347,7 +347,8 @@ struct Extra {
     // where the sums hold one, they are made again with `scrub`, the finite part as before and
     // the rest added to the adapter's own rows.  (That the sums are looked at: 331.5 us instead
     // of 331 at 5000 x 4096 x 8192, 24 of rank 64; 118.6 instead of 113.9 at 1000 x 2048 x 4096
-    // with 64 of rank 16 mixed row by row.)
+    // with 64 of rank 16 mixed row by row.  One broken adapter: 1160 and 340 us; a broken row of
+    // x: 325 and 178.)
     static constexpr bool HOLD = L::RB * L::CB <= 8, KC = OpP::which(1, 0) == 0;
     static __device__ __forceinline__ bool nonfinite(uint32_t v) {
         constexpr uint32_t EXPONENT = DT == 0 ? 0x7f80u : 0x7c00u;
@@ -356,15 +357,21 @@ struct Extra {
     static __device__ __forceinline__ u32x4 masked(u32x4 v, bool keep) {
         return u32x4{keep ? v[0] : 0u, keep ? v[1] : 0u, keep ? v[2] : 0u, keep ? v[3] : 0u};
     }
-    // scrub: an adapter's slab without its infinities and NaN.  Between barriers.
-    static __device__ __forceinline__ void clear_nonfinite(char *stage) {
+    // scrub: an adapter's slab without its infinities and NaN, and whether the thread saw any.
+    // Between barriers.
+    static __device__ __forceinline__ bool clear_nonfinite(char *stage) {
+        bool any = false;
         for (int f = threadIdx.x; f < STAGE / 16; f += L::NT) {
             u32x4 v = *reinterpret_cast<u32x4 *>(stage + 16 * f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] &= (nonfinite(v[i]) ? 0u : 0xffffu) | (nonfinite(v[i] >> 16) ? 0u : 0xffff0000u);
+            for (int i = 0; i < 4; ++i) {
+                any |= nonfinite(v[i]) || nonfinite(v[i] >> 16);
+                v[i] &= (nonfinite(v[i]) ? 0u : 0xffffu) | (nonfinite(v[i] >> 16) ? 0u : 0xffff0000u);
+            }
             *reinterpret_cast<u32x4 *>(stage + 16 * f) = v;
         }
         __syncthreads();
+        return any;
     }
     // scrub: what the slab's infinities and NaN add to the rows of their own adapter (a slice
     // adds those of every adapter: twice is the same).
@@ -400,7 +407,18 @@ struct Extra {
             }
         }
     }
-    // Whether a sum of the workgroup's is infinite or NaN.  The LDS is free, before and after.
+    // Whether any thread of the workgroup says so.  The LDS is free, before and after.
+    static __device__ __forceinline__ bool any_thread(bool mine, char *lds) {
+        int *flag = reinterpret_cast<int *>(lds);
+        if (threadIdx.x == 0) *flag = 0;
+        __syncthreads();
+        if (mine) *flag = 1;
+        __syncthreads();
+        const bool any = __builtin_amdgcn_readfirstlane(*flag);
+        __syncthreads();
+        return any;
+    }
+    // Whether a sum of the workgroup's is infinite or NaN.
     static __device__ __forceinline__ bool any_nonfinite(const typename L::Acc &acc, char *lds) {
         float zero = 0.0f;
 #pragma unroll
@@ -409,14 +427,7 @@ struct Extra {
             for (int j = 0; j < L::CB; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) zero = __builtin_fmaf(acc.v[b][j][e], 0.0f, zero);
-        int *flag = reinterpret_cast<int *>(lds);
-        if (threadIdx.x == 0) *flag = 0;
-        __syncthreads();
-        if (zero != 0.0f) *flag = 1;
-        __syncthreads();
-        const bool any = __builtin_amdgcn_readfirstlane(*flag);
-        __syncthreads();
-        return any;
+        return any_thread(zero != 0.0f, lds);
     }
 
     static __device__ __forceinline__ void run(const L &loop, char *lds, const WideParams &p, int64_t p0, int64_t q0,
@@ -470,6 +481,7 @@ struct Extra {
 #pragma unroll
                     for (int j = 0; j < L::CB; ++j) q[step][j] = narrow(step, j);
             int st = 0;
+            bool cleared = false;
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -494,7 +506,7 @@ struct Extra {
                         }
                     }
                 } else {
-                    if (scrub) clear_nonfinite(lds + o);
+                    if (scrub) cleared |= clear_nonfinite(lds + o);
 #pragma unroll
                     for (int step = 0; step < 2; ++step) {
 #pragma unroll
@@ -515,7 +527,7 @@ struct Extra {
                 st = st + 1 == NS ? 0 : st + 1;
             }
             if constexpr (!HOLD)
-                if (scrub) {
+                if (scrub && any_thread(cleared, lds)) {
                     add_nonfinite(loop, lds + ROWS_AT, p, p0, slab, id, acc);
                     __syncthreads();   // the rows have been read
                 }
